@@ -23,6 +23,14 @@
  *   gptq_dequant_order            channels sorted by group, codes repacked
  *   gptq_dequant_matmul_ordered   y = x W^T on the reordered layer
  *
+ * A model of quantized layers is served with
+ *
+ *   gptq_quantize_tokens, gptq_integer_weight, gptq_integer_matmul
+ *                             y = x W^T in 8-bit integers for layers with one group per channel
+ *   gptq_cache_write, gptq_cache_read
+ *                             a paged key/value cache in 8- or 4-bit codes
+ *   gptq_cache_attention      attention of new tokens over that cache
+ *
  * Conventions shared by every call
  *   - All array pointers are DEVICE pointers on the current HIP device; the
  *     caller owns every buffer (inputs, outputs, workspaces).  The library
@@ -64,7 +72,11 @@ typedef enum {
 
 /* Element types of X, W and x, passed as int32_t (any other value:
  * GPTQ_ERR_INVALID_ARG, or 0 from a size query). */
-typedef enum { GPTQ_F32 = 0, GPTQ_BF16 = 1 } gptq_dtype;
+typedef enum {
+  GPTQ_F32 = 0,
+  GPTQ_BF16 = 1,
+  GPTQ_I8 = 2 /* codes of gptq_quantize_tokens; gptq_integer_matmul's x only */
+} gptq_dtype;
 
 /*
  * Quantization parameters, named after BaseQuantizeConfig (AutoGPTQ examples
@@ -298,6 +310,141 @@ gptq_status gptq_dequant_matmul_ordered(const void* x, int32_t xt, int64_t m, in
                                         const int32_t* qweight, const float* scales, const int32_t* zeros,
                                         const int32_t* g_idx, const int32_t* order, int32_t bits, int64_t d_out,
                                         int32_t n_groups, float* y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Integer codes of activations: for each token (row) of x, with
+ * amax = max |x|, scale = amax / 127 in fp32 and
+ * codes[t, k] = the integer nearest to 127 x[t, k] / amax, ties to the even
+ * one (the exact quotient decides; chapter 5, section 5.1.1, symmetric), so
+ * codes lie in [-127, 127] and the value held is scale * code.
+ * A row of zeros has scale 0.  A row that holds a NaN or an infinity has
+ * scale NaN and codes 0, so everything computed from it is NaN.
+ *   x        [n_tokens, ldx] bf16 or fp32; the first d_in entries of a row are
+ *            used (any d_in up to 2^20 and any alignment; 16-byte aligned rows
+ *            and d_in % 8 == 0 are read and written in whole vectors)
+ *   codes    [n_tokens, d_in] int8, scales [n_tokens] fp32
+ *   sums_or_null  optional [n_tokens] int32: the sum of a row's codes
+ *            (gptq_integer_matmul needs it for layers with offsets)
+ * 0 <= n_tokens <= 2^30.
+ */
+gptq_status gptq_quantize_tokens(const void* x, int32_t xt, int64_t n_tokens, int64_t d_in, int64_t ldx, int8_t* codes,
+                                 float* scales, int32_t* sums_or_null, void* stream);
+
+/*
+ * A layer with one group per output channel (group_size -1) laid out for
+ * gptq_integer_matmul, once: w[n, k] = code(n, k) - 2^(bits-1) as int8 rows and
+ * offsets[n] = zeros[n] - 2^(bits-1), so that W[n, k] = scale[n] (w[n, k] -
+ * offsets[n]).  A symmetric layer's offsets are all 0.
+ *   qweight  [d_in * bits / 32, d_out] int32 as written by gptq_pack
+ *   zeros    [d_out] int32 (the one row of gptq_quantize_layer's zeros)
+ *   w        [d_out, d_in] int8, 16-byte aligned; offsets [d_out] int32
+ * Requires d_in % 32 == 0.
+ */
+gptq_status gptq_integer_weight(const int32_t* qweight, const int32_t* zeros, int32_t bits, int64_t d_in, int64_t d_out,
+                                int8_t* w, int32_t* offsets, void* stream);
+
+/*
+ * y = x W^T in 8-bit integers, a scale per token and per output channel:
+ *   y[t, n] = x_scale[t] w_scale[n] (sum_k cx[t, k] w[n, k] - offset[n] sum_k cx[t, k])
+ * The sums are exact 32-bit integers; the result is rounded when the sum
+ * becomes fp32, at each scale, and to y's type (relative 3 2^-24, and 2^-9 for
+ * bf16).  Deterministic, and independent of how the work is split.
+ *   x        [m, ldx]: bf16 or fp32, quantized as by gptq_quantize_tokens in
+ *            the workspace (x_scales and x_sums are not read); or GPTQ_I8 codes
+ *            with x_scales [m] and, for layers with offsets, x_sums [m].
+ *            GPTQ_I8: 16-byte aligned, ldx % 16 == 0, ldx <= 2^22
+ *   w        [d_out, d_in] int8, 16-byte aligned; w_scales [d_out] fp32;
+ *            w_offsets_or_null [d_out] int32 in [-128, 128]
+ *   y        [m, d_out] fp32 or bf16 (yt)
+ *   ws       device workspace of gptq_integer_workspace_size(m, xt, d_in, d_out)
+ *            bytes, 256-byte aligned; may be null when that size is 0
+ * Requires d_in % 32 == 0, d_in <= 2^16 (so the sums cannot overflow) and
+ * 0 <= m <= 2^30.
+ */
+size_t gptq_integer_workspace_size(int64_t m, int32_t xt, int64_t d_in, int64_t d_out);
+gptq_status gptq_integer_matmul(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                                int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
+                                const int32_t* w_offsets_or_null, int64_t d_out, void* y, int32_t yt, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * A paged key/value cache in integer codes.  A row (one head of one token's
+ * key or value) is held as codes and one fp32 scale by the rule of
+ * gptq_quantize_tokens, with 127 for 8 bits and 7 for 4.
+ *   k_codes, v_codes    [n_pages, n_kv_heads, page_size, head_dim * bits / 8]
+ *            bytes: int8 codes, or two 4-bit codes a byte (code + 8; the lower
+ *            dimension in the low nibble)
+ *   k_scales, v_scales  [n_pages, n_kv_heads, page_size] fp32
+ * All four device pointers 16-byte aligned.  bits 4 or 8; head_dim a multiple
+ * of 16 in [16, 256]; page_size 16, 32, 64, 128 or 256; 1 <= n_pages < 2^31;
+ * 1 <= n_kv_heads <= 2^16.
+ * A slot is a token's place: page * page_size + offset in the page.
+ */
+typedef struct {
+  int64_t n_pages;
+  int32_t page_size;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t bits;
+  void* k_codes;
+  void* v_codes;
+  float* k_scales;
+  float* v_scales;
+} gptq_cache;
+
+/*
+ * Quantizes the keys and values of n_tokens tokens into their slots.
+ *   k, v     token t, head h at element t * ldk + h * head_dim; bf16 or fp32,
+ *            16-byte aligned, ldk and ldv multiples of 8 (bf16) or 4 (fp32)
+ *   slots    [n_tokens] int64; a slot outside [0, n_pages * page_size) is
+ *            skipped (-1 marks padding).  Slots of one call have to differ: of
+ *            tokens with the same slot, codes and scale may come from different ones
+ * 0 <= n_tokens <= 2^30, n_tokens * n_kv_heads <= 2^33.
+ */
+gptq_status gptq_cache_write(const gptq_cache* cache, const void* k, const void* v, int32_t xt, int64_t n_tokens,
+                             int64_t ldk, int64_t ldv, const int64_t* slots, void* stream);
+
+/*
+ * The values held in the given slots: scale * code in fp32, rounded once for
+ * bf16.  k, v [n_tokens, n_kv_heads, head_dim] contiguous, 16-byte aligned;
+ * a slot outside the cache gives zeros; the same slot may be read many times.
+ */
+gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64_t n_tokens, void* k, void* v, int32_t yt,
+                            void* stream);
+
+/*
+ * Attention of new tokens over the cache, into which their own keys and
+ * values have been written.  Sequence i has the new tokens
+ * q_starts[i] .. q_starts[i + 1] - 1 and kv_lens[i] keys with those of the new
+ * tokens; new token t of n sees the keys 0 .. kv_lens[i] - n + t:
+ *   out = sum_j p_j v_j,  p = softmax_j(scale q . k_j),  k_j, v_j the held values
+ * Query head h reads key head h / (n_heads / n_kv_heads).  One new token per
+ * sequence is decoding, n = kv_len a whole prompt; both may stand in one call.
+ *   q        token t, head h at element t * ldq + h * head_dim, bf16 (qt
+ *            GPTQ_BF16), 16-byte aligned, ldq % 8 == 0; out likewise with ldo
+ *   page_table  [n_seq, pages_per_seq] int32: page of keys page_size * j ..
+ *            of sequence i at [i, j]; entries past a sequence's length are not read
+ *   q_starts [n_seq + 1] int32, non-decreasing; kv_lens [n_seq] int32
+ *   scale    > 0 and finite
+ * A token that sees no key (kv_len < n) gets zeros.  Rows of out outside
+ * [q_starts[0], q_starts[n_seq]) are left as they were.  Starts and lengths
+ * are clamped to n_tokens and pages_per_seq * page_size, and the keys of a page
+ * entry outside [0, n_pages) count as hidden, so no value in these arrays leads
+ * outside the buffers.  A key or value with a NaN scale makes the tokens that
+ * see it NaN.
+ * Products and sums are fp32; p_j times the value's scale is rounded to bf16
+ * for the second product (relative 2^-9 each).  Deterministic.
+ *   ws       device workspace of gptq_attention_workspace_size bytes, 256-byte
+ *            aligned (results of key splits); may be null when that size is 0
+ * Requires n_heads % n_kv_heads == 0, n_tokens * n_heads < 2^30,
+ * n_seq <= 2^20, n_seq * n_kv_heads < 2^30 and pages_per_seq * page_size <= 2^30.
+ */
+size_t gptq_attention_workspace_size(const gptq_cache* cache, int64_t n_tokens, int32_t n_heads, int32_t n_seq,
+                                     int64_t pages_per_seq);
+gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
+                                 int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
+                                 const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale, void* out,
+                                 int64_t ldo, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Per-phase launch timing, a measurement aid (not part of the solve; the pages

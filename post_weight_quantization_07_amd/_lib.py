@@ -17,14 +17,16 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq.so")
 
 GPTQ_OK, GPTQ_ERR_INVALID_ARG, GPTQ_ERR_NOT_SPD, GPTQ_ERR_HIP, GPTQ_ERR_WORKSPACE, GPTQ_ERR_TOO_LARGE = range(6)
-GPTQ_F32, GPTQ_BF16 = 0, 1
+GPTQ_F32, GPTQ_BF16, GPTQ_I8 = 0, 1, 2
 
 EXPORTS = ("gptq_config_validate", "gptq_status_string", "gptq_hessian_workspace_size",
            "gptq_hessian_accumulate", "gptq_prepare_workspace_size", "gptq_prepare_hinv",
            "gptq_workspace_size", "gptq_quantize_layer", "gptq_pack", "gptq_dequant_workspace_size",
            "gptq_dequant_matmul", "gptq_dequant_order", "gptq_dequant_ordered_workspace_size",
            "gptq_dequant_matmul_ordered", "gptq_dequant_scratch_bytes", "gptq_dequant_noalloc_need",
-           "gptq_dequant_matmul_noalloc", "gptq_phase_timing", "gptq_phase_count", "gptq_phase_name",
+           "gptq_dequant_matmul_noalloc", "gptq_quantize_tokens", "gptq_integer_weight",
+           "gptq_integer_workspace_size", "gptq_integer_matmul", "gptq_cache_write", "gptq_cache_read",
+           "gptq_attention_workspace_size", "gptq_cache_attention", "gptq_phase_timing", "gptq_phase_count", "gptq_phase_name",
            "gptq_phase_read")
 
 
@@ -48,6 +50,12 @@ class _CConfig(ctypes.Structure):
                 ("block_size", c_int32)]
 
 
+class _CCache(ctypes.Structure):
+    _fields_ = [("n_pages", c_int64), ("page_size", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("bits", c_int32), ("k_codes", c_void_p), ("v_codes", c_void_p), ("k_scales", c_void_p),
+                ("v_scales", c_void_p)]
+
+
 _LIB = None
 
 
@@ -59,7 +67,7 @@ def _lib():
                               "or python -m post_weight_quantization_07_amd.build")
         lib = ctypes.CDLL(LIB_PATH)
         vp, i64, sz = c_void_p, c_int64, c_size_t
-        cfgp = ctypes.POINTER(_CConfig)
+        cfgp, cachep = ctypes.POINTER(_CConfig), ctypes.POINTER(_CCache)
         sig = {
             "gptq_config_validate": (c_int32, [cfgp]),
             "gptq_status_string": (ctypes.c_char_p, [c_int32]),
@@ -82,6 +90,16 @@ def _lib():
             "gptq_dequant_noalloc_need": (sz, [i64, c_int32, i64, c_int32, i64]),
             "gptq_dequant_matmul_noalloc": (c_int32, [vp, c_int32, i64, i64, vp, vp, vp, vp, c_int32, i64, c_int32,
                                                       vp, vp]),
+            "gptq_quantize_tokens": (c_int32, [vp, c_int32, i64, i64, i64, vp, vp, vp, vp]),
+            "gptq_integer_weight": (c_int32, [vp, vp, c_int32, i64, i64, vp, vp, vp]),
+            "gptq_integer_workspace_size": (sz, [i64, c_int32, i64, i64]),
+            "gptq_integer_matmul": (c_int32, [vp, c_int32, vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, c_int32, vp, sz,
+                                              vp]),
+            "gptq_cache_write": (c_int32, [cachep, vp, vp, c_int32, i64, i64, i64, vp, vp]),
+            "gptq_cache_read": (c_int32, [cachep, vp, i64, vp, vp, c_int32, vp]),
+            "gptq_attention_workspace_size": (sz, [cachep, i64, c_int32, c_int32, i64]),
+            "gptq_cache_attention": (c_int32, [cachep, vp, c_int32, i64, i64, c_int32, vp, i64, vp, vp, c_int32, c_float,
+                                               vp, i64, vp, sz, vp]),
             "gptq_phase_timing": (c_int32, [c_int32]),
             "gptq_phase_count": (c_int32, []),
             "gptq_phase_name": (ctypes.c_char_p, [c_int32]),
@@ -400,3 +418,285 @@ def gptq_dequant_matmul_ordered(x: torch.Tensor, qweight: torch.Tensor, scales: 
                                               n_groups, _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
            "gptq_dequant_matmul_ordered")
     return y
+
+
+# --------------------------------------------------------------------------
+# serving: the product in 8-bit integers, the quantized cache, its attention
+# --------------------------------------------------------------------------
+
+_TYPE = {torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
+
+
+def _on_device(what: str, *ts) -> int:
+    """The index of the current device, on which every given tensor has to lie."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what}: the tensors must be on the current GPU (cuda:{dev})")
+    return dev
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
+
+
+def _type_code(what: str, dtype: torch.dtype) -> int:
+    code = _TYPE.get(dtype)
+    if code is None:
+        raise ValueError(f"{what}: unsupported dtype {dtype}: expected bfloat16 or float32")
+    return code
+
+
+def gptq_quantize_tokens(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                         sums: Optional[torch.Tensor] = None, stream=None):
+    """The 8-bit codes of the rows of x [m, d_in] (bf16 or fp32; rows may be
+    strided): (codes int8 [m, d_in], scales fp32 [m], sums int32 [m]), the sums
+    being those of a row's codes.  gptq_integer_matmul takes the three in x's place."""
+    what = "gptq_quantize_tokens"
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError(f"{what}: x must be 2-D with unit column stride")
+    code = _type_code(what, x.dtype)
+    dev = _on_device(what, x, codes, scales, sums)
+    m, d = x.shape
+    if codes is None:
+        codes = torch.empty((m, d), dtype=torch.int8, device=x.device)
+    if scales is None:
+        scales = torch.empty(m, dtype=torch.float32, device=x.device)
+    if sums is None:
+        sums = torch.empty(m, dtype=torch.int32, device=x.device)
+    if (codes.shape != (m, d) or codes.dtype != torch.int8 or not codes.is_contiguous() or scales.shape != (m,)
+            or scales.dtype != torch.float32 or not scales.is_contiguous() or sums.shape != (m,)
+            or sums.dtype != torch.int32 or not sums.is_contiguous()):
+        raise ValueError(f"{what}: codes, scales and sums must be contiguous int8 [m, d_in], float32 [m] and int32 [m]")
+    _check(_lib().gptq_quantize_tokens(x.data_ptr(), code, m, d, max(x.stride(0), d), codes.data_ptr(), scales.data_ptr(),
+                                       sums.data_ptr(), _raw_stream(stream, dev)), what)
+    return codes, scales, sums
+
+
+def gptq_integer_weight(qweight: torch.Tensor, zeros: torch.Tensor, bits: int, stream=None):
+    """A layer with one group per output channel laid out for
+    gptq_integer_matmul: (w int8 [d_out, d_in], offsets int32 [d_out]) with
+    W = scale (w - offset).  zeros: [d_out] or [1, d_out] int32."""
+    what = "gptq_integer_weight"
+    dev = _on_device(what, qweight, zeros)
+    if bits not in (2, 3, 4, 8) or qweight.dim() != 2 or (qweight.shape[0] * 32) % bits != 0:
+        raise ValueError(f"{what}: qweight does not match bits")
+    d_in, d_out = qweight.shape[0] * 32 // bits, qweight.shape[1]
+    if qweight.dtype != torch.int32 or zeros.dtype != torch.int32 or zeros.numel() != d_out or zeros.shape[-1] != d_out:
+        raise ValueError(f"{what}: qweight and zeros must be int32 [d_in * bits / 32, d_out] and [d_out]: "
+                         "the layer needs one group per output channel")
+    w = torch.empty((d_out, d_in), dtype=torch.int8, device=qweight.device)
+    offsets = torch.empty(d_out, dtype=torch.int32, device=qweight.device)
+    _check(_lib().gptq_integer_weight(_ptr(qweight.contiguous()), _ptr(zeros.contiguous()), int(bits), d_in, d_out,
+                                      _ptr(w), _ptr(offsets), _raw_stream(stream, dev)), what)
+    return w, offsets
+
+
+def gptq_integer_workspace_size(m: int, dtype: torch.dtype, d_in: int, d_out: int) -> int:
+    """dtype: of x (int8: codes)."""
+    code = GPTQ_I8 if dtype == torch.int8 else _type_code("gptq_integer_workspace_size", dtype)
+    return int(_lib().gptq_integer_workspace_size(m, code, d_in, d_out))
+
+
+def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                        out_dtype: torch.dtype = torch.float32, y: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [m, d_out] = x W^T in 8-bit integers, W = w_scales (w - offsets) as laid
+    out by gptq_integer_weight (offsets None: all zero).  x is [m, d_in] bf16 or
+    fp32 (rows may be strided), quantized per token on the way, or what
+    gptq_quantize_tokens returned for it."""
+    what = "gptq_integer_matmul"
+    x_scales = x_sums = None
+    if isinstance(x, tuple):
+        x, x_scales, x_sums = x
+        code = GPTQ_I8
+        m = x.shape[0]
+        if (x.dtype != torch.int8 or x_scales.shape != (m,) or x_scales.dtype != torch.float32
+                or not x_scales.is_contiguous() or (x_sums is not None and (x_sums.shape != (m,)
+                                                    or x_sums.dtype != torch.int32 or not x_sums.is_contiguous()))):
+            raise ValueError(f"{what}: expected the codes, scales and sums of gptq_quantize_tokens")
+        if offsets is not None and x_sums is None:
+            raise ValueError(f"{what}: a layer with offsets needs the sums of the codes")
+    else:
+        code = _type_code(what, x.dtype)
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError(f"{what}: x must be 2-D with unit column stride")
+    dev = _on_device(what, x, w, w_scales, offsets, x_scales, x_sums, y, ws)
+    m, d_in = x.shape
+    d_out = w.shape[0]
+    if (w.shape != (d_out, d_in) or w.dtype != torch.int8 or not w.is_contiguous() or w_scales.numel() != d_out
+            or w_scales.dtype != torch.float32 or not w_scales.is_contiguous()):
+        raise ValueError(f"{what}: w and w_scales must be contiguous int8 [d_out, d_in] and float32 [d_out]")
+    if offsets is not None and (offsets.shape != (d_out,) or offsets.dtype != torch.int32 or not offsets.is_contiguous()):
+        raise ValueError(f"{what}: offsets must be contiguous int32 [d_out]")
+    if y is None:
+        yt = _type_code(what, out_dtype)
+        y = torch.empty((m, d_out), dtype=out_dtype, device=x.device)
+    else:
+        yt = _type_code(what, y.dtype)
+        if y.shape != (m, d_out) or not y.is_contiguous():
+            raise ValueError(f"{what}: y must be contiguous [m, d_out]")
+    lib = _lib()
+    if ws is None and code != GPTQ_I8:
+        ws = torch.empty(lib.gptq_integer_workspace_size(m, code, d_in, d_out), dtype=torch.uint8, device=x.device)
+    _check(lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, max(x.stride(0), d_in),
+                                   w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), d_out, y.data_ptr(), yt, _ptr(ws),
+                                   0 if ws is None else ws.numel(), _raw_stream(stream, dev)), what)
+    return y
+
+
+class QuantizedCache:
+    """A paged key/value cache in 8- or 4-bit codes (gptq_cache of the C ABI)
+    over the caller's tensors: codes [n_pages, n_kv_heads, page_size,
+    head_dim * bits / 8] (int8 for 8 bits, uint8 for 4), scales [n_pages,
+    n_kv_heads, page_size] fp32, all contiguous and on one GPU."""
+
+    def __init__(self, k_codes: torch.Tensor, v_codes: torch.Tensor, k_scales: torch.Tensor, v_scales: torch.Tensor,
+                 bits: int = 8):
+        what = "QuantizedCache"
+        if bits not in (4, 8):
+            raise ValueError(f"{what}: bits must be 4 or 8, got {bits}")
+        if k_codes.dim() != 4:
+            raise ValueError(f"{what}: codes must be [n_pages, n_kv_heads, page_size, head_dim * bits / 8]")
+        n_pages, n_kv, page, width = k_codes.shape
+        dtype = torch.int8 if bits == 8 else torch.uint8
+        for t in (k_codes, v_codes):
+            if t.shape != k_codes.shape or t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+                raise ValueError(f"{what}: k_codes and v_codes must be alike: contiguous {dtype} on the GPU")
+        for t in (k_scales, v_scales):
+            if t.shape != (n_pages, n_kv, page) or t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError(f"{what}: scales must be contiguous float32 [n_pages, n_kv_heads, page_size]")
+        if any(t.get_device() != k_codes.get_device() for t in (v_codes, k_scales, v_scales)):
+            raise ValueError(f"{what}: the tensors must be on one GPU")
+        if page not in (16, 32, 64, 128, 256):
+            raise ValueError(f"{what}: page_size must be 16, 32, 64, 128 or 256, got {page}")
+        self.head_dim = width * 8 // bits
+        if self.head_dim % 16 != 0 or not 16 <= self.head_dim <= 256:
+            raise ValueError(f"{what}: head_dim must be a multiple of 16 up to 256, got {self.head_dim}")
+        if n_pages < 1 or n_kv < 1:
+            raise ValueError(f"{what}: a cache needs a page and a head")
+        self.n_pages, self.n_kv_heads, self.page_size, self.bits = n_pages, n_kv, page, bits
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.device = k_codes.device
+        self._index = k_codes.get_device()
+        self._c = _CCache(n_pages, page, n_kv, self.head_dim, bits, k_codes.data_ptr(), v_codes.data_ptr(),
+                          k_scales.data_ptr(), v_scales.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, bits: int = 8,
+              device="cuda:0") -> "QuantizedCache":
+        """A cache of zeros."""
+        if bits not in (4, 8):
+            raise ValueError(f"QuantizedCache: bits must be 4 or 8, got {bits}")
+        if head_dim % 16 != 0 or not 16 <= head_dim <= 256:
+            raise ValueError(f"QuantizedCache: head_dim must be a multiple of 16 up to 256, got {head_dim}")
+        shape = (n_pages, n_kv_heads, page_size)
+        dtype = torch.int8 if bits == 8 else torch.uint8
+        codes = [torch.full((*shape, head_dim * bits // 8), 0 if bits == 8 else 0x88, dtype=dtype, device=device)
+                 for _ in range(2)]
+        scales = [torch.zeros(shape, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales, bits)
+
+    def _here(self, what: str, *ts) -> int:
+        dev = _on_device(what, *ts)
+        if dev != self._index:
+            raise ValueError(f"{what}: the cache is on cuda:{self._index}, not on the current GPU")
+        return dev
+
+
+def _slots(what: str, slots: torch.Tensor) -> int:
+    if slots.dim() != 1 or slots.dtype != torch.int64 or not slots.is_contiguous():
+        raise ValueError(f"{what}: slots must be a contiguous int64 vector")
+    return slots.shape[0]
+
+
+def gptq_cache_write(cache: QuantizedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, stream=None) -> None:
+    """Quantize k, v [n, n_kv_heads, head_dim] (bf16 or fp32; tokens may be
+    strided, as in a slice of a fused projection) into the cache's slots
+    (page * page_size + offset; int64 [n], different from each other; one
+    outside the cache is skipped)."""
+    what = "gptq_cache_write"
+    n = _slots(what, slots)
+    code = _type_code(what, k.dtype)
+    hd = cache.head_dim
+    shape = (n, cache.n_kv_heads, hd)
+    for t in (k, v):
+        if t.shape != shape or t.dtype != k.dtype or (n > 0 and (t.stride(2) != 1 or t.stride(1) != hd)):
+            raise ValueError(f"{what}: k and v must be [n, {cache.n_kv_heads}, {hd}] of one dtype, heads contiguous")
+    dev = cache._here(what, k, v, slots)
+    width = cache.n_kv_heads * hd
+    ldk, ldv = (k.stride(0), v.stride(0)) if n > 1 else (width, width)
+    _check(_lib().gptq_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), code, n, ldk, ldv, slots.data_ptr(),
+                                   _raw_stream(stream, dev)), what)
+
+
+def gptq_cache_read(cache: QuantizedCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                    k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
+    """The values held in the given slots: (k, v), each [n, n_kv_heads,
+    head_dim]; zeros for a slot outside the cache."""
+    what = "gptq_cache_read"
+    n = _slots(what, slots)
+    shape = (n, cache.n_kv_heads, cache.head_dim)
+    k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
+    v = torch.empty(shape, dtype=k.dtype, device=slots.device) if v is None else v
+    code = _type_code(what, k.dtype)
+    for t in (k, v):
+        if t.shape != shape or t.dtype != k.dtype or not t.is_contiguous():
+            raise ValueError(f"{what}: k and v must be contiguous [n, n_kv_heads, head_dim] of one dtype")
+    dev = cache._here(what, slots, k, v)
+    _check(_lib().gptq_cache_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), code,
+                                  _raw_stream(stream, dev)), what)
+    return k, v
+
+
+def gptq_attention_workspace_size(cache: QuantizedCache, n_tokens: int, n_heads: int, n_seq: int,
+                                  pages_per_seq: int) -> int:
+    return int(_lib().gptq_attention_workspace_size(cache._ref, n_tokens, n_heads, n_seq, pages_per_seq))
+
+
+def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: torch.Tensor, q_starts: torch.Tensor,
+                         kv_lens: torch.Tensor, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Causal attention of the new tokens q [n_tokens, n_heads, head_dim] bf16
+    over the cache, which holds their keys and values already.  Sequence i owns
+    the tokens q_starts[i] .. q_starts[i + 1] - 1 (int32 [n_seq + 1]), has
+    kv_lens[i] keys (int32 [n_seq]) and its pages in page_table[i] (int32
+    [n_seq, pages_per_seq]).  scale: 1 / sqrt(head_dim) unless given.  Rows of
+    out outside the sequences are left as they were."""
+    what = "gptq_cache_attention"
+    hd = cache.head_dim
+    if q.dim() != 3 or q.shape[2] != hd or q.dtype != torch.bfloat16:
+        raise ValueError(f"{what}: q must be bfloat16 [n_tokens, n_heads, {hd}]")
+    n, heads = q.shape[0], q.shape[1]
+    if heads < 1 or heads % cache.n_kv_heads != 0:
+        raise ValueError(f"{what}: {heads} query heads do not divide over {cache.n_kv_heads} key heads")
+    if n > 0 and (q.stride(2) != 1 or q.stride(1) != hd):
+        raise ValueError(f"{what}: the heads of a token must be contiguous in q")
+    if (page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous()
+            or kv_lens.dtype != torch.int32 or q_starts.dtype != torch.int32 or not kv_lens.is_contiguous()
+            or not q_starts.is_contiguous() or kv_lens.shape != (page_table.shape[0],)
+            or q_starts.shape != (page_table.shape[0] + 1,)):
+        raise ValueError(f"{what}: page_table, q_starts and kv_lens must be contiguous int32 [n_seq, pages_per_seq], "
+                         "[n_seq + 1] and [n_seq]")
+    width = heads * hd
+    if out is None:
+        out = torch.empty((n, heads, hd), dtype=torch.bfloat16, device=q.device)
+    elif (out.shape != q.shape or out.dtype != torch.bfloat16
+          or (n > 0 and (out.stride(2) != 1 or out.stride(1) != hd))):
+        raise ValueError(f"{what}: out must be bfloat16 like q, the heads of a token contiguous")
+    dev = cache._here(what, q, page_table, q_starts, kv_lens, out, ws)
+    n_seq, pages = page_table.shape
+    ldq, ldo = (q.stride(0), out.stride(0)) if n > 1 else (width, width)
+    lib = _lib()
+    if ws is None:
+        need = lib.gptq_attention_workspace_size(cache._ref, n, heads, n_seq, pages)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+    _check(lib.gptq_cache_attention(cache._ref, q.data_ptr(), GPTQ_BF16, n, ldq, heads, page_table.data_ptr(), pages,
+                                    q_starts.data_ptr(), kv_lens.data_ptr(), n_seq,
+                                    hd ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(ws),
+                                    0 if ws is None else ws.numel(), _raw_stream(stream, dev)), what)
+    return out

@@ -42,6 +42,24 @@ bool packable(int64_t d_in, int32_t bits) {
   return d_in % m == 0;
 }
 
+// the serving calls: rows (tokens) of one call, and a product of sizes that
+// stays below 2^31
+constexpr int64_t kMaxRows = int64_t{1} << 30;
+constexpr int64_t kMaxIntDim = int64_t{1} << 16;  // 32-bit sums of int8 products stay exact
+bool rows_ok(int64_t n) { return n >= 0 && n <= kMaxRows; }
+
+bool cache_shape(const gptq_cache* c, gptq::CacheShape* out) {
+  if (!c || !c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return false;
+  if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
+    return false;
+  if (c->bits != 4 && c->bits != 8) return false;
+  if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16 != 0) return false;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)) != 0) return false;
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 65536 || c->n_pages < 1 || c->n_pages > (int64_t{1} << 31) - 1) return false;
+  *out = gptq::CacheShape{c->n_pages, c->page_size, c->n_kv_heads, c->head_dim, c->bits};
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -215,6 +233,110 @@ gptq_status gptq_dequant_matmul_ordered(const void* x, int32_t xt, int64_t m, in
   return from_hip(gptq::dequant_matmul_ordered_launch(x, xt == GPTQ_BF16, m, d_in, qweight, scales, zeros, g_idx,
                                                       order, bits, d_out, n_groups, y, ws,
                                                       static_cast<hipStream_t>(stream)));
+}
+
+gptq_status gptq_quantize_tokens(const void* x, int32_t xt, int64_t n_tokens, int64_t d_in, int64_t ldx, int8_t* codes,
+                                 float* scales, int32_t* sums_or_null, void* stream) {
+  if ((xt != GPTQ_F32 && xt != GPTQ_BF16) || !rows_ok(n_tokens) || !dim_ok(d_in) || ldx < d_in) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (!x || !codes || !scales) return GPTQ_ERR_INVALID_ARG;
+  return from_hip(gptq::token_codes_launch(x, xt == GPTQ_BF16, n_tokens, d_in, ldx, codes, scales, sums_or_null,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+gptq_status gptq_integer_weight(const int32_t* qweight, const int32_t* zeros, int32_t bits, int64_t d_in, int64_t d_out,
+                                int8_t* w, int32_t* offsets, void* stream) {
+  if (!qweight || !zeros || !w || !offsets || !bits_ok(bits)) return GPTQ_ERR_INVALID_ARG;
+  if (!dim_ok(d_in) || !dim_ok(d_out) || d_in % 32 != 0 || !aligned16(w)) return GPTQ_ERR_INVALID_ARG;
+  return from_hip(gptq::integer_weight_launch(qweight, zeros, bits, d_in, d_out, w, offsets,
+                                              static_cast<hipStream_t>(stream)));
+}
+
+size_t gptq_integer_workspace_size(int64_t m, int32_t xt, int64_t d_in, int64_t d_out) {
+  if (m <= 0 || !rows_ok(m) || !dim_ok(d_in) || !dim_ok(d_out) || d_in % 32 != 0 || d_in > kMaxIntDim) return 0;
+  if (xt != GPTQ_F32 && xt != GPTQ_BF16 && xt != GPTQ_I8) return 0;
+  return gptq::integer_matmul_workspace(m, d_in, d_out, xt == GPTQ_I8, device_cus());
+}
+
+gptq_status gptq_integer_matmul(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                                int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
+                                const int32_t* w_offsets_or_null, int64_t d_out, void* y, int32_t yt, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if ((xt != GPTQ_F32 && xt != GPTQ_BF16 && xt != GPTQ_I8) || (yt != GPTQ_F32 && yt != GPTQ_BF16))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!rows_ok(m) || !dim_ok(d_in) || !dim_ok(d_out) || d_in % 32 != 0 || d_in > kMaxIntDim || ldx < d_in)
+    return GPTQ_ERR_INVALID_ARG;
+  if (m == 0) return GPTQ_OK;
+  if (!x || !w || !w_scales || !y || !aligned16(w)) return GPTQ_ERR_INVALID_ARG;
+  if (xt == GPTQ_I8) {
+    if (!x_scales || (w_offsets_or_null && !x_sums) || ldx % 16 != 0 || ldx > (int64_t{1} << 22) || !aligned16(x))
+      return GPTQ_ERR_INVALID_ARG;
+  }
+  const int cus = device_cus();
+  const size_t need = gptq::integer_matmul_workspace(m, d_in, d_out, xt == GPTQ_I8, cus);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
+  return from_hip(gptq::integer_matmul_launch(x, xt, x_scales, x_sums, m, d_in, ldx, w, w_scales, w_offsets_or_null,
+                                              d_out, y, yt == GPTQ_BF16, ws, cus, static_cast<hipStream_t>(stream)));
+}
+
+gptq_status gptq_cache_write(const gptq_cache* cache, const void* k, const void* v, int32_t xt, int64_t n_tokens,
+                             int64_t ldk, int64_t ldv, const int64_t* slots, void* stream) {
+  gptq::CacheShape c;
+  if (!cache_shape(cache, &c) || (xt != GPTQ_F32 && xt != GPTQ_BF16) || !rows_ok(n_tokens)) return GPTQ_ERR_INVALID_ARG;
+  const int64_t vec = (xt == GPTQ_BF16) ? 8 : 4, width = int64_t{c.n_kv} * c.hd;
+  if (ldk < width || ldv < width || ldk % vec != 0 || ldv % vec != 0 || n_tokens * c.n_kv > (int64_t{1} << 33))
+    return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return GPTQ_ERR_INVALID_ARG;
+  return from_hip(gptq::cache_write_launch(c, cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales, k, v,
+                                           xt == GPTQ_BF16, n_tokens, ldk, ldv, slots,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64_t n_tokens, void* k, void* v, int32_t yt,
+                            void* stream) {
+  gptq::CacheShape c;
+  if (!cache_shape(cache, &c) || (yt != GPTQ_F32 && yt != GPTQ_BF16) || !rows_ok(n_tokens)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens * c.n_kv > (int64_t{1} << 33)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return GPTQ_ERR_INVALID_ARG;
+  return from_hip(gptq::cache_read_launch(c, cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales, slots,
+                                          n_tokens, k, v, yt == GPTQ_BF16, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+bool attention_sizes(const gptq::CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t pages_per_seq) {
+  return n_heads >= 1 && n_heads % c.n_kv == 0 && rows_ok(n_tokens) && n_tokens * n_heads < (int64_t{1} << 30) &&
+         n_seq >= 0 && n_seq <= (1 << 20) && int64_t{n_seq} * c.n_kv < (int64_t{1} << 30) && pages_per_seq >= 1 &&
+         pages_per_seq * c.page <= (int64_t{1} << 30);
+}
+}  // namespace
+
+size_t gptq_attention_workspace_size(const gptq_cache* cache, int64_t n_tokens, int32_t n_heads, int32_t n_seq,
+                                     int64_t pages_per_seq) {
+  gptq::CacheShape c;
+  if (!cache_shape(cache, &c) || !attention_sizes(c, n_tokens, n_heads, n_seq, pages_per_seq)) return 0;
+  if (n_tokens == 0 || n_seq == 0) return 0;
+  return gptq::attention_plan(c, n_tokens, n_heads, n_seq, pages_per_seq, device_cus()).ws_bytes;
+}
+
+gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
+                                 int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
+                                 const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale, void* out,
+                                 int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  gptq::CacheShape c;
+  if (!cache_shape(cache, &c) || qt != GPTQ_BF16 || !(scale > 0.0f && scale <= 3.402823466e38f))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!attention_sizes(c, n_tokens, n_heads, n_seq, pages_per_seq)) return GPTQ_ERR_INVALID_ARG;
+  const int64_t width = int64_t{n_heads} * c.hd;
+  if (ldq < width || ldo < width || ldq % 8 != 0 || ldo % 8 != 0) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0 || n_seq == 0) return GPTQ_OK;
+  if (!q || !out || !page_table || !q_starts || !kv_lens || !aligned16(q) || !aligned16(out)) return GPTQ_ERR_INVALID_ARG;
+  const gptq::AttnPlan plan = gptq::attention_plan(c, n_tokens, n_heads, n_seq, pages_per_seq, device_cus());
+  if (plan.ws_bytes > 0 && (!ws || ws_bytes < plan.ws_bytes || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
+  return from_hip(gptq::attention_launch(plan, c, q, ldq, n_tokens, n_heads, cache->k_codes, cache->v_codes,
+                                         cache->k_scales, cache->v_scales, page_table, pages_per_seq, q_starts, kv_lens,
+                                         n_seq, scale, out, ldo, ws, static_cast<hipStream_t>(stream)));
 }
 
 gptq_status gptq_phase_timing(int32_t enable) { return from_hip(gptq::phase_timing_set(enable != 0)); }

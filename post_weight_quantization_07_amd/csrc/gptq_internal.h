@@ -140,4 +140,42 @@ hipError_t dequant_matmul_ordered_launch(const void* x, bool x_bf16, int64_t m, 
                                          const int32_t* order, int bits, int64_t d_out, int n_groups, float* y,
                                          void* ws, hipStream_t stream);
 
+// ---------------------------------------------------------------- integer --
+enum { kXF32 = 0, kXBf16 = 1, kXInt8 = 2 };  // gptq_dtype
+hipError_t token_codes_launch(const void* x, bool bf16, int64_t m, int64_t d, int64_t ldx, int8_t* codes,
+                              float* scales, int32_t* sums, hipStream_t stream);
+hipError_t integer_weight_launch(const int32_t* qweight, const int32_t* zeros, int bits, int64_t d_in, int64_t d_out,
+                                 int8_t* w, int32_t* offsets, hipStream_t stream);
+size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool codes_given, int n_cu);
+hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                                 int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
+                                 const int32_t* w_offsets, int64_t d_out, void* y, bool y_bf16, void* ws, int n_cu,
+                                 hipStream_t stream);
+
+// ------------------------------------------------------------------ cache --
+struct CacheShape {
+  int64_t n_pages;
+  int32_t page, n_kv, hd, bits;
+};
+hipError_t cache_write_launch(const CacheShape& c, void* kc, void* vc, float* ks, float* vs, const void* k,
+                              const void* v, bool bf16, int64_t n, int64_t ldk, int64_t ldv, const int64_t* slots,
+                              hipStream_t stream);
+hipError_t cache_read_launch(const CacheShape& c, const void* kc, const void* vc, const float* ks, const float* vs,
+                             const int64_t* slots, int64_t n, void* k, void* v, bool bf16, hipStream_t stream);
+
+// -------------------------------------------------------------- attention --
+struct AttnPlan {
+  int tile_rows;          // rows (token, head of the group) of a tile
+  int target, min_units;  // how the keys are split
+  int64_t blocks, joins;  // workgroups of the two kernels; joins 0: nothing can be split
+  int64_t slots;          // partial results
+  size_t ws_bytes;
+};
+AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t ld_table,
+                        int n_cu);
+hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const void* q, int64_t ldq, int64_t n_tokens,
+                            int32_t n_heads, const void* kc, const void* vc, const float* ks, const float* vs,
+                            const int32_t* table, int64_t ld_table, const int32_t* starts, const int32_t* lens,
+                            int32_t n_seq, float scale, void* out, int64_t ldo, void* ws, hipStream_t stream);
+
 }  // namespace gptq

@@ -1,0 +1,268 @@
+"""Attention over the quantized cache against its 64-bit form.
+
+The bound, per output element, with u = 2^-24 (fp32) and the reference's sums
+A = sum p |v|, B = sum p sv, W = max over seen keys of scale sk sum_d |q_d| (|ck_d| + 24):
+  scores  products are exact, summed in fp32 over head_dim (4 bits: of q (24 +
+          code) - 24 q): (hd + 2) u W; two scales, the maximum's difference and
+          the sum: 5 u W more.  e^s turns it into a relative error of p, in the
+          numerator and in the denominator: 2 (hd + 7) u W
+  p       exp2 to an ulp (2 u), the value scale (u), bf16: 2^-8
+  sums    L terms and their rescalings in fp32, numerator and denominator:
+          (L + 64) 4 u of A; at 4 bits the values enter as 24 + code, at most 32:
+          another (L + 64) 2 u of 32 B
+  output  bf16: 2^-8 of the value
+tolerance = A (1 + 2^-8) (2^-8 + 2 (hd + 7) u W + (L + 64) 4 u) + [4 bits] 32 B (L + 64) 2 u + 2^-8 (1 + 2^-6) |out|."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import banner, dev
+from oracle import serving_oracle as S
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def G():
+    import post_weight_quantization_07_amd as G
+    assert torch.cuda.is_available()
+    return G
+
+
+class Case:
+    """A cache in use, its sequences' pages in random order.  Every slot that no
+    sequence holds has random codes and scale NaN: nothing may read it."""
+
+    def __init__(self, G, lens, heads, kv, hd, page, bits, seed=0, extra=5):
+        r = np.random.default_rng(seed + hd + page)
+        self.lens, self.heads, self.kv, self.hd, self.page, self.bits = lens, heads, kv, hd, page, bits
+        need = [-(-length // page) for _, length in lens]
+        n_pages = sum(need) + extra
+        order = r.permutation(n_pages)
+        width = max(1, max(need, default=1)) + 1
+        self.table = np.full((len(lens), width), -7, np.int32)               # what is past a sequence is not read
+        top = 127 if bits == 8 else 7
+        self.codes = [S.pack_rows(r.integers(-top, top + 1, (n_pages, kv, page, hd)), bits) for _ in range(2)]
+        self.scales = [np.full((n_pages, kv, page), np.nan, np.float32) for _ in range(2)]
+        at = 0
+        for i, n in enumerate(need):
+            self.table[i, :n] = order[at:at + n]
+            at += n
+            for j, p in enumerate(self.table[i, :n]):
+                fill = min(page, lens[i][1] - j * page)
+                for s in self.scales:
+                    s[p, :, :fill] = (np.exp(0.5 * r.standard_normal((kv, fill))) * 2.0 / top).astype(np.float32)
+        starts = np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        self.starts = starts
+        self.total = int(starts[-1])
+        q = torch.from_numpy(r.standard_normal((self.total, heads, hd)).astype(np.float32) * 1.5).to(torch.bfloat16)
+        self.q_host = q.double().numpy()
+        self.q = q.to(dev())
+        d = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev())
+        self.cache = G.QuantizedCache(*[d(c) for c in self.codes], *[d(s) for s in self.scales], bits)
+        self.args = (d(self.table), d(starts), d(np.array([length for _, length in lens], np.int32)))
+
+    def check(self, out, scale=None, rows=None):
+        scale = self.hd ** -0.5 if scale is None else scale
+        got = out.double().cpu().numpy()
+        for i, (n, length) in enumerate(self.lens):
+            pages = self.table[i, :-(-length // self.page)]
+            a = int(self.starts[i])
+            for h in range(self.heads):
+                if length == 0:
+                    assert (got[a:a + n] == 0).all()
+                    continue
+                k, v = (S.cache_rows(c, s, self.bits, pages, h // (self.heads // self.kv), length)
+                        for c, s in zip(self.codes, self.scales))
+                pick = np.arange(n) if n <= 40 else np.unique(np.r_[0:8, n // 2 - 4:n // 2 + 4, n - 8:n])
+                # the chosen rows only: row t of n sees length - n + t + 1 keys
+                for t in pick:
+                    seen = length - n + t + 1
+                    if seen <= 0:
+                        assert (got[a + t, h] == 0).all(), (i, h, t)
+                        continue
+                    ref, A, B, W = S.attention(self.q_host[a + t:a + t + 1, h], (k[0][:seen], k[1][:seen]),
+                                               (v[0][:seen], v[1][:seen]), scale)
+                    tol = (A * (1 + 2.0 ** -8) * (2.0 ** -8 + 2 * (self.hd + 7) * U * W[0] + (seen + 64) * 4 * U)
+                           + (32 * B * (seen + 64) * 2 * U if self.bits == 4 else 0) + 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(ref))
+                    err = np.abs(got[a + t, h] - ref[0])
+                    assert (err <= tol[0] + 1e-30).all(), (i, h, t, float((err / (tol[0] + 1e-30)).max()))
+
+
+# lens: (new tokens, keys); heads, key heads, head_dim, page
+CASES = [
+    ([(1, 1)], 1, 1, 16, 16),
+    ([(1, 2), (1, 15), (1, 16), (1, 17), (1, 31), (1, 33), (1, 64), (1, 65)], 4, 2, 64, 16),
+    ([(1, 300)], 32, 32, 128, 16),
+    ([(1, 5000), (1, 3), (1, 700)], 8, 1, 128, 32),
+    ([(1, 9000)], 16, 2, 128, 64),
+    ([(1, 2100), (1, 0), (2, 1), (3, 3)], 6, 2, 96, 16),                 # no key at all, fewer keys than tokens
+    ([(5, 5), (1, 40), (17, 33), (0, 9), (40, 100)], 6, 3, 80, 32),      # a sequence without new tokens
+    ([(4, 260), (2, 1030)], 7, 1, 32, 256),
+    ([(3, 515)], 12, 4, 256, 128),
+    ([(2, 70)], 5, 5, 144, 16),
+    ([(130, 130)], 2, 2, 128, 64),
+    ([(200, 712), (65, 65), (128, 3000)], 8, 2, 64, 32),
+    ([(300, 1111)], 4, 4, 128, 16),
+    ([(257, 900), (3, 500)], 14, 2, 112, 128),
+    ([(96, 96)], 3, 1, 256, 16),
+    ([(700, 4000)], 2, 1, 48, 64),
+]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", CASES)
+def test_attention(G, lens, heads, kv, hd, page, bits):
+    banner(f"attention {lens} {heads}/{kv}x{hd} page {page} int{bits}")
+    c = Case(G, lens, heads, kv, hd, page, bits)
+    out = G.gptq_cache_attention(c.q, c.cache, *c.args)
+    c.check(out)
+    assert torch.equal(out, G.gptq_cache_attention(c.q, c.cache, *c.args))     # deterministic
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_many_sequences(G, bits):
+    """More sequences than one wave scans at a time, decoding and prompts mixed."""
+    banner(f"attention: 150 ragged sequences, int{bits}")
+    r = np.random.default_rng(1)
+    lens = [(int(n), int(n + c)) for n, c in zip(r.choice([0, 1, 1, 1, 2, 9], 150), r.integers(0, 400, 150))]
+    lens[70] = (1, 4000)
+    c = Case(G, lens, 4, 2, 64, 16, bits, seed=4)
+    c.check(G.gptq_cache_attention(c.q, c.cache, *c.args))
+
+
+def test_sharp_and_flat(G):
+    """Scores so far apart that one key takes all, and a scale so small that all keys weigh the same."""
+    banner("attention: large and small scales")
+    c = Case(G, [(1, 600), (20, 300)], 4, 2, 64, 16, 8, seed=9)
+    for scale in (3.0, 1e-6):
+        c.check(G.gptq_cache_attention(c.q, c.cache, *c.args, scale=scale), scale=scale)
+
+
+def test_rows_outside_strides_and_given_buffers(G):
+    banner("attention: rows outside the sequences, strided q and out, given workspace")
+    c = Case(G, [(3, 90), (1, 2000), (6, 6)], 4, 2, 64, 16, 8, seed=2)
+    want = G.gptq_cache_attention(c.q, c.cache, *c.args)
+    table, starts, lens = c.args
+    pad = 5
+    fused = torch.randn(c.total + 2 * pad, 3 * 4 * 64, device=dev()).to(torch.bfloat16)
+    q = fused[:, 4 * 64:8 * 64].unflatten(1, (4, 64))
+    q[pad:pad + c.total] = c.q
+    hold = torch.full((c.total + 2 * pad, 2 * 4 * 64), 7.0, dtype=torch.bfloat16, device=dev())
+    out = hold[:, 4 * 64:].unflatten(1, (4, 64))
+    need = G.gptq_attention_workspace_size(c.cache, q.shape[0], 4, 3, table.shape[1])
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev())
+    G.gptq_cache_attention(q, c.cache, table, starts + pad, lens, out=out, ws=ws)
+    assert torch.equal(out[pad:pad + c.total], want)
+    assert (hold[:pad] == 7).all() and (hold[pad + c.total:] == 7).all() and (hold[:, :4 * 64] == 7).all()
+
+
+def test_values_that_do_not_fit(G):
+    """Page entries outside the cache hide their keys; lengths past the table and starts past the tokens are cut."""
+    banner("attention: bad pages, lengths and starts")
+    c = Case(G, [(1, 200), (4, 150)], 4, 2, 64, 16, 8, seed=5)
+    table, starts, lens = c.args
+    bad = table.clone()
+    bad[0, 3], bad[1, 2] = -1, c.cache.n_pages
+    out = G.gptq_cache_attention(c.q, c.cache, bad, starts, lens).double().cpu().numpy()
+    for i, (page_bad, (n, length)) in enumerate(zip((3, 2), c.lens)):
+        pages = c.table[i, :-(-length // 16)]
+        hidden = np.arange(length) // 16 == page_bad
+        for h in range(4):
+            k, v = (S.cache_rows(x, s, 8, pages, h // 2, length) for x, s in zip(c.codes, c.scales))
+            a = int(c.starts[i])
+            ref, A, _, W = S.attention(c.q_host[a:a + n, h], k, v, 0.125, hidden)
+            tol = A * (1 + 2.0 ** -8) * (2.0 ** -8 + 2 * 71 * U * W[:, None] + (length + 64) * 4 * U) + 2.0 ** -8 * 1.02 * np.abs(ref)
+            assert (np.abs(out[a:a + n, h] - ref) <= tol).all()
+    all_bad = torch.full_like(table, -1)
+    assert not G.gptq_cache_attention(c.q, c.cache, all_bad, starts, lens).any()
+    # a length past the table's pages is cut to them (those pages hold no keys here: the table ends with -7)
+    long = lens.clone()
+    long[0] = 1 << 30
+    G.gptq_cache_attention(c.q, c.cache, table, starts, long)
+    wild = torch.tensor([-5, 3, 1 << 30], dtype=torch.int32, device=dev())
+    G.gptq_cache_attention(c.q, c.cache, table, wild, lens)
+    G.gptq_cache_attention(c.q, c.cache, table, torch.tensor([4, 2, -1], dtype=torch.int32, device=dev()), lens - 1000)
+    torch.cuda.synchronize()
+    c.check(G.gptq_cache_attention(c.q, c.cache, *c.args))
+
+
+def test_nan_scale_reaches_only_who_sees_it(G):
+    banner("attention: a key with a NaN scale")
+    c = Case(G, [(6, 60), (1, 30)], 2, 1, 64, 16, 8, seed=6)
+    table, starts, lens = c.args
+    c.cache.k_scales[int(c.table[0, 57 // 16]), 0, 57 % 16] = float("nan")
+    out = G.gptq_cache_attention(c.q, c.cache, *c.args)
+    nan = torch.isnan(out).flatten(1)
+    assert nan[3:6].all() and not nan[:3].any() and not nan[6].any()       # tokens 54 .. 59 of 60; the third sees key 56
+
+
+def test_refusals_and_empty(G):
+    banner("attention: refusals, no tokens")
+    c = Case(G, [(2, 20)], 4, 2, 64, 16, 8)
+    t, s, n = c.args
+    call = G.gptq_cache_attention
+    for bad in (lambda: call(c.q.float(), c.cache, t, s, n), lambda: call(c.q[:, :3], c.cache, t, s, n),
+                lambda: call(c.q[..., :32], c.cache, t, s, n), lambda: call(c.q, c.cache, t.long(), s, n),
+                lambda: call(c.q, c.cache, t, s[:1], n), lambda: call(c.q, c.cache, t, s, n.long()),
+                lambda: call(c.q, c.cache, t.cpu(), s, n), lambda: call(c.q.transpose(0, 1), c.cache, t, s, n),
+                lambda: call(c.q, c.cache, t, s, n, out=c.q.float())):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(G.GptqError):
+        call(c.q, c.cache, t, s, n, scale=-1.0)
+    big = Case(G, [(1, 3000)], 4, 2, 64, 16, 8)
+    with pytest.raises(G.GptqError, match="workspace"):
+        call(big.q, big.cache, *big.args, ws=torch.empty(256, dtype=torch.uint8, device=dev()))
+    assert call(c.q[:0], c.cache, t, torch.zeros_like(s), n).shape == (0, 4, 64)
+    assert call(c.q, c.cache, t[:0], s[:1], n[:0]).shape == c.q.shape
+
+
+@pytest.mark.parametrize("lens", [[(1, 2500), (1, 90)], [(70, 70), (130, 600)]])
+def test_stream_and_graph(G, lens):
+    """Captured once and replayed with other lengths, queries and pages."""
+    banner(f"attention: another stream, a graph, {lens}")
+    c = Case(G, lens, 8, 2, 128, 16, 8, seed=3)
+    other = Case(G, [(n, length - 1) for n, length in lens], 8, 2, 128, 16, 8, seed=8)
+    want = [G.gptq_cache_attention(x.q, x.cache, *x.args) for x in (c, other)]
+    c.check(want[0])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = G.gptq_cache_attention(c.q, c.cache, *c.args, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want[0])
+    n_pages = max(c.cache.n_pages, other.cache.n_pages)
+    width = max(c.args[0].shape[1], other.args[0].shape[1])
+
+    def grown(x):
+        bufs = []
+        for t in (x.cache.k_codes, x.cache.v_codes, x.cache.k_scales, x.cache.v_scales):
+            g = torch.zeros((n_pages, *t.shape[1:]), dtype=t.dtype, device=dev())
+            g[:t.shape[0]] = t
+            bufs.append(g)
+        table = torch.zeros((len(lens), width), dtype=torch.int32, device=dev())
+        table[:, :x.args[0].shape[1]] = x.args[0]
+        return bufs + [table, x.args[1], x.args[2], x.q]
+    sets = [grown(c), grown(other)]
+    hold = [t.clone() for t in sets[0]]
+    cache = G.QuantizedCache(*hold[:4], 8)
+    out = torch.empty_like(hold[7])
+    ws = torch.empty(max(256, G.gptq_attention_workspace_size(cache, out.shape[0], 8, len(lens), width)), dtype=torch.uint8,
+                     device=dev())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        G.gptq_cache_attention(hold[7], cache, *hold[4:7], out=out, ws=ws)
+    for i in (1, 0, 1, 1, 0):
+        for a, b in zip(hold, sets[i]):
+            a.copy_(b)
+        out.zero_()
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        again = G.gptq_cache_attention(hold[7], cache, *hold[4:7])
+        assert torch.equal(out, again)
+        if i == 0:
+            c.check(out)
+        else:
+            other.check(out)

@@ -1,0 +1,160 @@
+"""The serving operators on the host: their plain forms against rational
+arithmetic and closed forms, and the argument checks of their entry points
+(every call here returns before anything is enqueued)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as S
+
+FAKE = ctypes.c_void_p(1 << 20)      # never dereferenced: the checks fail first
+ODD = ctypes.c_void_p((1 << 20) + 4)
+
+
+@pytest.fixture(scope="module")
+def L():
+    import post_weight_quantization_07_amd._lib as L
+    L._lib()
+    return L
+
+
+@pytest.mark.parametrize("top", [127, 7])
+def test_codes_against_rationals(top):
+    r = np.random.default_rng(top)
+    rows = [r.standard_normal(40).astype(np.float32),
+            (r.integers(-64, 65, 40) / 64).astype(np.float32),             # many exact ties (max/2 -> 63.5)
+            np.array([1.0, 0.5, 0.25, -0.5, 1.5 / 127, -2.5 / 127, 0.0], np.float32),
+            np.array([3e-41, 1e-41, -2e-41], np.float32),                    # subnormal
+            np.array([3e38, -1.5e38, 1e30], np.float32), np.zeros(4, np.float32)]
+    for x in rows:
+        codes, scale = S.row_codes(x[None], top)
+        assert codes[0].tolist() == S.row_codes_slow(x, top)
+        assert scale[0] == np.float32(np.abs(x).max().astype(np.float64) / top)
+    codes, scale = S.row_codes(np.array([[1.0, np.nan, 2.0], [np.inf, 1.0, 1.0]], np.float32), top)
+    assert (codes == 0).all() and np.isnan(scale).all()
+
+
+def test_pack_roundtrip():
+    c = np.arange(-7, 9).clip(-7, 7).reshape(1, 16)
+    np.testing.assert_array_equal(S.unpack_rows(S.pack_rows(c, 4), 4), c)
+    assert S.pack_rows(c, 4)[0, 0] == (c[0, 0] + 8) | ((c[0, 1] + 8) << 4)
+
+
+def test_attention_plain_form():
+    """Equal keys: the mean of the values seen; one key: its value; no key: zeros."""
+    r = np.random.default_rng(0)
+    L_, d = 5, 16
+    kc, vc = np.zeros((L_, d)), r.integers(-127, 128, (L_, d)).astype(float)
+    one = np.ones(L_)
+    out, absv, plain, _ = S.attention(r.standard_normal((7, d)), (kc, one), (vc, one), 0.25)
+    np.testing.assert_array_equal(out[:2], 0.0)              # 7 new tokens, 5 keys: two rows see nothing
+    for t in range(2, 7):
+        np.testing.assert_allclose(out[t], vc[:t - 1].mean(axis=0), rtol=1e-12)
+    assert (absv >= np.abs(out) - 1e-12).all()
+
+
+def _cache(L, **kw):
+    a = dict(n_pages=8, page_size=16, n_kv_heads=2, head_dim=64, bits=8, k=1 << 20, v=1 << 20, ks=1 << 20, vs=1 << 20)
+    a.update(kw)
+    return L._CCache(a["n_pages"], a["page_size"], a["n_kv_heads"], a["head_dim"], a["bits"], a["k"], a["v"], a["ks"],
+                     a["vs"])
+
+
+BAD_CACHES = [dict(bits=2), dict(bits=16), dict(bits=0), dict(head_dim=0), dict(head_dim=24), dict(head_dim=272),
+              dict(head_dim=-16), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(page_size=0),
+              dict(page_size=-16), dict(n_pages=0), dict(n_pages=1 << 31), dict(n_kv_heads=0), dict(n_kv_heads=1 << 17),
+              dict(k=None), dict(vs=None), dict(v=(1 << 20) + 8), dict(ks=(1 << 20) + 4)]
+
+
+@pytest.mark.parametrize("bad", BAD_CACHES)
+def test_bad_caches_are_refused(L, bad):
+    lib, c = L._lib(), _cache(L, **bad)
+    ref = ctypes.byref(c)
+    assert lib.gptq_cache_write(ref, FAKE, FAKE, 1, 4, 1 << 20, 1 << 20, FAKE, None) == 1
+    assert lib.gptq_cache_read(ref, FAKE, 4, FAKE, FAKE, 1, None) == 1
+    heads = max(1, bad.get("n_kv_heads", 2))
+    assert lib.gptq_attention_workspace_size(ref, 4, heads, 1, 4) == 0
+    assert lib.gptq_cache_attention(ref, FAKE, 1, 4, 1 << 20, heads, FAKE, 4, FAKE, FAKE, 1, 0.1, FAKE, 1 << 20, FAKE,
+                                    1 << 30, None) == 1
+
+
+def test_cache_calls_refuse(L):
+    lib, ref = L._lib(), ctypes.byref(_cache(L))
+    w = lambda k=FAKE, v=FAKE, t=1, n=4, ldk=128, ldv=128, s=FAKE: lib.gptq_cache_write(ref, k, v, t, n, ldk, ldv, s, None)
+    assert lib.gptq_cache_write(None, FAKE, FAKE, 1, 4, 128, 128, FAKE, None) == 1
+    assert w(k=None) == 1 and w(v=None) == 1 and w(s=None) == 1 and w(k=ODD) == 1 and w(v=ODD) == 1
+    assert w(t=2) == 1 and w(t=-1) == 1 and w(n=-1) == 1 and w(n=(1 << 30) + 1) == 1
+    assert w(ldk=120) == 1 and w(ldv=127) == 1 and w(ldk=132) == 1   # shorter than a token, not whole vectors
+    assert w(k=None, v=None, s=None, n=0) == 0                         # no tokens: nothing to do
+    r = lambda s=FAKE, n=4, k=FAKE, v=FAKE, t=0: lib.gptq_cache_read(ref, s, n, k, v, t, None)
+    assert r(s=None) == 1 and r(k=None) == 1 and r(v=ODD) == 1 and r(t=2) == 1 and r(n=-2) == 1
+    assert r(n=0, s=None, k=None, v=None) == 0
+
+
+def test_attention_refuses(L):
+    lib, ref = L._lib(), ctypes.byref(_cache(L))
+    nan, inf = float("nan"), float("inf")
+
+    def call(q=FAKE, qt=1, n=4, ldq=512, heads=8, table=FAKE, pages=64, starts=FAKE, lens=FAKE, n_seq=2, scale=0.125,
+             out=FAKE, ldo=512, ws=FAKE, nb=1 << 32):
+        return lib.gptq_cache_attention(ref, q, qt, n, ldq, heads, table, pages, starts, lens, n_seq, scale, out, ldo, ws,
+                                        nb, None)
+    for kw in (dict(q=None), dict(q=ODD), dict(out=None), dict(out=ODD), dict(table=None), dict(starts=None),
+               dict(lens=None), dict(qt=0), dict(qt=2), dict(heads=7), dict(heads=0), dict(heads=-2), dict(n=-1),
+               dict(n=1 << 28), dict(ldq=511), dict(ldq=504), dict(ldo=500), dict(ldo=516), dict(pages=0),
+               dict(pages=1 << 40), dict(n_seq=-1), dict(n_seq=(1 << 20) + 1), dict(scale=0.0), dict(scale=-1.0),
+               dict(scale=nan), dict(scale=inf)):
+        assert call(**kw) == 1, kw
+    assert call(n=0) == 0 and call(n_seq=0) == 0
+    need = lib.gptq_attention_workspace_size(ref, 4, 8, 2, 64)
+    assert need > 0
+    assert call(ws=None) == 4 and call(nb=need - 1) == 4 and call(ws=ctypes.c_void_p((1 << 20) + 16)) == 4
+    assert lib.gptq_attention_workspace_size(ref, 4, 8, 2, 0) == 0
+    assert lib.gptq_attention_workspace_size(ref, 0, 8, 2, 64) == 0
+
+
+def test_integer_calls_refuse(L):
+    lib = L._lib()
+    q = lambda x=FAKE, t=1, n=4, d=64, ld=64, c=FAKE, s=FAKE: lib.gptq_quantize_tokens(x, t, n, d, ld, c, s, None, None)
+    for kw in (dict(x=None), dict(t=2), dict(t=5), dict(n=-1), dict(n=(1 << 30) + 1), dict(d=0), dict(d=(1 << 20) + 1),
+               dict(ld=63), dict(c=None), dict(s=None)):
+        assert q(**kw) == 1, kw
+    assert q(n=0, x=None, c=None, s=None) == 0
+    w = lambda qw=FAKE, z=FAKE, b=8, i=64, o=8, w_=FAKE, off=FAKE: lib.gptq_integer_weight(qw, z, b, i, o, w_, off, None)
+    for kw in (dict(qw=None), dict(z=None), dict(b=5), dict(i=48), dict(i=0), dict(o=0), dict(w_=None), dict(w_=ODD),
+               dict(off=None)):
+        assert w(**kw) == 1, kw
+
+    def mm(x=FAKE, t=1, xs=None, sums=None, m=4, d=64, ld=64, w=FAKE, ws=FAKE, off=None, o=8, y=FAKE, yt=0, buf=FAKE,
+           nb=1 << 30):
+        return lib.gptq_integer_matmul(x, t, xs, sums, m, d, ld, w, ws, off, o, y, yt, buf, nb, None)
+    for kw in (dict(x=None), dict(t=3), dict(m=-1), dict(m=(1 << 30) + 1), dict(d=48, ld=64), dict(d=1 << 17, ld=1 << 17),
+               dict(ld=32), dict(w=None), dict(w=ODD), dict(ws=None), dict(o=0), dict(y=None), dict(yt=2),
+               dict(t=2), dict(t=2, xs=FAKE, off=FAKE), dict(t=2, xs=FAKE, x=ODD), dict(t=2, xs=FAKE, ld=72),
+               dict(t=2, xs=FAKE, ld=(1 << 22) + 16)):
+        assert mm(**kw) == 1, kw
+    assert mm(m=0, x=None, w=None, y=None) == 0
+    need = lib.gptq_integer_workspace_size(4, 1, 64, 8)
+    assert need > 0
+    assert mm(buf=None) == 4 and mm(nb=need - 1) == 4 and mm(buf=ctypes.c_void_p((1 << 20) + 16)) == 4
+    for bad in ((0, 1, 64, 8), (4, 3, 64, 8), (4, 1, 48, 8), (4, 1, 1 << 17, 8), (4, 1, 64, 0)):
+        assert lib.gptq_integer_workspace_size(*bad) == 0
+
+
+def test_python_cache_checks(L):
+    """QuantizedCache refuses tensors that do not make a cache (CPU tensors among them)."""
+    import post_weight_quantization_07_amd as G
+    c = torch.zeros((2, 1, 16, 64), dtype=torch.int8)
+    s = torch.zeros((2, 1, 16))
+    with pytest.raises(ValueError, match="on the GPU"):
+        G.QuantizedCache(c, c, s, s, 8)
+    with pytest.raises(ValueError, match="bits"):
+        G.QuantizedCache(c, c, s, s, 2)
+    with pytest.raises(ValueError, match="codes must be"):
+        G.QuantizedCache(c[0], c[0], s, s, 8)
+    with pytest.raises(ValueError, match="head_dim"):
+        G.QuantizedCache.empty(2, 16, 1, 24, device="cpu")
+    with pytest.raises(ValueError, match="bits"):
+        G.QuantizedCache.empty(2, 16, 1, 64, bits=3, device="cpu")
