@@ -539,8 +539,10 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
         if y.shape != (m, d_out) or not y.is_contiguous():
             raise ValueError(f"{what}: y must be contiguous [m, d_out]")
     lib = _lib()
-    if ws is None and code != GPTQ_I8:
-        ws = torch.empty(lib.gptq_integer_workspace_size(m, code, d_in, d_out), dtype=torch.uint8, device=x.device)
+    if ws is None:
+        need = lib.gptq_integer_workspace_size(m, code, d_in, d_out)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     _check(lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, max(x.stride(0), d_in),
                                    w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), d_out, y.data_ptr(), yt, _ptr(ws),
                                    0 if ws is None else ws.numel(), _raw_stream(stream, dev)), what)

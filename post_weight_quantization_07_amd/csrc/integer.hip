@@ -254,6 +254,259 @@ __global__ __launch_bounds__(256) void integer_stream_kernel(IntParams p) {
   }
 }
 
+// Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
+// of 32 WM x 32 WN each.  Rows of both operands are k-contiguous, so a 64-byte
+// step of a tile goes to LDS by buffer_load ... lds as it lies in memory, through
+// a ring of four steps, and the MFMA operands are 16-byte LDS reads.  Each half
+// step's operands are read while the previous half's products run; one barrier
+// a step publishes the next step's data and frees the slot read two halves ago.
+// LDS rows are 64 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 2) & 3), so
+// 16 lanes that read one chunk of 16 rows touch all 64 banks once.
+constexpr int kTStep = 64, kTSlots = 4;
+
+#define GPTQ_VMCNT(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0F70)
+
+GPTQ_DEV __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* base, int64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+  const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+  const int n = __builtin_amdgcn_readfirstlane(static_cast<int>(bytes));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo),
+                                           static_cast<short>(0), n, 0x00020000);
+}
+
+// one piece (16 rows x 64 bytes) of a step to LDS
+GPTQ_DEV void tile_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* piece, uint32_t voff, int kc, int k0, int d_in) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)piece, 16, (k0 + kc < d_in) ? voff + k0 : 0x80000000u, 0, 0,
+                                           0);
+}
+
+template <int W>
+GPTQ_DEV void tile_read(const uint8_t* op, uint32_t off, i32x4_t (&f)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) f[i] = *reinterpret_cast<const i32x4_t*>(op + off + i * 2048);
+}
+
+template <int WM, int WN>
+GPTQ_DEV void tile_half(const i32x4_t (&a)[WM], const i32x4_t (&b)[WN], const uint8_t* nA, const uint8_t* nB,
+                        uint32_t offA, uint32_t offB, i32x4_t (&na)[WM], i32x4_t (&nb)[WN], i32x16_t (&acc)[WM][WN]) {
+  tile_read<WM>(nA, offA, na);
+  tile_read<WN>(nB, offB, nb);
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
+  // the next half's reads and this half's loads spread over the products
+  constexpr int kProd = WM * WN / (WM + WN);
+#pragma unroll
+  for (int k = 0; k < WM + WN; ++k) {
+    __builtin_amdgcn_sched_group_barrier(0x008, kProd, 0);                // products
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                    // one LDS read
+    if ((k & 1) == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // one load to LDS
+  }
+}
+
+struct TileGrid {
+  int32_t nm, nn;      // tiles along m and d_out
+  int32_t slices, per; // K slices and steps of each
+  int32_t* partial;    // [slice][m][d_out] when slices > 1
+};
+
+// Workgroups go round-robin over the 8 XCDs, each with its own L2: the tiles are
+// cut into 8 runs, and a run walks up to eight tiles of m before the next one of
+// d_out, so the workgroups of one XCD share rows of both operands.
+GPTQ_DEV void tile_of(const TileGrid& g, int b, int& tm, int& tn, int& slice) {
+  const int total = g.nm * g.nn * g.slices;
+  const int x = b & 7, base = total >> 3, rem = total & 7;
+  int q = x * base + min(x, rem) + (b >> 3);
+  slice = q / (g.nm * g.nn);
+  q -= slice * (g.nm * g.nn);
+  const int strip = q / (8 * g.nn), rows = min(8, g.nm - 8 * strip);
+  q -= strip * 8 * g.nn;
+  tm = 8 * strip + q % rows;
+  tn = q / rows;
+}
+
+enum { kOutF32 = 0, kOutBf16 = 1, kOutPart = 2 };
+
+template <int WM, int WN, int OUT>
+__global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid g) {
+  constexpr int kA = WM * 64 * kTStep, kB = WN * 64 * kTStep;
+  // one array per slot: the compiler then sees that reads of one slot do not alias loads in flight into another
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA], sA3[kA];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[kB], sB1[kB], sB2[kB], sB3[kB];
+  int tm, tn, slice;
+  tile_of(g, static_cast<int>(blockIdx.x), tm, tn, slice);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int64_t m0 = static_cast<int64_t>(tm) * (64 * WM), n0 = static_cast<int64_t>(tn) * (64 * WN);
+  const int mrows = static_cast<int>(min(p.m - m0, int64_t{64 * WM}));
+  const int nrows = static_cast<int>(min(p.d_out - n0, int64_t{64 * WN}));
+  const __amdgpu_buffer_rsrc_t ra = rows_rsrc(p.x + m0 * p.ldx, (mrows - 1) * p.ldx + p.d_in);
+  const __amdgpu_buffer_rsrc_t rb = rows_rsrc(p.w + n0 * p.d_in, static_cast<int64_t>(nrows) * p.d_in);
+  const int kc = (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
+  uint32_t va[WM], vb[WN];
+#pragma unroll
+  for (int u = 0; u < WM; ++u) {
+    const int row = (wave * WM + u) * 16 + (lane >> 2);
+    va[u] = row < mrows ? static_cast<uint32_t>(row * static_cast<int>(p.ldx) + kc) : 0x80000000u;
+  }
+#pragma unroll
+  for (int u = 0; u < WN; ++u) {
+    const int row = (wave * WN + u) * 16 + (lane >> 2);
+    vb[u] = row < nrows ? static_cast<uint32_t>(row * p.d_in + kc) : 0x80000000u;
+  }
+  const int s0 = slice * g.per;
+  const int steps = min(g.per, (p.d_in + kTStep - 1) / kTStep - s0);
+  auto slotA = [&](int u) -> uint8_t* { return (u & 3) == 0 ? sA0 : (u & 3) == 1 ? sA1 : (u & 3) == 2 ? sA2 : sA3; };
+  auto slotB = [&](int u) -> uint8_t* { return (u & 3) == 0 ? sB0 : (u & 3) == 1 ? sB1 : (u & 3) == 2 ? sB2 : sB3; };
+  // steps past the slice's end load nothing (every lane out of range: zeros)
+  auto issue_a = [&](int s, int slot) {
+    const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in;
+#pragma unroll
+    for (int u = 0; u < WM; ++u) tile_dma(ra, slotA(slot) + (wave * WM + u) * 1024, va[u], kc, k0, p.d_in);
+  };
+  auto issue_b = [&](int s, int slot) {
+    const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in;
+#pragma unroll
+    for (int u = 0; u < WN; ++u) tile_dma(rb, slotB(slot) + (wave * WN + u) * 1024, vb[u], kc, k0, p.d_in);
+  };
+  // operand reads: row l % 32 of a 32-row tile, chunk 2 half + l / 32
+  const int r = lane & 31, hi = lane >> 5;
+  uint32_t oa[2], ob[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t o = static_cast<uint32_t>(r * 64 + (((2 * h + hi) ^ ((r >> 2) & 3)) * 16));
+    oa[h] = o + wm * WM * 2048;
+    ob[h] = o + wn * WN * 2048;
+  }
+  i32x16_t acc[WM][WN];
+#pragma unroll
+  for (int i = 0; i < WM; ++i)
+#pragma unroll
+    for (int j = 0; j < WN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+  i32x4_t a0[WM], b0[WN], a1[WM], b1[WN];
+  constexpr int kL = WM + WN;  // loads of one step, per wave
+#pragma unroll
+  for (int u = 0; u < 3; ++u) {
+    issue_a(u, u);
+    issue_b(u, u);
+  }
+  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(2 * kL));
+  __builtin_amdgcn_s_barrier();
+  tile_read<WM>(sA0, oa[0], a0);
+  tile_read<WN>(sB0, ob[0], b0);
+  // steps in blocks of four; the ones past the end multiply zeros
+  for (int s = 0; s < steps; s += 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(kL));
+      __builtin_amdgcn_s_barrier();
+      issue_a(s + u + 3, u + 3);
+      tile_half<WM, WN>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
+      issue_b(s + u + 3, u + 3);
+      tile_half<WM, WN>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
+    }
+  }
+  // Element e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
+  // Stores go through buffer resources over the tile's rows: rows past m and
+  // columns past d_out (offset 2^31) are dropped in hardware.
+  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(0));  // the loads past the end still write LDS
+  const int dout = static_cast<int>(p.d_out);
+  const uint32_t row0 = static_cast<uint32_t>(wm * WM * 32 + 4 * hi);
+  if (OUT == kOutPart) {
+    const __amdgpu_buffer_rsrc_t rp =
+        rows_rsrc(reinterpret_cast<int8_t*>(g.partial + (static_cast<int64_t>(slice) * p.m + m0) * p.d_out),
+                  static_cast<int64_t>(mrows) * dout * 4);
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      const int col = static_cast<int>(n0) + (wn * WN + j) * 32 + r;
+#pragma unroll
+      for (int i = 0; i < WM; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint32_t row = row0 + 32 * i + 8 * (e >> 2) + (e & 3);
+          __builtin_amdgcn_raw_buffer_store_b32(acc[i][j][e], rp, col < dout ? (row * dout + col) * 4 : 0x80000000u, 0, 0);
+        }
+    }
+    return;
+  }
+  __syncthreads();  // the operands' LDS now holds the tile's row scales and code sums
+  float* lsc = reinterpret_cast<float*>(sA0);
+  int* lsm = reinterpret_cast<int*>(sB0);
+  for (int e = threadIdx.x; e < mrows; e += 256) {
+    lsc[e] = p.x_scales[m0 + e];
+    lsm[e] = p.w_offsets ? p.x_sums[m0 + e] : 0;
+  }
+  __syncthreads();
+  constexpr int size = OUT == kOutBf16 ? 2 : 4;
+  const __amdgpu_buffer_rsrc_t ry =
+      rows_rsrc(static_cast<const int8_t*>(p.y) + m0 * p.d_out * size, static_cast<int64_t>(mrows) * dout * size);
+#pragma unroll
+  for (int j = 0; j < WN; ++j) {
+    const int col = static_cast<int>(n0) + (wn * WN + j) * 32 + r;
+    const float sw = col < dout ? p.w_scales[col] : 0.f;
+    const int off = (col < dout && p.w_offsets) ? p.w_offsets[col] : 0;
+    const uint32_t at = col < dout ? static_cast<uint32_t>(col * size) : 0x80000000u;
+#pragma unroll
+    for (int i = 0; i < WM; ++i) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t row = row0 + 32 * i + 8 * q;
+        const f32x4_t sc = *reinterpret_cast<const f32x4_t*>(lsc + row);
+        const i32x4_t sm = *reinterpret_cast<const i32x4_t*>(lsm + row);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = (static_cast<float>(acc[i][j][4 * q + e] - off * sm[e]) * sc[e]) * sw;
+          const uint32_t to = at + (row + e) * static_cast<uint32_t>(dout * size);
+          if (OUT == kOutBf16)
+            __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(f32_to_bf16(v)), ry, to, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), ry, to, 0, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// sums of the K slices (integers: any order gives the same)
+__global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid g) {
+  const int64_t total = p.m * p.d_out;
+  for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < total; e += gridDim.x * 256ll) {
+    int s = 0;
+    for (int k = 0; k < g.slices; ++k) s += g.partial[k * total + e];
+    const int64_t row = e / p.d_out, col = e - row * p.d_out;
+    int_store(p, row, col, s, p.w_offsets ? p.w_offsets[col] : 0, p.w_scales[col]);
+  }
+}
+
+// The launch of a product: kernel, tile and K slices.
+struct IntPlan {
+  int kind;  // 0: stream, 1: 128 x 128 tiles, 2: 256 x 256
+  int slices, per;
+  size_t partial_bytes;
+};
+
+IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
+  IntPlan a{0, 1, 0, 0};
+  if (m <= 64) return a;
+  const int64_t t256 = ((m + 255) / 256) * ((d_out + 255) / 256), t128 = ((m + 127) / 128) * ((d_out + 127) / 128);
+  a.kind = t256 >= n_cu / 2 + 1 ? 2 : 1;
+  const int64_t tiles = a.kind == 2 ? t256 : t128;
+  const int steps = static_cast<int>((d_in + kTStep - 1) / kTStep);
+  const int64_t room = a.kind == 2 ? n_cu : 2 * n_cu;
+  int64_t sl = std::max<int64_t>(1, room / tiles);
+  sl = std::min<int64_t>(sl, std::max(1, steps / 16));
+  a.per = static_cast<int>((steps + sl - 1) / sl);
+  a.slices = (steps + a.per - 1) / a.per;
+  if (a.slices > 1) a.partial_bytes = static_cast<size_t>(a.slices) * m * d_out * 4;
+  return a;
+}
+
 }  // namespace
 
 hipError_t token_codes_launch(const void* x, bool bf16, int64_t m, int64_t d, int64_t ldx, int8_t* codes, float* scales,
@@ -274,27 +527,37 @@ hipError_t integer_weight_launch(const int32_t* qweight, const int32_t* zeros, i
   return hipGetLastError();
 }
 
+namespace {
+template <int WM, int WN>
+void tile_go(const IntParams& p, const TileGrid& g, unsigned blocks, hipStream_t st) {
+  if (g.slices > 1) integer_tile_kernel<WM, WN, kOutPart><<<blocks, 256, 0, st>>>(p, g);
+  else if (p.y_bf16) integer_tile_kernel<WM, WN, kOutBf16><<<blocks, 256, 0, st>>>(p, g);
+  else integer_tile_kernel<WM, WN, kOutF32><<<blocks, 256, 0, st>>>(p, g);
+}
+size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
+}  // namespace
+
+// workspace: the K slices' sums, then (x not given as codes) codes, scales and sums
 size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool codes_given, int n_cu) {
-  if (codes_given) return 0;
-  auto up = [](size_t v) { return (v + 255) & ~size_t{255}; };
-  return up(static_cast<size_t>(m) * d_in) + 2 * up(static_cast<size_t>(m) * 4);
+  const size_t part = up256(int_plan(m, d_in, d_out, n_cu).partial_bytes);
+  return codes_given ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
 }
 
 hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, const int32_t* x_sums, int64_t m,
                                  int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
                                  const int32_t* w_offsets, int64_t d_out, void* y, bool y_bf16, void* ws, int n_cu,
                                  hipStream_t st) {
+  const IntPlan plan = int_plan(m, d_in, d_out, n_cu);
   IntParams p;
   p.x = static_cast<const int8_t*>(x);
   p.ldx = ldx;
   p.x_scales = x_scales;
   p.x_sums = x_sums;
   if (xt != kXInt8) {
-    auto up = [](size_t v) { return (v + 255) & ~size_t{255}; };
-    uint8_t* b = static_cast<uint8_t*>(ws);
+    uint8_t* b = static_cast<uint8_t*>(ws) + up256(plan.partial_bytes);
     int8_t* codes = reinterpret_cast<int8_t*>(b);
-    float* sc = reinterpret_cast<float*>(b + up(static_cast<size_t>(m) * d_in));
-    int32_t* sm = reinterpret_cast<int32_t*>(b + up(static_cast<size_t>(m) * d_in) + up(static_cast<size_t>(m) * 4));
+    float* sc = reinterpret_cast<float*>(b + up256(static_cast<size_t>(m) * d_in));
+    int32_t* sm = reinterpret_cast<int32_t*>(b + up256(static_cast<size_t>(m) * d_in) + up256(static_cast<size_t>(m) * 4));
     const hipError_t e = token_codes_launch(x, xt == kXBf16, m, d_in, ldx, codes, sc, w_offsets ? sm : nullptr, st);
     if (e != hipSuccess) return e;
     p.x = codes;
@@ -310,9 +573,26 @@ hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, c
   p.d_out = d_out;
   p.d_in = static_cast<int32_t>(d_in);
   p.y_bf16 = y_bf16 ? 1 : 0;
-  const unsigned gx = static_cast<unsigned>((d_out + 15) / 16);
-  if (m <= 16) integer_stream_kernel<1><<<dim3(gx, 1), 256, 0, st>>>(p);
-  else integer_stream_kernel<2><<<dim3(gx, static_cast<unsigned>((m + 31) / 32)), 256, 0, st>>>(p);
+  if (plan.kind == 0) {
+    const unsigned gx = static_cast<unsigned>((d_out + 15) / 16);
+    if (m <= 16) integer_stream_kernel<1><<<dim3(gx, 1), 256, 0, st>>>(p);
+    else integer_stream_kernel<2><<<dim3(gx, static_cast<unsigned>((m + 31) / 32)), 256, 0, st>>>(p);
+    return hipGetLastError();
+  }
+  const int64_t edge = plan.kind == 2 ? 256 : 128;
+  TileGrid g{};
+  g.nm = static_cast<int32_t>((m + edge - 1) / edge);
+  g.nn = static_cast<int32_t>((d_out + edge - 1) / edge);
+  g.slices = plan.slices;
+  g.per = plan.per;
+  g.partial = static_cast<int32_t*>(ws);
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(g.nm) * g.nn * g.slices);
+  if (plan.kind == 2) tile_go<4, 4>(p, g, blocks, st);
+  else tile_go<2, 2>(p, g, blocks, st);
+  if (g.slices > 1) {
+    const unsigned jb = static_cast<unsigned>(std::min<int64_t>((m * d_out + 255) / 256, int64_t{n_cu} * 16));
+    integer_join_kernel<<<jb, 256, 0, st>>>(p, g);
+  }
   return hipGetLastError();
 }
 

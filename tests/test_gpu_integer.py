@@ -98,7 +98,8 @@ def test_layer_layout(G, bits, sym):
 
 SHAPES = [(1, 32, 1), (1, 96, 17), (1, 4096, 300), (2, 160, 33), (15, 4096, 64), (16, 224, 48), (17, 1024, 100),
           (31, 352, 257), (33, 2048, 130), (64, 4096, 272), (65, 32, 500), (100, 4128, 260), (128, 768, 768),
-          (129, 288, 511), (200, 11008, 70), (257, 1056, 300), (300, 96, 1030), (513, 4096, 520)]
+          (129, 288, 511), (200, 11008, 70), (257, 1056, 300), (300, 96, 1030), (513, 4096, 520), (4100, 96, 4200),
+          (2049, 352, 8300)]
 
 
 @pytest.mark.parametrize("m,d_in,d_out", SHAPES)
