@@ -70,13 +70,12 @@ def attention(q: np.ndarray, k: Tuple[np.ndarray, np.ndarray], v: Tuple[np.ndarr
               hidden: np.ndarray | None = None):
     """One sequence, one head: q [n, d] fp64, (codes, scales) of its L keys and
     values; token t sees the keys 0 .. L - n + t that are not hidden.  Returns
-    out [n, d] and the sums over the softmax that the tests' bounds take:
-    sum p |v|, sum p sv, and per row max_j over seen keys of
-    scale sk_j sum_d |q_d| (|ck_jd| + 24)."""
+    out [n, d] and what the tests' bounds take: sum p |v|, sum p sv, and per
+    row max_j over seen keys of scale sk_j sum_d |q_d| (|ck_jd| + 24) and max_j p_j."""
     (kc, ks), (vc, vs) = k, v
     n, L = q.shape[0], kc.shape[0]
     out, absv, plain = (np.zeros((n, vc.shape[1])) for _ in range(3))
-    worst = np.zeros(n)
+    worst, peak = np.zeros(n), np.zeros(n)
     for t in range(n):
         see = np.arange(L) <= L - n + t
         if hidden is not None:
@@ -90,5 +89,6 @@ def attention(q: np.ndarray, k: Tuple[np.ndarray, np.ndarray], v: Tuple[np.ndarr
         out[t] = (p * vs[see]) @ vc[see]
         absv[t] = (p * vs[see]) @ np.abs(vc[see])
         plain[t] = (p * vs[see]).sum()
+        peak[t] = p.max()
         worst[t] = (scale * ks[see] * ((np.abs(kc[see]) + 24.0) @ np.abs(q[t]))).max()
-    return out, absv, plain, worst
+    return out, absv, plain, worst, peak

@@ -4,10 +4,12 @@
 // h and its key head, over the keys j <= a:
 //   s_j = scale (q . ck_j) sk_j,  p = softmax(s),  out = sum_j p_j sv_j cv_j
 // in one pass over the keys with the running maximum and sum of the softmax.
-// The integer codes are exact in bf16 and enter the matrix cores as they are;
-// the key scale multiplies the score in fp32 and the value scale multiplies
-// p_j before its one rounding to bf16 (2^-9 relative, at most), so the scales
-// cost no precision and the products and sums are fp32.
+// Scores: q and the key codes are exact in bf16, their products are summed in
+// fp32 and the key scale multiplies the sum in fp32.  Output: the second
+// product runs in fp16, whose 11 bits round eight times finer than bf16's 8: an
+// operand is off by 2^-11 relative (2^-25 absolute, against values of up to 1,
+// below 2^-14).  fp16's range is kept by a power of two per workgroup, so that
+// the largest value scale seen so far stays in [1/2, 1) (ValueRange).
 //
 // The query heads that share a key head are rows of one tile: row r of a
 // sequence is token r / G, head r % G of its group, and M rows make a tile.
@@ -23,7 +25,13 @@
 namespace gptq {
 namespace {
 
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
+
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences stay defined
 constexpr int kUnit = 64;  // keys per unit of the work split
 
 struct AttnParams {
@@ -153,11 +161,28 @@ GPTQ_DEV float sum_over_groups(float v) {
 GPTQ_DEV uint32_t pack_hi(float lo, float hi) {  // two values exact in bf16
   return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
 }
-GPTQ_DEV uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(r) : "v"(lo), "v"(hi));
-  return r;
+GPTQ_DEV uint32_t pack_f16(float lo, float hi) {  // v_cvt_pk_f16_f32, nearest even
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), f16x2_t));
 }
+GPTQ_DEV float add_f16(uint32_t pair, float c) {  // c + both halves (v_dot2 with ones)
+  return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, pair), f16x2_t{1, 1}, c, false);
+}
+
+// The power of two that value scales are taken relative to: 2^(e - 126) is
+// above the largest finite scale seen (e: its biased exponent, 1 .. 252), so
+// scale * down() < 1.
+struct ValueRange {
+  int e;
+  GPTQ_DEV float down() const { return __uint_as_float(static_cast<uint32_t>(253 - e) << 23); }
+  GPTQ_DEV float up() const { return __uint_as_float(static_cast<uint32_t>(e + 1) << 23); }
+  GPTQ_DEV static int of(float scale) {
+    return min(max(static_cast<int>((__float_as_uint(scale) >> 23) & 255u), 1), 252);
+  }
+};
+GPTQ_DEV float exp2_int(int d) {  // 2^d for d <= 0 (0 below -126)
+  return d < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+}
+
 template <int B>
 GPTQ_DEV float sbyte(uint32_t w) {
   return static_cast<float>(static_cast<int8_t>(w >> (8 * B)));
@@ -177,25 +202,29 @@ GPTQ_DEV bf16x8_t row4(uint32_t a) {
                      ((a >> 5) & kNibMask) | kNibOne, ((a >> 9) & kNibMask) | kNibOne};
   return __builtin_bit_cast(bf16x8_t, v);
 }
-// byte B of eight keys' words
+// byte B of eight keys' words, in fp16 (exact)
 template <int B>
-GPTQ_DEV bf16x8_t col8(const uint32_t (&w)[8]) {
-  const u32x4_t v = {pack_hi(sbyte<B>(w[0]), sbyte<B>(w[1])), pack_hi(sbyte<B>(w[2]), sbyte<B>(w[3])),
-                     pack_hi(sbyte<B>(w[4]), sbyte<B>(w[5])), pack_hi(sbyte<B>(w[6]), sbyte<B>(w[7]))};
-  return __builtin_bit_cast(bf16x8_t, v);
+GPTQ_DEV f16x8_t col8(const uint32_t (&w)[8]) {
+  const u32x4_t v = {pack_f16(sbyte<B>(w[0]), sbyte<B>(w[1])), pack_f16(sbyte<B>(w[2]), sbyte<B>(w[3])),
+                     pack_f16(sbyte<B>(w[4]), sbyte<B>(w[5])), pack_f16(sbyte<B>(w[6]), sbyte<B>(w[7]))};
+  return __builtin_bit_cast(f16x8_t, v);
 }
-// both nibbles of byte B of eight keys' words, as 24 + code
+// both nibbles of byte B of eight keys' words, as 24 + code in fp16 (16 +
+// nibble: 0x4C00 | nibble << 6, exact)
+GPTQ_DEV uint32_t nib_pair(uint32_t w0, uint32_t w1, int byte) {
+  return __builtin_amdgcn_perm(w1, w0, 0x0C000C00u | ((4u + byte) << 16) | byte);
+}
 template <int B>
-GPTQ_DEV void col4(const uint32_t (&w)[8], bf16x8_t& lo, bf16x8_t& hi) {
+GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
   u32x4_t a, b;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t t = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], 0x0C000C00u | ((4u + B) << 16) | B);
-    a[i] = ((t << 3) & kNibMask) | kNibOne;
-    b[i] = ((t >> 1) & kNibMask) | kNibOne;
+    const uint32_t t = nib_pair(w[2 * i], w[2 * i + 1], B);
+    a[i] = ((t << 6) & 0x03C003C0u) | 0x4C004C00u;
+    b[i] = ((t << 2) & 0x03C003C0u) | 0x4C004C00u;
   }
-  lo = __builtin_bit_cast(bf16x8_t, a);
-  hi = __builtin_bit_cast(bf16x8_t, b);
+  lo = __builtin_bit_cast(f16x8_t, a);
+  hi = __builtin_bit_cast(f16x8_t, b);
 }
 
 // ---------------------------------------------------- keys split over waves --
@@ -265,6 +294,7 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 
   f32x4_t acc[MT][kTiles];
   float m[MT], l[MT], psum[MT];
+  ValueRange vr{1};
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     m[i] = kNegInf;
@@ -330,7 +360,31 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
         for (int r = 0; r < 4; ++r) s[i][4 * b + r] = a[r] * (ks[b][r] * p.scale_log2e);
       }
     }
-    bf16x8_t pop[MT];
+    // value scales: those of hidden keys may be anything, and count as 0
+    float vn[8], vtop = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      vn[j] = vs[j >> 2][j & 3];
+      if (masked && !(ok[j >> 2] && k0 + 16 * (j >> 2) + 4 * g + (j & 3) < vis)) vn[j] = 0.f;
+      vtop = fmaxf(vtop, vn[j]);
+    }
+    if (__any(ValueRange::of(vtop) > vr.e)) {
+      const int e = max(ValueRange::of(max_over_groups(vtop)), vr.e);
+      const float f = exp2_int(vr.e - e);
+      vr.e = e;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        psum[i] *= f;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][t][r] *= f;
+      }
+    }
+    const float down = vr.down();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) vn[j] *= down;
+    f16x8_t pop[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       bool see[8];
@@ -364,20 +418,19 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
       for (int j = 0; j < 8; ++j) {
         const float e = fast_exp2(s[i][j] - mm);
         l[i] += e;
-        pv[j] = e * vs[j >> 2][j & 3];
-        if (masked && !see[j]) pv[j] = 0.f;  // the scale of a key that is not there may be anything
+        pv[j] = e * vn[j];
+        if (masked && !see[j]) pv[j] = 0.f;  // a NaN scale reaches only the rows that see the key
       }
-      const u32x4_t pk = {pack_bf16(pv[0], pv[1]), pack_bf16(pv[2], pv[3]), pack_bf16(pv[4], pv[5]),
-                          pack_bf16(pv[6], pv[7])};
+      const u32x4_t pk = {pack_f16(pv[0], pv[1]), pack_f16(pv[2], pv[3]), pack_f16(pv[4], pv[5]), pack_f16(pv[6], pv[7])};
       if (BITS == 4) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) psum[i] += __uint_as_float(pk[e] << 16) + __uint_as_float(pk[e] & 0xFFFF0000u);
+        for (int e = 0; e < 4; ++e) psum[i] = add_f16(pk[e], psum[i]);
       }
-      pop[i] = __builtin_bit_cast(bf16x8_t, pk);
+      pop[i] = __builtin_bit_cast(f16x8_t, pk);
     }
 #pragma unroll
     for (int e = 0; e < kVW; ++e) {
-      bf16x8_t vop[8];
+      f16x8_t vop[8];
       if (BITS == 8) {
         vop[0] = col8<0>(vw[e]);
         vop[1] = col8<1>(vw[e]);
@@ -396,7 +449,7 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
       for (int t = 0; t < kPer; ++t)
 #pragma unroll
         for (int i = 0; i < MT; ++i)
-          acc[i][e * kPer + t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vop[t], pop[i], acc[i][e * kPer + t], 0, 0, 0);
+          acc[i][e * kPer + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vop[t], pop[i], acc[i][e * kPer + t], 0, 0, 0);
     }
   }
 
@@ -422,7 +475,7 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
     float top = kNegInf;
 #pragma unroll
     for (int v = 0; v < NW; ++v) top = fmaxf(top, wm[v][16 * i + c]);
-    const float f = fast_exp2(m[i] - (top == kNegInf ? 0.f : top));
+    const float f = fast_exp2(m[i] - (top == kNegInf ? 0.f : top)) * vr.up();
     // lane l: dims g HDP / 4 + r HDP / 16 + t
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -469,11 +522,365 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
   }
 }
 
+// ------------------------------------------------- rows split over waves --
+// A workgroup owns 32 NW rows of one (sequence, key head) and one key split;
+// each wave has 32 of the rows and all walk the keys in tiles of 64.
+//
+// Per tile the codes are turned into operands once, into LDS: the key codes
+// as bf16 integers, the values as fp16 code * scale * 2^-range (2^-11, like p).
+// 32x32x16 products: S^T = K Q^T leaves lane l (query row l % 32, half h = l / 32)
+// with keys 8 a + 4 h + b of a 32-key block; 16 of them in that order are the
+// P^T operand of O^T = V^T P^T, so V's operand holds keys 4 h + b and 8 + 4 h + b
+// of its 16, and P never moves between lanes.  An operand is 64 lanes of 16
+// bytes, stored lane by lane (1040-byte stride: the writers of one operand then
+// touch all banks), so every LDS read is contiguous.
+//
+// Two tiles of LDS: while one is multiplied, the next one's codes, loaded to
+// registers a tile ahead, are converted into the other; one barrier a tile.
+// The row maximum is only moved when some p would exceed 2^10 (fp16 holds 2^15;
+// p keeps its relative precision): the usual tile then costs a multiply-add and
+// an exp2 per score, half a maximum, half a conversion and half a sum.
+constexpr int kFrag = 1040;  // bytes of an operand in LDS
+constexpr float kGrow = 1024.f;
+
+template <int HDP, int BITS>
+struct TileRegs {
+  static constexpr int kKW = HDP * BITS / 128;   // words of K a thread converts: HDP / 4 dims of a key
+  static constexpr int kVB = HDP * BITS / 256;   // bytes of V per key: HDP / 32 dims of 8 keys
+  static constexpr int kVW = (kVB + 3) / 4;
+  uint32_t k[kKW], v[kVW][8];
+  f32x4_t vs[2];
+  float ks, kvs;   // lanes 0..15: scales of the wave's 16 keys
+  float vall;      // value scale of key `lane` of the tile (0: hidden)
+  uint32_t hide;   // bit i: the page of keys 16 i .. is not there
+};
+
+template <int HDP, int BITS, int NW>
+__global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_kernel(AttnParams p) {
+  using R = TileRegs<HDP, BITS>;
+  constexpr int kKeys = 64, kM = 32 * NW;
+  constexpr int kSteps = HDP / 16, kDb = HDP / 32;
+  constexpr int kKF = 2 * kSteps, kVF = 4 * kDb;  // operands of a tile
+  constexpr bool kBoth = NW == 4;                 // every wave converts keys and values; NW = 8: waves 0-3 keys, 4-7 values
+  __shared__ __attribute__((aligned(16))) uint8_t lk[2][kKF * kFrag], lv[2][kVF * kFrag];
+  __shared__ __attribute__((aligned(16))) float lks[2][kKeys];
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int c = lane & 31, hf = lane >> 5;
+  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.n_kv));
+  Work w;
+  if (!find_work<true>(p, blockIdx.x / static_cast<unsigned>(p.n_kv), w)) return;
+  const int rows = w.s.n * p.group;
+  const int r0 = w.tile * kM;
+  const int vis = w.s.len - w.s.n + (min(r0 + kM, rows) - 1) / p.group + 1;
+  const int units = vis > 0 ? (vis - 1) / kUnit + 1 : 0;
+  const int per = (units + w.n_split - 1) / w.n_split;
+  const int key0 = w.split * per * kUnit, key1 = min(vis, (w.split + 1) * per * kUnit);
+
+  // this wave's rows: their last keys, and the query operand
+  const int r = r0 + 32 * wave + c;
+  const bool live = r < rows;
+  const int tok = live ? r / p.group : 0, qh = live ? r % p.group : 0;
+  const int lim = live ? w.s.len - w.s.n + tok : -1;
+  const int wfirst = w.s.len - w.s.n + (r0 + 32 * wave) / p.group;  // last key of the wave's first row
+  const int wlast = r0 + 32 * wave < rows ? w.s.len - w.s.n + (min(r0 + 32 * wave + 32, rows) - 1) / p.group : -1;
+  bf16x8_t q[kSteps];
+  float bias = 0.f;
+  {
+    const uint16_t* src = p.q + static_cast<int64_t>(w.s.q0 + tok) * p.ldq + static_cast<int64_t>(h * p.group + qh) * p.hd;
+    float sum = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int d = 16 * s + 8 * hf;
+      u32x4_t v = {0u, 0u, 0u, 0u};
+      if (live && d < p.hd) v = *reinterpret_cast<const u32x4_t*>(src + d);
+      if (BITS == 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum += __uint_as_float(v[e] << 16) + __uint_as_float(v[e] & 0xFFFF0000u);
+        v = u32x4_t{(v[0] & 0xFFFFu) | (v[2] << 16), (v[0] >> 16) | (v[2] & 0xFFFF0000u),
+                    (v[1] & 0xFFFFu) | (v[3] << 16), (v[1] >> 16) | (v[3] & 0xFFFF0000u)};
+      }
+      q[s] = __builtin_bit_cast(bf16x8_t, v);
+    }
+    if (BITS == 4) bias = -24.f * (sum + __shfl_xor(sum, 32));
+  }
+
+  f32x16_t acc[kDb];
+#pragma unroll
+  for (int t = 0; t < kDb; ++t)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
+  float m = kNoMax, l = 0.f;
+  ValueRange vr{1}, vr_next{1};
+
+  const int row_bytes = p.hd * BITS / 8;
+  const int page_mask = (1 << p.page_shift) - 1;
+  const int32_t* table = p.table + static_cast<int64_t>(w.seq) * p.ld_table;
+  const int st = static_cast<int>(threadIdx.x) & 255;  // place in the converting group
+  const int sg = wave & 3;                             // its 16 keys of a tile
+  const int kkey = st >> 2, kpart = st & 3;            // K: a quarter of a key's dims
+  const int vdq = st & 31, vh = (st >> 5) & 1;         // V: HDP / 32 dims of keys 4 vh + b and 8 + 4 vh + b
+
+  auto load_page = [&](int base) -> int {
+    const int key = base + lane;
+    return key < key1 ? table[key >> p.page_shift] : -1;
+  };
+  auto load_tile = [&](int base, int page, R& t) {
+    const bool ok = page >= 0 && page < p.n_pages;
+    const uint64_t there = __ballot(ok);
+    t.hide = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t.hide |= ((there >> (16 * i)) & 1u) ? 0u : (1u << i);
+    const int key = base + lane;
+    const int pg = ok ? page : 0;
+    const int64_t all = ((static_cast<int64_t>(pg) * p.n_kv + h) << p.page_shift) + (key & page_mask);
+    t.vall = (ok && key < vis) ? p.scales[1][all] : 0.f;
+    const int pw = __builtin_amdgcn_readlane(pg, 16 * sg);
+    const int64_t row = ((static_cast<int64_t>(pw) * p.n_kv + h) << p.page_shift) + ((base + 16 * sg) & page_mask);
+    if (kBoth || wave < 4) {
+      const uint8_t* kp = p.codes[0] + (row + (kkey & 15)) * row_bytes + kpart * (R::kKW * 4);
+#pragma unroll
+      for (int e = 0; e < R::kKW; e += (BITS == 8 ? 2 : 1)) {
+        const bool in = kpart * (HDP / 4) + e * (32 / BITS) < p.hd;
+        if (BITS == 8) {
+          const uint2 v = in ? *reinterpret_cast<const uint2*>(kp + 4 * e) : make_uint2(0u, 0u);
+          t.k[e] = v.x;
+          t.k[e + 1] = v.y;
+        } else {
+          t.k[e] = in ? *reinterpret_cast<const uint32_t*>(kp + 4 * e) : 0u;
+        }
+      }
+      t.ks = p.scales[0][row + (lane & 15)];
+      t.kvs = p.scales[1][row + (lane & 15)];
+    }
+    if (kBoth || wave >= 4) {
+      const bool in = vdq * (HDP / 32) < p.hd;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint8_t* one = p.codes[1] + (row + 4 * vh + (j & 3) + 8 * (j >> 2)) * row_bytes + vdq * R::kVB;
+        if (R::kVB == 1) t.v[0][j] = in ? *one : 0u;
+        if (R::kVB == 2) t.v[0][j] = in ? *reinterpret_cast<const uint16_t*>(one) : 0u;
+        if (R::kVB >= 4) {
+#pragma unroll
+          for (int e = 0; e < R::kVW; ++e) t.v[e][j] = in ? *reinterpret_cast<const uint32_t*>(one + 4 * e) : 0u;
+        }
+      }
+      t.vs[0] = *reinterpret_cast<const f32x4_t*>(p.scales[1] + row + 4 * vh);
+      t.vs[1] = *reinterpret_cast<const f32x4_t*>(p.scales[1] + row + 8 + 4 * vh);
+    }
+  };
+  // codes in registers -> operands in LDS; moves vr_next to hold the tile's value scales
+  auto convert = [&](int base, const R& t, int buf) {
+    float top = fabsf(t.vall) < __builtin_inff() ? t.vall : 0.f;  // finite ones
+    if (__any(ValueRange::of(top) > vr_next.e)) {
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+      vr_next.e = max(vr_next.e, ValueRange::of(top));
+    }
+    if (kBoth || wave < 4) {
+#pragma unroll
+      for (int i = 0; i < HDP / 32; ++i) {
+        const int d = kpart * (HDP / 4) + 8 * i;
+        const bf16x8_t v = BITS == 8 ? row8(t.k[2 * i % R::kKW], t.k[(2 * i + 1) % R::kKW]) : row4(t.k[i % R::kKW]);
+        *reinterpret_cast<bf16x8_t*>(&lk[buf][((kkey >> 5) * kSteps + (d >> 4)) * kFrag + ((kkey & 31) + 4 * (d & 8)) * 16]) = v;
+      }
+      // a value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
+      // reaches only the rows that see the key
+      if (lane < 16) {
+        const bool bad = !(fabsf(t.kvs) < __builtin_inff());
+        lks[buf][16 * sg + lane] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
+      }
+    }
+    if (kBoth || wave >= 4) {
+      const float down = vr_next.down();
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = t.vs[j >> 2][j & 3];
+        const int key = base + 16 * sg + 4 * vh + (j & 3) + 8 * (j >> 2);
+        f[j] = (fabsf(s) < __builtin_inff() && key < vis && !((t.hide >> sg) & 1u)) ? s * down : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kDb; ++i) {
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (BITS == 8) {
+            const uint32_t word = t.v[(i >> 2) % R::kVW][j];
+            const float code = (i & 3) == 0 ? sbyte<0>(word) : (i & 3) == 1 ? sbyte<1>(word) : (i & 3) == 2 ? sbyte<2>(word) : sbyte<3>(word);
+            x[j] = code * f[j];
+          } else {
+            const uint32_t n = (t.v[(i >> 3) % R::kVW][j] >> (4 * (i & 7))) & 15u;
+            x[j] = (static_cast<float>(n) - 8.f) * f[j];
+          }
+        }
+        const u32x4_t o = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7])};
+        *reinterpret_cast<u32x4_t*>(&lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16]) = o;
+      }
+    }
+  };
+
+  R t;
+  uint32_t hide = 0u, hide_next = 0u;
+  int page = 0;
+  if (key0 < key1) {
+    page = load_page(key0);
+    load_tile(key0, page, t);
+    page = load_page(key0 + kKeys);
+    convert(key0, t, 0);
+    hide_next = t.hide;
+    load_tile(key0 + kKeys, page, t);
+    page = load_page(key0 + 2 * kKeys);
+  }
+  int buf = 0;
+  for (int base = key0; base < key1; base += kKeys, buf ^= 1) {
+    // this tile's operands are written, and the other buffer's have been read
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    hide = hide_next;
+    const bool work = base <= wlast;  // a causal tile past the wave's rows: nothing to multiply
+    const int e_tile = vr_next.e;     // the range this tile's values were written in
+    f32x16_t s[2];
+    if (work) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[b][e] = bias;
+#pragma unroll
+        for (int e = 0; e < kSteps; ++e)
+          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              *reinterpret_cast<const bf16x8_t*>(&lk[buf][(b * kSteps + e) * kFrag + lane * 16]), q[e], s[b], 0, 0, 0);
+      }
+    }
+    if (base + kKeys < key1) {
+      convert(base + kKeys, t, buf ^ 1);
+      hide_next = t.hide;
+      load_tile(base + 2 * kKeys, page, t);
+      page = load_page(base + 3 * kKeys);
+    }
+    if (!work) continue;
+    if (e_tile > vr.e) {
+      const float f = exp2_int(vr.e - e_tile);
+      vr.e = e_tile;
+#pragma unroll
+      for (int i = 0; i < kDb; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+    }
+    // scores, in units of log2
+    float x[2][16];
+    const bool masked = base + kKeys - 1 > wfirst || hide != 0u;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[b][4 * a + e] = s[b][4 * a + e] * ks[e];
+      }
+    if (masked) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int key = 32 * b + 8 * (e >> 2) + 4 * hf + (e & 3);
+          if (base + key > lim || ((hide >> (2 * b + (e >> 3))) & 1u)) x[b][e] = kNegInf;
+        }
+    }
+    float pv[2][16], top = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        pv[b][e] = fast_exp2(x[b][e] - m);
+        top = fmaxf(top, pv[b][e]);
+      }
+    if (__any(top > kGrow)) {
+      float mx = kNoMax;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[b][e]);
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      mx = fmaxf(mx, m);
+      const float f = fast_exp2(m - mx);
+      m = mx;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < kDb; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pv[b][e] = fast_exp2(x[b][e] - m);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        u32x4_t pk;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          pk[e] = pack_f16(pv[b][8 * a + 2 * e], pv[b][8 * a + 2 * e + 1]);
+          l = add_f16(pk[e], l);
+        }
+        const f16x8_t pop = __builtin_bit_cast(f16x8_t, pk);
+#pragma unroll
+        for (int i = 0; i < kDb; ++i)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * i + 2 * b + a) * kFrag + lane * 16]), pop, acc[i], 0, 0, 0);
+      }
+  }
+
+  // lane l: query row c, dims (8 a + 4 hf + b) HDP / 32 + i: for each a a run of 4 HDP / 32 dims
+  l += __shfl_xor(l, 32);
+  const int64_t slot = (w.slot + w.split) * p.n_kv + h;
+  const float up = vr.up();
+  if (w.n_split > 1) {
+    if (slot >= p.max_slots) return;
+    float* part = p.partial + slot * (kM * (HDP + 2));
+    const int row = 32 * wave + c;
+    if (hf == 0) {
+      part[kM * HDP + row] = m == kNoMax ? kNegInf : m;
+      part[kM * HDP + kM + row] = l;
+    }
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int e = 0; e < HDP / 32; ++e) {
+        f32x4_t o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = acc[(4 * e + j) % kDb][4 * a + (4 * e + j) / kDb] * up;
+        *reinterpret_cast<f32x4_t*>(part + row * HDP + (8 * a + 4 * hf) * (HDP / 32) + 4 * e) = o;
+      }
+    return;
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : up / l;
+  uint16_t* dst = p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(h * p.group + qh) * p.hd;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int e = 0; e < HDP / 64; ++e) {
+      const int d = (8 * a + 4 * hf) * (HDP / 32) + 8 * e;
+      u32x4_t o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int u = 8 * e + 2 * j;
+        o[j] = f32_to_bf16(acc[u % kDb][4 * a + u / kDb] * inv) |
+               (static_cast<uint32_t>(f32_to_bf16(acc[(u + 1) % kDb][4 * a + (u + 1) / kDb] * inv)) << 16);
+      }
+      if (d < p.hd) *reinterpret_cast<u32x4_t*>(dst + d) = o;
+    }
+}
+
 // Joins the splits of a tile, in their order.  One workgroup per (tile, key
 // head); tiles that were not split were written by the kernel above.
-template <int HDP, int MT>
+template <int HDP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
-  constexpr int kM = 16 * MT;
+  const int kM = p.tile_rows;
   const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.n_kv));
   Work w;
   if (!find_work<false>(p, blockIdx.x / static_cast<unsigned>(p.n_kv), w) || w.n_split == 1) return;
@@ -510,18 +917,21 @@ int head_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 
 template <int HDP, int BITS>
 void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
-  attn_split_kernel<HDP, BITS, 1, 8><<<blocks, 512, 0, st>>>(p);
-  if (joins) attn_join_kernel<HDP, 1><<<joins, 256, 0, st>>>(p);
+  switch (p.tile_rows) {
+    case 16: attn_split_kernel<HDP, BITS, 1, 8><<<blocks, 512, 0, st>>>(p); break;
+    default: attn_tile_kernel<HDP, BITS, 4><<<blocks, 256, 0, st>>>(p); break;
+  }
+  if (joins) attn_join_kernel<HDP><<<joins, 256, 0, st>>>(p);
 }
 
 }  // namespace
 
 AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t ld_table, int n_cu) {
   AttnPlan a{};
-  a.tile_rows = 16;
+  const int64_t group = n_heads / c.n_kv;
+  a.tile_rows = n_tokens * group <= 32ll * n_seq ? 16 : 128;
   a.target = 2 * n_cu;
   a.min_units = 4;
-  const int64_t group = n_heads / c.n_kv;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
   a.joins = tiles * c.n_kv;
   a.blocks = a.joins + a.target;

@@ -1,17 +1,25 @@
 """Attention over the quantized cache against its 64-bit form.
 
-The bound, per output element, with u = 2^-24 (fp32) and the reference's sums
-A = sum p |v|, B = sum p sv, W = max over seen keys of scale sk sum_d |q_d| (|ck_d| + 24):
+The bound, per output element, with u = 2^-24 (fp32), h = 2^-11 (fp16), L keys
+seen, c the largest code, and the reference's A = sum p |v|, B = sum p sv,
+P = max p, V = the sequence's largest value scale and
+W = max over seen keys of scale sk sum_d |q_d| (|ck_d| + 24):
   scores  products are exact, summed in fp32 over head_dim (4 bits: of q (24 +
           code) - 24 q): (hd + 2) u W; two scales, the maximum's difference and
           the sum: 5 u W more.  e^s turns it into a relative error of p, in the
           numerator and in the denominator: 2 (hd + 7) u W
-  p       exp2 to an ulp (2 u), the value scale (u), bf16: 2^-8
+  fp16    p (numerator, and denominator where the sum is of the rounded p) and
+          the values: h relative each, 3 h (1 + 2^-9) A.  Below 2^-14 the error
+          is absolute instead, 2^-25 of the unit: for p the unit is the largest p,
+          so L terms of at most c V give 2^-25 L c V P, and as much through the
+          denominator; where p carries the value scale, and for the values
+          themselves, the unit is at most 2 V: 2^-24 L c V P and 2^-24 V.
+          Together at most 2^-23 V (1 + c L P)
   sums    L terms and their rescalings in fp32, numerator and denominator:
           (L + 64) 4 u of A; at 4 bits the values enter as 24 + code, at most 32:
           another (L + 64) 2 u of 32 B
   output  bf16: 2^-8 of the value
-tolerance = A (1 + 2^-8) (2^-8 + 2 (hd + 7) u W + (L + 64) 4 u) + [4 bits] 32 B (L + 64) 2 u + 2^-8 (1 + 2^-6) |out|."""
+"""
 import numpy as np
 import pytest
 import torch
@@ -21,6 +29,13 @@ from oracle import serving_oracle as S
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
+
+
+def bound(ref, A, B, W, P, V, seen, hd, bits):
+    top = 127 if bits == 8 else 7
+    return (A * (3 * 2.0 ** -11 * (1 + 2.0 ** -9) + 2 * (hd + 7) * U * W + (seen + 64) * 4 * U)
+            + (32 * B * (seen + 64) * 2 * U if bits == 4 else 0) + 2.0 ** -23 * V * (1 + top * seen * P)
+            + 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(ref))
 
 
 @pytest.fixture(scope="module")
@@ -82,10 +97,9 @@ class Case:
                     if seen <= 0:
                         assert (got[a + t, h] == 0).all(), (i, h, t)
                         continue
-                    ref, A, B, W = S.attention(self.q_host[a + t:a + t + 1, h], (k[0][:seen], k[1][:seen]),
-                                               (v[0][:seen], v[1][:seen]), scale)
-                    tol = (A * (1 + 2.0 ** -8) * (2.0 ** -8 + 2 * (self.hd + 7) * U * W[0] + (seen + 64) * 4 * U)
-                           + (32 * B * (seen + 64) * 2 * U if self.bits == 4 else 0) + 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(ref))
+                    ref, A, B, W, P = S.attention(self.q_host[a + t:a + t + 1, h], (k[0][:seen], k[1][:seen]),
+                                                  (v[0][:seen], v[1][:seen]), scale)
+                    tol = bound(ref, A, B, W[0], P[0], v[1].max(), seen, self.hd, self.bits)
                     err = np.abs(got[a + t, h] - ref[0])
                     assert (err <= tol[0] + 1e-30).all(), (i, h, t, float((err / (tol[0] + 1e-30)).max()))
 
@@ -172,8 +186,8 @@ def test_values_that_do_not_fit(G):
         for h in range(4):
             k, v = (S.cache_rows(x, s, 8, pages, h // 2, length) for x, s in zip(c.codes, c.scales))
             a = int(c.starts[i])
-            ref, A, _, W = S.attention(c.q_host[a:a + n, h], k, v, 0.125, hidden)
-            tol = A * (1 + 2.0 ** -8) * (2.0 ** -8 + 2 * 71 * U * W[:, None] + (length + 64) * 4 * U) + 2.0 ** -8 * 1.02 * np.abs(ref)
+            ref, A, B, W, P = S.attention(c.q_host[a:a + n, h], k, v, 0.125, hidden)
+            tol = bound(ref, A, B, W[:, None], P[:, None], v[1].max(), length, 64, 8)
             assert (np.abs(out[a:a + n, h] - ref) <= tol).all()
     all_bad = torch.full_like(table, -1)
     assert not G.gptq_cache_attention(c.q, c.cache, all_bad, starts, lens).any()

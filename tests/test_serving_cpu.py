@@ -48,11 +48,12 @@ def test_attention_plain_form():
     L_, d = 5, 16
     kc, vc = np.zeros((L_, d)), r.integers(-127, 128, (L_, d)).astype(float)
     one = np.ones(L_)
-    out, absv, plain, _ = S.attention(r.standard_normal((7, d)), (kc, one), (vc, one), 0.25)
+    out, absv, plain, _, peak = S.attention(r.standard_normal((7, d)), (kc, one), (vc, one), 0.25)
     np.testing.assert_array_equal(out[:2], 0.0)              # 7 new tokens, 5 keys: two rows see nothing
     for t in range(2, 7):
         np.testing.assert_allclose(out[t], vc[:t - 1].mean(axis=0), rtol=1e-12)
     assert (absv >= np.abs(out) - 1e-12).all()
+    np.testing.assert_allclose(peak[2:], 1.0 / np.arange(1, 6), rtol=1e-12)
 
 
 def _cache(L, **kw):
