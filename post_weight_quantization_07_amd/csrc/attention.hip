@@ -131,7 +131,7 @@ GPTQ_DEV bool find_work(const AttnParams& p, int64_t u, Work& w) {
       const int64_t local = u - __shfl(end - cnt, l);
       w.slot = __shfl(slot_end - slot, l);
       if (SPLITS) {
-        w.tile = static_cast<int>(local / w.n_split);
+        w.tile = w.s.tiles - 1 - static_cast<int>(local / w.n_split);  // the ones that see most keys first
         w.split = static_cast<int>(local % w.n_split);
       } else {
         w.tile = static_cast<int>(local);
@@ -523,8 +523,10 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 }
 
 // ------------------------------------------------- rows split over waves --
-// A workgroup owns 32 NW rows of one (sequence, key head) and one key split;
-// each wave has 32 of the rows and all walk the keys in tiles of 64.
+// A workgroup owns 128 rows of one (sequence, key head) and one key split; each
+// of its four waves has 32 of the rows, and all walk the keys in tiles of 64.
+// (Eight waves of 32 rows, one workgroup a CU, convert half as often but wait
+// for each other: 267 us against 259 for four 2048-token prompts, 32 heads.)
 //
 // Per tile the codes are turned into operands once, into LDS: the key codes
 // as bf16 integers, the values as fp16 code * scale * 2^-range (2^-11, like p).
@@ -549,21 +551,19 @@ struct TileRegs {
   static constexpr int kVB = HDP * BITS / 256;   // bytes of V per key: HDP / 32 dims of 8 keys
   static constexpr int kVW = (kVB + 3) / 4;
   uint32_t k[kKW], v[kVW][8];
-  f32x4_t vs[2];
   float ks, kvs;   // lanes 0..15: scales of the wave's 16 keys
   float vall;      // value scale of key `lane` of the tile (0: hidden)
   uint32_t hide;   // bit i: the page of keys 16 i .. is not there
 };
 
-template <int HDP, int BITS, int NW>
-__global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_kernel(AttnParams p) {
+template <int HDP, int BITS>
+__global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
   using R = TileRegs<HDP, BITS>;
-  constexpr int kKeys = 64, kM = 32 * NW;
+  constexpr int kKeys = 64, kM = 128;
   constexpr int kSteps = HDP / 16, kDb = HDP / 32;
   constexpr int kKF = 2 * kSteps, kVF = 4 * kDb;  // operands of a tile
-  constexpr bool kBoth = NW == 4;                 // every wave converts keys and values; NW = 8: waves 0-3 keys, 4-7 values
   __shared__ __attribute__((aligned(16))) uint8_t lk[2][kKF * kFrag], lv[2][kVF * kFrag];
-  __shared__ __attribute__((aligned(16))) float lks[2][kKeys];
+  __shared__ __attribute__((aligned(16))) float lks[2][kKeys], lf[4][kKeys];  // lf: one row per wave
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 31, hf = lane >> 5;
@@ -616,10 +616,19 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
   const int row_bytes = p.hd * BITS / 8;
   const int page_mask = (1 << p.page_shift) - 1;
   const int32_t* table = p.table + static_cast<int64_t>(w.seq) * p.ld_table;
-  const int st = static_cast<int>(threadIdx.x) & 255;  // place in the converting group
-  const int sg = wave & 3;                             // its 16 keys of a tile
+  const int st = static_cast<int>(threadIdx.x);
+  const int sg = wave;                                 // the 16 keys of a tile that this wave converts
   const int kkey = st >> 2, kpart = st & 3;            // K: a quarter of a key's dims
   const int vdq = st & 31, vh = (st >> 5) & 1;         // V: HDP / 32 dims of keys 4 vh + b and 8 + 4 vh + b
+  // a thread whose dims lie past head_dim reads the row's first ones instead: q
+  // is zero there, and what V gives there is not stored
+  uint32_t koff[HDP / 32], voff;
+#pragma unroll
+  for (int i = 0; i < HDP / 32; ++i) {
+    const int d = kpart * (HDP / 4) + 8 * i;
+    koff[i] = static_cast<uint32_t>((kkey & 15) * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
+  }
+  voff = static_cast<uint32_t>(4 * vh * row_bytes + (vdq * (HDP / 32) < p.hd ? vdq * R::kVB : 0));
 
   auto load_page = [&](int base) -> int {
     const int key = base + lane;
@@ -637,47 +646,46 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
     t.vall = (ok && key < vis) ? p.scales[1][all] : 0.f;
     const int pw = __builtin_amdgcn_readlane(pg, 16 * sg);
     const int64_t row = ((static_cast<int64_t>(pw) * p.n_kv + h) << p.page_shift) + ((base + 16 * sg) & page_mask);
-    if (kBoth || wave < 4) {
-      const uint8_t* kp = p.codes[0] + (row + (kkey & 15)) * row_bytes + kpart * (R::kKW * 4);
+    {
+      const uint8_t* kp = p.codes[0] + row * row_bytes;
 #pragma unroll
       for (int e = 0; e < R::kKW; e += (BITS == 8 ? 2 : 1)) {
-        const bool in = kpart * (HDP / 4) + e * (32 / BITS) < p.hd;
         if (BITS == 8) {
-          const uint2 v = in ? *reinterpret_cast<const uint2*>(kp + 4 * e) : make_uint2(0u, 0u);
+          const uint2 v = *reinterpret_cast<const uint2*>(kp + koff[e / 2]);
           t.k[e] = v.x;
           t.k[e + 1] = v.y;
         } else {
-          t.k[e] = in ? *reinterpret_cast<const uint32_t*>(kp + 4 * e) : 0u;
+          t.k[e] = *reinterpret_cast<const uint32_t*>(kp + koff[e]);
         }
       }
-      t.ks = p.scales[0][row + (lane & 15)];
-      t.kvs = p.scales[1][row + (lane & 15)];
+      t.ks = (p.scales[0] + row)[lane & 15];
+      t.kvs = (p.scales[1] + row)[lane & 15];
     }
-    if (kBoth || wave >= 4) {
-      const bool in = vdq * (HDP / 32) < p.hd;
+    {
+      const uint8_t* vp = p.codes[1] + row * row_bytes;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const uint8_t* one = p.codes[1] + (row + 4 * vh + (j & 3) + 8 * (j >> 2)) * row_bytes + vdq * R::kVB;
-        if (R::kVB == 1) t.v[0][j] = in ? *one : 0u;
-        if (R::kVB == 2) t.v[0][j] = in ? *reinterpret_cast<const uint16_t*>(one) : 0u;
-        if (R::kVB >= 4) {
-#pragma unroll
-          for (int e = 0; e < R::kVW; ++e) t.v[e][j] = in ? *reinterpret_cast<const uint32_t*>(one + 4 * e) : 0u;
+        const uint8_t* one = vp + static_cast<uint32_t>(((j & 3) + 8 * (j >> 2)) * row_bytes);
+        if (R::kVB == 1) t.v[0][j] = one[voff];
+        if (R::kVB == 2) t.v[0][j] = *reinterpret_cast<const uint16_t*>(one + voff);
+        if (R::kVB == 4) t.v[0][j] = *reinterpret_cast<const uint32_t*>(one + voff);
+        if (R::kVB == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(one + voff);
+          t.v[0][j] = v.x;
+          t.v[R::kVW - 1][j] = v.y;
         }
       }
-      t.vs[0] = *reinterpret_cast<const f32x4_t*>(p.scales[1] + row + 4 * vh);
-      t.vs[1] = *reinterpret_cast<const f32x4_t*>(p.scales[1] + row + 8 + 4 * vh);
     }
   };
   // codes in registers -> operands in LDS; moves vr_next to hold the tile's value scales
-  auto convert = [&](int base, const R& t, int buf) {
+  auto convert = [&](const R& t, int buf) {
     float top = fabsf(t.vall) < __builtin_inff() ? t.vall : 0.f;  // finite ones
     if (__any(ValueRange::of(top) > vr_next.e)) {
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
       vr_next.e = max(vr_next.e, ValueRange::of(top));
     }
-    if (kBoth || wave < 4) {
+    {
 #pragma unroll
       for (int i = 0; i < HDP / 32; ++i) {
         const int d = kpart * (HDP / 4) + 8 * i;
@@ -691,14 +699,15 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
         lks[buf][16 * sg + lane] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
       }
     }
-    if (kBoth || wave >= 4) {
-      const float down = vr_next.down();
+    {
+      // each key's factor, by its lane, then the eight of this thread's keys
+      lf[wave][lane] = fabsf(t.vall) < __builtin_inff() ? t.vall * vr_next.down() : 0.f;
       float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = t.vs[j >> 2][j & 3];
-        const int key = base + 16 * sg + 4 * vh + (j & 3) + 8 * (j >> 2);
-        f[j] = (fabsf(s) < __builtin_inff() && key < vis && !((t.hide >> sg) & 1u)) ? s * down : 0.f;
+      for (int j = 0; j < 8; j += 4) {
+        const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 2 * j]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[j + e] = four[e];
       }
 #pragma unroll
       for (int i = 0; i < kDb; ++i) {
@@ -727,7 +736,7 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
     page = load_page(key0);
     load_tile(key0, page, t);
     page = load_page(key0 + kKeys);
-    convert(key0, t, 0);
+    convert(t, 0);
     hide_next = t.hide;
     load_tile(key0 + kKeys, page, t);
     page = load_page(key0 + 2 * kKeys);
@@ -744,17 +753,18 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
     f32x16_t s[2];
     if (work) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e) s[b][e] = bias;
 #pragma unroll
-        for (int e = 0; e < kSteps; ++e)
+      for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)  // two sums in turn
           s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
               *reinterpret_cast<const bf16x8_t*>(&lk[buf][(b * kSteps + e) * kFrag + lane * 16]), q[e], s[b], 0, 0, 0);
-      }
     }
     if (base + kKeys < key1) {
-      convert(base + kKeys, t, buf ^ 1);
+      convert(t, buf ^ 1);
       hide_next = t.hide;
       load_tile(base + 2 * kKeys, page, t);
       page = load_page(base + 3 * kKeys);
@@ -770,7 +780,6 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
     }
     // scores, in units of log2
     float x[2][16];
-    const bool masked = base + kKeys - 1 > wfirst || hide != 0u;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -779,14 +788,15 @@ __global__ __launch_bounds__(64 * NW, (HDP <= 128 ? 2 : NW / 4)) void attn_tile_
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[b][4 * a + e] = s[b][4 * a + e] * ks[e];
       }
-    if (masked) {
+    if (__builtin_expect(base + kKeys - 1 > wfirst || hide != 0u, 0)) {
+      const int rel = lim - base - 4 * hf;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int key = 32 * b + 8 * (e >> 2) + 4 * hf + (e & 3);
-          if (base + key > lim || ((hide >> (2 * b + (e >> 3))) & 1u)) x[b][e] = kNegInf;
-        }
+        for (int e = 0; e < 16; ++e)
+          if (32 * b + 8 * (e >> 2) + (e & 3) > rel || ((hide >> (2 * b + (e >> 3))) & 1u)) x[b][e] = kNegInf;
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");  // keeps this a branch: most tiles skip it
     }
     float pv[2][16], top = 0.f;
 #pragma unroll
@@ -919,7 +929,7 @@ template <int HDP, int BITS>
 void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
   switch (p.tile_rows) {
     case 16: attn_split_kernel<HDP, BITS, 1, 8><<<blocks, 512, 0, st>>>(p); break;
-    default: attn_tile_kernel<HDP, BITS, 4><<<blocks, 256, 0, st>>>(p); break;
+    default: attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p); break;
   }
   if (joins) attn_join_kernel<HDP><<<joins, 256, 0, st>>>(p);
 }
