@@ -46,9 +46,12 @@ struct AttnParams {
   int64_t ldq, ldo, ld_table;
   int64_t n_tokens, n_pages, max_slots;
   int32_t n_seq, n_kv, group, hd, page_shift;
-  int32_t tile_rows;   // M
-  int32_t target;      // workgroups the keys are split for
-  int32_t min_units;   // fewest units of a split
+  int32_t tile_rows, tile_shift;    // M, a power of two
+  int32_t max_len;                  // keys that a row of the table can name
+  float inv_target;                 // n_kv / the workgroups the keys are split for
+  float min_units;                  // fewest units of a split
+  uint32_t group_mul, group_shift;  // division by group
+  uint32_t kv_mul, kv_shift;        // division by n_kv
   float scale_log2e;
 };
 
@@ -56,92 +59,92 @@ struct Seq {
   int q0, n, len, tiles, units;
 };
 
+// n / d for 0 <= n < 2^30 by the multiplier and shift of exact_divisor()
+GPTQ_DEV int div_by(int n, uint32_t mul, uint32_t shift) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+}
+
 // everything read from the caller's device arrays is clamped, so that no value
 // in them makes an access leave its buffer
 GPTQ_DEV Seq seq_info(const AttnParams& p, int i) {
   Seq s;
-  const int64_t total = p.n_tokens;
-  const int64_t a = min(max(static_cast<int64_t>(p.starts[i]), int64_t{0}), total);
-  const int64_t b = min(max(static_cast<int64_t>(p.starts[i + 1]), a), total);
-  const int64_t cap = p.ld_table << p.page_shift;
-  s.q0 = static_cast<int>(a);
-  s.n = static_cast<int>(b - a);
-  s.len = static_cast<int>(min(max(static_cast<int64_t>(p.lens[i]), int64_t{0}), cap));
-  s.tiles = s.n > 0 ? (s.n * p.group - 1) / p.tile_rows + 1 : 0;
-  s.units = s.len > 0 ? (s.len - 1) / kUnit + 1 : 1;
+  const int total = static_cast<int>(p.n_tokens);
+  const int a = min(max(p.starts[i], 0), total);
+  const int b = min(max(p.starts[i + 1], a), total);
+  s.q0 = a;
+  s.n = b - a;
+  s.len = min(max(p.lens[i], 0), p.max_len);
+  s.tiles = (s.n * p.group + p.tile_rows - 1) >> p.tile_shift;
+  s.units = max((s.len + kUnit - 1) / kUnit, 1);
   return s;
 }
 
-GPTQ_DEV int64_t wave_scan(int64_t v, int lane) {
+template <typename T>
+GPTQ_DEV T wave_scan(T v, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int64_t o = __shfl_up(v, d);
+    const T o = __shfl_up(v, d);
     if (lane >= d) v += o;
   }
   return v;
 }
+GPTQ_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 struct Work {
   Seq s;
   int seq, tile, split, n_split;
-  int64_t slot;  // of the unit's first split (for this key head: times n_kv, plus h)
+  int slot;  // of the unit's first split (for this key head: times n_kv, plus h)
 };
 
 // Entry u of the list (SPLITS: of (tile, split) pairs; otherwise of tiles).
-// The keys of a sequence are split so that a split has at least `per` units,
-// per = (all units) / target: a batch with enough tiles is not split, a long
-// sequence among short ones is.
+// A sequence's keys are split into parts of at least `per` units, per = (all
+// units) / target: a batch with enough tiles is not split, a long sequence among
+// short ones is.  per is the same fp32 number in every workgroup; being off by
+// rounding it only moves where the parts end.
 template <bool SPLITS>
-GPTQ_DEV bool find_work(const AttnParams& p, int64_t u, Work& w) {
+GPTQ_DEV bool find_work(const AttnParams& p, int u, Work& w) {
   const int lane = lane_id();
-  int64_t total = 0;
+  Seq s{};
+  float total = 0.f;
   for (int i0 = 0; i0 < p.n_seq; i0 += 64) {
-    int64_t v = 0;
-    if (i0 + lane < p.n_seq) {
-      const Seq s = seq_info(p, i0 + lane);
-      v = static_cast<int64_t>(s.tiles) * s.units;
-    }
-    total += __shfl(wave_scan(v, lane), 63);
+    s = Seq{0, 0, 0, 0, 1};
+    if (i0 + lane < p.n_seq) s = seq_info(p, i0 + lane);
+    float v = static_cast<float>(s.tiles) * static_cast<float>(s.units);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+    total += v;
   }
-  const int64_t all = total * p.n_kv;
-  const int64_t per = max((all + p.target - 1) / p.target, static_cast<int64_t>(p.min_units));
-  int64_t base = 0, slots = 0;
+  const float inv_per = 1.f / fmaxf(total * p.inv_target, p.min_units);
+  int base = 0, slots = 0;
   for (int i0 = 0; i0 < p.n_seq; i0 += 64) {
-    Seq s{};
-    int64_t cnt = 0, slot = 0;
-    int n_split = 1;
-    if (i0 + lane < p.n_seq) {
-      s = seq_info(p, i0 + lane);
-      n_split = static_cast<int>((s.units + per - 1) / per);
-      slot = n_split > 1 ? static_cast<int64_t>(s.tiles) * n_split : 0;
-      cnt = SPLITS ? static_cast<int64_t>(s.tiles) * n_split : s.tiles;
+    if (p.n_seq > 64) {
+      s = Seq{0, 0, 0, 0, 1};
+      if (i0 + lane < p.n_seq) s = seq_info(p, i0 + lane);
     }
-    const int64_t end = base + wave_scan(cnt, lane);
-    const int64_t slot_end = slots + wave_scan(slot, lane);
+    const int n_split = max(static_cast<int>(ceilf(static_cast<float>(s.units) * inv_per)), 1);
+    const int pairs = s.tiles * n_split;
+    const int cnt = SPLITS ? pairs : s.tiles;
+    const int end = base + wave_scan(cnt, lane);
+    const int slot_end = slots + wave_scan(n_split > 1 ? pairs : 0, lane);
     const uint64_t hit = __ballot(u < end);
     if (hit) {
-      const int l = __builtin_ctzll(hit);
+      const int l = uniform(__builtin_ctzll(hit));
       w.seq = i0 + l;
-      w.s.q0 = __shfl(s.q0, l);
-      w.s.n = __shfl(s.n, l);
-      w.s.len = __shfl(s.len, l);
-      w.s.tiles = __shfl(s.tiles, l);
-      w.s.units = __shfl(s.units, l);
-      w.n_split = __shfl(n_split, l);
-      const int64_t local = u - __shfl(end - cnt, l);
-      w.slot = __shfl(slot_end - slot, l);
-      if (SPLITS) {
-        w.tile = w.s.tiles - 1 - static_cast<int>(local / w.n_split);  // the ones that see most keys first
-        w.split = static_cast<int>(local % w.n_split);
-      } else {
-        w.tile = static_cast<int>(local);
-        w.split = 0;
-      }
-      w.slot += static_cast<int64_t>(w.tile) * w.n_split;
-      return true;
+      w.s.q0 = __builtin_amdgcn_readlane(s.q0, l);
+      w.s.n = __builtin_amdgcn_readlane(s.n, l);
+      w.s.len = __builtin_amdgcn_readlane(s.len, l);
+      w.s.tiles = __builtin_amdgcn_readlane(s.tiles, l);
+      w.n_split = __builtin_amdgcn_readlane(n_split, l);
+      const int local = u - __builtin_amdgcn_readlane(end - cnt, l);
+      w.slot = __builtin_amdgcn_readlane(n_split > 1 ? slot_end - pairs : 0, l);
+      const int tile = SPLITS ? uniform(local / w.n_split) : local;
+      w.split = SPLITS ? local - tile * w.n_split : 0;
+      w.tile = SPLITS ? w.s.tiles - 1 - tile : tile;  // the ones that see most keys first
+      w.slot += w.tile * w.n_split;
+      return local >= 0 && w.tile >= 0;
     }
-    base = __shfl(end, 63);
-    slots = __shfl(slot_end, 63);
+    base = __builtin_amdgcn_readlane(end, 63);
+    slots = __builtin_amdgcn_readlane(slot_end, 63);
   }
   return false;
 }
@@ -163,6 +166,10 @@ GPTQ_DEV uint32_t pack_hi(float lo, float hi) {  // two values exact in bf16
 }
 GPTQ_DEV uint32_t pack_f16(float lo, float hi) {  // v_cvt_pk_f16_f32, nearest even
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), f16x2_t));
+}
+GPTQ_DEV uint32_t pack_bf16(float lo, float hi) {  // v_cvt_pk_bf16_f32, nearest even
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
 }
 GPTQ_DEV float add_f16(uint32_t pair, float c) {  // c + both halves (v_dot2 with ones)
   return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, pair), f16x2_t{1, 1}, c, false);
@@ -251,13 +258,14 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.n_kv));
+  const int u = uniform(div_by(static_cast<int>(blockIdx.x), p.kv_mul, p.kv_shift));
+  const int h = static_cast<int>(blockIdx.x) - u * p.n_kv;
   Work w;
-  if (!find_work<true>(p, blockIdx.x / static_cast<unsigned>(p.n_kv), w)) return;
+  if (!find_work<true>(p, u, w)) return;
   const int rows = w.s.n * p.group;
   const int r0 = w.tile * kM;
-  const int first = w.s.len - w.s.n + r0 / p.group;                              // last key of the tile's first row
-  const int vis = w.s.len - w.s.n + (min(r0 + kM, rows) - 1) / p.group + 1;       // keys any of its rows sees
+  const int first = w.s.len - w.s.n + uniform(div_by(r0, p.group_mul, p.group_shift));                              // last key of the tile's first row
+  const int vis = w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1;       // keys any of its rows sees
   const int units = vis > 0 ? (vis - 1) / kUnit + 1 : 0;
   const int per = (units + w.n_split - 1) / w.n_split;
   const int key0 = w.split * per * kUnit, key1 = min(vis, (w.split + 1) * per * kUnit);
@@ -270,10 +278,10 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
   for (int i = 0; i < MT; ++i) {
     const int r = r0 + 16 * i + c;
     const bool live = r < rows;
-    const int tok = live ? r / p.group : 0;
+    const int tok = live ? div_by(r, p.group_mul, p.group_shift) : 0;
     lim[i] = live ? w.s.len - w.s.n + tok : -1;
     const uint16_t* src = p.q + static_cast<int64_t>(w.s.q0 + tok) * p.ldq +
-                          static_cast<int64_t>(h * p.group + (live ? r % p.group : 0)) * p.hd;
+                          static_cast<int64_t>(h * p.group + (live ? r - tok * p.group : 0)) * p.hd;
     float sum = 0.f;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
@@ -466,7 +474,7 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
     }
   }
   __syncthreads();
-  const int64_t slot = (w.slot + w.split) * p.n_kv + h;
+  const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const bool whole = w.n_split == 1;
   if (!whole && slot >= p.max_slots) return;  // the whole workgroup
   float* part = p.partial + slot * (kM * (HDP + 2));
@@ -511,11 +519,10 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
         }
       } else if (r < rows && d < p.hd) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint2 b;
-        b.x = f32_to_bf16(o[0] * inv) | (static_cast<uint32_t>(f32_to_bf16(o[1] * inv)) << 16);
-        b.y = f32_to_bf16(o[2] * inv) | (static_cast<uint32_t>(f32_to_bf16(o[3] * inv)) << 16);
-        *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + r / p.group) * p.ldo +
-                                  static_cast<int64_t>(h * p.group + r % p.group) * p.hd + d) = b;
+        const int tok = div_by(r, p.group_mul, p.group_shift);
+        const uint2 b = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo +
+                                  static_cast<int64_t>(h * p.group + r - tok * p.group) * p.hd + d) = b;
       }
     }
     __syncthreads();
@@ -529,7 +536,7 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 // for each other: 267 us against 259 for four 2048-token prompts, 32 heads.)
 //
 // Per tile the codes are turned into operands once, into LDS: the key codes
-// as bf16 integers, the values as fp16 code * scale * 2^-range (2^-11, like p).
+// as bf16 integers, the values as fp16 code * (scale * 2^-range) (two roundings).
 // 32x32x16 products: S^T = K Q^T leaves lane l (query row l % 32, half h = l / 32)
 // with keys 8 a + 4 h + b of a 32-key block; 16 of them in that order are the
 // P^T operand of O^T = V^T P^T, so V's operand holds keys 4 h + b and 8 + 4 h + b
@@ -539,9 +546,9 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 //
 // Two tiles of LDS: while one is multiplied, the next one's codes, loaded to
 // registers a tile ahead, are converted into the other; one barrier a tile.
-// The row maximum is only moved when some p would exceed 2^10 (fp16 holds 2^15;
-// p keeps its relative precision): the usual tile then costs a multiply-add and
-// an exp2 per score, half a maximum, half a conversion and half a sum.
+// The row maximum is only moved when a lane's weights sum to more than 2^10 (fp16
+// holds 2^15; p keeps its relative precision): the usual tile then costs a multiply-add and
+// an exp2 per score, half a conversion and half a sum.
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 1024.f;
 
@@ -567,12 +574,13 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 31, hf = lane >> 5;
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.n_kv));
+  const int u = uniform(div_by(static_cast<int>(blockIdx.x), p.kv_mul, p.kv_shift));
+  const int h = static_cast<int>(blockIdx.x) - u * p.n_kv;
   Work w;
-  if (!find_work<true>(p, blockIdx.x / static_cast<unsigned>(p.n_kv), w)) return;
+  if (!find_work<true>(p, u, w)) return;
   const int rows = w.s.n * p.group;
   const int r0 = w.tile * kM;
-  const int vis = w.s.len - w.s.n + (min(r0 + kM, rows) - 1) / p.group + 1;
+  const int vis = w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1;
   const int units = vis > 0 ? (vis - 1) / kUnit + 1 : 0;
   const int per = (units + w.n_split - 1) / w.n_split;
   const int key0 = w.split * per * kUnit, key1 = min(vis, (w.split + 1) * per * kUnit);
@@ -580,10 +588,10 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
   // this wave's rows: their last keys, and the query operand
   const int r = r0 + 32 * wave + c;
   const bool live = r < rows;
-  const int tok = live ? r / p.group : 0, qh = live ? r % p.group : 0;
+  const int tok = live ? div_by(r, p.group_mul, p.group_shift) : 0, qh = live ? r - tok * p.group : 0;
   const int lim = live ? w.s.len - w.s.n + tok : -1;
-  const int wfirst = w.s.len - w.s.n + (r0 + 32 * wave) / p.group;  // last key of the wave's first row
-  const int wlast = r0 + 32 * wave < rows ? w.s.len - w.s.n + (min(r0 + 32 * wave + 32, rows) - 1) / p.group : -1;
+  const int wfirst = w.s.len - w.s.n + uniform(div_by(r0 + 32 * wave, p.group_mul, p.group_shift));  // last key of the wave's first row
+  const int wlast = r0 + 32 * wave < rows ? w.s.len - w.s.n + uniform(div_by(min(r0 + 32 * wave + 32, rows) - 1, p.group_mul, p.group_shift)) : -1;
   bf16x8_t q[kSteps];
   float bias = 0.f;
   {
@@ -702,28 +710,32 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
     {
       // each key's factor, by its lane, then the eight of this thread's keys
       lf[wave][lane] = fabsf(t.vall) < __builtin_inff() ? t.vall * vr_next.down() : 0.f;
-      float f[8];
+      f16x2_t f[4];
 #pragma unroll
-      for (int j = 0; j < 8; j += 4) {
-        const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 2 * j]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[j + e] = four[e];
+      for (int j = 0; j < 4; j += 2) {
+        const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 4 * j]);
+        f[j] = __builtin_bit_cast(f16x2_t, pack_f16(four[0], four[1]));
+        f[j + 1] = __builtin_bit_cast(f16x2_t, pack_f16(four[2], four[3]));
       }
 #pragma unroll
       for (int i = 0; i < kDb; ++i) {
-        float x[8];
+        u32x4_t o;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
+          f16x2_t code;
           if (BITS == 8) {
-            const uint32_t word = t.v[(i >> 2) % R::kVW][j];
-            const float code = (i & 3) == 0 ? sbyte<0>(word) : (i & 3) == 1 ? sbyte<1>(word) : (i & 3) == 2 ? sbyte<2>(word) : sbyte<3>(word);
-            x[j] = code * f[j];
+            const uint32_t w0 = t.v[(i >> 2) % R::kVW][2 * j], w1 = t.v[(i >> 2) % R::kVW][2 * j + 1];
+            code = __builtin_bit_cast(f16x2_t, (i & 3) == 0   ? pack_f16(sbyte<0>(w0), sbyte<0>(w1))
+                                               : (i & 3) == 1 ? pack_f16(sbyte<1>(w0), sbyte<1>(w1))
+                                               : (i & 3) == 2 ? pack_f16(sbyte<2>(w0), sbyte<2>(w1))
+                                                              : pack_f16(sbyte<3>(w0), sbyte<3>(w1)));
           } else {
-            const uint32_t n = (t.v[(i >> 3) % R::kVW][j] >> (4 * (i & 7))) & 15u;
-            x[j] = (static_cast<float>(n) - 8.f) * f[j];
+            const uint32_t n = nib_pair(t.v[(i >> 3) % R::kVW][2 * j], t.v[(i >> 3) % R::kVW][2 * j + 1], (i >> 1) & 3);
+            const uint32_t c24 = (((i & 1) ? n << 2 : n << 6) & 0x03C003C0u) | 0x4C004C00u;
+            code = __builtin_bit_cast(f16x2_t, c24) - f16x2_t{24, 24};  // exact
           }
+          o[j] = __builtin_bit_cast(uint32_t, static_cast<f16x2_t>(code * f[j]));
         }
-        const u32x4_t o = {pack_f16(x[0], x[1]), pack_f16(x[2], x[3]), pack_f16(x[4], x[5]), pack_f16(x[6], x[7])};
         *reinterpret_cast<u32x4_t*>(&lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16]) = o;
       }
     }
@@ -778,42 +790,57 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][e] *= f;
     }
-    // scores, in units of log2
-    float x[2][16];
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[b][4 * a + e] = s[b][4 * a + e] * ks[e];
-      }
-    if (__builtin_expect(base + kKeys - 1 > wfirst || hide != 0u, 0)) {
+    // bit 16 b + e: key 32 b + 8 (e / 4) + 4 hf + e % 4 is seen; asked for in the last tiles only
+    const bool masked = base + kKeys - 1 > wfirst || hide != 0u;
+    uint32_t see = 0xFFFFFFFFu;
+    if (masked) {
       const int rel = lim - base - 4 * hf;
+      see = 0u;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-          if (32 * b + 8 * (e >> 2) + (e & 3) > rel || ((hide >> (2 * b + (e >> 3))) & 1u)) x[b][e] = kNegInf;
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" ::: "memory");  // keeps this a branch: most tiles skip it
+          if (32 * b + 8 * (e >> 2) + (e & 3) <= rel && !((hide >> (2 * b + (e >> 3))) & 1u)) see |= 1u << (16 * b + e);
     }
-    float pv[2][16], top = 0.f;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        pv[b][e] = fast_exp2(x[b][e] - m);
-        top = fmaxf(top, pv[b][e]);
-      }
-    if (__any(top > kGrow)) {
-      float mx = kNoMax;
+    u32x4_t pk[4];
+    float lt = 0.f;
+    // p = 2^(s sk - m), rounded to fp16, and its sum
+    auto weights = [&](bool mask) {
+      lt = 0.f;
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[b][e]);
+        for (int a = 0; a < 4; ++a) {
+          const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
+          float pv[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            pv[e] = fast_exp2(fmaf(s[b][4 * a + e], ks[e], -m));
+            if (mask) pv[e] = (see >> (16 * b + 4 * a + e)) & 1u ? pv[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t two = pack_f16(pv[2 * e], pv[2 * e + 1]);
+            pk[2 * b + (a >> 1)][2 * (a & 1) + e] = two;
+            lt = add_f16(two, lt);
+          }
+        }
+    };
+    if (masked) weights(true);
+    else weights(false);
+    // a lane's 32 weights sum to more than 2^10: one may be (a row's first keys: all are)
+    if (__any(lt > kGrow)) {
+      float mx = m;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx = fmaxf(mx, (see >> (16 * b + 4 * a + e)) & 1u ? s[b][4 * a + e] * ks[e] : kNegInf);
+        }
       mx = fmaxf(mx, __shfl_xor(mx, 32));
-      mx = fmaxf(mx, m);
       const float f = fast_exp2(m - mx);
       m = mx;
       l *= f;
@@ -821,32 +848,22 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       for (int i = 0; i < kDb; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pv[b][e] = fast_exp2(x[b][e] - m);
+      weights(true);
     }
+    l += lt;
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int t4 = 0; t4 < 4; ++t4) {
+      const f16x8_t pop = __builtin_bit_cast(f16x8_t, pk[t4]);
 #pragma unroll
-      for (int a = 0; a < 2; ++a) {
-        u32x4_t pk;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pk[e] = pack_f16(pv[b][8 * a + 2 * e], pv[b][8 * a + 2 * e + 1]);
-          l = add_f16(pk[e], l);
-        }
-        const f16x8_t pop = __builtin_bit_cast(f16x8_t, pk);
-#pragma unroll
-        for (int i = 0; i < kDb; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * i + 2 * b + a) * kFrag + lane * 16]), pop, acc[i], 0, 0, 0);
-      }
+      for (int i = 0; i < kDb; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+            *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * i + t4) * kFrag + lane * 16]), pop, acc[i], 0, 0, 0);
+    }
   }
 
   // lane l: query row c, dims (8 a + 4 hf + b) HDP / 32 + i: for each a a run of 4 HDP / 32 dims
   l += __shfl_xor(l, 32);
-  const int64_t slot = (w.slot + w.split) * p.n_kv + h;
+  const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const float up = vr.up();
   if (w.n_split > 1) {
     if (slot >= p.max_slots) return;
@@ -891,13 +908,14 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
 template <int HDP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   const int kM = p.tile_rows;
-  const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.n_kv));
+  const int u = uniform(div_by(static_cast<int>(blockIdx.x), p.kv_mul, p.kv_shift));
+  const int h = static_cast<int>(blockIdx.x) - u * p.n_kv;
   Work w;
-  if (!find_work<false>(p, blockIdx.x / static_cast<unsigned>(p.n_kv), w) || w.n_split == 1) return;
+  if (!find_work<false>(p, u, w) || w.n_split == 1) return;
   const int rows = w.s.n * p.group, r0 = w.tile * kM;
-  if ((w.slot + w.n_split - 1) * p.n_kv + h >= p.max_slots) return;
+  if (static_cast<int64_t>(w.slot + w.n_split - 1) * p.n_kv + h >= p.max_slots) return;
   const int64_t step = static_cast<int64_t>(p.n_kv) * (kM * (HDP + 2));
-  const float* part = p.partial + (w.slot * p.n_kv + h) * (kM * (HDP + 2));
+  const float* part = p.partial + (static_cast<int64_t>(w.slot) * p.n_kv + h) * (kM * (HDP + 2));
   for (int e = threadIdx.x; e < kM * HDP / 4; e += 256) {
     const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
     const int r = r0 + row;
@@ -915,12 +933,21 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
       for (int j = 0; j < 4; ++j) o[j] += f * a[j];
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint2 b;
-    b.x = f32_to_bf16(o[0] * inv) | (static_cast<uint32_t>(f32_to_bf16(o[1] * inv)) << 16);
-    b.y = f32_to_bf16(o[2] * inv) | (static_cast<uint32_t>(f32_to_bf16(o[3] * inv)) << 16);
-    *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + r / p.group) * p.ldo +
-                              static_cast<int64_t>(h * p.group + r % p.group) * p.hd + d) = b;
+    const int tok = div_by(r, p.group_mul, p.group_shift);
+    const uint2 b = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+    *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo +
+                              static_cast<int64_t>(h * p.group + r - tok * p.group) * p.hd + d) = b;
   }
+}
+
+// (n * mul) >> shift == n / d for 0 <= n < 2^30: mul = ceil(2^(30 + L) / d) with
+// 2^L >= d exceeds 2^(30 + L) / d by less than 1, which adds less than
+// n / 2^(30 + L) < 1 / d to the quotient
+void exact_divisor(int32_t d, uint32_t* mul, uint32_t* shift) {
+  uint32_t l = 0;
+  while ((int64_t{1} << l) < d) ++l;
+  *shift = 30 + l;
+  *mul = static_cast<uint32_t>(((uint64_t{1} << (30 + l)) + d - 1) / d);
 }
 
 int head_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
@@ -944,14 +971,14 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   a.min_units = 4;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
   a.joins = tiles * c.n_kv;
-  a.blocks = a.joins + a.target;
+  a.blocks = a.joins + a.target + 64;  // 64: the split is decided in fp32
   // no sequence can have more units than one split holds: nothing to join
   const int64_t most = (ld_table * c.page + kUnit - 1) / kUnit;
   if (most <= a.min_units) {
     a.joins = 0;
     a.blocks = tiles * c.n_kv;
   } else {
-    a.slots = 2 * static_cast<int64_t>(a.target);
+    a.slots = 2 * static_cast<int64_t>(a.target) + 64;  // a split sequence has fewer than 2 units / per parts
     a.ws_bytes = static_cast<size_t>(a.slots) * a.tile_rows * (head_pad(c.hd) + 2) * 4;
   }
   return a;
@@ -984,8 +1011,12 @@ hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const voi
   p.hd = c.hd;
   p.page_shift = __builtin_ctz(static_cast<unsigned>(c.page));
   p.tile_rows = plan.tile_rows;
-  p.target = plan.target;
-  p.min_units = plan.min_units;
+  p.tile_shift = __builtin_ctz(static_cast<unsigned>(plan.tile_rows));
+  p.max_len = static_cast<int32_t>(ld_table * c.page);
+  p.inv_target = static_cast<float>(c.n_kv) / static_cast<float>(plan.target);
+  p.min_units = static_cast<float>(plan.min_units);
+  exact_divisor(p.group, &p.group_mul, &p.group_shift);
+  exact_divisor(p.n_kv, &p.kv_mul, &p.kv_shift);
   p.scale_log2e = scale * 1.4426950408889634f;
   const unsigned b = static_cast<unsigned>(plan.blocks), j = static_cast<unsigned>(plan.joins);
   const int hp = head_pad(c.hd);
