@@ -685,180 +685,256 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       }
     }
   };
-  // codes in registers -> operands in LDS; moves vr_next to hold the tile's value scales
-  auto convert = [&](const R& t, int buf) {
+  // codes in registers -> operands in LDS, in pieces: the range of the tile's
+  // value scales, the key scales, 8 dims of a key, one output block of the values
+  auto convert_range = [&](const R& t) {
     float top = fabsf(t.vall) < __builtin_inff() ? t.vall : 0.f;  // finite ones
     if (__any(ValueRange::of(top) > vr_next.e)) {
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-      vr_next.e = max(vr_next.e, ValueRange::of(top));
+      vr_next.e = max(vr_next.e, uniform(ValueRange::of(top)));
     }
-    {
+    // each key's factor, by its lane; value_factors reads the eight of the thread's keys
+    lf[wave][lane] = fabsf(t.vall) < __builtin_inff() ? t.vall * vr_next.down() : 0.f;
+  };
+  auto key_scales = [&](const R& t, int buf) {
+    // a value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
+    // reaches only the rows that see the key; four lanes write each of the 16 scales
+    const bool bad = !(fabsf(t.kvs) < __builtin_inff());
+    lks[buf][16 * sg + (lane & 15)] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
+  };
+  auto convert_key = [&](const R& t, int buf, int i) {
+    const int d = kpart * (HDP / 4) + 8 * i;
+    const bf16x8_t v = BITS == 8 ? row8(t.k[2 * i % R::kKW], t.k[(2 * i + 1) % R::kKW]) : row4(t.k[i % R::kKW]);
+    *reinterpret_cast<bf16x8_t*>(&lk[buf][((kkey >> 5) * kSteps + (d >> 4)) * kFrag + ((kkey & 31) + 4 * (d & 8)) * 16]) = v;
+  };
+  auto value_factors = [&](f16x2_t (&f)[4]) {
 #pragma unroll
-      for (int i = 0; i < HDP / 32; ++i) {
-        const int d = kpart * (HDP / 4) + 8 * i;
-        const bf16x8_t v = BITS == 8 ? row8(t.k[2 * i % R::kKW], t.k[(2 * i + 1) % R::kKW]) : row4(t.k[i % R::kKW]);
-        *reinterpret_cast<bf16x8_t*>(&lk[buf][((kkey >> 5) * kSteps + (d >> 4)) * kFrag + ((kkey & 31) + 4 * (d & 8)) * 16]) = v;
-      }
-      // a value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
-      // reaches only the rows that see the key
-      if (lane < 16) {
-        const bool bad = !(fabsf(t.kvs) < __builtin_inff());
-        lks[buf][16 * sg + lane] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
-      }
+    for (int j = 0; j < 4; j += 2) {
+      const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 4 * j]);
+      f[j] = __builtin_bit_cast(f16x2_t, pack_f16(four[0], four[1]));
+      f[j + 1] = __builtin_bit_cast(f16x2_t, pack_f16(four[2], four[3]));
     }
-    {
-      // each key's factor, by its lane, then the eight of this thread's keys
-      lf[wave][lane] = fabsf(t.vall) < __builtin_inff() ? t.vall * vr_next.down() : 0.f;
-      f16x2_t f[4];
+  };
+  auto convert_value = [&](const R& t, const f16x2_t (&f)[4], int buf, int i) {
+    u32x4_t o;
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 4 * j]);
-        f[j] = __builtin_bit_cast(f16x2_t, pack_f16(four[0], four[1]));
-        f[j + 1] = __builtin_bit_cast(f16x2_t, pack_f16(four[2], four[3]));
+    for (int j = 0; j < 4; ++j) {
+      f16x2_t code;
+      if (BITS == 8) {
+        const uint32_t w0 = t.v[(i >> 2) % R::kVW][2 * j], w1 = t.v[(i >> 2) % R::kVW][2 * j + 1];
+        code = __builtin_bit_cast(f16x2_t, (i & 3) == 0   ? pack_f16(sbyte<0>(w0), sbyte<0>(w1))
+                                           : (i & 3) == 1 ? pack_f16(sbyte<1>(w0), sbyte<1>(w1))
+                                           : (i & 3) == 2 ? pack_f16(sbyte<2>(w0), sbyte<2>(w1))
+                                                          : pack_f16(sbyte<3>(w0), sbyte<3>(w1)));
+      } else {
+        const uint32_t n = nib_pair(t.v[(i >> 3) % R::kVW][2 * j], t.v[(i >> 3) % R::kVW][2 * j + 1], (i >> 1) & 3);
+        const uint32_t c24 = (((i & 1) ? n << 2 : n << 6) & 0x03C003C0u) | 0x4C004C00u;
+        code = __builtin_bit_cast(f16x2_t, c24) - f16x2_t{24, 24};  // exact
       }
+      o[j] = __builtin_bit_cast(uint32_t, static_cast<f16x2_t>(code * f[j]));
+    }
+    *reinterpret_cast<u32x4_t*>(&lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16]) = o;
+  };
+  auto convert_all = [&](const R& t, int buf) {
+    key_scales(t, buf);
 #pragma unroll
-      for (int i = 0; i < kDb; ++i) {
-        u32x4_t o;
+    for (int i = 0; i < HDP / 32; ++i) convert_key(t, buf, i);
+    f16x2_t f[4];
+    value_factors(f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f16x2_t code;
-          if (BITS == 8) {
-            const uint32_t w0 = t.v[(i >> 2) % R::kVW][2 * j], w1 = t.v[(i >> 2) % R::kVW][2 * j + 1];
-            code = __builtin_bit_cast(f16x2_t, (i & 3) == 0   ? pack_f16(sbyte<0>(w0), sbyte<0>(w1))
-                                               : (i & 3) == 1 ? pack_f16(sbyte<1>(w0), sbyte<1>(w1))
-                                               : (i & 3) == 2 ? pack_f16(sbyte<2>(w0), sbyte<2>(w1))
-                                                              : pack_f16(sbyte<3>(w0), sbyte<3>(w1)));
-          } else {
-            const uint32_t n = nib_pair(t.v[(i >> 3) % R::kVW][2 * j], t.v[(i >> 3) % R::kVW][2 * j + 1], (i >> 1) & 3);
-            const uint32_t c24 = (((i & 1) ? n << 2 : n << 6) & 0x03C003C0u) | 0x4C004C00u;
-            code = __builtin_bit_cast(f16x2_t, c24) - f16x2_t{24, 24};  // exact
-          }
-          o[j] = __builtin_bit_cast(uint32_t, static_cast<f16x2_t>(code * f[j]));
+    for (int i = 0; i < kDb; ++i) convert_value(t, f, buf, i);
+  };
+
+  // products on operand x of a 32-key block b of the tile in `buf`
+  auto key_operand = [&](int buf, int b, int x) {
+    return *reinterpret_cast<const bf16x8_t*>(&lk[buf][(b * kSteps + x) * kFrag + lane * 16]);
+  };
+  auto value_operand = [&](int buf, int b, int x) {  // x = kDb a + i: 16 keys a, output block i
+    return *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * (x % kDb) + 2 * b + x / kDb) * kFrag + lane * 16]);
+  };
+  constexpr int kPv = 2 * kDb;
+  R t;
+  int page = 0;
+
+  // A tile as it comes: masks, a maximum that moves, a range that grows.  Taken for
+  // the first tile of a workgroup, the last ones of causal rows and wherever
+  // the plain tile below finds that it does not fit.  half 1: its first 32
+  // keys are done already.
+  auto careful_tile = [&](int base, int buf, uint32_t hide, int half, int range) {
+    const int rel = lim - base - 4 * hf;
+    auto seen = [&](int b, int e) {  // element e of block b: key 32 b + 8 (e / 4) + 4 hf + e % 4
+      return 32 * b + 8 * (e >> 2) + (e & 3) <= rel && !((hide >> (2 * b + (e >> 3))) & 1u);
+    };
+    float f = 1.f;
+    if (range > vr.e) {
+      f = exp2_int(vr.e - range);
+      vr.e = range;
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b < half) continue;
+      f32x16_t s;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = bias;
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(buf, b, x), q[x], s, 0, 0, 0);
+      float mx = m;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[4 * a + e] *= ks[e];
+          if (!seen(b, 4 * a + e)) s[4 * a + e] = kNegInf;
+          mx = fmaxf(mx, s[4 * a + e]);
         }
-        *reinterpret_cast<u32x4_t*>(&lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16]) = o;
       }
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float fm = fast_exp2(m - mx);
+      m = mx;
+      l *= fm;
+      f *= fm;
+#pragma unroll
+      for (int i = 0; i < kDb; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+      f = 1.f;
+      u32x4_t pk[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        pk[e >> 2][e & 3] = pack_f16(fast_exp2(s[2 * e] - m), fast_exp2(s[2 * e + 1] - m));
+        l = add_f16(pk[e >> 2][e & 3], l);
+      }
+#pragma unroll
+      for (int x = 0; x < kPv; ++x)
+        acc[x % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(value_operand(buf, b, x), __builtin_bit_cast(f16x8_t, pk[x / kDb]),
+                                                              acc[x % kDb], 0, 0, 0);
     }
   };
 
-  R t;
-  uint32_t hide = 0u, hide_next = 0u;
-  int page = 0;
+  uint32_t hide = 0u;
+  int buf = 0, base = key0;
   if (key0 < key1) {
     page = load_page(key0);
     load_tile(key0, page, t);
     page = load_page(key0 + kKeys);
-    convert(t, 0);
-    hide_next = t.hide;
+    convert_range(t);
+    convert_all(t, 0);
+    hide = t.hide;
     load_tile(key0 + kKeys, page, t);
     page = load_page(key0 + 2 * kKeys);
   }
-  int buf = 0;
-  for (int base = key0; base < key1; base += kKeys, buf ^= 1) {
-    // this tile's operands are written, and the other buffer's have been read
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    hide = hide_next;
-    const bool work = base <= wlast;  // a causal tile past the wave's rows: nothing to multiply
-    const int e_tile = vr_next.e;     // the range this tile's values were written in
-    f32x16_t s[2];
-    if (work) {
+  // The next tile is converted past the last one too: the registers then hold
+  // keys of page 0, and nothing reads the operands.
+  while (base < key1) {
+    int half = 0, range = 0;
+    bool fits = true;
+    while (base < key1) {
+      // this tile's operands are written, and the other buffer's have been read
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      half = 0;
+      range = vr_next.e;  // the one this tile's values were written in (the next tile's may be wider)
+      fits = base > key0 && base + kKeys - 1 <= wfirst && hide == 0u && range == vr.e;
+      if (!fits) break;
+      // The plain tile: every key seen, the maximum and the range as they were.
+      // Four groups of products, each with arithmetic between them that does not
+      // depend on it, so that the matrix cores run while the wave goes on:
+      //   scores of keys 0..31   | next tile's key codes -> operands
+      //   scores of keys 32..63  | weights of keys 0..31
+      //   output of keys 0..31   | weights of keys 32..63
+      //   output of keys 32..63  | next tile's value codes -> operands
+      f32x16_t s0, s1;
+      u32x4_t pk[4];
+      f32x4_t ks[4];
+      float l0 = 0.f, l1 = 0.f;
+      // n of the 16 weights 2^(s sk - m) of a block, rounded to fp16, and their sum
+      auto weights = [&](const f32x16_t& s, int b, int from, int to, float& sum) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+        for (int e = 0; e < 16; e += 2)
+          if (e >= from && e < to) {
+            const uint32_t two = pack_f16(fast_exp2(fmaf(s[e], ks[e >> 2][e & 3], -m)),
+                                          fast_exp2(fmaf(s[e + 1], ks[e >> 2][(e & 3) + 1], -m)));
+            pk[2 * b + (e >> 3)][(e >> 1) & 3] = two;
+            sum = add_f16(two, sum);
+          }
+      };
+      auto scales_of = [&](int b) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[b][e] = bias;
+        for (int a = 0; a < 4; ++a) ks[a] = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
+      };
+      constexpr int kAhead = 2;  // operands read before they are needed
+      bf16x8_t ko[kSteps];
+      f16x8_t vo[kPv];
 #pragma unroll
-      for (int e = 0; e < kSteps; ++e)
+      for (int e = 0; e < 16; ++e) s0[e] = s1[e] = bias;
 #pragma unroll
-        for (int b = 0; b < 2; ++b)  // two sums in turn
-          s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              *reinterpret_cast<const bf16x8_t*>(&lk[buf][(b * kSteps + e) * kFrag + lane * 16]), q[e], s[b], 0, 0, 0);
-    }
-    if (base + kKeys < key1) {
-      convert(t, buf ^ 1);
-      hide_next = t.hide;
+      for (int x = 0; x < kAhead; ++x) ko[x] = key_operand(buf, 0, x);
+      convert_range(t);
+      key_scales(t, buf ^ 1);
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) {
+        if (x + kAhead < kSteps) ko[x + kAhead] = key_operand(buf, 0, x + kAhead);
+        s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ko[x], q[x], s0, 0, 0, 0);
+        if (x & 1) convert_key(t, buf ^ 1, x >> 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      scales_of(0);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) ko[x] = key_operand(buf, 1, x);
+#pragma unroll
+      for (int x = 0; x < kSteps; ++x) {
+        if (x + kAhead < kSteps) ko[x + kAhead] = key_operand(buf, 1, x + kAhead);
+        s1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ko[x], q[x], s1, 0, 0, 0);
+        weights(s0, 0, 16 * x / kSteps, 16 * (x + 1) / kSteps, l0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // a lane's 16 weights sum to more than 2^10: one may be
+      fits = !__any(l0 > kGrow);
+      if (!fits) break;
+      l += l0;
+      scales_of(1);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) vo[x] = value_operand(buf, 0, x);
+#pragma unroll
+      for (int x = 0; x < kPv; ++x) {
+        if (x + kAhead < kPv) vo[x + kAhead] = value_operand(buf, 0, x + kAhead);
+        acc[x % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vo[x], __builtin_bit_cast(f16x8_t, pk[x / kDb]), acc[x % kDb], 0, 0, 0);
+        weights(s1, 1, 16 * x / kPv, 16 * (x + 1) / kPv, l1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      half = 1;
+      fits = !__any(l1 > kGrow);
+      if (!fits) break;
+      l += l1;
+      f16x2_t f[4];
+      value_factors(f);
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) vo[x] = value_operand(buf, 1, x);
+#pragma unroll
+      for (int x = 0; x < kPv; ++x) {
+        if (x + kAhead < kPv) vo[x + kAhead] = value_operand(buf, 1, x + kAhead);
+        acc[x % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vo[x], __builtin_bit_cast(f16x8_t, pk[2 + x / kDb]), acc[x % kDb], 0, 0, 0);
+        if (x & 1) convert_value(t, f, buf ^ 1, x >> 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      hide = t.hide;
       load_tile(base + 2 * kKeys, page, t);
       page = load_page(base + 3 * kKeys);
+      base += kKeys;
+      buf ^= 1;
     }
-    if (!work) continue;
-    if (e_tile > vr.e) {
-      const float f = exp2_int(vr.e - e_tile);
-      vr.e = e_tile;
-#pragma unroll
-      for (int i = 0; i < kDb; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-    }
-    // bit 16 b + e: key 32 b + 8 (e / 4) + 4 hf + e % 4 is seen; asked for in the last tiles only
-    const bool masked = base + kKeys - 1 > wfirst || hide != 0u;
-    uint32_t see = 0xFFFFFFFFu;
-    if (masked) {
-      const int rel = lim - base - 4 * hf;
-      see = 0u;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (32 * b + 8 * (e >> 2) + (e & 3) <= rel && !((hide >> (2 * b + (e >> 3))) & 1u)) see |= 1u << (16 * b + e);
-    }
-    u32x4_t pk[4];
-    float lt = 0.f;
-    // p = 2^(s sk - m), rounded to fp16, and its sum
-    auto weights = [&](bool mask) {
-      lt = 0.f;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
-          float pv[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            pv[e] = fast_exp2(fmaf(s[b][4 * a + e], ks[e], -m));
-            if (mask) pv[e] = (see >> (16 * b + 4 * a + e)) & 1u ? pv[e] : 0.f;
-          }
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t two = pack_f16(pv[2 * e], pv[2 * e + 1]);
-            pk[2 * b + (a >> 1)][2 * (a & 1) + e] = two;
-            lt = add_f16(two, lt);
-          }
-        }
-    };
-    if (masked) weights(true);
-    else weights(false);
-    // a lane's 32 weights sum to more than 2^10: one may be (a row's first keys: all are)
-    if (__any(lt > kGrow)) {
-      float mx = m;
-#pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-          const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx = fmaxf(mx, (see >> (16 * b + 4 * a + e)) & 1u ? s[b][4 * a + e] * ks[e] : kNegInf);
-        }
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float f = fast_exp2(m - mx);
-      m = mx;
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < kDb; ++i)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-      weights(true);
-    }
-    l += lt;
-#pragma unroll
-    for (int t4 = 0; t4 < 4; ++t4) {
-      const f16x8_t pop = __builtin_bit_cast(f16x8_t, pk[t4]);
-#pragma unroll
-      for (int i = 0; i < kDb; ++i)
-        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-            *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * i + t4) * kFrag + lane * 16]), pop, acc[i], 0, 0, 0);
-    }
+    if (fits) break;
+    if (base <= wlast) careful_tile(base, buf, hide, half, range);  // else a causal tile past the wave's rows
+    convert_range(t);
+    convert_all(t, buf ^ 1);
+    hide = t.hide;
+    load_tile(base + 2 * kKeys, page, t);
+    page = load_page(base + 3 * kKeys);
+    base += kKeys;
+    buf ^= 1;
   }
 
   // lane l: query row c, dims (8 a + 4 hf + b) HDP / 32 + i: for each a a run of 4 HDP / 32 dims
