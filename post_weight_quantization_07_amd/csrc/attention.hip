@@ -21,6 +21,7 @@
 #include "quant_row.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace gptq {
 namespace {
@@ -79,15 +80,31 @@ GPTQ_DEV Seq seq_info(const AttnParams& p, int i) {
   return s;
 }
 
-template <typename T>
-GPTQ_DEV T wave_scan(T v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const T o = __shfl_up(v, d);
-    if (lane >= d) v += o;
-  }
+// inclusive sums over the wave, in DPP steps (row shifts by 1, 2, 4, 8, then the last lane of a row to
+// the next one and of the first two rows to the others); lane 63 has the total
+template <int CTRL, int ROWS>
+GPTQ_DEV int dpp_or_zero(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+GPTQ_DEV int wave_scan(int v) {
+  v += dpp_or_zero<0x111, 0xF>(v);
+  v += dpp_or_zero<0x112, 0xF>(v);
+  v += dpp_or_zero<0x114, 0xF>(v);
+  v += dpp_or_zero<0x118, 0xF>(v);
+  v += dpp_or_zero<0x142, 0xA>(v);
+  v += dpp_or_zero<0x143, 0xC>(v);
   return v;
 }
+GPTQ_DEV float wave_scan(float v) {
+  v += __int_as_float(dpp_or_zero<0x111, 0xF>(__float_as_int(v)));
+  v += __int_as_float(dpp_or_zero<0x112, 0xF>(__float_as_int(v)));
+  v += __int_as_float(dpp_or_zero<0x114, 0xF>(__float_as_int(v)));
+  v += __int_as_float(dpp_or_zero<0x118, 0xF>(__float_as_int(v)));
+  v += __int_as_float(dpp_or_zero<0x142, 0xA>(__float_as_int(v)));
+  v += __int_as_float(dpp_or_zero<0x143, 0xC>(__float_as_int(v)));
+  return v;
+}
+GPTQ_DEV float lane_value(float v, int l) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l)); }
 GPTQ_DEV int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 struct Work {
@@ -96,7 +113,8 @@ struct Work {
   int slot;  // of the unit's first split (for this key head: times n_kv, plus h)
 };
 
-// Entry u of the list (SPLITS: of (tile, split) pairs; otherwise of tiles).
+// Entry u of the list (SPLITS: of (tile, split) pairs; otherwise of the tiles
+// whose keys are split).
 // A sequence's keys are split into parts of at least `per` units, per = (all
 // units) / target: a batch with enough tiles is not split, a long sequence among
 // short ones is.  per is the same fp32 number in every workgroup; being off by
@@ -109,10 +127,7 @@ GPTQ_DEV bool find_work(const AttnParams& p, int u, Work& w) {
   for (int i0 = 0; i0 < p.n_seq; i0 += 64) {
     s = Seq{0, 0, 0, 0, 1};
     if (i0 + lane < p.n_seq) s = seq_info(p, i0 + lane);
-    float v = static_cast<float>(s.tiles) * static_cast<float>(s.units);
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-    total += v;
+    total += lane_value(wave_scan(static_cast<float>(s.tiles) * static_cast<float>(s.units)), 63);
   }
   const float inv_per = 1.f / fmaxf(total * p.inv_target, p.min_units);
   int base = 0, slots = 0;
@@ -123,9 +138,9 @@ GPTQ_DEV bool find_work(const AttnParams& p, int u, Work& w) {
     }
     const int n_split = max(static_cast<int>(ceilf(static_cast<float>(s.units) * inv_per)), 1);
     const int pairs = s.tiles * n_split;
-    const int cnt = SPLITS ? pairs : s.tiles;
-    const int end = base + wave_scan(cnt, lane);
-    const int slot_end = slots + wave_scan(n_split > 1 ? pairs : 0, lane);
+    const int cnt = SPLITS ? pairs : n_split > 1 ? s.tiles : 0;
+    const int end = base + wave_scan(cnt);
+    const int slot_end = slots + wave_scan(n_split > 1 ? pairs : 0);
     const uint64_t hit = __ballot(u < end);
     if (hit) {
       const int l = uniform(__builtin_ctzll(hit));
@@ -545,32 +560,34 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 // touch all banks), so every LDS read is contiguous.
 //
 // Two tiles of LDS: while one is multiplied, the next one's codes, loaded to
-// registers a tile ahead, are converted into the other; one barrier a tile.
+// registers two tiles ahead, are converted into the other; one barrier a tile.
 // The row maximum is only moved when a lane's weights sum to more than 2^10 (fp16
 // holds 2^15; p keeps its relative precision): the usual tile then costs a multiply-add and
 // an exp2 per score, half a conversion and half a sum.
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 1024.f;
 
-template <int HDP, int BITS>
+template <int HDP, int BITS, int NW>
 struct TileRegs {
-  static constexpr int kKW = HDP * BITS / 128;   // words of K a thread converts: HDP / 4 dims of a key
-  static constexpr int kVB = HDP * BITS / 256;   // bytes of V per key: HDP / 32 dims of 8 keys
+  static constexpr int kKD = HDP / NW;                 // dims of a key that a thread converts
+  static constexpr int kKW = kKD * BITS / 32;          // their words
+  static constexpr int kVK = 32 / NW;                  // keys of which it converts HDP / 32 dims
+  static constexpr int kVB = HDP * BITS / 256;         // their bytes per key
   static constexpr int kVW = (kVB + 3) / 4;
-  uint32_t k[kKW], v[kVW][8];
-  float ks, kvs;   // lanes 0..15: scales of the wave's 16 keys
-  float vall;      // value scale of key `lane` of the tile (0: hidden)
+  uint32_t k[kKW], v[kVW][kVK];
+  float ks, vall;  // scales of key `lane` of the tile (the value's: 0 if the key is hidden)
   uint32_t hide;   // bit i: the page of keys 16 i .. is not there
 };
 
-template <int HDP, int BITS>
-__global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
-  using R = TileRegs<HDP, BITS>;
-  constexpr int kKeys = 64, kM = 128;
+template <int HDP, int BITS, int NW>
+__global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
+  using R = TileRegs<HDP, BITS, NW>;
+  constexpr int kKeys = 64, kM = 32 * NW;
+  static_assert(NW == 4 || NW == 8, "");
   constexpr int kSteps = HDP / 16, kDb = HDP / 32;
   constexpr int kKF = 2 * kSteps, kVF = 4 * kDb;  // operands of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lk[2][kKF * kFrag], lv[2][kVF * kFrag];
-  __shared__ __attribute__((aligned(16))) float lks[2][kKeys], lf[4][kKeys];  // lf: one row per wave
+  __shared__ __attribute__((aligned(16))) float lks[2][kKeys], lf[NW][kKeys];  // lf: one row per wave
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 31, hf = lane >> 5;
@@ -624,19 +641,22 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
   const int row_bytes = p.hd * BITS / 8;
   const int page_mask = (1 << p.page_shift) - 1;
   const int32_t* table = p.table + static_cast<int64_t>(w.seq) * p.ld_table;
-  const int st = static_cast<int>(threadIdx.x);
-  const int sg = wave;                                 // the 16 keys of a tile that this wave converts
-  const int kkey = st >> 2, kpart = st & 3;            // K: a quarter of a key's dims
-  const int vdq = st & 31, vh = (st >> 5) & 1;         // V: HDP / 32 dims of keys 4 vh + b and 8 + 4 vh + b
+  // conversion of a tile: NW / 4 waves share 16 of its keys (group sg).  K: NW
+  // threads a key, HDP / NW dims each.  V: a thread has HDP / 32 dims of the keys
+  // 4 vh + b and 8 + 4 vh + b (NW = 8: of one of the two fours, by wave & 1).
+  constexpr int kGW = NW / 4;
+  const int sg = wave / kGW, vfour = NW == 8 ? wave & 1 : 0;
+  const int kkey = (static_cast<int>(threadIdx.x) & (64 * kGW - 1)) / NW, kpart = static_cast<int>(threadIdx.x) % NW;
+  const int vdq = lane & 31, vh = lane >> 5;
   // a thread whose dims lie past head_dim reads the row's first ones instead: q
   // is zero there, and what V gives there is not stored
-  uint32_t koff[HDP / 32], voff;
+  uint32_t koff[R::kKD / 8], voff;
 #pragma unroll
-  for (int i = 0; i < HDP / 32; ++i) {
-    const int d = kpart * (HDP / 4) + 8 * i;
-    koff[i] = static_cast<uint32_t>((kkey & 15) * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
+  for (int i = 0; i < R::kKD / 8; ++i) {
+    const int d = kpart * R::kKD + 8 * i;
+    koff[i] = static_cast<uint32_t>(kkey * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
   }
-  voff = static_cast<uint32_t>(4 * vh * row_bytes + (vdq * (HDP / 32) < p.hd ? vdq * R::kVB : 0));
+  voff = static_cast<uint32_t>((4 * vh + 8 * vfour) * row_bytes + (vdq * (HDP / 32) < p.hd ? vdq * R::kVB : 0));
 
   auto load_page = [&](int base) -> int {
     const int key = base + lane;
@@ -652,36 +672,31 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
     const int pg = ok ? page : 0;
     const int64_t all = ((static_cast<int64_t>(pg) * p.n_kv + h) << p.page_shift) + (key & page_mask);
     t.vall = (ok && key < vis) ? p.scales[1][all] : 0.f;
+    t.ks = p.scales[0][all];
     const int pw = __builtin_amdgcn_readlane(pg, 16 * sg);
     const int64_t row = ((static_cast<int64_t>(pw) * p.n_kv + h) << p.page_shift) + ((base + 16 * sg) & page_mask);
-    {
-      const uint8_t* kp = p.codes[0] + row * row_bytes;
+    const uint8_t* kp = p.codes[0] + row * row_bytes;
 #pragma unroll
-      for (int e = 0; e < R::kKW; e += (BITS == 8 ? 2 : 1)) {
-        if (BITS == 8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(kp + koff[e / 2]);
-          t.k[e] = v.x;
-          t.k[e + 1] = v.y;
-        } else {
-          t.k[e] = *reinterpret_cast<const uint32_t*>(kp + koff[e]);
-        }
+    for (int i = 0; i < R::kKD / 8; ++i) {
+      if (BITS == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(kp + koff[i]);
+        t.k[2 * i % R::kKW] = v.x;
+        t.k[(2 * i + 1) % R::kKW] = v.y;
+      } else {
+        t.k[i % R::kKW] = *reinterpret_cast<const uint32_t*>(kp + koff[i]);
       }
-      t.ks = (p.scales[0] + row)[lane & 15];
-      t.kvs = (p.scales[1] + row)[lane & 15];
     }
-    {
-      const uint8_t* vp = p.codes[1] + row * row_bytes;
+    const uint8_t* vp = p.codes[1] + row * row_bytes;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint8_t* one = vp + static_cast<uint32_t>(((j & 3) + 8 * (j >> 2)) * row_bytes);
-        if (R::kVB == 1) t.v[0][j] = one[voff];
-        if (R::kVB == 2) t.v[0][j] = *reinterpret_cast<const uint16_t*>(one + voff);
-        if (R::kVB == 4) t.v[0][j] = *reinterpret_cast<const uint32_t*>(one + voff);
-        if (R::kVB == 8) {
-          const uint2 v = *reinterpret_cast<const uint2*>(one + voff);
-          t.v[0][j] = v.x;
-          t.v[R::kVW - 1][j] = v.y;
-        }
+    for (int j = 0; j < R::kVK; ++j) {
+      const uint8_t* one = vp + static_cast<uint32_t>(((j & 3) + 8 * (j >> 2)) * row_bytes);
+      if (R::kVB == 1) t.v[0][j] = one[voff];
+      if (R::kVB == 2) t.v[0][j] = *reinterpret_cast<const uint16_t*>(one + voff);
+      if (R::kVB == 4) t.v[0][j] = *reinterpret_cast<const uint32_t*>(one + voff);
+      if (R::kVB == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(one + voff);
+        t.v[0][j] = v.x;
+        t.v[R::kVW - 1][j] = v.y;
       }
     }
   };
@@ -699,27 +714,28 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
   };
   auto key_scales = [&](const R& t, int buf) {
     // a value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
-    // reaches only the rows that see the key; four lanes write each of the 16 scales
-    const bool bad = !(fabsf(t.kvs) < __builtin_inff());
-    lks[buf][16 * sg + (lane & 15)] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
+    // reaches only the rows that see the key; every wave writes the same 64 scales
+    const bool bad = !(fabsf(t.vall) < __builtin_inff());
+    lks[buf][lane] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
   };
   auto convert_key = [&](const R& t, int buf, int i) {
-    const int d = kpart * (HDP / 4) + 8 * i;
+    const int key = 16 * sg + kkey, d = kpart * R::kKD + 8 * i;
     const bf16x8_t v = BITS == 8 ? row8(t.k[2 * i % R::kKW], t.k[(2 * i + 1) % R::kKW]) : row4(t.k[i % R::kKW]);
-    *reinterpret_cast<bf16x8_t*>(&lk[buf][((kkey >> 5) * kSteps + (d >> 4)) * kFrag + ((kkey & 31) + 4 * (d & 8)) * 16]) = v;
+    *reinterpret_cast<bf16x8_t*>(&lk[buf][((key >> 5) * kSteps + (d >> 4)) * kFrag + ((key & 31) + 4 * (d & 8)) * 16]) = v;
   };
-  auto value_factors = [&](f16x2_t (&f)[4]) {
+  constexpr int kVP = R::kVK / 2;  // pairs of keys
+  auto value_factors = [&](f16x2_t (&f)[kVP]) {
 #pragma unroll
-    for (int j = 0; j < 4; j += 2) {
-      const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 4 * j]);
+    for (int j = 0; j < kVP; j += 2) {
+      const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 8 * vfour + 4 * j]);
       f[j] = __builtin_bit_cast(f16x2_t, pack_f16(four[0], four[1]));
       f[j + 1] = __builtin_bit_cast(f16x2_t, pack_f16(four[2], four[3]));
     }
   };
-  auto convert_value = [&](const R& t, const f16x2_t (&f)[4], int buf, int i) {
-    u32x4_t o;
+  auto convert_value = [&](const R& t, const f16x2_t (&f)[kVP], int buf, int i) {
+    uint32_t o[kVP];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kVP; ++j) {
       f16x2_t code;
       if (BITS == 8) {
         const uint32_t w0 = t.v[(i >> 2) % R::kVW][2 * j], w1 = t.v[(i >> 2) % R::kVW][2 * j + 1];
@@ -734,13 +750,15 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       }
       o[j] = __builtin_bit_cast(uint32_t, static_cast<f16x2_t>(code * f[j]));
     }
-    *reinterpret_cast<u32x4_t*>(&lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16]) = o;
+    uint8_t* to = &lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16 + 8 * vfour];
+    if (NW == 4) *reinterpret_cast<u32x4_t*>(to) = u32x4_t{o[0], o[1], o[kVP - 2], o[kVP - 1]};
+    else *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
   };
   auto convert_all = [&](const R& t, int buf) {
     key_scales(t, buf);
 #pragma unroll
-    for (int i = 0; i < HDP / 32; ++i) convert_key(t, buf, i);
-    f16x2_t f[4];
+    for (int i = 0; i < R::kKD / 8; ++i) convert_key(t, buf, i);
+    f16x2_t f[kVP];
     value_factors(f);
 #pragma unroll
     for (int i = 0; i < kDb; ++i) convert_value(t, f, buf, i);
@@ -754,7 +772,7 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
     return *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * (x % kDb) + 2 * b + x / kDb) * kFrag + lane * 16]);
   };
   constexpr int kPv = 2 * kDb;
-  R t;
+  R t, ahead;  // the next tile's codes, and those of the one after, still on their way
   int page = 0;
 
   // A tile as it comes: masks, a maximum that moves, a range that grows.  Taken for
@@ -771,39 +789,47 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       f = exp2_int(vr.e - range);
       vr.e = range;
     }
+    f32x16_t s[2];
+    float mx = m;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       if (b < half) continue;
-      f32x16_t s;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = bias;
+      for (int e = 0; e < 16; ++e) s[b][e] = bias;
 #pragma unroll
-      for (int x = 0; x < kSteps; ++x) s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(buf, b, x), q[x], s, 0, 0, 0);
-      float mx = m;
+      for (int x = 0; x < kSteps; ++x)
+        s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key_operand(buf, b, x), q[x], s[b], 0, 0, 0);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b < half) continue;
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
         const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[4 * a + e] *= ks[e];
-          if (!seen(b, 4 * a + e)) s[4 * a + e] = kNegInf;
-          mx = fmaxf(mx, s[4 * a + e]);
+          s[b][4 * a + e] *= ks[e];
+          if (!seen(b, 4 * a + e)) s[b][4 * a + e] = kNegInf;
+          mx = fmaxf(mx, s[b][4 * a + e]);
         }
       }
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      const float fm = fast_exp2(m - mx);
-      m = mx;
-      l *= fm;
-      f *= fm;
+    }
+    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    const float fm = fast_exp2(m - mx);
+    m = mx;
+    l *= fm;
+    f *= fm;
 #pragma unroll
-      for (int i = 0; i < kDb; ++i)
+    for (int i = 0; i < kDb; ++i)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-      f = 1.f;
+      for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      if (b < half) continue;
       u32x4_t pk[2];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        pk[e >> 2][e & 3] = pack_f16(fast_exp2(s[2 * e] - m), fast_exp2(s[2 * e + 1] - m));
+        pk[e >> 2][e & 3] = pack_f16(fast_exp2(s[b][2 * e] - m), fast_exp2(s[b][2 * e + 1] - m));
         l = add_f16(pk[e >> 2][e & 3], l);
       }
 #pragma unroll
@@ -816,14 +842,13 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
   uint32_t hide = 0u;
   int buf = 0, base = key0;
   if (key0 < key1) {
-    page = load_page(key0);
-    load_tile(key0, page, t);
-    page = load_page(key0 + kKeys);
+    const int page0 = load_page(key0), page1 = load_page(key0 + kKeys);
+    page = load_page(key0 + 2 * kKeys);
+    load_tile(key0, page0, t);
+    load_tile(key0 + kKeys, page1, ahead);
     convert_range(t);
     convert_all(t, 0);
     hide = t.hide;
-    load_tile(key0 + kKeys, page, t);
-    page = load_page(key0 + 2 * kKeys);
   }
   // The next tile is converted past the last one too: the registers then hold
   // keys of page 0, and nothing reads the operands.
@@ -835,6 +860,9 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      t = ahead;
+      load_tile(base + 2 * kKeys, page, ahead);
+      page = load_page(base + 3 * kKeys);
       half = 0;
       range = vr_next.e;  // the one this tile's values were written in (the next tile's may be wider)
       fits = base > key0 && base + kKeys - 1 <= wfirst && hide == 0u && range == vr.e;
@@ -852,6 +880,7 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       float l0 = 0.f, l1 = 0.f;
       // n of the 16 weights 2^(s sk - m) of a block, rounded to fp16, and their sum
       auto weights = [&](const f32x16_t& s, int b, int from, int to, float& sum) {
+        asm volatile("" : "+v"(m));  // not before this place between the products
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
           if (e >= from && e < to) {
@@ -878,7 +907,8 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       for (int x = 0; x < kSteps; ++x) {
         if (x + kAhead < kSteps) ko[x + kAhead] = key_operand(buf, 0, x + kAhead);
         s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ko[x], q[x], s0, 0, 0, 0);
-        if (x & 1) convert_key(t, buf ^ 1, x >> 1);
+        constexpr int kEvery = kSteps / (R::kKD / 8);
+        if (x % kEvery == kEvery - 1) convert_key(t, buf ^ 1, x / kEvery);
         __builtin_amdgcn_sched_barrier(0);
       }
       scales_of(0);
@@ -909,7 +939,7 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
       fits = !__any(l1 > kGrow);
       if (!fits) break;
       l += l1;
-      f16x2_t f[4];
+      f16x2_t f[kVP];
       value_factors(f);
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) vo[x] = value_operand(buf, 1, x);
@@ -921,8 +951,6 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
         __builtin_amdgcn_sched_barrier(0);
       }
       hide = t.hide;
-      load_tile(base + 2 * kKeys, page, t);
-      page = load_page(base + 3 * kKeys);
       base += kKeys;
       buf ^= 1;
     }
@@ -931,8 +959,6 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
     convert_range(t);
     convert_all(t, buf ^ 1);
     hide = t.hide;
-    load_tile(base + 2 * kKeys, page, t);
-    page = load_page(base + 3 * kKeys);
     base += kKeys;
     buf ^= 1;
   }
@@ -979,15 +1005,15 @@ __global__ __launch_bounds__(256, HDP <= 128 ? 2 : 1) void attn_tile_kernel(Attn
     }
 }
 
-// Joins the splits of a tile, in their order.  One workgroup per (tile, key
-// head); tiles that were not split were written by the kernel above.
+// Joins the splits of a tile, in their order.  One workgroup per (split tile, key
+// head); the other tiles were written by the kernels above.
 template <int HDP>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   const int kM = p.tile_rows;
   const int u = uniform(div_by(static_cast<int>(blockIdx.x), p.kv_mul, p.kv_shift));
   const int h = static_cast<int>(blockIdx.x) - u * p.n_kv;
   Work w;
-  if (!find_work<false>(p, u, w) || w.n_split == 1) return;
+  if (!find_work<false>(p, u, w)) return;
   const int rows = w.s.n * p.group, r0 = w.tile * kM;
   if (static_cast<int64_t>(w.slot + w.n_split - 1) * p.n_kv + h >= p.max_slots) return;
   const int64_t step = static_cast<int64_t>(p.n_kv) * (kM * (HDP + 2));
@@ -1032,7 +1058,8 @@ template <int HDP, int BITS>
 void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
   switch (p.tile_rows) {
     case 16: attn_split_kernel<HDP, BITS, 1, 8><<<blocks, 512, 0, st>>>(p); break;
-    default: attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p); break;
+    case 128: attn_tile_kernel<HDP, BITS, 4><<<blocks, 256, 0, st>>>(p); break;
+    default: attn_tile_kernel<HDP, BITS, 8><<<blocks, 512, 0, st>>>(p); break;
   }
   if (joins) attn_join_kernel<HDP><<<joins, 256, 0, st>>>(p);
 }
@@ -1043,7 +1070,8 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   AttnPlan a{};
   const int64_t group = n_heads / c.n_kv;
   a.tile_rows = n_tokens * group <= 32ll * n_seq ? 16 : 128;
-  a.target = 2 * n_cu;
+  if (getenv("ATT_ROWS") && a.tile_rows == 128) a.tile_rows = atoi(getenv("ATT_ROWS"));
+  a.target = a.tile_rows == 256 ? n_cu : 2 * n_cu;
   a.min_units = 4;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
   a.joins = tiles * c.n_kv;
@@ -1054,6 +1082,7 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
     a.joins = 0;
     a.blocks = tiles * c.n_kv;
   } else {
+    a.joins = std::min(a.joins, static_cast<int64_t>(a.target) + 64);  // tiles of two parts and more
     a.slots = 2 * static_cast<int64_t>(a.target) + 64;  // a split sequence has fewer than 2 units / per parts
     a.ws_bytes = static_cast<size_t>(a.slots) * a.tile_rows * (head_pad(c.hd) + 2) * 4;
   }
