@@ -21,13 +21,13 @@
 #include "quant_row.h"
 
 #include <algorithm>
-#include <cstdlib>
 
 namespace gptq {
 namespace {
 
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4_t;
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
 
@@ -548,16 +548,17 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 // A workgroup owns 128 rows of one (sequence, key head) and one key split; each
 // of its four waves has 32 of the rows, and all walk the keys in tiles of 64.
 // (Eight waves of 32 rows, one workgroup a CU, convert half as often but wait
-// for each other: 267 us against 259 for four 2048-token prompts, 32 heads.)
+// for each other: 202 us against 205 for four 2048-token prompts of 32 heads, 476
+// against 345 for the chunks of 300 to 700 tokens with 64-wide heads.)
 //
 // Per tile the codes are turned into operands once, into LDS: the key codes
 // as bf16 integers, the values as fp16 code * (scale * 2^-range) (two roundings).
 // 32x32x16 products: S^T = K Q^T leaves lane l (query row l % 32, half h = l / 32)
 // with keys 8 a + 4 h + b of a 32-key block; 16 of them in that order are the
 // P^T operand of O^T = V^T P^T, so V's operand holds keys 4 h + b and 8 + 4 h + b
-// of its 16, and P never moves between lanes.  An operand is 64 lanes of 16
+// of its 16, and P never moves between lanes.  A key operand is 64 lanes of 16
 // bytes, stored lane by lane (1040-byte stride: the writers of one operand then
-// touch all banks), so every LDS read is contiguous.
+// touch all banks), so its LDS reads are contiguous.
 //
 // Two tiles of LDS: while one is multiplied, the next one's codes, loaded to
 // registers two tiles ahead, are converted into the other; one barrier a tile.
@@ -567,27 +568,23 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 1024.f;
 
-template <int HDP, int BITS, int NW>
-struct TileRegs {
-  static constexpr int kKD = HDP / NW;                 // dims of a key that a thread converts
-  static constexpr int kKW = kKD * BITS / 32;          // their words
-  static constexpr int kVK = 32 / NW;                  // keys of which it converts HDP / 32 dims
-  static constexpr int kVB = HDP * BITS / 256;         // their bytes per key
-  static constexpr int kVW = (kVB + 3) / 4;
-  uint32_t k[kKW], v[kVW][kVK];
-  float ks, vall;  // scales of key `lane` of the tile (the value's: 0 if the key is hidden)
-  uint32_t hide;   // bit i: the page of keys 16 i .. is not there
+// what a thread holds of a tile on its way: its dims of one key or of one value
+template <int HDP, int BITS>
+struct TileShare {
+  static constexpr int kD = HDP / 4;             // dims
+  static constexpr int kCD = kD < 16 ? kD : 16;  // dims of one load
+  static constexpr int kW = kD * BITS / 32;      // words
+  uint32_t w[kW];
 };
 
-template <int HDP, int BITS, int NW>
-__global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
-  using R = TileRegs<HDP, BITS, NW>;
-  constexpr int kKeys = 64, kM = 32 * NW;
-  static_assert(NW == 4 || NW == 8, "");
+template <int HDP, int BITS>
+__global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
+  using R = TileShare<HDP, BITS>;
+  constexpr int kKeys = 64, kM = 128;
   constexpr int kSteps = HDP / 16, kDb = HDP / 32;
-  constexpr int kKF = 2 * kSteps, kVF = 4 * kDb;  // operands of a tile
-  __shared__ __attribute__((aligned(16))) uint8_t lk[2][kKF * kFrag], lv[2][kVF * kFrag];
-  __shared__ __attribute__((aligned(16))) float lks[2][kKeys], lf[NW][kKeys];  // lf: one row per wave
+  constexpr int kKF = 2 * kSteps;  // key operands of a tile
+  __shared__ __attribute__((aligned(16))) uint8_t lk[2][kKF * kFrag], lv[2][kKeys * HDP * 2];
+  __shared__ __attribute__((aligned(16))) float lks[2][kKeys];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 31, hf = lane >> 5;
@@ -641,148 +638,148 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
   const int row_bytes = p.hd * BITS / 8;
   const int page_mask = (1 << p.page_shift) - 1;
   const int32_t* table = p.table + static_cast<int64_t>(w.seq) * p.ld_table;
-  // conversion of a tile: NW / 4 waves share 16 of its keys (group sg).  K: NW
-  // threads a key, HDP / NW dims each.  V: a thread has HDP / 32 dims of the keys
-  // 4 vh + b and 8 + 4 vh + b (NW = 8: of one of the two fours, by wave & 1).
-  constexpr int kGW = NW / 4;
-  const int sg = wave / kGW, vfour = NW == 8 ? wave & 1 : 0;
-  const int kkey = (static_cast<int>(threadIdx.x) & (64 * kGW - 1)) / NW, kpart = static_cast<int>(threadIdx.x) % NW;
-  const int vdq = lane & 31, vh = lane >> 5;
-  // a thread whose dims lie past head_dim reads the row's first ones instead: q
-  // is zero there, and what V gives there is not stored
-  uint32_t koff[R::kKD / 8], voff;
+  // conversion of a tile: wave sg has 16 of its keys, four threads a key, a quarter of
+  // the dims of its key and of its value each.  A thread whose dims lie past
+  // head_dim reads the row's first ones instead: q is zero there, and what the
+  // values give there is not stored.
+  const int sg = wave, kkey = lane / 4, kpart = lane % 4;
+  const int own = 16 * sg + kkey;  // the thread's key of a tile
+  uint32_t coff[R::kD / R::kCD];
 #pragma unroll
-  for (int i = 0; i < R::kKD / 8; ++i) {
-    const int d = kpart * R::kKD + 8 * i;
-    koff[i] = static_cast<uint32_t>(kkey * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
+  for (int i = 0; i < R::kD / R::kCD; ++i) {
+    const int d = kpart * R::kD + R::kCD * i;
+    coff[i] = static_cast<uint32_t>(kkey * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
   }
-  voff = static_cast<uint32_t>((4 * vh + 8 * vfour) * row_bytes + (vdq * (HDP / 32) < p.hd ? vdq * R::kVB : 0));
-
-  auto load_page = [&](int base) -> int {
-    const int key = base + lane;
-    return key < key1 ? table[key >> p.page_shift] : -1;
+  // Values lie in LDS as rows of fp16 (a key's dims side by side) and are read transposed:
+  // ds_read_b64_tr_b16 gives each lane of 16 the column of its number of a block of
+  // 4 rows x 16 columns, of which each lane names 4 columns of a row.  64-byte
+  // block b of row r sits at block b ^ (r & 3) (rows of two blocks: b ^ bit 1 of
+  // r) and 16-byte chunk j of it at j ^ (r & 1): four rows of a transposed read
+  // and the eight threads of two keys that write at once each touch all banks once.
+  auto value_at = [&](int r, int byte) {
+    const int b = byte >> 6, j = (byte >> 4) & 3;
+    const int bb = HDP == 64 ? b ^ ((r >> 1) & 1) : b ^ (r & 3);
+    return r * (HDP * 2) + bb * 64 + ((j ^ (r & 1)) * 16) + (byte & 15);
   };
-  auto load_tile = [&](int base, int page, R& t) {
-    const bool ok = page >= 0 && page < p.n_pages;
-    const uint64_t there = __ballot(ok);
-    t.hide = 0u;
+
+  // A tile's keys are loaded while the tile two before it is multiplied, its
+  // values one tile before; no load is under a condition, so that the loads stay
+  // between the products: past the last key the row's last page is read again,
+  // and a page that is not there is read as page 0.
+  R tk, tv;              // codes: of the next tile's keys until they are converted, then the one's after; of its values
+  float ks, vall;        // scales of key `lane` of the keys' tile
+  bool vlive;            // that key is there
+  int page;              // its page entry, loaded a tile earlier
+  uint64_t there;        // the keys of the tile whose page is there
+  int64_t vrow = 0;      // the wave's 16 keys of that tile: their first row in the cache
+  auto load_page = [&](int base) { page = table[min(base + lane, key1 - 1) >> p.page_shift]; };
+  auto load_codes = [&](const uint8_t* src, R& t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) t.hide |= ((there >> (16 * i)) & 1u) ? 0u : (1u << i);
+    for (int i = 0; i < R::kD / R::kCD; ++i) {
+      constexpr int kWords = R::kCD * BITS / 32;
+      if (kWords == 4) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src + coff[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t.w[(4 * i + e) % R::kW] = v[e];
+      } else if (kWords == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(src + coff[i]);
+        t.w[(2 * i) % R::kW] = v.x;
+        t.w[(2 * i + 1) % R::kW] = v.y;
+      } else {
+        t.w[i % R::kW] = *reinterpret_cast<const uint32_t*>(src + coff[i]);
+      }
+    }
+  };
+  auto load_keys = [&](int base, R& t) {  // by `page`
     const int key = base + lane;
+    const bool ok = key < key1 && page >= 0 && page < p.n_pages;
+    there = __ballot(ok);
     const int pg = ok ? page : 0;
     const int64_t all = ((static_cast<int64_t>(pg) * p.n_kv + h) << p.page_shift) + (key & page_mask);
-    t.vall = (ok && key < vis) ? p.scales[1][all] : 0.f;
-    t.ks = p.scales[0][all];
+    vlive = ok;
+    vall = p.scales[1][all];
+    ks = p.scales[0][all];
     const int pw = __builtin_amdgcn_readlane(pg, 16 * sg);
-    const int64_t row = ((static_cast<int64_t>(pw) * p.n_kv + h) << p.page_shift) + ((base + 16 * sg) & page_mask);
-    const uint8_t* kp = p.codes[0] + row * row_bytes;
-#pragma unroll
-    for (int i = 0; i < R::kKD / 8; ++i) {
-      if (BITS == 8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(kp + koff[i]);
-        t.k[2 * i % R::kKW] = v.x;
-        t.k[(2 * i + 1) % R::kKW] = v.y;
-      } else {
-        t.k[i % R::kKW] = *reinterpret_cast<const uint32_t*>(kp + koff[i]);
-      }
-    }
-    const uint8_t* vp = p.codes[1] + row * row_bytes;
-#pragma unroll
-    for (int j = 0; j < R::kVK; ++j) {
-      const uint8_t* one = vp + static_cast<uint32_t>(((j & 3) + 8 * (j >> 2)) * row_bytes);
-      if (R::kVB == 1) t.v[0][j] = one[voff];
-      if (R::kVB == 2) t.v[0][j] = *reinterpret_cast<const uint16_t*>(one + voff);
-      if (R::kVB == 4) t.v[0][j] = *reinterpret_cast<const uint32_t*>(one + voff);
-      if (R::kVB == 8) {
-        const uint2 v = *reinterpret_cast<const uint2*>(one + voff);
-        t.v[0][j] = v.x;
-        t.v[R::kVW - 1][j] = v.y;
-      }
-    }
+    vrow = ((static_cast<int64_t>(pw) * p.n_kv + h) << p.page_shift) + ((base + 16 * sg) & page_mask);
+    load_codes(p.codes[0] + vrow * row_bytes, t);
   };
+  auto load_values = [&](R& t) { load_codes(p.codes[1] + vrow * row_bytes, t); };
   // codes in registers -> operands in LDS, in pieces: the range of the tile's
-  // value scales, the key scales, 8 dims of a key, one output block of the values
-  auto convert_range = [&](const R& t) {
-    float top = fabsf(t.vall) < __builtin_inff() ? t.vall : 0.f;  // finite ones
+  // value scales, the key scales, 8 dims of the thread's key, 8 of its value
+  auto convert_range = [&](float v) {
+    float top = fabsf(v) < __builtin_inff() ? v : 0.f;  // finite ones
     if (__any(ValueRange::of(top) > vr_next.e)) {
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
       vr_next.e = max(vr_next.e, uniform(ValueRange::of(top)));
     }
-    // each key's factor, by its lane; value_factors reads the eight of the thread's keys
-    lf[wave][lane] = fabsf(t.vall) < __builtin_inff() ? t.vall * vr_next.down() : 0.f;
   };
-  auto key_scales = [&](const R& t, int buf) {
-    // a value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
-    // reaches only the rows that see the key; every wave writes the same 64 scales
-    const bool bad = !(fabsf(t.vall) < __builtin_inff());
-    lks[buf][lane] = bad ? __uint_as_float(0x7FC00000u) : t.ks * p.scale_log2e;
+  // A value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
+  // reaches only the rows that see the key.  Every wave writes the same 64 scales.  Returns the value
+  // scale of key `lane` (0: no such key)
+  auto key_scales = [&](int buf) {
+    const float v = vlive ? vall : 0.f;
+    lks[buf][lane] = fabsf(v) < __builtin_inff() ? ks * p.scale_log2e : __uint_as_float(0x7FC00000u);
+    return v;
   };
   auto convert_key = [&](const R& t, int buf, int i) {
-    const int key = 16 * sg + kkey, d = kpart * R::kKD + 8 * i;
-    const bf16x8_t v = BITS == 8 ? row8(t.k[2 * i % R::kKW], t.k[(2 * i + 1) % R::kKW]) : row4(t.k[i % R::kKW]);
-    *reinterpret_cast<bf16x8_t*>(&lk[buf][((key >> 5) * kSteps + (d >> 4)) * kFrag + ((key & 31) + 4 * (d & 8)) * 16]) = v;
+    const int d = kpart * R::kD + 8 * i;
+    const bf16x8_t v = BITS == 8 ? row8(t.w[2 * i % R::kW], t.w[(2 * i + 1) % R::kW]) : row4(t.w[i % R::kW]);
+    *reinterpret_cast<bf16x8_t*>(&lk[buf][((own >> 5) * kSteps + (d >> 4)) * kFrag + ((own & 31) + 4 * (d & 8)) * 16]) = v;
   };
-  constexpr int kVP = R::kVK / 2;  // pairs of keys
-  auto value_factors = [&](f16x2_t (&f)[kVP]) {
-#pragma unroll
-    for (int j = 0; j < kVP; j += 2) {
-      const f32x4_t four = *reinterpret_cast<const f32x4_t*>(&lf[wave][16 * sg + 4 * vh + 8 * vfour + 4 * j]);
-      f[j] = __builtin_bit_cast(f16x2_t, pack_f16(four[0], four[1]));
-      f[j + 1] = __builtin_bit_cast(f16x2_t, pack_f16(four[2], four[3]));
-    }
+  // the factor of the thread's value, twice in fp16
+  auto value_factor = [&](float v) {
+    const float f = __shfl(fabsf(v) < __builtin_inff() ? v * vr_next.down() : 0.f, own);
+    return __builtin_bit_cast(f16x2_t, pack_f16(f, f));
   };
-  auto convert_value = [&](const R& t, const f16x2_t (&f)[kVP], int buf, int i) {
-    uint32_t o[kVP];
+  auto convert_value = [&](const R& t, f16x2_t f, int buf, int i) {
+    u32x4_t o;
 #pragma unroll
-    for (int j = 0; j < kVP; ++j) {
-      f16x2_t code;
+    for (int j = 0; j < 4; ++j) {
+      f16x2_t code;  // exact
       if (BITS == 8) {
-        const uint32_t w0 = t.v[(i >> 2) % R::kVW][2 * j], w1 = t.v[(i >> 2) % R::kVW][2 * j + 1];
-        code = __builtin_bit_cast(f16x2_t, (i & 3) == 0   ? pack_f16(sbyte<0>(w0), sbyte<0>(w1))
-                                           : (i & 3) == 1 ? pack_f16(sbyte<1>(w0), sbyte<1>(w1))
-                                           : (i & 3) == 2 ? pack_f16(sbyte<2>(w0), sbyte<2>(w1))
-                                                          : pack_f16(sbyte<3>(w0), sbyte<3>(w1)));
+        // 1024 + (code + 128) in fp16 is 0x6400 | (code ^ 0x80)
+        const uint32_t w = t.w[(2 * i + (j >> 1)) % R::kW] ^ 0x80808080u;
+        code = __builtin_bit_cast(f16x2_t, __builtin_amdgcn_perm(0x64646464u, w, (j & 1) ? 0x04030402u : 0x04010400u)) -
+               f16x2_t{1152, 1152};
       } else {
-        const uint32_t n = nib_pair(t.v[(i >> 3) % R::kVW][2 * j], t.v[(i >> 3) % R::kVW][2 * j + 1], (i >> 1) & 3);
-        const uint32_t c24 = (((i & 1) ? n << 2 : n << 6) & 0x03C003C0u) | 0x4C004C00u;
-        code = __builtin_bit_cast(f16x2_t, c24) - f16x2_t{24, 24};  // exact
+        const uint32_t w = t.w[i % R::kW] >> (8 * j);
+        code = __builtin_bit_cast(f16x2_t, (w & 0x0Fu) | ((w & 0xF0u) << 12) | 0x64006400u) - f16x2_t{1032, 1032};
       }
-      o[j] = __builtin_bit_cast(uint32_t, static_cast<f16x2_t>(code * f[j]));
+      o[j] = __builtin_bit_cast(uint32_t, static_cast<f16x2_t>(code * f));
     }
-    uint8_t* to = &lv[buf][(4 * i + sg) * kFrag + (32 * vh + vdq) * 16 + 8 * vfour];
-    if (NW == 4) *reinterpret_cast<u32x4_t*>(to) = u32x4_t{o[0], o[1], o[kVP - 2], o[kVP - 1]};
-    else *reinterpret_cast<uint2*>(to) = make_uint2(o[0], o[1]);
-  };
-  auto convert_all = [&](const R& t, int buf) {
-    key_scales(t, buf);
-#pragma unroll
-    for (int i = 0; i < R::kKD / 8; ++i) convert_key(t, buf, i);
-    f16x2_t f[kVP];
-    value_factors(f);
-#pragma unroll
-    for (int i = 0; i < kDb; ++i) convert_value(t, f, buf, i);
+    *reinterpret_cast<u32x4_t*>(&lv[buf][value_at(own, (kpart * R::kD + 8 * i) * 2)]) = o;
   };
 
   // products on operand x of a 32-key block b of the tile in `buf`
   auto key_operand = [&](int buf, int b, int x) {
     return *reinterpret_cast<const bf16x8_t*>(&lk[buf][(b * kSteps + x) * kFrag + lane * 16]);
   };
-  auto value_operand = [&](int buf, int b, int x) {  // x = kDb a + i: 16 keys a, output block i
-    return *reinterpret_cast<const f16x8_t*>(&lv[buf][(4 * (x % kDb) + 2 * b + x / kDb) * kFrag + lane * 16]);
+  // x = kDb a + i: keys 32 b + 16 a .., output block i; the lane's address names row 4 hf + s / 4 and
+  // columns 16 (group & 1) + 4 (s % 4) of the block, s = lane % 16
+  typedef __attribute__((address_space(3))) s16x4_t lds_s16x4_t;
+  uint32_t voff[kDb];  // of the first such block; rows of other blocks differ by multiples of 8, which move no swizzle
+#pragma unroll
+  for (int i = 0; i < kDb; ++i)
+    voff[i] = static_cast<uint32_t>(value_at(4 * hf + ((lane & 15) >> 2), 64 * i + ((lane >> 4) & 1) * 32 + 8 * (lane & 3)));
+  auto value_operand = [&](int buf, int b, int x) {
+    uint8_t* lo = &lv[buf][voff[x % kDb]] + (32 * b + 16 * (x / kDb)) * (HDP * 2);
+    uint8_t* hi = lo + 8 * (HDP * 2);
+    const s16x4_t u = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)lo);
+    const s16x4_t v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_t*)hi);
+    typedef __attribute__((__vector_size__(8 * sizeof(short)))) short s16x8_t;
+    return __builtin_bit_cast(f16x8_t, (s16x8_t{u[0], u[1], u[2], u[3], v[0], v[1], v[2], v[3]}));
   };
   constexpr int kPv = 2 * kDb;
-  R t, ahead;  // the next tile's codes, and those of the one after, still on their way
-  int page = 0;
 
   // A tile as it comes: masks, a maximum that moves, a range that grows.  Taken for
   // the first tile of a workgroup, the last ones of causal rows and wherever
   // the plain tile below finds that it does not fit.  half 1: its first 32
   // keys are done already.
-  auto careful_tile = [&](int base, int buf, uint32_t hide, int half, int range) {
+  auto careful_tile = [&](int base, int buf, uint64_t shown, int half, int range) {
     const int rel = lim - base - 4 * hf;
     auto seen = [&](int b, int e) {  // element e of block b: key 32 b + 8 (e / 4) + 4 hf + e % 4
-      return 32 * b + 8 * (e >> 2) + (e & 3) <= rel && !((hide >> (2 * b + (e >> 3))) & 1u);
+      return 32 * b + 8 * (e >> 2) + (e & 3) <= rel && ((shown >> (32 * b + 16 * (e >> 3))) & 1u);  // 16 keys share a page
     };
     float f = 1.f;
     if (range > vr.e) {
@@ -839,33 +836,39 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
     }
   };
 
-  uint32_t hide = 0u;
+  uint64_t shown = 0, shown_next = 0;  // `there` of the current tile, and the next one's
   int buf = 0, base = key0;
+  float vs_next = 0.f;
   if (key0 < key1) {
-    const int page0 = load_page(key0), page1 = load_page(key0 + kKeys);
-    page = load_page(key0 + 2 * kKeys);
-    load_tile(key0, page0, t);
-    load_tile(key0 + kKeys, page1, ahead);
-    convert_range(t);
-    convert_all(t, 0);
-    hide = t.hide;
+    R k0;
+    load_page(key0);
+    load_keys(key0, k0);
+    load_page(key0 + kKeys);
+    load_values(tv);
+    vs_next = key_scales(0);
+    shown = there;
+    load_keys(key0 + kKeys, tk);
+    load_page(key0 + 2 * kKeys);
+    convert_range(vs_next);
+    const f16x2_t f = value_factor(vs_next);
+#pragma unroll
+    for (int i = 0; i < R::kD / 8; ++i) convert_key(k0, 0, i);
+#pragma unroll
+    for (int i = 0; i < R::kD / 8; ++i) convert_value(tv, f, 0, i);
   }
-  // The next tile is converted past the last one too: the registers then hold
-  // keys of page 0, and nothing reads the operands.
+  // The next tile is converted past the last one too; nothing reads it then.
   while (base < key1) {
     int half = 0, range = 0;
-    bool fits = true;
+    bool fits = true, keys_done = false;
     while (base < key1) {
       // this tile's operands are written, and the other buffer's have been read
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-      t = ahead;
-      load_tile(base + 2 * kKeys, page, ahead);
-      page = load_page(base + 3 * kKeys);
       half = 0;
+      keys_done = false;
       range = vr_next.e;  // the one this tile's values were written in (the next tile's may be wider)
-      fits = base > key0 && base + kKeys - 1 <= wfirst && hide == 0u && range == vr.e;
+      fits = base > key0 && base + kKeys - 1 <= wfirst && shown == ~uint64_t{0} && range == vr.e;
       if (!fits) break;
       // The plain tile: every key seen, the maximum and the range as they were.
       // Four groups of products, each with arithmetic between them that does not
@@ -901,16 +904,19 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
       for (int e = 0; e < 16; ++e) s0[e] = s1[e] = bias;
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) ko[x] = key_operand(buf, 0, x);
-      convert_range(t);
-      key_scales(t, buf ^ 1);
+      shown_next = there;
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int x = 0; x < kSteps; ++x) {
         if (x + kAhead < kSteps) ko[x + kAhead] = key_operand(buf, 0, x + kAhead);
         s0 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ko[x], q[x], s0, 0, 0, 0);
-        constexpr int kEvery = kSteps / (R::kKD / 8);
-        if (x % kEvery == kEvery - 1) convert_key(t, buf ^ 1, x / kEvery);
+        if (x == 0) load_values(tv);
+        if (x == 1) vs_next = key_scales(buf ^ 1);
+        constexpr int kEvery = kSteps / (R::kD / 8);
+        if (x % kEvery == kEvery - 1) convert_key(tk, buf ^ 1, x / kEvery);
         __builtin_amdgcn_sched_barrier(0);
       }
+      keys_done = true;
       scales_of(0);
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) ko[x] = key_operand(buf, 1, x);
@@ -918,6 +924,8 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
       for (int x = 0; x < kSteps; ++x) {
         if (x + kAhead < kSteps) ko[x + kAhead] = key_operand(buf, 1, x + kAhead);
         s1 = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ko[x], q[x], s1, 0, 0, 0);
+        if (x == 0) load_keys(base + 2 * kKeys, tk);
+        if (x == 1) load_page(base + 3 * kKeys);
         weights(s0, 0, 16 * x / kSteps, 16 * (x + 1) / kSteps, l0);
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -939,31 +947,43 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
       fits = !__any(l1 > kGrow);
       if (!fits) break;
       l += l1;
-      f16x2_t f[kVP];
-      value_factors(f);
+      convert_range(vs_next);
+      const f16x2_t f = value_factor(vs_next);
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) vo[x] = value_operand(buf, 1, x);
 #pragma unroll
       for (int x = 0; x < kPv; ++x) {
         if (x + kAhead < kPv) vo[x + kAhead] = value_operand(buf, 1, x + kAhead);
         acc[x % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vo[x], __builtin_bit_cast(f16x8_t, pk[2 + x / kDb]), acc[x % kDb], 0, 0, 0);
-        if (x & 1) convert_value(t, f, buf ^ 1, x >> 1);
+        constexpr int kEvery = kPv / (R::kD / 8);
+        if (x % kEvery == kEvery - 1) convert_value(tv, f, buf ^ 1, x / kEvery);
         __builtin_amdgcn_sched_barrier(0);
       }
-      hide = t.hide;
+      shown = shown_next;
       base += kKeys;
       buf ^= 1;
     }
     if (fits) break;
-    if (base <= wlast) careful_tile(base, buf, hide, half, range);  // else a causal tile past the wave's rows
-    convert_range(t);
-    convert_all(t, buf ^ 1);
-    hide = t.hide;
+    if (!keys_done) {
+      shown_next = there;
+      load_values(tv);
+      vs_next = key_scales(buf ^ 1);
+#pragma unroll
+      for (int i = 0; i < R::kD / 8; ++i) convert_key(tk, buf ^ 1, i);
+      load_keys(base + 2 * kKeys, tk);
+      load_page(base + 3 * kKeys);
+    }
+    if (base <= wlast) careful_tile(base, buf, shown, half, range);  // else a causal tile past the wave's rows
+    convert_range(vs_next);
+    const f16x2_t f = value_factor(vs_next);
+#pragma unroll
+    for (int i = 0; i < R::kD / 8; ++i) convert_value(tv, f, buf ^ 1, i);
+    shown = shown_next;
     base += kKeys;
     buf ^= 1;
   }
 
-  // lane l: query row c, dims (8 a + 4 hf + b) HDP / 32 + i: for each a a run of 4 HDP / 32 dims
+  // lane l: query row c, dims 32 i + 8 a + 4 hf + e
   l += __shfl_xor(l, 32);
   const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const float up = vr.up();
@@ -976,13 +996,13 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
       part[kM * HDP + kM + row] = l;
     }
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
+    for (int i = 0; i < kDb; ++i)
 #pragma unroll
-      for (int e = 0; e < HDP / 32; ++e) {
+      for (int a = 0; a < 4; ++a) {
         f32x4_t o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = acc[(4 * e + j) % kDb][4 * a + (4 * e + j) / kDb] * up;
-        *reinterpret_cast<f32x4_t*>(part + row * HDP + (8 * a + 4 * hf) * (HDP / 32) + 4 * e) = o;
+        for (int e = 0; e < 4; ++e) o[e] = acc[i][4 * a + e] * up;
+        *reinterpret_cast<f32x4_t*>(part + row * HDP + 32 * i + 8 * a + 4 * hf) = o;
       }
     return;
   }
@@ -990,18 +1010,13 @@ __global__ __launch_bounds__(64 * NW, HDP <= 64 ? 3 : NW == 8 || HDP <= 128 ? 2 
   const float inv = l == 0.f ? 0.f : up / l;
   uint16_t* dst = p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(h * p.group + qh) * p.hd;
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int i = 0; i < kDb; ++i)
 #pragma unroll
-    for (int e = 0; e < HDP / 64; ++e) {
-      const int d = (8 * a + 4 * hf) * (HDP / 32) + 8 * e;
-      u32x4_t o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int u = 8 * e + 2 * j;
-        o[j] = f32_to_bf16(acc[u % kDb][4 * a + u / kDb] * inv) |
-               (static_cast<uint32_t>(f32_to_bf16(acc[(u + 1) % kDb][4 * a + (u + 1) / kDb] * inv)) << 16);
-      }
-      if (d < p.hd) *reinterpret_cast<u32x4_t*>(dst + d) = o;
+    for (int a = 0; a < 4; ++a) {
+      const int d = 32 * i + 8 * a + 4 * hf;
+      if (d < p.hd)
+        *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_bf16(acc[i][4 * a] * inv, acc[i][4 * a + 1] * inv),
+                                                        pack_bf16(acc[i][4 * a + 2] * inv, acc[i][4 * a + 3] * inv));
     }
 }
 
@@ -1058,8 +1073,7 @@ template <int HDP, int BITS>
 void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
   switch (p.tile_rows) {
     case 16: attn_split_kernel<HDP, BITS, 1, 8><<<blocks, 512, 0, st>>>(p); break;
-    case 128: attn_tile_kernel<HDP, BITS, 4><<<blocks, 256, 0, st>>>(p); break;
-    default: attn_tile_kernel<HDP, BITS, 8><<<blocks, 512, 0, st>>>(p); break;
+    default: attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p); break;
   }
   if (joins) attn_join_kernel<HDP><<<joins, 256, 0, st>>>(p);
 }
@@ -1070,8 +1084,7 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   AttnPlan a{};
   const int64_t group = n_heads / c.n_kv;
   a.tile_rows = n_tokens * group <= 32ll * n_seq ? 16 : 128;
-  if (getenv("ATT_ROWS") && a.tile_rows == 128) a.tile_rows = atoi(getenv("ATT_ROWS"));
-  a.target = a.tile_rows == 256 ? n_cu : 2 * n_cu;
+  a.target = 2 * n_cu;
   a.min_units = 4;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
   a.joins = tiles * c.n_kv;
