@@ -263,7 +263,7 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 // makes the operand of output tile t.  Lane l then ends up with query row
 // l % 16, dims g HDP / 4 ... in order.
 template <int HDP, int BITS, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
+__global__ __launch_bounds__(64 * NW, HDP <= 128 && MT == 1 ? 4 : 2) void attn_split_kernel(AttnParams p) {
   constexpr int kKW = HDP * BITS / 128;        // words of K a lane holds per key: HDP / 4 dims
   constexpr int kVB = HDP * BITS / 128;        // bytes of V a lane holds per key: HDP / 16 dims
   constexpr int kVW = (kVB + 3) / 4;
@@ -330,6 +330,16 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
   const int row_bytes = p.hd * BITS / 8;
   const int page_mask = (1 << p.page_shift) - 1;
   const int32_t* table = p.table + static_cast<int64_t>(w.seq) * p.ld_table;
+  // a lane whose dims lie past head_dim reads the row's first ones instead: q is
+  // zero there, and what V gives there is not stored
+  constexpr int kKL = kKW < 4 ? kKW : 4;  // words of one K load
+  uint32_t koff[kKW / kKL], voff;
+#pragma unroll
+  for (int e = 0; e < kKW / kKL; ++e) {
+    const int d = g * (HDP / 4) + e * kKL * (32 / BITS);
+    koff[e] = static_cast<uint32_t>(c * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
+  }
+  voff = static_cast<uint32_t>(4 * g * row_bytes + (c * (HDP / 16) < p.hd ? c * kVB : 0));
   for (int k0 = key0 + 32 * wave; k0 < key1; k0 += 32 * NW) {
     uint32_t kw[2][kKW], vw[kVW][8];
     f32x4_t ks[2], vs[2];
@@ -337,34 +347,41 @@ __global__ __launch_bounds__(64 * NW) void attn_split_kernel(AttnParams p) {
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int k = k0 + 16 * b;
-      const int page = (k < key1) ? table[k >> p.page_shift] : -1;
-      ok[b] = page >= 0 && page < p.n_pages;
+      const int page = table[min(k, key1 - 1) >> p.page_shift];
+      ok[b] = k < key1 && page >= 0 && page < p.n_pages;
       const int64_t row = ((static_cast<int64_t>(ok[b] ? page : 0) * p.n_kv + h) << p.page_shift) + (k & page_mask);
-      const uint8_t* kp = p.codes[0] + (row + c) * row_bytes + g * (kKW * 4);
+      const uint8_t* kp = p.codes[0] + row * row_bytes;
 #pragma unroll
-      for (int e = 0; e < kKW; e += (BITS == 8 ? 2 : 1)) {
-        const bool in = g * (HDP / 4) + e * (32 / BITS) < p.hd;
-        if (BITS == 8) {
-          const uint2 v = in ? *reinterpret_cast<const uint2*>(kp + 4 * e) : make_uint2(0u, 0u);
-          kw[b][e] = v.x;
-          kw[b][e + 1] = v.y;
+      for (int e = 0; e < kKW / kKL; ++e) {
+        if (kKL == 4) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(kp + koff[e]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) kw[b][(4 * e + j) % kKW] = v[j];
         } else {
-          kw[b][e] = in ? *reinterpret_cast<const uint32_t*>(kp + 4 * e) : 0u;
+          const uint2 v = *reinterpret_cast<const uint2*>(kp + koff[e]);
+          kw[b][0] = v.x;
+          kw[b][1] = v.y;
         }
       }
-      const bool vin = c * (HDP / 16) < p.hd;
-      const uint8_t* vp = p.codes[1] + (row + 4 * g) * row_bytes + c * kVB;
+      const uint8_t* vp = p.codes[1] + row * row_bytes;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const uint8_t* one = vp + r * row_bytes;
-        if (kVB == 2) vw[0][4 * b + r] = vin ? *reinterpret_cast<const uint16_t*>(one) : 0u;
-        if (kVB >= 4) {
+        const uint8_t* one = vp + static_cast<uint32_t>(r * row_bytes);
+        if (kVB == 2) vw[0][4 * b + r] = *reinterpret_cast<const uint16_t*>(one + voff);
+        if (kVB == 4) vw[0][4 * b + r] = *reinterpret_cast<const uint32_t*>(one + voff);
+        if (kVB == 8) {
+          const uint2 v = *reinterpret_cast<const uint2*>(one + voff);
+          vw[0][4 * b + r] = v.x;
+          vw[kVW - 1][4 * b + r] = v.y;
+        }
+        if (kVB == 16) {
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(one + voff);
 #pragma unroll
-          for (int e = 0; e < kVW; ++e) vw[e][4 * b + r] = vin ? *reinterpret_cast<const uint32_t*>(one + 4 * e) : 0u;
+          for (int e = 0; e < 4; ++e) vw[e % kVW][4 * b + r] = v[e];
         }
       }
-      ks[b] = *reinterpret_cast<const f32x4_t*>(p.scales[0] + row + 4 * g);
-      vs[b] = *reinterpret_cast<const f32x4_t*>(p.scales[1] + row + 4 * g);
+      ks[b] = (reinterpret_cast<const f32x4_t*>(p.scales[0] + row))[g];
+      vs[b] = (reinterpret_cast<const f32x4_t*>(p.scales[1] + row))[g];
     }
     const bool masked = k0 + 31 > first || !ok[0] || !ok[1];
 
