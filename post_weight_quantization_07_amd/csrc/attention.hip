@@ -1039,8 +1039,11 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
 
 // Joins the splits of a tile, in their order.  One workgroup per (split tile, key
 // head); the other tiles were written by the kernels above.
+// Latency of the parts' loads bounds it: eight parts are in flight at a time
+// (32 tiles of 25 parts: 16.4 us one at a time).
 template <int HDP>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
+__global__ __launch_bounds__(512) void attn_join_kernel(AttnParams p) {
+  constexpr int kAt = 8;
   const int kM = p.tile_rows;
   const int u = uniform(div_by(static_cast<int>(blockIdx.x), p.kv_mul, p.kv_shift));
   const int h = static_cast<int>(blockIdx.x) - u * p.n_kv;
@@ -1050,27 +1053,47 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnParams p) {
   if (static_cast<int64_t>(w.slot + w.n_split - 1) * p.n_kv + h >= p.max_slots) return;
   const int64_t step = static_cast<int64_t>(p.n_kv) * (kM * (HDP + 2));
   const float* part = p.partial + (static_cast<int64_t>(w.slot) * p.n_kv + h) * (kM * (HDP + 2));
-  for (int e = threadIdx.x; e < kM * HDP / 4; e += 256) {
+  for (int e = threadIdx.x; e < kM * HDP / 4; e += 512) {
     const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
     const int r = r0 + row;
     if (r >= rows || d >= p.hd) continue;
-    float top = kNegInf;
-    for (int s = 0; s < w.n_split; ++s) top = fmaxf(top, part[s * step + kM * HDP + row]);
-    const float safe = top == kNegInf ? 0.f : top;
-    float sum = 0.f;
+    float top = kNoMax, sum = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < w.n_split; ++s) {
-      const float f = fast_exp2(part[s * step + kM * HDP + row] - safe);
-      sum += f * part[s * step + kM * HDP + kM + row];
-      const f32x4_t a = *reinterpret_cast<const f32x4_t*>(part + s * step + row * HDP + d);
+    for (int s0 = 0; s0 < w.n_split; s0 += kAt) {
+      float m[kAt], l[kAt], mx = top;
+      f32x4_t v[kAt];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] += f * a[j];
+      for (int j = 0; j < kAt; ++j) {
+        const float* one = part + min(s0 + j, w.n_split - 1) * step;
+        m[j] = one[kM * HDP + row];
+        l[j] = one[kM * HDP + kM + row];
+        v[j] = *reinterpret_cast<const f32x4_t*>(one + row * HDP + d);
+      }
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        if (s0 + j >= w.n_split) m[j] = kNegInf;
+        mx = fmaxf(mx, m[j]);
+      }
+      const float f0 = fast_exp2(top - mx);
+      top = mx;
+      sum *= f0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] *= f0;
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const float f = fast_exp2(m[j] - top);  // 0 for a part that saw nothing
+        if (s0 + j < w.n_split) {
+          sum += f * l[j];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] += f * v[j][i];
+        }
+      }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int tok = div_by(r, p.group_mul, p.group_shift);
-    const uint2 b = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
     *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo +
-                              static_cast<int64_t>(h * p.group + r - tok * p.group) * p.hd + d) = b;
+                              static_cast<int64_t>(h * p.group + r - tok * p.group) * p.hd + d) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
   }
 }
 
@@ -1089,10 +1112,10 @@ int head_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 template <int HDP, int BITS>
 void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
   switch (p.tile_rows) {
-    case 16: attn_split_kernel<HDP, BITS, 1, 8><<<blocks, 512, 0, st>>>(p); break;
+    case 16: attn_split_kernel<HDP, BITS, 1, 4><<<blocks, 256, 0, st>>>(p); break;
     default: attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p); break;
   }
-  if (joins) attn_join_kernel<HDP><<<joins, 256, 0, st>>>(p);
+  if (joins) attn_join_kernel<HDP><<<joins, 512, 0, st>>>(p);
 }
 
 }  // namespace
@@ -1101,7 +1124,9 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   AttnPlan a{};
   const int64_t group = n_heads / c.n_kv;
   a.tile_rows = n_tokens * group <= 32ll * n_seq ? 16 : 128;
-  a.target = 2 * n_cu;
+  // split kernel: a little under the workgroups that fit (four a CU, two for wide
+  // heads), so that few are left for a second round
+  a.target = a.tile_rows == 16 && c.hd <= 128 ? 3 * n_cu : 2 * n_cu;
   a.min_units = 4;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
   a.joins = tiles * c.n_kv;

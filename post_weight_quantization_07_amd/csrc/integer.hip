@@ -22,12 +22,10 @@ typedef __attribute__((__vector_size__(16 * sizeof(int)))) int i32x16_t;
 typedef __attribute__((address_space(3))) void lds_void_t;
 
 // ------------------------------------------------------------ token codes --
-// T threads per row (T = 64: four rows a workgroup), a row of up to 32 T
+// T threads per row (T = 64: four rows a workgroup), a row of up to 8 CH T
 // values in registers between the maximum and the codes, so x is read once;
 // longer rows are read a second time (from the caches).  VEC: rows are
 // 16-byte aligned and d a multiple of 8.  Bound: HBM (x read, codes written).
-constexpr int kChunks = 4;
-
 template <bool BF16, bool VEC>
 GPTQ_DEV void tok_load(const void* x, int64_t row0, int64_t e, int64_t d, float (&v)[8]) {
   if (VEC) {
@@ -64,7 +62,7 @@ GPTQ_DEV int tok_store(int8_t* codes, int64_t at, int64_t e, int64_t d, const fl
   return sum;
 }
 
-template <int T, bool BF16, bool VEC>
+template <int T, int CH, bool BF16, bool VEC>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void token_codes_kernel(const void* __restrict__ x, int64_t m, int64_t d,
                                                                         int64_t ldx, int8_t* __restrict__ codes,
                                                                         float* __restrict__ scales,
@@ -75,14 +73,14 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void token_codes_kernel(const vo
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + ((T == 64) ? (threadIdx.x >> 6) : 0);
   if (row >= m) return;  // T == 64: whole waves, and there is no barrier below
   const int64_t x0 = row * ldx, c0 = row * d;
-  const bool held = d <= static_cast<int64_t>(T) * 8 * kChunks;
-  float v[kChunks][8];
+  const bool held = d <= static_cast<int64_t>(T) * 8 * CH;
+  float v[CH][8];
   uint32_t am = 0u;
   if (held) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) tok_load<BF16, VEC>(x, x0, (static_cast<int64_t>(c) * T + t) * 8, d, v[c]);
+    for (int c = 0; c < CH; ++c) tok_load<BF16, VEC>(x, x0, (static_cast<int64_t>(c) * T + t) * 8, d, v[c]);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < CH; ++c)
 #pragma unroll
       for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[c][i]));
   } else {
@@ -105,7 +103,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void token_codes_kernel(const vo
   int sum = 0;
   if (held) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) sum += tok_store<VEC>(codes, c0, (static_cast<int64_t>(c) * T + t) * 8, d, v[c], rs);
+    for (int c = 0; c < CH; ++c) sum += tok_store<VEC>(codes, c0, (static_cast<int64_t>(c) * T + t) * 8, d, v[c], rs);
   } else {
     for (int64_t e = static_cast<int64_t>(t) * 8; e < d; e += T * 8) {
       tok_load<BF16, VEC>(x, x0, e, d, v[0]);
@@ -128,15 +126,15 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void token_codes_kernel(const vo
   }
 }
 
-template <int T>
+template <int T, int CH>
 void token_codes_go(const void* x, bool bf16, bool vec, int64_t m, int64_t d, int64_t ldx, int8_t* codes, float* scales,
                     int32_t* sums, hipStream_t st) {
   const dim3 grid(static_cast<unsigned>(T == 64 ? (m + 3) / 4 : m));
   const int b = T == 64 ? 256 : T;
-  if (bf16 && vec) token_codes_kernel<T, true, true><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
-  else if (bf16) token_codes_kernel<T, true, false><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
-  else if (vec) token_codes_kernel<T, false, true><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
-  else token_codes_kernel<T, false, false><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
+  if (bf16 && vec) token_codes_kernel<T, CH, true, true><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
+  else if (bf16) token_codes_kernel<T, CH, true, false><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
+  else if (vec) token_codes_kernel<T, CH, false, true><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
+  else token_codes_kernel<T, CH, false, false><<<grid, b, 0, st>>>(x, m, d, ldx, codes, scales, sums);
 }
 
 // ---------------------------------------------------------- layer layout --
@@ -187,71 +185,173 @@ struct IntParams {
   int64_t m, d_out, ldx;
   int32_t d_in;
   int32_t y_bf16;
+  const void* xraw;      // x not yet quantized (the fused stream kernel), its row stride,
+  int64_t ldxraw;
+  int32_t xvec;          // and whether its rows are 16-byte aligned
 };
 
-GPTQ_DEV void int_store(const IntParams& p, int64_t row, int64_t col, int acc, int off, float sw) {
-  if (p.w_offsets) acc -= off * p.x_sums[row];
-  const float v = (static_cast<float>(acc) * p.x_scales[row]) * sw;
+GPTQ_DEV void int_put(const IntParams& p, int64_t row, int64_t col, float v) {
   if (p.y_bf16)
     static_cast<uint16_t*>(p.y)[row * p.d_out + col] = f32_to_bf16(v);
   else
     static_cast<float*>(p.y)[row * p.d_out + col] = v;
 }
+GPTQ_DEV void int_store(const IntParams& p, int64_t row, int64_t col, int acc, int off, float sw) {
+  if (p.w_offsets) acc -= off * p.x_sums[row];
+  int_put(p, row, col, (static_cast<float>(acc) * p.x_scales[row]) * sw);
+}
 
-// Few tokens: the weights are streamed once.  A workgroup owns 16 output
-// channels, its four waves take turns of 256 k, and each 16x16x64 product
-// takes its 16 weight rows straight from global memory (16 bytes a lane) and
-// the tokens' codes from the caches.  The waves' sums meet in LDS.
-template <int MT>
-__global__ __launch_bounds__(256) void integer_stream_kernel(IntParams p) {
-  constexpr int kNW = 4, kU = 4;  // waves; 64-byte steps per turn
+// Few tokens: the weights are streamed once, bound by HBM.  A workgroup owns 16 R
+// output channels; its eight waves take turns of 64 kU k, and each 16x16x64
+// product takes its 16 weight rows straight from global memory (16 bytes a
+// lane) and the tokens' codes from the caches or LDS.  The next turn's weights are
+// loaded before the current one's products (loading its x early too measured no faster).  The waves' sums meet in LDS.
+// R: the tokens' codes are as many bytes as 16 weight rows, so with R = 1 half of
+// what the CUs load is x; R row blocks share each load of x where d_out gives
+// every CU a workgroup all the same (16 tokens through 28672 x 8192: 67 us with
+// R = 1, 49 us with x not read at all).
+// FUSED (one to four tokens): x is quantized here, by every workgroup for
+// itself and into LDS, while its first weights are on their way: one launch, and
+// reading the tokens again from L2 costs less than a second one.
+constexpr int kSW = 8;                // waves
+constexpr int kFusedElems = 16384;    // tokens * d_in at most
+
+template <int R, int MT, int FUSED>  // FUSED: 0 codes given, 1 bf16, 2 fp32
+__global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p) {
+  constexpr int kU = R == 1 && MT == 1 ? 8 : R == 4 || MT == 4 ? 2 : 4;
+  constexpr int kTurn = kSW * 64 * kU;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16 * R;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
-  const int8_t* wrow = p.w + min(n0 + c, p.d_out - 1) * p.d_in;
+  const int8_t* wrow[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) wrow[j] = p.w + min(n0 + 16 * j + c, p.d_out - 1) * p.d_in + 16 * g;
   const int8_t* xrow[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) xrow[i] = p.x + min(t0 + 16 * i + c, p.m - 1) * p.ldx;
-  i32x4_t acc[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = i32x4_t{0, 0, 0, 0};
+  for (int i = 0; i < MT; ++i) xrow[i] = p.x + min(t0 + 16 * i + c, p.m - 1) * p.ldx + 16 * g;
   const i32x4_t zero = {0, 0, 0, 0};
-  for (int k0 = wave * 64 * kU; k0 < p.d_in; k0 += kNW * 64 * kU) {
-    i32x4_t b[kU], a[kU][MT];
+  auto load_w = [&](int k0, i32x4_t (&b)[kU][R]) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int k = k0 + 64 * u + 16 * g;
-      const bool in = k < p.d_in;
-      b[u] = in ? *reinterpret_cast<const i32x4_t*>(wrow + k) : zero;
+      const int k = k0 + 64 * u;
 #pragma unroll
-      for (int i = 0; i < MT; ++i) a[u][i] = in ? *reinterpret_cast<const i32x4_t*>(xrow[i] + k) : zero;
+      for (int j = 0; j < R; ++j) b[u][j] = k + 16 * g < p.d_in ? *reinterpret_cast<const i32x4_t*>(wrow[j] + k) : zero;
     }
+  };
+  i32x4_t b[kU][R];
+  load_w(wave * 64 * kU, b);
+
+  __shared__ __attribute__((aligned(16))) int8_t xl[FUSED ? kFusedElems : 16];
+  __shared__ float xs[4];
+  __shared__ int xsum[4];
+  if (FUSED) {
+    constexpr bool kBf16 = FUSED == 1;
+    __shared__ uint32_t red[kSW];
+    __shared__ int redsum[kSW];
+    const int chunks = p.d_in / 8;
+    for (int t = 0; t < static_cast<int>(p.m); ++t) {
+      constexpr int kQ = kFusedElems / 8 / (64 * kSW);  // chunks a thread, at most
+      float v[kQ][8];
+      uint32_t am = 0u;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int e = q * 64 * kSW + static_cast<int>(threadIdx.x);
+        if (e < chunks && p.xvec) {
+          load8<kBf16>(p.xraw, t * p.ldxraw + 8 * e, v[q]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[q][i] = e < chunks ? load1<kBf16>(p.xraw, t * p.ldxraw + 8 * e + i) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[q][i]));
+      }
+      am = group_max<64>(am);
+      if (lane == 0) red[wave] = am;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) am = max(am, red[w]);
+      const RowScale rs = row_scale(am, 127.f);
+      int sum = 0;
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int e = q * 64 * kSW + static_cast<int>(threadIdx.x);
+        if (e < chunks) sum += tok_store<true>(xl, static_cast<int64_t>(t) * p.d_in, 8 * e, p.d_in, v[q], rs);
+      }
+      sum = group_sum<64>(sum);
+      if (lane == 0) redsum[wave] = sum;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kSW; ++w) all += redsum[w];
+        xs[t] = rs.scale;
+        xsum[t] = all;
+      }
+      __syncthreads();
+    }
+  }
+
+  i32x4_t acc[R][MT];
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = zero;
+  for (int k0 = wave * 64 * kU; k0 < p.d_in; k0 += kTurn) {
+    i32x4_t a[kU][MT], next[kU][R];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int k = k0 + 64 * u;
+      const bool in = k + 16 * g < p.d_in;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        if (FUSED) a[u][i] = in ? *reinterpret_cast<const i32x4_t*>(xl + min(c, static_cast<int>(p.m) - 1) * p.d_in + k + 16 * g) : zero;
+        else a[u][i] = in ? *reinterpret_cast<const i32x4_t*>(xrow[i] + k) : zero;
+      }
+    }
+    load_w(k0 + kTurn, next);
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][i], b[u], acc[i], 0, 0, 0);
+      for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][i], b[u][j], acc[j][i], 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+#pragma unroll
+      for (int j = 0; j < R; ++j) b[u][j] = next[u][j];
   }
-  __shared__ int part[kNW][MT][16][17];
+  __shared__ int part[kSW][R][MT][16][17];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int j = 0; j < R; ++j)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) part[wave][i][4 * g + r][c] = acc[i][r];
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[wave][j][i][4 * g + r][c] = acc[j][i][r];
   __syncthreads();
-  const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-  const int64_t col = n0 + tc;
-  if (col >= p.d_out) return;
-  const float sw = p.w_scales[col];
-  const int off = p.w_offsets ? p.w_offsets[col] : 0;
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t row = t0 + 16 * i + tr;
-    if (row >= p.m) break;
+  for (int e = threadIdx.x; e < R * MT * 256; e += 64 * kSW) {
+    const int tc = e & 15, j = (e >> 4) % R, tr = (e / (16 * R)) & 15, i = e / (256 * R);
+    const int64_t col = n0 + 16 * j + tc, row = t0 + 16 * i + tr;
+    if (col >= p.d_out || row >= p.m) continue;
     int s = 0;
 #pragma unroll
-    for (int w = 0; w < kNW; ++w) s += part[w][i][tr][tc];
-    int_store(p, row, col, s, off, sw);
+    for (int w = 0; w < kSW; ++w) s += part[w][j][i][tr][tc];
+    const int off = p.w_offsets ? p.w_offsets[col] : 0;
+    const float sw = p.w_scales[col];
+    if (FUSED) int_put(p, row, col, (static_cast<float>(s - off * xsum[tr & 3]) * xs[tr & 3]) * sw);
+    else int_store(p, row, col, s, off, sw);
   }
+}
+
+template <int R>
+void stream_go(const IntParams& p, int fused, hipStream_t st) {
+  const dim3 grid(static_cast<unsigned>((p.d_out + 16 * R - 1) / (16 * R)));
+  const int t = 64 * kSW;
+  if (fused == 1) integer_stream_kernel<R, 1, 1><<<grid, t, 0, st>>>(p);
+  else if (fused == 2) integer_stream_kernel<R, 1, 2><<<grid, t, 0, st>>>(p);
+  else if (p.m <= 16) integer_stream_kernel<R, 1, 0><<<grid, t, 0, st>>>(p);
+  else if (p.m <= 32) integer_stream_kernel<R, 2, 0><<<grid, t, 0, st>>>(p);
+  else integer_stream_kernel<(R > 2 ? 2 : R), 4, 0><<<dim3(static_cast<unsigned>((p.d_out + (R > 2 ? 31 : 16 * R - 1)) / (R > 2 ? 32 : 16 * R))), t, 0, st>>>(p);
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
@@ -262,7 +362,7 @@ __global__ __launch_bounds__(256) void integer_stream_kernel(IntParams p) {
 // a step publishes the next step's data and frees the slot read two halves ago.
 // LDS rows are 64 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 2) & 3), so
 // 16 lanes that read one chunk of 16 rows touch all 64 banks once.
-constexpr int kTStep = 64, kTSlots = 4;
+constexpr int kTStep = 64, kSlots = 4;
 
 #define GPTQ_VMCNT(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0F70)
 
@@ -359,8 +459,16 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   }
   const int s0 = slice * g.per;
   const int steps = min(g.per, (p.d_in + kTStep - 1) / kTStep - s0);
-  auto slotA = [&](int u) -> uint8_t* { return (u & 3) == 0 ? sA0 : (u & 3) == 1 ? sA1 : (u & 3) == 2 ? sA2 : sA3; };
-  auto slotB = [&](int u) -> uint8_t* { return (u & 3) == 0 ? sB0 : (u & 3) == 1 ? sB1 : (u & 3) == 2 ? sB2 : sB3; };
+  auto slotA = [&](int u) -> uint8_t* {
+    switch (u % kSlots) {
+      case 0: return sA0; case 1: return sA1; case 2: return sA2; default: return sA3;
+    }
+  };
+  auto slotB = [&](int u) -> uint8_t* {
+    switch (u % kSlots) {
+      case 0: return sB0; case 1: return sB1; case 2: return sB2; default: return sB3;
+    }
+  };
   // steps past the slice's end load nothing (every lane out of range: zeros)
   auto issue_a = [&](int s, int slot) {
     const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in;
@@ -391,23 +499,23 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   i32x4_t a0[WM], b0[WN], a1[WM], b1[WN];
   constexpr int kL = WM + WN;  // loads of one step, per wave
 #pragma unroll
-  for (int u = 0; u < 3; ++u) {
+  for (int u = 0; u < kSlots - 1; ++u) {
     issue_a(u, u);
     issue_b(u, u);
   }
-  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(2 * kL));
+  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 2) * kL));
   __builtin_amdgcn_s_barrier();
   tile_read<WM>(sA0, oa[0], a0);
   tile_read<WN>(sB0, ob[0], b0);
-  // steps in blocks of four; the ones past the end multiply zeros
-  for (int s = 0; s < steps; s += 4) {
+  // steps in blocks of a ring's length; the ones past the end multiply zeros
+  for (int s = 0; s < steps; s += kSlots) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(kL));
+    for (int u = 0; u < kSlots; ++u) {
+      __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 3) * kL));
       __builtin_amdgcn_s_barrier();
-      issue_a(s + u + 3, u + 3);
+      issue_a(s + u + kSlots - 1, u + kSlots - 1);
       tile_half<WM, WN>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
-      issue_b(s + u + 3, u + 3);
+      issue_b(s + u + kSlots - 1, u + kSlots - 1);
       tile_half<WM, WN>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
     }
   }
@@ -473,14 +581,27 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   }
 }
 
-// sums of the K slices (integers: any order gives the same)
+// sums of the K slices (integers: any order gives the same), four columns a
+// thread where rows are whole vectors
+template <int V>
 __global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid g) {
-  const int64_t total = p.m * p.d_out;
-  for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < total; e += gridDim.x * 256ll) {
-    int s = 0;
-    for (int k = 0; k < g.slices; ++k) s += g.partial[k * total + e];
-    const int64_t row = e / p.d_out, col = e - row * p.d_out;
-    int_store(p, row, col, s, p.w_offsets ? p.w_offsets[col] : 0, p.w_scales[col]);
+  typedef int ivec_t __attribute__((ext_vector_type(V)));
+  const int64_t col = (blockIdx.x * 256ll + threadIdx.x) * V;
+  if (col >= p.d_out) return;
+  float sw[V];
+  int off[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    sw[j] = p.w_scales[col + j];
+    off[j] = p.w_offsets ? p.w_offsets[col + j] : 0;
+  }
+  for (int64_t row = blockIdx.y; row < p.m; row += gridDim.y) {
+    ivec_t s = {};
+    for (int k = 0; k < g.slices; ++k) s += *reinterpret_cast<const ivec_t*>(g.partial + (k * p.m + row) * p.d_out + col);
+    const float sx = p.x_scales[row];
+    const int sum = p.w_offsets ? p.x_sums[row] : 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) int_put(p, row, col + j, (static_cast<float>(s[j] - off[j] * sum) * sx) * sw[j]);
   }
 }
 
@@ -514,9 +635,11 @@ hipError_t token_codes_launch(const void* x, bool bf16, int64_t m, int64_t d, in
   const int64_t e = bf16 ? 8 : 4;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 &&
                    ldx % e == 0 && d % 8 == 0;
-  if (d <= 64 * 8 * kChunks) token_codes_go<64>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
-  else if (d <= 256 * 8 * kChunks) token_codes_go<256>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
-  else token_codes_go<1024>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
+  if (d <= 2048) token_codes_go<64, 4>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
+  else if (d <= 8192) token_codes_go<256, 4>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
+  else if (d <= 16384) token_codes_go<256, 8>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
+  else if (d <= 32768) token_codes_go<512, 8>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
+  else token_codes_go<1024, 4>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
   return hipGetLastError();
 }
 
@@ -534,13 +657,15 @@ void tile_go(const IntParams& p, const TileGrid& g, unsigned blocks, hipStream_t
   else if (p.y_bf16) integer_tile_kernel<WM, WN, kOutBf16><<<blocks, 256, 0, st>>>(p, g);
   else integer_tile_kernel<WM, WN, kOutF32><<<blocks, 256, 0, st>>>(p, g);
 }
+// few tokens of few values: quantized by every workgroup of the stream kernel itself
+bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; }
 size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
 }  // namespace
 
 // workspace: the K slices' sums, then (x not given as codes) codes, scales and sums
 size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool codes_given, int n_cu) {
   const size_t part = up256(int_plan(m, d_in, d_out, n_cu).partial_bytes);
-  return codes_given ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
+  return codes_given || fuses(m, d_in) ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
 }
 
 hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, const int32_t* x_sums, int64_t m,
@@ -548,12 +673,18 @@ hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, c
                                  const int32_t* w_offsets, int64_t d_out, void* y, bool y_bf16, void* ws, int n_cu,
                                  hipStream_t st) {
   const IntPlan plan = int_plan(m, d_in, d_out, n_cu);
-  IntParams p;
+  IntParams p{};
   p.x = static_cast<const int8_t*>(x);
   p.ldx = ldx;
   p.x_scales = x_scales;
   p.x_sums = x_sums;
-  if (xt != kXInt8) {
+  const int64_t vec = xt == kXBf16 ? 8 : 4;
+  const bool fused = xt != kXInt8 && fuses(m, d_in);
+  if (fused) {
+    p.xraw = x;
+    p.ldxraw = ldx;
+    p.xvec = ldx % vec == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
+  } else if (xt != kXInt8) {
     uint8_t* b = static_cast<uint8_t*>(ws) + up256(plan.partial_bytes);
     int8_t* codes = reinterpret_cast<int8_t*>(b);
     float* sc = reinterpret_cast<float*>(b + up256(static_cast<size_t>(m) * d_in));
@@ -574,9 +705,10 @@ hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, c
   p.d_in = static_cast<int32_t>(d_in);
   p.y_bf16 = y_bf16 ? 1 : 0;
   if (plan.kind == 0) {
-    const unsigned gx = static_cast<unsigned>((d_out + 15) / 16);
-    if (m <= 16) integer_stream_kernel<1><<<dim3(gx, 1), 256, 0, st>>>(p);
-    else integer_stream_kernel<2><<<dim3(gx, static_cast<unsigned>((m + 31) / 32)), 256, 0, st>>>(p);
+    const int f = !fused ? 0 : xt == kXBf16 ? 1 : 2;
+    if (d_out >= 64ll * n_cu) stream_go<4>(p, f, st);
+    else if (d_out >= 32ll * n_cu) stream_go<2>(p, f, st);
+    else stream_go<1>(p, f, st);
     return hipGetLastError();
   }
   const int64_t edge = plan.kind == 2 ? 256 : 128;
@@ -590,8 +722,11 @@ hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, c
   if (plan.kind == 2) tile_go<4, 4>(p, g, blocks, st);
   else tile_go<2, 2>(p, g, blocks, st);
   if (g.slices > 1) {
-    const unsigned jb = static_cast<unsigned>(std::min<int64_t>((m * d_out + 255) / 256, int64_t{n_cu} * 16));
-    integer_join_kernel<<<jb, 256, 0, st>>>(p, g);
+    const unsigned rows = static_cast<unsigned>(std::min<int64_t>(m, 32768));
+    if (d_out % 4 == 0)
+      integer_join_kernel<4><<<dim3(static_cast<unsigned>((d_out / 4 + 255) / 256), rows), 256, 0, st>>>(p, g);
+    else
+      integer_join_kernel<1><<<dim3(static_cast<unsigned>((d_out + 255) / 256), rows), 256, 0, st>>>(p, g);
   }
   return hipGetLastError();
 }

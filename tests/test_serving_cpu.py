@@ -137,9 +137,10 @@ def test_integer_calls_refuse(L):
                dict(t=2, xs=FAKE, ld=(1 << 22) + 16)):
         assert mm(**kw) == 1, kw
     assert mm(m=0, x=None, w=None, y=None) == 0
-    need = lib.gptq_integer_workspace_size(4, 1, 64, 8)
-    assert need > 0
-    assert mm(buf=None) == 4 and mm(nb=need - 1) == 4 and mm(buf=ctypes.c_void_p((1 << 20) + 16)) == 4
+    need = lib.gptq_integer_workspace_size(40, 1, 64, 8)
+    assert need >= 40 * 64
+    big = dict(m=40)
+    assert mm(buf=None, **big) == 4 and mm(nb=need - 1, **big) == 4 and mm(buf=ctypes.c_void_p((1 << 20) + 16), **big) == 4
     for bad in ((0, 1, 64, 8), (4, 3, 64, 8), (4, 1, 48, 8), (4, 1, 1 << 17, 8), (4, 1, 64, 0)):
         assert lib.gptq_integer_workspace_size(*bad) == 0
 
