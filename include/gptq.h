@@ -336,7 +336,8 @@ gptq_status gptq_quantize_tokens(const void* x, int32_t xt, int64_t n_tokens, in
  * offsets[n] = zeros[n] - 2^(bits-1), so that W[n, k] = scale[n] (w[n, k] -
  * offsets[n]).  A symmetric layer's offsets are all 0.
  *   qweight  [d_in * bits / 32, d_out] int32 as written by gptq_pack
- *   zeros    [d_out] int32 (the one row of gptq_quantize_layer's zeros)
+ *   zeros    [d_out] int32 (the one row of gptq_quantize_layer's zeros, which
+ *            lie in [0, 2^bits - 1])
  *   w        [d_out, d_in] int8, 16-byte aligned; offsets [d_out] int32
  * Requires d_in % 32 == 0.
  */

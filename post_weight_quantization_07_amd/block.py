@@ -16,7 +16,10 @@ Each group shares one input, so it is solved against one H and one U
 (solve_layers_shared).  The block is Llama-shaped: RMSNorm with unit weights,
 causal multi-head attention without position encoding, a SiLU-gated MLP.
 The block's own arithmetic (norms, attention, activation) is the driver's
-plumbing and runs in torch (fp32); the layer solves run in libgptq.so.
+plumbing and runs in torch (fp32); the layer solves run in libgptq.so.  For a
+model that will be served with a quantized key/value cache, cache_bits runs
+the attention over such a cache, so that o_proj and the layers after it are
+calibrated on the outputs they will see.
 """
 from __future__ import annotations
 
@@ -27,7 +30,7 @@ import torch
 import torch.nn.functional as F
 
 from . import solve_layers_shared
-from ._lib import QuantizeConfig
+from ._lib import QuantizeConfig, QuantizedCache, gptq_cache_attention, gptq_cache_write
 
 QUANT_ORDER: List[List[str]] = [["k_proj", "v_proj", "q_proj"], ["o_proj"], ["up_proj", "gate_proj"],
                                 ["down_proj"]]
@@ -64,6 +67,27 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_seq: int, seq
     return out
 
 
+def cached_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, n_seq: int, seq_len: int, n_heads: int,
+                     bits: int, page_size: int = 64) -> torch.Tensor:
+    """attention() with the keys and values held as `bits`-bit codes in a
+    QuantizedCache, queries in bf16, out in q's dtype.  A head's dimension is a
+    multiple of 16 up to 256."""
+    hd = q.shape[1] // n_heads
+    pages = -(-seq_len // page_size)
+    cache = QuantizedCache.empty(n_seq * pages, page_size, n_heads, hd, bits, q.device)
+    table = torch.arange(n_seq * pages, dtype=torch.int32, device=q.device).view(n_seq, pages)
+    starts = torch.arange(0, n_seq * seq_len + 1, seq_len, dtype=torch.int32, device=q.device)
+    lens = torch.full((n_seq,), seq_len, dtype=torch.int32, device=q.device)
+    tok = torch.arange(n_seq * seq_len, device=q.device)
+    slots = torch.div(tok, seq_len, rounding_mode="floor") * (pages * page_size) + tok % seq_len
+
+    def heads(t):
+        return t.reshape(n_seq * seq_len, n_heads, hd).contiguous()
+    gptq_cache_write(cache, heads(k), heads(v), slots)
+    o = gptq_cache_attention(heads(q).to(torch.bfloat16), cache, table, starts, lens)
+    return o.reshape(q.shape).to(q.dtype)
+
+
 @dataclass
 class BlockResult:
     layers: Dict[str, dict] = field(default_factory=dict)   # per layer: solve outputs
@@ -73,13 +97,15 @@ class BlockResult:
 
 
 def quantize_block(block: Block, x0: torch.Tensor, n_seq: int, seq_len: int, cfg: QuantizeConfig,
-                   keep_inputs: bool = False, timed: bool = False) -> BlockResult:
+                   keep_inputs: bool = False, timed: bool = False, cache_bits: Optional[int] = None) -> BlockResult:
     """Quantize the block's seven layers group by group (true-sequential).
     x0: hidden states entering the block, [n_seq * seq_len, d_model] fp32.
     Each quantized layer's weights are replaced by its dequantized Q before the
     next group's input is computed.  Returns the solve outputs per layer, the
     block output computed with the quantized weights, optionally each group's
-    input (bf16, as accumulated into H) and, with `timed`, per-stage times."""
+    input (bf16, as accumulated into H) and, with `timed`, per-stage times.
+    cache_bits (8 or 4): attention reads its keys and values from a cache of
+    that many bits (cached_attention); None: fp32."""
     res = BlockResult()
     W = block.weights
     ev = {}
@@ -106,8 +132,12 @@ def quantize_block(block: Block, x0: torch.Tensor, n_seq: int, seq_len: int, cfg
     mark("forward 1 end")
     solve(QUANT_ORDER[0], xn1)
     mark("forward 2 start")
-    att = attention(F.linear(xn1, W["q_proj"]), F.linear(xn1, W["k_proj"]), F.linear(xn1, W["v_proj"]), n_seq,
-                    seq_len, block.n_heads)
+    qkv = [F.linear(xn1, W[n]) for n in ("q_proj", "k_proj", "v_proj")]
+    if cache_bits is None:
+        att = attention(*qkv, n_seq, seq_len, block.n_heads)
+    else:
+        att = cached_attention(*qkv, n_seq, seq_len, block.n_heads, cache_bits)
+    del qkv
     mark("forward 2 end")
     solve(QUANT_ORDER[1], att)
     mark("forward 3 start")

@@ -115,3 +115,34 @@ def dequant_apply(x: torch.Tensor, layer: Mapping[str, torch.Tensor], bits: int,
         return gptq_dequant_matmul_ordered(x, layer["qweight"], layer["scales"], layer["zeros"], layer["g_idx"],
                                            layer["order"], bits, **kw)
     return gptq_dequant_matmul(x, layer["qweight"], layer["scales"], layer["zeros"], layer["g_idx"], bits, **kw)
+
+
+def integer_layer(r: Mapping[str, torch.Tensor], bits: int, device="cuda:0") -> Dict[str, torch.Tensor]:
+    """A loaded layer with one group per output channel (group_size -1) in the
+    form the integer product reads, on `device`: int8 w [d_out, d_in], fp32
+    scales [d_out] (the stored float16 values) and, unless they are all zero,
+    int32 offsets [d_out].  It takes d_in * d_out bytes; the packed layer is
+    not needed any more.  Apply it with integer_apply."""
+    from ._lib import gptq_integer_weight
+    if r["scales"].shape[0] != 1 or r["zeros"].shape[0] != 1:
+        raise ValueError("integer_layer: the layer needs one group per output channel (group_size -1), "
+                         f"got {r['scales'].shape[0]} groups")
+    dev = torch.device(device)
+    with torch.cuda.device(dev):
+        w, offsets = gptq_integer_weight(r["qweight"].to(dev, torch.int32).contiguous(),
+                                         r["zeros"].to(dev).round().to(torch.int32).contiguous(), bits)
+    out = {"w": w, "scales": r["scales"].to(dev, torch.float32).reshape(-1).contiguous()}
+    most = int(offsets.abs().max())
+    if most > 128:
+        raise ValueError(f"integer_layer: zero points outside the codes of {bits} bits")
+    if most > 0:
+        out["offsets"] = offsets
+    return out
+
+
+def integer_apply(x, layer: Mapping[str, torch.Tensor], **kw) -> torch.Tensor:
+    """y = x W^T in 8-bit integers for a layer prepared by integer_layer; x as
+    gptq_integer_matmul takes it.  Layers that read the same x share its codes:
+    pass them what gptq_quantize_tokens returned for it."""
+    from ._lib import gptq_integer_matmul
+    return gptq_integer_matmul(x, layer["w"], layer["scales"], layer.get("offsets"), **kw)
