@@ -189,3 +189,18 @@ def test_stream_and_graph(G):
             torch.cuda.synchronize()
             assert torch.equal(y, want[i])
             G.gptq_integer_matmul(xs[i], dw, ds, doff)      # eager work between the replays
+
+
+@pytest.mark.parametrize("m,d_in,d_out,asym", [(5, 4096, 16401, True), (16, 8192, 16384, False), (16, 288, 20000, True),
+                                               (1, 32, 65536, False), (13, 11008, 16400, True)])
+def test_many_channels(G, m, d_in, d_out, asym):
+    """Few tokens, codes given, through more row blocks than the card has CUs."""
+    banner(f"integer product {m}x{d_in}->{d_out}")
+    w, s, off = _layer(d_out, d_in, d_in, asym)
+    x = _x(m, d_in, "bf16", m)
+    xq = G.gptq_quantize_tokens(x)
+    codes, sx = S.row_codes(host(x), 127)
+    ref = S.integer_matmul(codes, sx, w, s, off)
+    for dtype in (torch.float32, torch.bfloat16):
+        y = host(G.gptq_integer_matmul(xq, _d(w), _d(s), _d(off) if asym else None, out_dtype=dtype)).astype(np.float64)
+        assert np.all(np.abs(y - ref) <= REL[dtype] * np.abs(ref))
