@@ -251,7 +251,7 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 
 // ---------------------------------------------------- keys split over waves --
 // A workgroup owns 16 MT rows of one (sequence, key head) and one key split;
-// its NW waves take turns of 32 keys, straight from global memory into the
+// its four waves take turns of 32 keys, straight from global memory into the
 // operands, and their results meet in LDS at the end.
 //
 // Scores are computed transposed, S^T = K Q^T (16x16x32): lane l holds key
@@ -262,14 +262,16 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 // 16 + 4 g + r, dims (l % 16) HDP / 16 + t, and byte t of its eight words
 // makes the operand of output tile t.  Lane l then ends up with query row
 // l % 16, dims g HDP / 4 ... in order.
-template <int HDP, int BITS, int MT, int NW>
-__global__ __launch_bounds__(64 * NW, HDP <= 128 && MT == 1 ? 4 : 2) void attn_split_kernel(AttnParams p) {
+constexpr int kSplitWaves = 4;
+
+template <int HDP, int BITS, int MT>
+__global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) void attn_split_kernel(AttnParams p) {
   constexpr int kKW = HDP * BITS / 128;        // words of K a lane holds per key: HDP / 4 dims
   constexpr int kVB = HDP * BITS / 128;        // bytes of V a lane holds per key: HDP / 16 dims
   constexpr int kVW = (kVB + 3) / 4;
   constexpr int kSteps = HDP / 32;             // products of a 16-key score tile
   constexpr int kTiles = HDP / 16;             // output tiles
-  constexpr int kM = 16 * MT;
+  constexpr int kM = 16 * MT, NW = kSplitWaves;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -508,7 +510,7 @@ __global__ __launch_bounds__(64 * NW, HDP <= 128 && MT == 1 ? 4 : 2) void attn_s
   __syncthreads();
   const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const bool whole = w.n_split == 1;
-  if (!whole && slot >= p.max_slots) return;  // the whole workgroup
+  if (!whole && static_cast<uint64_t>(slot) >= static_cast<uint64_t>(p.max_slots)) return;  // the whole workgroup
   float* part = p.partial + slot * (kM * (HDP + 2));
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -1005,7 +1007,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const float up = vr.up();
   if (w.n_split > 1) {
-    if (slot >= p.max_slots) return;
+    if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(p.max_slots)) return;
     float* part = p.partial + slot * (kM * (HDP + 2));
     const int row = 32 * wave + c;
     if (hf == 0) {
@@ -1050,9 +1052,10 @@ __global__ __launch_bounds__(512) void attn_join_kernel(AttnParams p) {
   Work w;
   if (!find_work<false>(p, u, w)) return;
   const int rows = w.s.n * p.group, r0 = w.tile * kM;
-  if (static_cast<int64_t>(w.slot + w.n_split - 1) * p.n_kv + h >= p.max_slots) return;
+  const int64_t slot0 = static_cast<int64_t>(w.slot) * p.n_kv + h;
+  if (slot0 < 0 || slot0 + static_cast<int64_t>(w.n_split - 1) * p.n_kv >= p.max_slots) return;
   const int64_t step = static_cast<int64_t>(p.n_kv) * (kM * (HDP + 2));
-  const float* part = p.partial + (static_cast<int64_t>(w.slot) * p.n_kv + h) * (kM * (HDP + 2));
+  const float* part = p.partial + slot0 * (kM * (HDP + 2));
   for (int e = threadIdx.x; e < kM * HDP / 4; e += 512) {
     const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
     const int r = r0 + row;
@@ -1111,10 +1114,10 @@ int head_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 
 template <int HDP, int BITS>
 void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
-  switch (p.tile_rows) {
-    case 16: attn_split_kernel<HDP, BITS, 1, 4><<<blocks, 256, 0, st>>>(p); break;
-    default: attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p); break;
-  }
+  constexpr int t = 64 * kSplitWaves;
+  if (p.tile_rows == 128) attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p);
+  else if (HDP <= 128 && p.tile_rows == 32) attn_split_kernel<HDP, BITS, HDP <= 128 ? 2 : 1><<<blocks, t, 0, st>>>(p);
+  else attn_split_kernel<HDP, BITS, 1><<<blocks, t, 0, st>>>(p);
   if (joins) attn_join_kernel<HDP><<<joins, 512, 0, st>>>(p);
 }
 
@@ -1123,9 +1126,16 @@ void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t s
 AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t ld_table, int n_cu) {
   AttnPlan a{};
   const int64_t group = n_heads / c.n_kv;
-  a.tile_rows = n_tokens * group <= 32ll * n_seq ? 16 : 128;
+  // Rows a sequence, on average: up to 16, one row block, for single tokens; up to
+  // 64, two row blocks that share the conversion of the keys (32 sequences of
+  // 4096 keys, 32 rows: 83 us in tiles of 16, 69 in tiles of 32; 48 rows over 2000
+  // keys: 13.4 us, 18.4 in tiles of 128; at 64 rows over 4096 keys 57.8 and 57.3).
+  // Heads wider than 128 have no registers for the second block (256 wide, over
+  // 4096 keys: 32 rows 148 us in tiles of 16, 278 in tiles of 128; 64 rows 109 and 168).
+  const int64_t per_seq = (n_tokens * group + n_seq - 1) / n_seq;
+  a.tile_rows = per_seq > 64 ? 128 : per_seq > 16 && c.hd <= 128 ? 32 : 16;
   // split kernel: a little under the workgroups that fit (four a CU, two for wide
-  // heads), so that few are left for a second round
+  // heads or two row blocks), so that few are left for a second round
   a.target = a.tile_rows == 16 && c.hd <= 128 ? 3 * n_cu : 2 * n_cu;
   a.min_units = 4;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);

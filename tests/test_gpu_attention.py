@@ -280,3 +280,20 @@ def test_stream_and_graph(G, lens):
             c.check(out)
         else:
             other.check(out)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", [
+    ([(17, 17)], 1, 1, 64, 16),
+    ([(4, 3000), (5, 6)], 8, 1, 128, 64),
+    ([(20, 900), (1, 33)], 3, 1, 256, 32),
+    ([(33, 2500), (31, 31), (2, 1)], 2, 1, 80, 16),
+    ([(64, 1300)], 2, 2, 16, 128),
+])
+def test_some_rows(G, lens, heads, kv, hd, page, bits):
+    """17 to 64 rows a sequence: a few tokens at a time, or one with many heads to a key head."""
+    banner(f"attention {lens} {heads}/{kv}x{hd} page {page} int{bits}")
+    c = Case(G, lens, heads, kv, hd, page, bits, seed=11)
+    out = G.gptq_cache_attention(c.q, c.cache, *c.args)
+    c.check(out)
+    assert torch.equal(out, G.gptq_cache_attention(c.q, c.cache, *c.args))
