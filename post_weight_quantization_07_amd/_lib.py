@@ -429,10 +429,12 @@ _TYPE = {torch.float32: GPTQ_F32, torch.bfloat16: GPTQ_BF16}
 
 def _on_device(what: str, *ts) -> int:
     """The index of the current device, on which every given tensor has to lie."""
-    dev = torch.cuda.current_device()
+    dev = ts[0].get_device()
     for t in ts:
         if t is not None and t.get_device() != dev:
-            raise ValueError(f"{what}: the tensors must be on the current GPU (cuda:{dev})")
+            dev = -1
+    if dev < 0 or dev != torch._C._cuda_getDevice():  # torch.cuda.current_device() without its initialization
+        raise ValueError(f"{what}: the tensors must be on the current GPU")
     return dev
 
 
@@ -461,11 +463,11 @@ def gptq_quantize_tokens(x: torch.Tensor, codes: Optional[torch.Tensor] = None, 
     dev = _on_device(what, x, codes, scales, sums)
     m, d = x.shape
     if codes is None:
-        codes = torch.empty((m, d), dtype=torch.int8, device=x.device)
+        codes = x.new_empty((m, d), dtype=torch.int8)
     if scales is None:
-        scales = torch.empty(m, dtype=torch.float32, device=x.device)
+        scales = x.new_empty(m, dtype=torch.float32)
     if sums is None:
-        sums = torch.empty(m, dtype=torch.int32, device=x.device)
+        sums = x.new_empty(m, dtype=torch.int32)
     if (codes.shape != (m, d) or codes.dtype != torch.int8 or not codes.is_contiguous() or scales.shape != (m,)
             or scales.dtype != torch.float32 or not scales.is_contiguous() or sums.shape != (m,)
             or sums.dtype != torch.int32 or not sums.is_contiguous()):
@@ -533,7 +535,7 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
         raise ValueError(f"{what}: offsets must be contiguous int32 [d_out]")
     if y is None:
         yt = _type_code(what, out_dtype)
-        y = torch.empty((m, d_out), dtype=out_dtype, device=x.device)
+        y = x.new_empty((m, d_out), dtype=out_dtype)
     else:
         yt = _type_code(what, y.dtype)
         if y.shape != (m, d_out) or not y.is_contiguous():
@@ -623,14 +625,12 @@ def gptq_cache_write(cache: QuantizedCache, k: torch.Tensor, v: torch.Tensor, sl
     what = "gptq_cache_write"
     n = _slots(what, slots)
     code = _type_code(what, k.dtype)
-    hd = cache.head_dim
-    shape = (n, cache.n_kv_heads, hd)
-    for t in (k, v):
-        if t.shape != shape or t.dtype != k.dtype or (n > 0 and (t.stride(2) != 1 or t.stride(1) != hd)):
-            raise ValueError(f"{what}: k and v must be [n, {cache.n_kv_heads}, {hd}] of one dtype, heads contiguous")
+    heads, hd = cache.n_kv_heads, cache.head_dim
+    shape, sk, sv = (n, heads, hd), k.stride(), v.stride()
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or (n > 0 and (sk[1:] != (hd, 1) or sv[1:] != (hd, 1))):
+        raise ValueError(f"{what}: k and v must be [n, {heads}, {hd}] of one dtype, heads contiguous")
     dev = cache._here(what, k, v, slots)
-    width = cache.n_kv_heads * hd
-    ldk, ldv = (k.stride(0), v.stride(0)) if n > 1 else (width, width)
+    ldk, ldv = (sk[0], sv[0]) if n > 1 else (heads * hd, heads * hd)
     _check(_lib().gptq_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), code, n, ldk, ldv, slots.data_ptr(),
                                    _raw_stream(stream, dev)), what)
 
@@ -642,12 +642,11 @@ def gptq_cache_read(cache: QuantizedCache, slots: torch.Tensor, dtype: torch.dty
     what = "gptq_cache_read"
     n = _slots(what, slots)
     shape = (n, cache.n_kv_heads, cache.head_dim)
+    code = _type_code(what, dtype if k is None else k.dtype)
     k = torch.empty(shape, dtype=dtype, device=slots.device) if k is None else k
-    v = torch.empty(shape, dtype=k.dtype, device=slots.device) if v is None else v
-    code = _type_code(what, k.dtype)
-    for t in (k, v):
-        if t.shape != shape or t.dtype != k.dtype or not t.is_contiguous():
-            raise ValueError(f"{what}: k and v must be contiguous [n, n_kv_heads, head_dim] of one dtype")
+    v = torch.empty_like(k) if v is None else v
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError(f"{what}: k and v must be contiguous [n, n_kv_heads, head_dim] of one dtype")
     dev = cache._here(what, slots, k, v)
     _check(_lib().gptq_cache_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), code,
                                   _raw_stream(stream, dev)), what)
@@ -685,7 +684,7 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
                          "[n_seq + 1] and [n_seq]")
     width = heads * hd
     if out is None:
-        out = torch.empty((n, heads, hd), dtype=torch.bfloat16, device=q.device)
+        out = q.new_empty((n, heads, hd))
     elif (out.shape != q.shape or out.dtype != torch.bfloat16
           or (n > 0 and (out.stride(2) != 1 or out.stride(1) != hd))):
         raise ValueError(f"{what}: out must be bfloat16 like q, the heads of a token contiguous")
