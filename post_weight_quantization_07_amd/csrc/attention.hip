@@ -255,13 +255,19 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 // operands, and their results meet in LDS at the end.
 //
 // Scores are computed transposed, S^T = K Q^T (16x16x32): lane l holds key
-// l % 16's codes at the 8 BPL dims of its group g = l / 16, and its results
+// l % 16's codes at the HDP / 4 dims of its group g = l / 16, and its results
 // are keys 4 g + r (r < 4) for query row l % 16.  Two such tiles (32 keys) are,
 // without any exchange between lanes, the P^T operand of O^T = V^T P^T, when
 // the sum over keys runs in that order; so lane l reads V at keys 4 g + r and
 // 16 + 4 g + r, dims (l % 16) HDP / 16 + t, and byte t of its eight words
 // makes the operand of output tile t.  Lane l then ends up with query row
 // l % 16, dims g HDP / 4 ... in order.
+//
+// Bound: HBM, by the loads that fit in flight beside the operands' registers.
+// 64 ragged sequences (292 MB of 8-bit keys and values) 62 us, 4.7 TB/s; four of
+// 131000 keys at 4 bits (570 MB) 143 us, 4.0 TB/s; one of 1000 keys 8.6 us, four
+// dependent trips to memory.  Four waves a workgroup and four workgroups a CU:
+// eight waves and two took 83 us for the ragged batch.
 constexpr int kSplitWaves = 4;
 
 template <int HDP, int BITS, int MT>
@@ -584,6 +590,11 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 // The row maximum is only moved when a lane's weights sum to more than 2^10 (fp16
 // holds 2^15; p keeps its relative precision): the usual tile then costs a multiply-add and
 // an exp2 per score, half a conversion and half a sum.
+//
+// Bound: the products, the exponentials and the codes' conversion share the
+// waves' issue slots: a 64-key tile of 128 rows x 128 dims takes about 3740 cycles, of
+// which its products need 2048.  Four prompts of 2048 tokens, 32 heads of 128: 206
+// us (0.67 PFLOP/s of the causal half); long ones come to 0.88 PFLOP/s.
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 1024.f;
 
@@ -1042,7 +1053,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
 // Joins the splits of a tile, in their order.  One workgroup per (split tile, key
 // head); the other tiles were written by the kernels above.
 // Latency of the parts' loads bounds it: eight parts are in flight at a time
-// (32 tiles of 25 parts: 16.4 us one at a time).
+// (32 tiles of 25 parts: 6.9 us; 16.4 us one at a time).
 template <int HDP>
 __global__ __launch_bounds__(512) void attn_join_kernel(AttnParams p) {
   constexpr int kAt = 8;

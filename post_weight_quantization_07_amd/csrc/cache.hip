@@ -9,8 +9,9 @@
 // rows, the heads of one token next to each other in k and v.  Once that fills
 // the card, a group of lanes takes four rows and loads them together: 16384
 // tokens of 32 heads x 128 in bf16 to int8 codes at scattered slots are written
-// in 103 us and read in 94 us, 4.0 and 4.3 TB/s (one row a group 117 and
-// 116 us; two rows 102 and 104; eight 115 and 90).
+// in 100 us and read in 95 us, 4.1 and 4.3 TB/s (one row a group 117 and 116 us;
+// two rows 102 and 104; eight 115 and 90).  64 tokens of 8 heads: 3.6 and 3.0 us,
+// a launch and two dependent loads.
 #include "gptq_common.h"
 #include "gptq_internal.h"
 #include "quant_row.h"
@@ -81,19 +82,18 @@ __global__ __launch_bounds__(256) void cache_write_kernel(CacheRows p) {
     am = group_max<L>(am);
     if (at[i] < 0 || !live) continue;
     const RowScale rs = row_scale(am, static_cast<float>(kTop));
-    int c[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = static_cast<int>(row_code<kTop>(v[i][j], rs));
+    uint32_t w[2];
     if (BITS == 8) {
-      uint32_t w[2] = {0u, 0u};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j >> 2] |= (static_cast<uint32_t>(c[j]) & 0xFFu) << (8 * (j & 3));
+      row_codes<kTop, 0>(v[i], rs, w);
       *reinterpret_cast<uint2*>(p.codes[which] + at[i] * p.hd + sub * 8) = make_uint2(w[0], w[1]);
     } else {
-      uint32_t w = 0u;
+      row_codes<kTop, 8>(v[i], rs, w);  // bytes of 1 .. 15: two to a byte, four in each word's low half
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w |= static_cast<uint32_t>(c[j] + 8) << (4 * j);
-      *reinterpret_cast<uint32_t*>(p.codes[which] + at[i] * (p.hd / 2) + sub * 4) = w;
+      for (int j = 0; j < 2; ++j) {
+        w[j] = (w[j] | (w[j] >> 4)) & 0x00FF00FFu;
+        w[j] |= w[j] >> 8;
+      }
+      *reinterpret_cast<uint32_t*>(p.codes[which] + at[i] * (p.hd / 2) + sub * 4) = (w[0] & 0xFFFFu) | (w[1] << 16);
     }
     if (sub == 0) p.scales[which][at[i]] = rs.scale;
   }

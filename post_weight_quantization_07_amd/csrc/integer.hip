@@ -6,8 +6,8 @@
 // cx are the codes of x's rows (quant_row.h), cw the layer's codes shifted
 // into int8, off its zero points shifted the same way (absent: symmetric).
 // Every sum is a 32-bit integer and exact: d_in <= 65536 keeps both below
-// 2^30 in magnitude and their difference below 2^31.  The only roundings are the conversion of the sum to
-// fp32, the two scales and the store.
+// 2^30 in magnitude and their difference below 2^31.  The only roundings are the
+// conversion of the sum to fp32, the two scales and the store.
 #include "gptq_common.h"
 #include "gptq_internal.h"
 #include "quant_row.h"
@@ -25,7 +25,9 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 // T threads per row (T = 64: four rows a workgroup), a row of up to 8 CH T
 // values in registers between the maximum and the codes, so x is read once;
 // longer rows are read a second time (from the caches).  VEC: rows are
-// 16-byte aligned and d a multiple of 8.  Bound: HBM (x read, codes written).
+// 16-byte aligned and d a multiple of 8.  Bound: HBM (x read, codes written):
+// 2048 x 28672 bf16 in 42 us, 4.2 TB/s; 509 x 11008 fp32, all of it in flight at
+// once, 7.9 us; 16 x 4096 4.2 us, a launch and one trip to HBM.
 template <bool BF16, bool VEC>
 GPTQ_DEV void tok_load(const void* x, int64_t row0, int64_t e, int64_t d, float (&v)[8]) {
   if (VEC) {
@@ -43,15 +45,10 @@ GPTQ_DEV void tok_load(const void* x, int64_t row0, int64_t e, int64_t d, float 
 
 template <bool VEC>
 GPTQ_DEV int tok_store(int8_t* codes, int64_t at, int64_t e, int64_t d, const float (&v)[8], const RowScale& rs) {
-  uint32_t w[2] = {0u, 0u};
-  int sum = 0;
   if (e >= d) return 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int c = static_cast<int>(row_code<127>(v[i], rs));
-    sum += c;
-    w[i >> 2] |= (static_cast<uint32_t>(c) & 0xFFu) << (8 * (i & 3));
-  }
+  uint32_t w[2];
+  row_codes<127, 0>(v, rs, w);
+  const int sum = __builtin_amdgcn_sdot4(w[0], 0x01010101, __builtin_amdgcn_sdot4(w[1], 0x01010101, 0, false), false);
   if (VEC) {
     *reinterpret_cast<uint2*>(codes + at + e) = make_uint2(w[0], w[1]);
   } else {
@@ -205,14 +202,18 @@ GPTQ_DEV void int_store(const IntParams& p, int64_t row, int64_t col, int acc, i
 // output channels; its eight waves take turns of 64 kU k, and each 16x16x64
 // product takes its 16 weight rows straight from global memory (16 bytes a
 // lane) and the tokens' codes from the caches or LDS.  The next turn's weights are
-// loaded before the current one's products (loading its x early too measured no faster).  The waves' sums meet in LDS.
+// loaded before the current one's products (loading its x early too measured no
+// faster).  The waves' sums meet in LDS.
 // R: the tokens' codes are as many bytes as 16 weight rows, so with R = 1 half of
 // what the CUs load is x; R row blocks share each load of x where d_out gives
 // every CU a workgroup all the same (16 tokens through 28672 x 8192: 67 us with
-// R = 1, 49 us with x not read at all).
+// R = 1, 63 with R = 4, 49 with x not read at all).
+// 16 tokens: 11008 x 4096 15.2 us (a kernel that only reads those 45 MB takes
+// 10 to 12), 8192 x 28672 57 us, 4.1 TB/s.  32 and 64 tokens of 11008 x 4096: 22 and 30 us.
 // FUSED (one to four tokens): x is quantized here, by every workgroup for
 // itself and into LDS, while its first weights are on their way: one launch, and
-// reading the tokens again from L2 costs less than a second one.
+// reading the tokens again from L2 costs less than a second one (4096 x 4096: 7.2 us
+// against 6.5 + 4.2).
 constexpr int kSW = 8;                // waves
 constexpr int kFusedElems = 16384;    // tokens * d_in at most
 
@@ -422,7 +423,10 @@ void stream_go(const IntParams& p, int fused, hipStream_t st) {
   else if (fused == 2) integer_stream_kernel<R, 1, 2><<<grid, t, 0, st>>>(p);
   else if (p.m <= 16) integer_stream_kernel<R, 1, 0><<<grid, t, 0, st>>>(p);
   else if (p.m <= 32) integer_stream_kernel<R, 2, 0><<<grid, t, 0, st>>>(p);
-  else integer_stream_kernel<(R > 2 ? 2 : R), 4, 0><<<dim3(static_cast<unsigned>((p.d_out + (R > 2 ? 31 : 16 * R - 1)) / (R > 2 ? 32 : 16 * R))), t, 0, st>>>(p);
+  else {  // four token blocks leave registers for two row blocks
+    constexpr int r = R > 2 ? 2 : R;
+    integer_stream_kernel<r, 4, 0><<<dim3(static_cast<unsigned>((p.d_out + 16 * r - 1) / (16 * r))), t, 0, st>>>(p);
+  }
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
@@ -433,6 +437,11 @@ void stream_go(const IntParams& p, int fused, hipStream_t st) {
 // a step publishes the next step's data and frees the slot read two halves ago.
 // LDS rows are 64 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 2) & 3), so
 // 16 lanes that read one chunk of 16 rows touch all 64 banks once.
+// Bound: the matrix cores, and the clock that they leave.  2048 x 28672 -> 8192 on
+// 256 x 256 tiles: 414 us, 2.32 POP/s.  Four waves of 128 x 128 read half the LDS
+// bytes a product of 64 x 64; 128 x 128 tiles are for grids too small for the others
+// (509 x 11008 -> 4096: 36 us in four K slices, 1.28 POP/s; an eight-step ring, one
+// workgroup a CU, 38 us).
 constexpr int kTStep = 64, kSlots = 4;
 
 #define GPTQ_VMCNT(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0F70)
@@ -653,7 +662,8 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
 }
 
 // sums of the K slices (integers: any order gives the same), four columns a
-// thread where rows are whole vectors
+// thread where rows are whole vectors.  Bound: the caches and HBM (four slices
+// of 509 x 4096, 33 MB, in 10 us).
 template <int V>
 __global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid g) {
   typedef int ivec_t __attribute__((ext_vector_type(V)));

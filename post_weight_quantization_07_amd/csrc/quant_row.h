@@ -4,10 +4,14 @@
 //   amax = max |x|, scale = amax / top (fp32, correctly rounded), top = 2^(b-1) - 1
 //   code = the integer nearest to top x / amax, ties to the even one
 // The code is that of the exact quotient: it is first taken from an fp32
-// product, whose error is under 2^-16 of a step, and where that lies within
-// 2^-13 of a rounding border the two sides 2 top |x| and (2 k + 1) amax are
-// compared in fp64, which holds both exactly.  A row of zeros has scale 0 and
-// codes 0; a row with a NaN or an infinity has scale NaN and codes 0.
+// product, whose error is under 2^-16 of a step (two roundings of 2^-24 on at
+// most 127), and where that lies within 2^-15 of a rounding border the two sides
+// 2 top |x| and (2 k + 1) amax are compared in fp64, which holds both exactly.
+// A row of zeros has scale 0 and codes 0; a row with a NaN or an infinity has
+// scale NaN and codes 0.
+// The kernels that use it would be bound by these instructions before HBM:
+// adding 3 2^22 rounds to the nearest even integer and leaves it in the low
+// byte, and eight values share one test for the border.
 #pragma once
 
 #include "gptq_common.h"
@@ -36,22 +40,48 @@ GPTQ_DEV RowScale row_scale(uint32_t amax_bits, float top) {
   return r;
 }
 
-// the code of x as an fp32 integer
+// the code of xs (times r.mul already) next to the border: t is the product that lies there
 template <int TOP>
-GPTQ_DEV float row_code(float x, const RowScale& r) {
-  if (r.inv == 0.0f) return 0.0f;
-  const float xs = x * r.mul;
-  const float t = xs * r.inv;
-  float q = rintf(t);
-  if (fabsf(t - q) > 0.5f - 0x1p-13f) {
-    const float lo = floorf(fabsf(t));
-    const double a = static_cast<double>(fabsf(xs)) * (2 * TOP);
-    const double b = static_cast<double>(r.amax) * static_cast<double>(2.0f * lo + 1.0f);
-    const bool odd = (static_cast<int>(lo) & 1) != 0;
-    const float m = (a > b || (a == b && odd)) ? lo + 1.0f : lo;
-    q = copysignf(m, t);
+GPTQ_DEV int border_code(float xs, float t, const RowScale& r) {
+  const float lo = floorf(fabsf(t));
+  const double a = static_cast<double>(fabsf(xs)) * (2 * TOP);
+  const double b = static_cast<double>(r.amax) * static_cast<double>(2.0f * lo + 1.0f);
+  const bool odd = (static_cast<int>(lo) & 1) != 0;
+  const float m = (a > b || (a == b && odd)) ? lo + 1.0f : lo;
+  return static_cast<int>(copysignf(m, t));
+}
+
+// the codes of eight values, plus BIAS, as bytes of two words
+template <int TOP, int BIAS>
+GPTQ_DEV void row_codes(const float (&x)[8], const RowScale& r, uint32_t (&w)[2]) {
+  constexpr float kMagic = 12582912.f + BIAS;  // 3 2^22
+  float v[8], t[8], most = 0.f;
+  uint32_t f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = x[i];
+  if (r.mul != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= r.mul;
   }
-  return q;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    t[i] = v[i] * r.inv;
+    const float s = t[i] + kMagic;
+    f[i] = __float_as_uint(s);
+    most = fmaxf(most, fabsf(t[i] - (s - kMagic)));
+  }
+  constexpr float kNear = 0.5f - 0x1p-15f;
+  if (most > kNear) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(t[i] - (__uint_as_float(f[i]) - kMagic)) > kNear)
+        f[i] = static_cast<uint32_t>(border_code<TOP>(v[i], t[i], r) + BIAS);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = __builtin_amdgcn_perm(f[4 * i + 1], f[4 * i], 0x0C0C0400u) |
+           __builtin_amdgcn_perm(f[4 * i + 3], f[4 * i + 2], 0x04000C0Cu);
+  if (r.inv == 0.0f) w[0] = w[1] = static_cast<uint32_t>(BIAS) * 0x01010101u;  // zeros, or not finite
 }
 
 // max over the lanes l ^ 1, ... of a group of N lanes (N a power of two up to 64)
