@@ -433,12 +433,12 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64
  * entry outside [0, n_pages) count as hidden, so no value in these arrays leads
  * outside the buffers.  A key or value with a NaN scale makes the tokens that
  * see it NaN.
- * Products and sums are fp32; p_j times the value's scale is rounded to bf16
- * for the second product (relative 2^-9 each).  Deterministic.
+ * Sums and softmax statistics are fp32; weights and values enter the second
+ * product in fp16 (2^-11 relative each, under out's own rounding).  Deterministic.
  *   ws       device workspace of gptq_attention_workspace_size bytes, 256-byte
  *            aligned (results of key splits); may be null when that size is 0
  * Requires n_heads % n_kv_heads == 0, n_tokens * n_heads < 2^30,
- * n_seq <= 2^20, n_seq * n_kv_heads < 2^30 and pages_per_seq * page_size <= 2^30.
+ * n_seq <= 2^20, n_seq * n_kv_heads <= 2^21 and pages_per_seq * page_size <= 2^30.
  */
 size_t gptq_attention_workspace_size(const gptq_cache* cache, int64_t n_tokens, int32_t n_heads, int32_t n_seq,
                                      int64_t pages_per_seq);

@@ -438,10 +438,23 @@ def _on_device(what: str, *ts) -> int:
     return dev
 
 
-def _raw_stream(stream, dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+def _on_stream(stream):
+    """The context in which `stream` is the current one: what a call allocates
+    (outputs, workspace, laid-out copies) then belongs to the stream that uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = _stream(stream)
+        stream = torch.cuda.ExternalStream(raw) if raw else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _row_stride(x: torch.Tensor) -> int:
+    """Of a matrix; that of a single row says nothing.  (One below the row's
+    length, as of an expanded row, is refused by the library.)"""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
 def _type_code(what: str, dtype: torch.dtype) -> int:
@@ -456,6 +469,9 @@ def gptq_quantize_tokens(x: torch.Tensor, codes: Optional[torch.Tensor] = None, 
     """The 8-bit codes of the rows of x [m, d_in] (bf16 or fp32; rows may be
     strided): (codes int8 [m, d_in], scales fp32 [m], sums int32 [m]), the sums
     being those of a row's codes.  gptq_integer_matmul takes the three in x's place."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_quantize_tokens(x, codes, scales, sums)
     what = "gptq_quantize_tokens"
     if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
         raise ValueError(f"{what}: x must be 2-D with unit column stride")
@@ -472,8 +488,8 @@ def gptq_quantize_tokens(x: torch.Tensor, codes: Optional[torch.Tensor] = None, 
             or scales.dtype != torch.float32 or not scales.is_contiguous() or sums.shape != (m,)
             or sums.dtype != torch.int32 or not sums.is_contiguous()):
         raise ValueError(f"{what}: codes, scales and sums must be contiguous int8 [m, d_in], float32 [m] and int32 [m]")
-    _check(_lib().gptq_quantize_tokens(x.data_ptr(), code, m, d, max(x.stride(0), d), codes.data_ptr(), scales.data_ptr(),
-                                       sums.data_ptr(), _raw_stream(stream, dev)), what)
+    _check(_lib().gptq_quantize_tokens(x.data_ptr(), code, m, d, _row_stride(x), codes.data_ptr(), scales.data_ptr(),
+                                       sums.data_ptr(), _raw_stream(dev)), what)
     return codes, scales, sums
 
 
@@ -481,6 +497,9 @@ def gptq_integer_weight(qweight: torch.Tensor, zeros: torch.Tensor, bits: int, s
     """A layer with one group per output channel laid out for
     gptq_integer_matmul: (w int8 [d_out, d_in], offsets int32 [d_out]) with
     W = scale (w - offset).  zeros: [d_out] or [1, d_out] int32."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_integer_weight(qweight, zeros, bits)
     what = "gptq_integer_weight"
     dev = _on_device(what, qweight, zeros)
     if bits not in (2, 3, 4, 8) or qweight.dim() != 2 or (qweight.shape[0] * 32) % bits != 0:
@@ -492,7 +511,7 @@ def gptq_integer_weight(qweight: torch.Tensor, zeros: torch.Tensor, bits: int, s
     w = torch.empty((d_out, d_in), dtype=torch.int8, device=qweight.device)
     offsets = torch.empty(d_out, dtype=torch.int32, device=qweight.device)
     _check(_lib().gptq_integer_weight(_ptr(qweight.contiguous()), _ptr(zeros.contiguous()), int(bits), d_in, d_out,
-                                      _ptr(w), _ptr(offsets), _raw_stream(stream, dev)), what)
+                                      _ptr(w), _ptr(offsets), _raw_stream(dev)), what)
     return w, offsets
 
 
@@ -509,6 +528,9 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
     out by gptq_integer_weight (offsets None: all zero).  x is [m, d_in] bf16 or
     fp32 (rows may be strided), quantized per token on the way, or what
     gptq_quantize_tokens returned for it."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_integer_matmul(x, w, w_scales, offsets, out_dtype, y, ws)
     what = "gptq_integer_matmul"
     x_scales = x_sums = None
     if isinstance(x, tuple):
@@ -545,9 +567,9 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
         need = lib.gptq_integer_workspace_size(m, code, d_in, d_out)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, max(x.stride(0), d_in),
+    _check(lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, _row_stride(x),
                                    w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), d_out, y.data_ptr(), yt, _ptr(ws),
-                                   0 if ws is None else ws.numel(), _raw_stream(stream, dev)), what)
+                                   0 if ws is None else ws.numel(), _raw_stream(dev)), what)
     return y
 
 
@@ -622,6 +644,9 @@ def gptq_cache_write(cache: QuantizedCache, k: torch.Tensor, v: torch.Tensor, sl
     strided, as in a slice of a fused projection) into the cache's slots
     (page * page_size + offset; int64 [n], different from each other; one
     outside the cache is skipped)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_cache_write(cache, k, v, slots)
     what = "gptq_cache_write"
     n = _slots(what, slots)
     code = _type_code(what, k.dtype)
@@ -632,13 +657,16 @@ def gptq_cache_write(cache: QuantizedCache, k: torch.Tensor, v: torch.Tensor, sl
     dev = cache._here(what, k, v, slots)
     ldk, ldv = (sk[0], sv[0]) if n > 1 else (heads * hd, heads * hd)
     _check(_lib().gptq_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), code, n, ldk, ldv, slots.data_ptr(),
-                                   _raw_stream(stream, dev)), what)
+                                   _raw_stream(dev)), what)
 
 
 def gptq_cache_read(cache: QuantizedCache, slots: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                     k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None, stream=None):
     """The values held in the given slots: (k, v), each [n, n_kv_heads,
     head_dim]; zeros for a slot outside the cache."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_cache_read(cache, slots, dtype, k, v)
     what = "gptq_cache_read"
     n = _slots(what, slots)
     shape = (n, cache.n_kv_heads, cache.head_dim)
@@ -649,7 +677,7 @@ def gptq_cache_read(cache: QuantizedCache, slots: torch.Tensor, dtype: torch.dty
         raise ValueError(f"{what}: k and v must be contiguous [n, n_kv_heads, head_dim] of one dtype")
     dev = cache._here(what, slots, k, v)
     _check(_lib().gptq_cache_read(cache._ref, slots.data_ptr(), n, k.data_ptr(), v.data_ptr(), code,
-                                  _raw_stream(stream, dev)), what)
+                                  _raw_stream(dev)), what)
     return k, v
 
 
@@ -667,6 +695,9 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
     kv_lens[i] keys (int32 [n_seq]) and its pages in page_table[i] (int32
     [n_seq, pages_per_seq]).  scale: 1 / sqrt(head_dim) unless given.  Rows of
     out outside the sequences are left as they were."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_cache_attention(q, cache, page_table, q_starts, kv_lens, scale, out, ws)
     what = "gptq_cache_attention"
     hd = cache.head_dim
     if q.dim() != 3 or q.shape[2] != hd or q.dtype != torch.bfloat16:
@@ -699,5 +730,5 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
     _check(lib.gptq_cache_attention(cache._ref, q.data_ptr(), GPTQ_BF16, n, ldq, heads, page_table.data_ptr(), pages,
                                     q_starts.data_ptr(), kv_lens.data_ptr(), n_seq,
                                     hd ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(ws),
-                                    0 if ws is None else ws.numel(), _raw_stream(stream, dev)), what)
+                                    0 if ws is None else ws.numel(), _raw_stream(dev)), what)
     return out

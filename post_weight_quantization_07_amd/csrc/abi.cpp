@@ -305,9 +305,11 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64
 }
 
 namespace {
+// a launch has fewer than 2^32 threads: at most 2^23 tiles of 128 rows, or three
+// per (sequence, key head) of fewer rows, and a workgroup of 256 for each
 bool attention_sizes(const gptq::CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t pages_per_seq) {
   return n_heads >= 1 && n_heads % c.n_kv == 0 && rows_ok(n_tokens) && n_tokens * n_heads < (int64_t{1} << 30) &&
-         n_seq >= 0 && n_seq <= (1 << 20) && int64_t{n_seq} * c.n_kv < (int64_t{1} << 30) && pages_per_seq >= 1 &&
+         n_seq >= 0 && n_seq <= (1 << 20) && int64_t{n_seq} * c.n_kv <= (int64_t{1} << 21) && pages_per_seq >= 1 &&
          pages_per_seq * c.page <= (int64_t{1} << 30);
 }
 }  // namespace

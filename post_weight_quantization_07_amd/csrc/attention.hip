@@ -265,7 +265,7 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 //
 // Bound: HBM, by the loads that fit in flight beside the operands' registers.
 // 64 ragged sequences (292 MB of 8-bit keys and values) 62 us, 4.7 TB/s; four of
-// 131000 keys at 4 bits (570 MB) 143 us, 4.0 TB/s; one of 1000 keys 8.6 us, four
+// 131000 keys at 4 bits (570 MB) 130 us, 4.4 TB/s; one of 1000 keys 8.6 us, four
 // dependent trips to memory.  Four waves a workgroup and four workgroups a CU:
 // eight waves and two took 83 us for the ragged batch.
 constexpr int kSplitWaves = 4;
@@ -287,8 +287,9 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
   if (!find_work<true>(p, u, w)) return;
   const int rows = w.s.n * p.group;
   const int r0 = w.tile * kM;
-  const int first = w.s.len - w.s.n + uniform(div_by(r0, p.group_mul, p.group_shift));                              // last key of the tile's first row
-  const int vis = w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1;       // keys any of its rows sees
+  // last key of the tile's first row, and the keys any of its rows sees
+  const int first = w.s.len - w.s.n + uniform(div_by(r0, p.group_mul, p.group_shift));
+  const int vis = w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1;
   const int units = vis > 0 ? (vis - 1) / kUnit + 1 : 0;
   const int per = (units + w.n_split - 1) / w.n_split;
   const int key0 = w.split * per * kUnit, key1 = min(vis, (w.split + 1) * per * kUnit);
@@ -592,9 +593,10 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 // an exp2 per score, half a conversion and half a sum.
 //
 // Bound: the products, the exponentials and the codes' conversion share the
-// waves' issue slots: a 64-key tile of 128 rows x 128 dims takes about 3740 cycles, of
-// which its products need 2048.  Four prompts of 2048 tokens, 32 heads of 128: 206
-// us (0.67 PFLOP/s of the causal half); long ones come to 0.88 PFLOP/s.
+// waves' issue slots: a 64-key tile of 128 rows x 128 dims takes about 3740 cycles,
+// of which the products of a CU's two workgroups need 2048.  Four prompts of 2048
+// tokens, 32 heads of 128: 206 us (0.67 PFLOP/s of the causal half); long ones come
+// to 0.88 PFLOP/s.
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 1024.f;
 

@@ -716,11 +716,19 @@ hipError_t token_codes_launch(const void* x, bool bf16, int64_t m, int64_t d, in
   const int64_t e = bf16 ? 8 : 4;
   const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7u) == 0 &&
                    ldx % e == 0 && d % 8 == 0;
-  if (d <= 2048) token_codes_go<64, 4>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
-  else if (d <= 8192) token_codes_go<256, 4>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
-  else if (d <= 16384) token_codes_go<256, 8>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
-  else if (d <= 32768) token_codes_go<512, 8>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
-  else token_codes_go<1024, 4>(x, bf16, vec, m, d, ldx, codes, scales, sums, st);
+  constexpr int64_t kMost = int64_t{1} << 21;  // rows of a launch, which has fewer than 2^32 threads
+  for (int64_t r = 0; r < m; r += kMost) {
+    const int64_t n = std::min(m - r, kMost);
+    const void* xr = static_cast<const char*>(x) + r * ldx * (bf16 ? 2 : 4);
+    int8_t* c = codes + r * d;
+    float* sc = scales + r;
+    int32_t* sm = sums ? sums + r : nullptr;
+    if (d <= 2048) token_codes_go<64, 4>(xr, bf16, vec, n, d, ldx, c, sc, sm, st);
+    else if (d <= 8192) token_codes_go<256, 4>(xr, bf16, vec, n, d, ldx, c, sc, sm, st);
+    else if (d <= 16384) token_codes_go<256, 8>(xr, bf16, vec, n, d, ldx, c, sc, sm, st);
+    else if (d <= 32768) token_codes_go<512, 8>(xr, bf16, vec, n, d, ldx, c, sc, sm, st);
+    else token_codes_go<1024, 4>(xr, bf16, vec, n, d, ldx, c, sc, sm, st);
+  }
   return hipGetLastError();
 }
 

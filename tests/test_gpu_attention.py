@@ -297,3 +297,23 @@ def test_some_rows(G, lens, heads, kv, hd, page, bits):
     out = G.gptq_cache_attention(c.q, c.cache, *c.args)
     c.check(out)
     assert torch.equal(out, G.gptq_cache_attention(c.q, c.cache, *c.args))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv", [([(5, 300)], 2, 1), ([(30, 300)], 2, 2), ([(200, 260)], 2, 1)])
+def test_query_that_is_not_finite(G, lens, heads, kv, bits):
+    """NaN and infinity in one token's query reach that token and head only."""
+    banner(f"attention: a query that is not finite, {lens}, int{bits}")
+    c = Case(G, lens, heads, kv, 64, 16, bits, seed=12)
+    want = G.gptq_cache_attention(c.q, c.cache, *c.args)
+    for bad in (float("nan"), float("inf")):
+        q = c.q.clone()
+        q[3, 1, 7] = bad
+        out = G.gptq_cache_attention(q, c.cache, *c.args)
+        assert torch.isnan(out[3, 1]).all()
+        keep = torch.ones(out.shape[:2], dtype=torch.bool, device=dev())
+        keep[3, 1] = False
+        # the others' running maxima may be moved at other tiles: equal up to the bound
+        assert torch.isfinite(out[keep]).all()
+        out[3, 1] = want[3, 1]
+        c.check(out)

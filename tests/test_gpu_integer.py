@@ -204,3 +204,29 @@ def test_many_channels(G, m, d_in, d_out, asym):
     for dtype in (torch.float32, torch.bfloat16):
         y = host(G.gptq_integer_matmul(xq, _d(w), _d(s), _d(off) if asym else None, out_dtype=dtype)).astype(np.float64)
         assert np.all(np.abs(y - ref) <= REL[dtype] * np.abs(ref))
+
+
+def test_more_rows_than_one_launch(G):
+    banner("token codes of 2^21 + 5 rows")
+    r = np.random.default_rng(3)
+    x = to_dev(r.standard_normal((2 ** 21 + 5, 8)).astype(np.float32), "bf16")
+    codes, scales, sums = G.gptq_quantize_tokens(x)
+    rows = np.r_[0:40, 2 ** 20:2 ** 20 + 40, 2 ** 21 - 40:2 ** 21 + 5]
+    ref, sref = S.row_codes(host(x[rows]), 127)
+    np.testing.assert_array_equal(codes[rows].cpu().numpy(), ref)
+    np.testing.assert_array_equal(scales[rows].cpu().numpy(), sref)
+    np.testing.assert_array_equal(sums[rows].cpu().numpy(), ref.sum(axis=1))
+
+
+def test_expanded_rows_are_refused(G):
+    """Rows that overlap have no row stride the kernels can use."""
+    banner("integer product: expanded rows")
+    x = torch.randn(1, 64, device=dev()).to(torch.bfloat16)
+    w, s = torch.ones(8, 64, dtype=torch.int8, device=dev()), torch.ones(8, device=dev())
+    for m in (3, 80):
+        with pytest.raises(G.GptqError):
+            G.gptq_quantize_tokens(x.expand(m, 64))
+        with pytest.raises(G.GptqError):
+            G.gptq_integer_matmul(x.expand(m, 64), w, s)
+    wide = torch.randn(1, 200, device=dev()).to(torch.bfloat16)[:, 8:72]        # one row of a wider matrix is fine
+    assert torch.equal(G.gptq_integer_matmul(wide, w, s), G.gptq_integer_matmul(wide.contiguous(), w, s))

@@ -231,3 +231,43 @@ def test_serve(G, bits):
     kc, ks, vc, vs = (np.concatenate(t) for t in held[3])
     np.testing.assert_array_equal(k.cpu().numpy(), kc.astype(np.float32) * ks[..., None])
     np.testing.assert_array_equal(v.cpu().numpy(), vc.astype(np.float32) * vs[..., None])
+
+
+def test_memory_of_another_stream(G):
+    """What a call on a given stream allocates is that stream's: memory that the
+    current stream has freed but still reads is not handed to it."""
+    banner("serving calls on a stream, with work pending on the current one")
+    big = torch.randn(4096, 4096, device=dev())
+    x = torch.randn(300, 1024, device=dev()).to(torch.bfloat16)
+    w, s = torch.ones(512, 1024, dtype=torch.int8, device=dev()), torch.ones(512, device=dev())
+    cache = G.QuantizedCache.empty(64, 64, 4, 64, 8, dev())
+    slots = torch.arange(4096, device=dev())
+    kv = torch.randn(4096, 4, 64, device=dev()).to(torch.bfloat16)
+    G.gptq_cache_write(cache, kv, kv, slots)
+    table, starts = torch.arange(64, dtype=torch.int32, device=dev()).view(1, 64), torch.tensor([0, 1], dtype=torch.int32)
+    q, args = kv[:1], (table, starts.to(dev()), torch.tensor([4096], dtype=torch.int32, device=dev()))
+    calls = {"tokens": lambda **k: G.gptq_quantize_tokens(x, **k), "product": lambda **k: G.gptq_integer_matmul(x, w, s, **k),
+             "read": lambda **k: G.gptq_cache_read(cache, slots, **k),
+             "attention": lambda **k: G.gptq_cache_attention(q, cache, *args, **k)}
+    want = {n: c() for n, c in calls.items()}
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for name, call in calls.items():
+        outs = want[name] if isinstance(want[name], tuple) else (want[name],)
+        held = [torch.full_like(t, 1) for t in outs]        # as large as what the call allocates
+        torch.cuda.synchronize()
+        y = big
+        for _ in range(20):                                  # the current stream is busy
+            y = y @ big
+        seen = [t.clone() for t in held]                     # and reads them later
+        del held
+        got = call(stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        for t in seen:
+            assert (t == 1).all(), name
+        for a, b in zip(got if isinstance(got, tuple) else (got,), outs):
+            assert torch.equal(a, b), name
+    got = G.gptq_integer_matmul(x, w, s, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, want["product"])

@@ -169,3 +169,13 @@ def test_integer_layer_refuses_groups():
          "g_idx": torch.arange(256, dtype=torch.int32) // 128}
     with pytest.raises(ValueError, match="one group per output channel"):
         integer_layer(r, 4)
+
+
+def test_attention_refuses_too_many_sequences(L):
+    """A launch is limited to 2^21 (sequence, key head) pairs."""
+    lib, ref, wide = L._lib(), ctypes.byref(_cache(L)), ctypes.byref(_cache(L, n_kv_heads=4))
+    assert lib.gptq_attention_workspace_size(ref, 4, 8, 1 << 20, 64) > 0          # 2 key heads
+    assert lib.gptq_attention_workspace_size(wide, 4, 8, 1 << 19, 64) > 0
+    assert lib.gptq_attention_workspace_size(wide, 4, 8, 1 << 20, 64) == 0
+    assert lib.gptq_cache_attention(wide, FAKE, 1, 4, 1 << 20, 8, FAKE, 4, FAKE, FAKE, 1 << 20, 0.1, FAKE, 1 << 20, FAKE,
+                                    1 << 40, None) == 1
