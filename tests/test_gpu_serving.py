@@ -271,3 +271,29 @@ def test_memory_of_another_stream(G):
     got = G.gptq_integer_matmul(x, w, s, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(got, want["product"])
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_cache_past_32_bits(G, bits):
+    """Pages whose bytes lie past 2^32 give what the same pages give in a small cache."""
+    banner(f"a cache of more than 2^32 bytes, int{bits}")
+    kv, hd, page, length = 8, 256, 256, 700
+    n_pages = 2 ** 32 // (kv * page * hd * bits // 8) + 40
+    r = torch.Generator(device="cuda").manual_seed(bits)
+    k, v = (torch.randn(length, kv, hd, generator=r, device=dev()).to(torch.bfloat16) for _ in range(2))
+    tok = torch.arange(length, device=dev())
+
+    def held(n, pages):
+        cache = G.QuantizedCache.empty(n, page, kv, hd, bits, dev())
+        table = torch.tensor([pages], dtype=torch.int32, device=dev())
+        slots = table[0].long()[tok // page] * page + tok % page
+        G.gptq_cache_write(cache, k, v, slots)
+        out = [*G.gptq_cache_read(cache, slots)]
+        for new in (1, 20, 300):                        # one row block, two, and tiles of 128
+            q = torch.randn(new, kv, hd, generator=torch.Generator(device="cuda").manual_seed(new), device=dev())
+            starts = torch.tensor([0, new], dtype=torch.int32, device=dev())
+            lens = torch.tensor([length], dtype=torch.int32, device=dev())
+            out.append(G.gptq_cache_attention(q.to(torch.bfloat16), cache, table, starts, lens))
+        return out
+    for a, b in zip(held(4, [2, 0, 3]), held(n_pages, [n_pages - 1, 1, n_pages - 3])):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
