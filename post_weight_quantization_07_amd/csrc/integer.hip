@@ -423,10 +423,7 @@ void stream_go(const IntParams& p, int fused, hipStream_t st) {
   else if (fused == 2) integer_stream_kernel<R, 1, 2><<<grid, t, 0, st>>>(p);
   else if (p.m <= 16) integer_stream_kernel<R, 1, 0><<<grid, t, 0, st>>>(p);
   else if (p.m <= 32) integer_stream_kernel<R, 2, 0><<<grid, t, 0, st>>>(p);
-  else {  // four token blocks leave registers for two row blocks
-    constexpr int r = R > 2 ? 2 : R;
-    integer_stream_kernel<r, 4, 0><<<dim3(static_cast<unsigned>((p.d_out + 16 * r - 1) / (16 * r))), t, 0, st>>>(p);
-  }
+  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0><<<dim3(grid.x, static_cast<unsigned>((p.m + 63) / 64)), t, 0, st>>>(p);
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
@@ -686,6 +683,31 @@ __global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid
   }
 }
 
+// few tokens of few values: quantized by every workgroup of the stream kernel itself
+bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; }
+
+// row blocks a workgroup of the stream kernel takes: as many as leave every CU one
+int stream_rows(int64_t m, int64_t d_out, int n_cu) {
+  const int r = d_out >= 64ll * n_cu ? 4 : d_out >= 32ll * n_cu ? 2 : 1;
+  return m > 32 ? std::min(r, 2) : r;
+}
+
+// The stream kernel reads the weights with less ado than the tiles do, but a
+// workgroup's turns also load its tokens' codes.  What that costs, fitted to
+// both kernels' times over 2 to 512 tokens and weights of 512 x 512 to
+// 28672 x 8192: 1 us and 31 ps a token (of its padded block) and k, for each
+// round of workgroups; against it the tiles' prologue, slices and join, 9.1 us and
+// 65 ns per MB of weights.  (us, stream and tiles: 64 x 4096 -> 4096 14.0, 14.8;
+// 100 of them 20.6, 15.8; 64 x 11008 -> 4096 30.7, 25.2; 24 of them 17.4, 22.9;
+// 64 x 28672 -> 1024 71, 22; 256 x 2048 -> 2048 12.4, 13.5; 512 x 512 -> 512 4.4, 7.6.)
+bool streams(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
+  if (fuses(m, d_in)) return true;
+  const int64_t rows = 16 * stream_rows(m, d_out, n_cu), pad = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  const double blocks = static_cast<double>((d_out + rows - 1) / rows) * static_cast<double>((m + 63) / 64);
+  const double extra = std::max(1.0, blocks / n_cu) * (1.0 + 31e-6 * static_cast<double>(pad * d_in));
+  return extra <= 9.1 + 6.5e-8 * static_cast<double>(d_in) * static_cast<double>(d_out);
+}
+
 // The launch of a product: kernel, tile and K slices.
 struct IntPlan {
   int kind;  // 0: stream, 1: 128 x 128 tiles, 2: 256 x 256
@@ -695,9 +717,13 @@ struct IntPlan {
 
 IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   IntPlan a{0, 1, 0, 0};
-  if (m <= 64) return a;
+  if (streams(m, d_in, d_out, n_cu)) return a;
+  // 256 x 256 tiles where they give more than half the CUs one, or where K is
+  // long enough for slices of 2048 that do (1024 x 11008 -> 4096 in four slices: 70 us, 88
+  // in 128 x 128 tiles; 2048 x 28672 -> 1024 in eight: 82 and 105; but 1024 x 1024 -> 4096: 23
+  // and 11; 509 x 11008 -> 4096 with its codes and join, in eight slices of 1376: 53.2 and 52.0)
   const int64_t t256 = ((m + 255) / 256) * ((d_out + 255) / 256), t128 = ((m + 127) / 128) * ((d_out + 127) / 128);
-  a.kind = t256 >= n_cu / 2 + 1 ? 2 : 1;
+  a.kind = t256 > n_cu / 2 || (d_in >= 8192 && m > 128 && t256 * 8 >= n_cu && t256 * d_in >= 2048ll * n_cu) ? 2 : 1;
   const int64_t tiles = a.kind == 2 ? t256 : t128;
   const int steps = static_cast<int>((d_in + kTStep - 1) / kTStep);
   const int64_t room = a.kind == 2 ? n_cu : 2 * n_cu;
@@ -746,8 +772,6 @@ void tile_go(const IntParams& p, const TileGrid& g, unsigned blocks, hipStream_t
   else if (p.y_bf16) integer_tile_kernel<WM, WN, kOutBf16><<<blocks, 256, 0, st>>>(p, g);
   else integer_tile_kernel<WM, WN, kOutF32><<<blocks, 256, 0, st>>>(p, g);
 }
-// few tokens of few values: quantized by every workgroup of the stream kernel itself
-bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; }
 size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
 }  // namespace
 
@@ -804,8 +828,9 @@ hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, c
                                 static_cast<size_t>(m * (d_in + 16)), st>>>(p);
       return hipGetLastError();
     }
-    if (d_out >= 64ll * n_cu) stream_go<4>(p, f, st);
-    else if (d_out >= 32ll * n_cu) stream_go<2>(p, f, st);
+    const int r = stream_rows(m, d_out, n_cu);
+    if (r == 4) stream_go<4>(p, f, st);
+    else if (r == 2) stream_go<2>(p, f, st);
     else stream_go<1>(p, f, st);
     return hipGetLastError();
   }

@@ -230,3 +230,29 @@ def test_expanded_rows_are_refused(G):
             G.gptq_integer_matmul(x.expand(m, 64), w, s)
     wide = torch.randn(1, 200, device=dev()).to(torch.bfloat16)[:, 8:72]        # one row of a wider matrix is fine
     assert torch.equal(G.gptq_integer_matmul(wide, w, s), G.gptq_integer_matmul(wide.contiguous(), w, s))
+
+
+@pytest.mark.parametrize("m,d_in,d_out", [(515, 1056, 2049), (1030, 8224, 1800), (1030, 16384, 1800), (140, 4096, 1000),
+                                        (70, 32768, 50)])
+@pytest.mark.parametrize("asym,xt,yt", [(True, "bf16", torch.float32), (False, "f32", torch.bfloat16)])
+def test_tiles(G, m, d_in, d_out, asym, xt, yt):
+    """Tiles of both sizes, with K slices and without, at sizes that end inside a tile."""
+    test_product(G, m, d_in, d_out, asym, xt, yt)
+
+
+def test_graph_with_slices(G):
+    banner("integer product in K slices, replayed with new inputs")
+    w, s, off = _layer(300, 4128, 6, True)
+    dw, ds, doff = _d(w), _d(s), _d(off)
+    xs = [torch.randn(150, 4128, device=dev()).to(torch.bfloat16) for _ in range(3)]
+    want = [G.gptq_integer_matmul(x, dw, ds, doff) for x in xs]
+    hold, graph = xs[0].clone(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = G.gptq_integer_matmul(hold, dw, ds, doff)
+    for i in (1, 2, 0, 1):
+        hold.copy_(xs[i])
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[i])
+        G.gptq_integer_matmul(xs[i], dw, ds, doff)          # eager work between the replays

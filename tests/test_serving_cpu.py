@@ -179,3 +179,13 @@ def test_attention_refuses_too_many_sequences(L):
     assert lib.gptq_attention_workspace_size(wide, 4, 8, 1 << 20, 64) == 0
     assert lib.gptq_cache_attention(wide, FAKE, 1, 4, 1 << 20, 8, FAKE, 4, FAKE, FAKE, 1 << 20, 0.1, FAKE, 1 << 20, FAKE,
                                     1 << 40, None) == 1
+
+
+def test_integer_workspace_follows_the_kernel(L):
+    """K slices take their sums' space, also where the codes are given; nothing for products in one piece."""
+    size = L._lib().gptq_integer_workspace_size
+    assert size(1, 1, 4096, 4096) == 0 and size(4, 1, 4096, 100) == 0             # quantized on the way
+    assert size(16, 2, 8192, 28672) == 0 and size(512, 2, 512, 512) == 0
+    assert size(70, 2, 32768, 50) >= 2 * 70 * 50 * 4 and size(1030, 2, 8224, 1800) >= 2 * 1030 * 1800 * 4
+    for m, d_in, d_out in ((1, 32, 1), (5, 4096, 64), (600, 4096, 512), (2048, 28672, 8192), (1 << 20, 32, 1)):
+        assert size(m, 1, d_in, d_out) >= size(m, 2, d_in, d_out)
