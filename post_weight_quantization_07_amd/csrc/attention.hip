@@ -50,7 +50,8 @@ struct AttnParams {
   int32_t tile_rows, tile_shift;    // M, a power of two
   int32_t max_len;                  // keys that a row of the table can name
   float inv_target;                 // n_kv / the workgroups the keys are split for
-  float min_units;                  // fewest units of a split
+  float min_units;                  // fewest units of a split,
+  float few;                        // or two while there are no more (tile, unit) pairs than this
   uint32_t group_mul, group_shift;  // division by group
   uint32_t kv_mul, kv_shift;        // division by n_kv
   float scale_log2e;
@@ -129,7 +130,7 @@ GPTQ_DEV bool find_work(const AttnParams& p, int u, Work& w) {
     if (i0 + lane < p.n_seq) s = seq_info(p, i0 + lane);
     total += lane_value(wave_scan(static_cast<float>(s.tiles) * static_cast<float>(s.units)), 63);
   }
-  const float inv_per = 1.f / fmaxf(total * p.inv_target, p.min_units);
+  const float inv_per = 1.f / fmaxf(total * p.inv_target, total <= p.few ? 2.f : p.min_units);
   int base = 0, slots = 0;
   for (int i0 = 0; i0 < p.n_seq; i0 += 64) {
     if (p.n_seq > 64) {
@@ -1150,7 +1151,11 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   // split kernel: a little under the workgroups that fit (four a CU, two for wide
   // heads or two row blocks), so that few are left for a second round
   a.target = a.tile_rows == 16 && c.hd <= 128 ? 3 * n_cu : 2 * n_cu;
+  // four units a split, one turn or two of a wave, so that there are few parts to
+  // join; two where that gives no CU a second workgroup (one token, 1000 keys, 32
+  // key heads: 10.7 us in fours, 9.4 in twos; 8000 keys, 8 key heads: 13.1 and 15.9)
   a.min_units = 4;
+  a.few = a.tile_rows == 128 ? 0 : 2 * n_cu / c.n_kv;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
   a.joins = tiles * c.n_kv;
   a.blocks = a.joins + a.target + 64;  // 64: the split is decided in fp32
@@ -1158,6 +1163,7 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   const int64_t most = (ld_table * c.page + kUnit - 1) / kUnit;
   if (most <= a.min_units) {
     a.joins = 0;
+    a.few = 0;
     a.blocks = tiles * c.n_kv;
   } else {
     a.joins = std::min(a.joins, static_cast<int64_t>(a.target) + 64);  // tiles of two parts and more
@@ -1198,6 +1204,7 @@ hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const voi
   p.max_len = static_cast<int32_t>(ld_table * c.page);
   p.inv_target = static_cast<float>(c.n_kv) / static_cast<float>(plan.target);
   p.min_units = static_cast<float>(plan.min_units);
+  p.few = static_cast<float>(plan.few);
   exact_divisor(p.group, &p.group_mul, &p.group_shift);
   exact_divisor(p.n_kv, &p.kv_mul, &p.kv_shift);
   p.scale_log2e = scale * 1.4426950408889634f;

@@ -167,6 +167,7 @@ hipError_t cache_read_launch(const CacheShape& c, const void* kc, const void* vc
 struct AttnPlan {
   int tile_rows;          // rows (token, head of the group) of a tile
   int target, min_units;  // how the keys are split
+  int few;                // (tile, unit) pairs that are split finer
   int64_t blocks, joins;  // workgroups of the two kernels; joins 0: nothing can be split
   int64_t slots;          // partial results
   size_t ws_bytes;
