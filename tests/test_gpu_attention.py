@@ -317,3 +317,15 @@ def test_query_that_is_not_finite(G, lens, heads, kv, bits):
         assert torch.isfinite(out[keep]).all()
         out[3, 1] = want[3, 1]
         c.check(out)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", [([(200, 50), (150, 0), (130, 1), (140, 139), (129, 64)], 2, 1, 64, 16),
+                                                   ([(300, 299), (260, 3)], 1, 1, 128, 64), ([(40, 7), (33, 0)], 1, 1, 32, 16)])
+def test_more_tokens_than_keys(G, lens, heads, kv, hd, page, bits):
+    """Whole tiles of rows that see no key: zeros, in each kernel."""
+    banner(f"attention: fewer keys than tokens {lens} int{bits}")
+    c = Case(G, lens, heads, kv, hd, page, bits, seed=13)
+    out = torch.full((c.total, heads, hd), 7.0, dtype=torch.bfloat16, device=dev())
+    G.gptq_cache_attention(c.q, c.cache, *c.args, out=out)
+    c.check(out)
