@@ -420,7 +420,8 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64
  * tokens; new token t of n sees the keys 0 .. kv_lens[i] - n + t:
  *   out = sum_j p_j v_j,  p = softmax_j(scale q . k_j),  k_j, v_j the held values
  * Query head h reads key head h / (n_heads / n_kv_heads).  One new token per
- * sequence is decoding, n = kv_len a whole prompt; both may stand in one call.
+ * sequence is decoding, n = kv_len a whole prompt; both may stand in one call
+ * (many single tokens beside long prompts are faster in a call of their own).
  *   q        token t, head h at element t * ldq + h * head_dim, bf16 (qt
  *            GPTQ_BF16), 16-byte aligned, ldq % 8 == 0; out likewise with ldo
  *   page_table  [n_seq, pages_per_seq] int32: page of keys page_size * j ..
