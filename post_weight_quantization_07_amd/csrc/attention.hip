@@ -265,8 +265,8 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 // l % 16, dims g HDP / 4 ... in order.
 //
 // Bound: HBM, by the loads that fit in flight beside the operands' registers.
-// 64 ragged sequences (292 MB of 8-bit keys and values) 62 us, 4.7 TB/s; four of
-// 131000 keys at 4 bits (570 MB) 130 us, 4.4 TB/s; one of 1000 keys 8.6 us, four
+// 64 ragged sequences (292 MB of 8-bit keys and values) 59 us, 4.9 TB/s; four of
+// 131000 keys at 4 bits (570 MB) 130 us, 4.4 TB/s; one of 1000 keys 6.5 us, four
 // dependent trips to memory.  Four waves a workgroup and four workgroups a CU:
 // eight waves and two took 83 us for the ragged batch.
 constexpr int kSplitWaves = 4;
@@ -540,6 +540,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
     for (int e = threadIdx.x; e < 16 * HDP / 4; e += 64 * NW) {
       const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
       const int r = r0 + 16 * i + row;
+      if (r >= rows || d >= p.hd) continue;  // nor does the join read the others
       float t2 = kNegInf;
 #pragma unroll
       for (int v = 0; v < NW; ++v) t2 = fmaxf(t2, wm[v][16 * i + row]);
@@ -559,7 +560,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
           part[kM * HDP + 16 * i + row] = t2;
           part[kM * HDP + kM + 16 * i + row] = sum;
         }
-      } else if (r < rows && d < p.hd) {
+      } else {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int tok = div_by(r, p.group_mul, p.group_shift);
         const uint2 b = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
@@ -1020,6 +1021,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   l += __shfl_xor(l, 32);
   const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const float up = vr.up();
+  if (!live) return;  // the join does not read such rows either
   if (w.n_split > 1) {
     if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(p.max_slots)) return;
     float* part = p.partial + slot * (kM * (HDP + 2));
@@ -1039,7 +1041,6 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       }
     return;
   }
-  if (!live) return;
   const float inv = l == 0.f ? 0.f : up / l;
   uint16_t* dst = p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(h * p.group + qh) * p.hd;
 #pragma unroll
@@ -1145,8 +1146,8 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   // 4096 keys, 32 rows: 83 us in tiles of 16, 69 in tiles of 32; 48 rows over 2000
   // keys: 13.4 us, 18.4 in tiles of 128; at 64 rows over 4096 keys 57.8 and 57.3).
   // A batch that mixes the two goes by the average: 32 single tokens over 4096 keys
-  // with a prompt of 1024 take 147 us, 56 and 43 in two calls; a launch of each kernel
-  // for every batch would cost the ones of one kind about 4 us.
+  // with a prompt of 1024 take 147 us, 56 and 43 in two calls; launching both kernels
+  // for every batch would cost short prompts two launches that find nothing.
   // Heads wider than 128 have no registers for the second block (256 wide, over
   // 4096 keys: 32 rows 148 us in tiles of 16, 278 in tiles of 128; 64 rows 109 and 168).
   const int64_t per_seq = (n_tokens * group + n_seq - 1) / n_seq;
@@ -1156,7 +1157,7 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   a.target = a.tile_rows == 16 && c.hd <= 128 ? 3 * n_cu : 2 * n_cu;
   // four units a split, one turn or two of a wave, so that there are few parts to
   // join; two where that gives no CU a second workgroup (one token, 1000 keys, 32
-  // key heads: 10.7 us in fours, 9.4 in twos; 8000 keys, 8 key heads: 13.1 and 15.9)
+  // key heads: 10.4 us in fours, 9.0 in twos; 8000 keys, 8 key heads: 12.7 and 15.4)
   a.min_units = 4;
   a.few = a.tile_rows == 128 ? 0 : 2 * n_cu / c.n_kv;
   const int64_t tiles = (n_tokens * group) / a.tile_rows + std::min<int64_t>(n_seq, n_tokens);
