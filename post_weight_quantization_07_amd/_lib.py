@@ -478,16 +478,15 @@ def gptq_quantize_tokens(x: torch.Tensor, codes: Optional[torch.Tensor] = None, 
     code = _type_code(what, x.dtype)
     dev = _on_device(what, x, codes, scales, sums)
     m, d = x.shape
-    if codes is None:
-        codes = x.new_empty((m, d), dtype=torch.int8)
-    if scales is None:
-        scales = x.new_empty(m, dtype=torch.float32)
-    if sums is None:
-        sums = x.new_empty(m, dtype=torch.int32)
-    if (codes.shape != (m, d) or codes.dtype != torch.int8 or not codes.is_contiguous() or scales.shape != (m,)
-            or scales.dtype != torch.float32 or not scales.is_contiguous() or sums.shape != (m,)
-            or sums.dtype != torch.int32 or not sums.is_contiguous()):
-        raise ValueError(f"{what}: codes, scales and sums must be contiguous int8 [m, d_in], float32 [m] and int32 [m]")
+
+    def place(t, shape, dtype):
+        if t is None:
+            return x.new_empty(shape, dtype=dtype)
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{what}: codes, scales and sums must be contiguous int8 [m, d_in], float32 [m] and "
+                             "int32 [m]")
+        return t
+    codes, scales, sums = place(codes, (m, d), torch.int8), place(scales, (m,), torch.float32), place(sums, (m,), torch.int32)
     _check(_lib().gptq_quantize_tokens(x.data_ptr(), code, m, d, _row_stride(x), codes.data_ptr(), scales.data_ptr(),
                                        sums.data_ptr(), _raw_stream(dev)), what)
     return codes, scales, sums

@@ -1055,9 +1055,13 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
 }
 
 // Joins the splits of a tile, in their order.  One workgroup per (split tile, key
-// head); the other tiles were written by the kernels above.
+// head) and 32 rows; the other tiles were written by the kernels above.
 // Latency of the parts' loads bounds it: eight parts are in flight at a time
-// (32 tiles of 25 parts: 6.9 us; 16.4 us one at a time).
+// (32 tiles of 25 parts: 6.9 us; 16.4 us one at a time), and a tile of 128 rows
+// goes to four workgroups (11 sequences of 80 to 160 rows over 3600 to 18000 keys, 3
+// heads: 10.6 us, 32.9 in one; eight workgroups 7.7, but 2 us more where nothing is split).
+constexpr int kJoinRows = 32;
+
 template <int HDP>
 __global__ __launch_bounds__(512) void attn_join_kernel(AttnParams p) {
   constexpr int kAt = 8;
@@ -1071,8 +1075,9 @@ __global__ __launch_bounds__(512) void attn_join_kernel(AttnParams p) {
   if (slot0 < 0 || slot0 + static_cast<int64_t>(w.n_split - 1) * p.n_kv >= p.max_slots) return;
   const int64_t step = static_cast<int64_t>(p.n_kv) * (kM * (HDP + 2));
   const float* part = p.partial + slot0 * (kM * (HDP + 2));
-  for (int e = threadIdx.x; e < kM * HDP / 4; e += 512) {
-    const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
+  const int row0 = static_cast<int>(blockIdx.y) * kJoinRows;
+  for (int e = threadIdx.x; e < min(kM, kJoinRows) * HDP / 4; e += 512) {
+    const int row = row0 + e / (HDP / 4), d = (e % (HDP / 4)) * 4;
     const int r = r0 + row;
     if (r >= rows || d >= p.hd) continue;
     float top = kNoMax, sum = 0.f;
@@ -1133,7 +1138,7 @@ void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t s
   if (p.tile_rows == 128) attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p);
   else if (HDP <= 128 && p.tile_rows == 32) attn_split_kernel<HDP, BITS, HDP <= 128 ? 2 : 1><<<blocks, t, 0, st>>>(p);
   else attn_split_kernel<HDP, BITS, 1><<<blocks, t, 0, st>>>(p);
-  if (joins) attn_join_kernel<HDP><<<joins, 512, 0, st>>>(p);
+  if (joins) attn_join_kernel<HDP><<<dim3(joins, (p.tile_rows + kJoinRows - 1) / kJoinRows), 512, 0, st>>>(p);
 }
 
 }  // namespace
