@@ -292,10 +292,7 @@ def _plain_attention(st):
 
 
 def _cache_of(G, st):
-    """The cache's handle, made once from the buffers in hand, as a program that serves from it keeps it."""
-    if "handle" not in st:
-        st["handle"] = G.QuantizedCache(st["codes"][0], st["codes"][1], st["scales"][0], st["scales"][1], st["bits"])
-    return st["handle"]
+    return G.QuantizedCache(st["codes"][0], st["codes"][1], st["scales"][0], st["scales"][1], st["bits"])
 
 
 def run(state):
