@@ -18,9 +18,11 @@
 // and kv_lens with a scan by one wave (find_work).
 #include "gptq_common.h"
 #include "gptq_internal.h"
+#include "key_lanes.h"
 #include "quant_row.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gptq {
 namespace {
@@ -29,6 +31,7 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __attribute__((__vector_size__(4 * sizeof(short)))) short s16x4_t;
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef u32x4_t u32x4_at8_t __attribute__((aligned(8)));
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
 
 constexpr float kNegInf = -__builtin_inff();
@@ -273,7 +276,8 @@ constexpr int kSplitWaves = 4;
 
 template <int HDP, int BITS, int MT>
 __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) void attn_split_kernel(AttnParams p) {
-  constexpr int kKW = HDP * BITS / 128;        // words of K a lane holds per key: HDP / 4 dims
+  using K = KeyLanes<HDP, BITS>;
+  constexpr int kKW = K::kWords;               // words of K a lane holds per key: HDP / 4 dims
   constexpr int kVB = HDP * BITS / 128;        // bytes of V a lane holds per key: HDP / 16 dims
   constexpr int kVW = (kVB + 3) / 4;
   constexpr int kSteps = HDP / 32;             // products of a 16-key score tile
@@ -310,9 +314,9 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
     float sum = 0.f;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const int d = g * (HDP / 4) + 8 * s;
+      const int d = K::q_dim(g, s, p.hd);
       u32x4_t v = {0u, 0u, 0u, 0u};
-      if (live && d < p.hd) v = *reinterpret_cast<const u32x4_t*>(src + d);
+      if (live && d >= 0) v = *reinterpret_cast<const u32x4_t*>(src + d);
       if (BITS == 4) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum += __uint_as_float(v[e] << 16) + __uint_as_float(v[e] & 0xFFFF0000u);
@@ -340,15 +344,12 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
   const int row_bytes = p.hd * BITS / 8;
   const int page_mask = (1 << p.page_shift) - 1;
   const int32_t* table = p.table + static_cast<int64_t>(w.seq) * p.ld_table;
-  // a lane whose dims lie past head_dim reads the row's first ones instead: q is
-  // zero there, and what V gives there is not stored
-  constexpr int kKL = kKW < 4 ? kKW : 4;  // words of one K load
-  uint32_t koff[kKW / kKL], voff;
+  constexpr int kKL = K::kLoad;
+  using k_vec_t = std::conditional_t<K::kAlign == 16, u32x4_t, u32x4_at8_t>;
+  uint32_t koff[K::kLoads], voff;
 #pragma unroll
-  for (int e = 0; e < kKW / kKL; ++e) {
-    const int d = g * (HDP / 4) + e * kKL * (32 / BITS);
-    koff[e] = static_cast<uint32_t>(c * row_bytes + (d < p.hd ? d * BITS / 8 : 0));
-  }
+  for (int e = 0; e < K::kLoads; ++e) koff[e] = static_cast<uint32_t>(c * row_bytes + K::begin(g, e, p.hd) * BITS / 8);
+  // of V too a lane whose dims lie past head_dim reads the row's first ones: what it gives is not stored
   voff = static_cast<uint32_t>(4 * g * row_bytes + (c * (HDP / 16) < p.hd ? c * kVB : 0));
   for (int k0 = key0 + 32 * wave; k0 < key1; k0 += 32 * NW) {
     uint32_t kw[2][kKW], vw[kVW][8];
@@ -362,9 +363,9 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       const int64_t row = ((static_cast<int64_t>(ok[b] ? page : 0) * p.n_kv + h) << p.page_shift) + (k & page_mask);
       const uint8_t* kp = p.codes[0] + row * row_bytes;
 #pragma unroll
-      for (int e = 0; e < kKW / kKL; ++e) {
+      for (int e = 0; e < K::kLoads; ++e) {
         if (kKL == 4) {
-          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(kp + koff[e]);
+          const u32x4_t v = *reinterpret_cast<const k_vec_t*>(kp + koff[e]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) kw[b][(4 * e + j) % kKW] = v[j];
         } else {
