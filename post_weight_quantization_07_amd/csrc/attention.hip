@@ -35,7 +35,7 @@ typedef u32x4_t u32x4_at8_t __attribute__((aligned(8)));
 typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16_t;
 
 constexpr float kNegInf = -__builtin_inff();
-constexpr float kNoMax = -1e30f;  // running maximum before any key: finite, so that differences stay defined
+constexpr float kNoMax = -3.402823466e38f;  // running maximum before any key: below every score, and finite, so that differences stay defined
 constexpr int kUnit = 64;  // keys per unit of the work split
 
 struct AttnParams {
@@ -602,6 +602,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 // to 0.88 PFLOP/s.
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 1024.f;
+constexpr float kFar = 0x1p20f;  // maxima past this leave the plain tile: see careful_tile
 
 // what a thread holds of a tile on its way: its dims of one key or of one value
 template <int HDP, int BITS>
@@ -811,6 +812,10 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   // the first tile of a workgroup, the last ones of causal rows and wherever
   // the plain tile below finds that it does not fit.  half 1: its first 32
   // keys are done already.
+  // The plain tile's s sk - m is one multiply-add, whose product is not rounded as
+  // m was: off by 2^-24 |m|.  Rows whose maximum lies past +-2^20 (or that have none)
+  // stay here, where equal scores give equal weights at any magnitude.
+  bool far = true;
   auto careful_tile = [&](int base, int buf, uint64_t shown, int half, int range) {
     const int rel = lim - base - 4 * hf;
     auto seen = [&](int b, int e) {  // element e of block b: key 32 b + 8 (e / 4) + 4 hf + e % 4
@@ -849,6 +854,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
     mx = fmaxf(mx, __shfl_xor(mx, 32));
     const float fm = fast_exp2(m - mx);
     m = mx;
+    far = __any(fabsf(m) > kFar);
     l *= fm;
     f *= fm;
 #pragma unroll
@@ -903,7 +909,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       half = 0;
       keys_done = false;
       range = vr_next.e;  // the one this tile's values were written in (the next tile's may be wider)
-      fits = base > key0 && base + kKeys - 1 <= wfirst && shown == ~uint64_t{0} && range == vr.e;
+      fits = base > key0 && base + kKeys - 1 <= wfirst && shown == ~uint64_t{0} && range == vr.e && !far;
       if (!fits) break;
       // The plain tile: every key seen, the maximum and the range as they were.
       // Four groups of products, each with arithmetic between them that does not
