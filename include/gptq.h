@@ -434,8 +434,11 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64
  * entry outside [0, n_pages) count as hidden, so no value in these arrays leads
  * outside the buffers.  A key or value with a NaN scale makes the tokens that
  * see it NaN.
- * Sums and softmax statistics are fp32; weights and values enter the second
- * product in fp16 (2^-11 relative each, under out's own rounding).  Deterministic.
+ * Sums and softmax statistics are fp32.  The second product runs in fp16: an
+ * output is off by 2^-11 relative, four times at most, of sum_j p_j |v_j|, and by
+ * what lies below fp16's normal range, under 2^-24 a key of the largest
+ * p_j |v_j| that its largest code could give, however far the value scales lie
+ * apart (past 2^8 prompts take up to a third longer).  Deterministic.
  *   ws       device workspace of gptq_attention_workspace_size bytes, 256-byte
  *            aligned (results of key splits); may be null when that size is 0
  * Requires n_heads % n_kv_heads == 0, n_tokens * n_heads < 2^30,

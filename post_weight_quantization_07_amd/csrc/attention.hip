@@ -7,9 +7,12 @@
 // Scores: q and the key codes are exact in bf16, their products are summed in
 // fp32 and the key scale multiplies the sum in fp32.  Output: the second
 // product runs in fp16, whose 11 bits round eight times finer than bf16's 8: an
-// operand is off by 2^-11 relative (2^-25 absolute, against values of up to 1,
-// below 2^-14).  fp16's range is kept by a power of two per workgroup, so that
-// the largest value scale seen so far stays in [1/2, 1) (ValueRange).
+// operand is off by 2^-11 relative.  fp16's range is narrow, and a key may have any
+// weight and any value scale.  So what it holds is taken relative to the largest
+// weight times value scale that a row has seen (ProductUnit), which is held above
+// 2^8, and what falls below fp16's normal range is off by 2^-33 of that a key at
+// most; where a kernel keeps weight and scale apart (the tile kernel, while the
+// scales are within 2^8 of each other), by less than 2^-24.
 //
 // The query heads that share a key head are rows of one tile: row r of a
 // sequence is token r / G, head r % G of its group, and M rows make a tile.
@@ -194,19 +197,20 @@ GPTQ_DEV float add_f16(uint32_t pair, float c) {  // c + both halves (v_dot2 wit
   return __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2_t, pair), f16x2_t{1, 1}, c, false);
 }
 
-// The power of two that value scales are taken relative to: 2^(e - 126) is
-// above the largest finite scale seen (e: its biased exponent, 1 .. 252), so
-// scale * down() < 1.
-struct ValueRange {
+// The power of two that fp16 operands are taken relative to: 2^(e - 126) is
+// above x, e its biased exponent (held in 24 .. 252, where the factors below are normal
+// fp32 numbers), so x * down() < 2^15.
+struct ProductUnit {
   int e;
-  GPTQ_DEV float down() const { return __uint_as_float(static_cast<uint32_t>(253 - e) << 23); }
-  GPTQ_DEV float up() const { return __uint_as_float(static_cast<uint32_t>(e + 1) << 23); }
-  GPTQ_DEV static int of(float scale) {
-    return min(max(static_cast<int>((__float_as_uint(scale) >> 23) & 255u), 1), 252);
+  GPTQ_DEV float down() const { return __uint_as_float(static_cast<uint32_t>(253 + 15 - e) << 23); }
+  GPTQ_DEV float up() const { return __uint_as_float(static_cast<uint32_t>(e + 1 - 15) << 23); }
+  static constexpr int kLeast = 24, kMost = 252;
+  GPTQ_DEV static int of(float x) {
+    return min(max(static_cast<int>((__float_as_uint(x) >> 23) & 255u), kLeast), kMost);
   }
 };
-GPTQ_DEV float exp2_int(int d) {  // 2^d for d <= 0 (0 below -126)
-  return d < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + d) << 23);
+GPTQ_DEV float exp2_int(int d) {  // 2^d for d <= 127 (0 below -126; 2^127 above)
+  return d < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + min(d, 127)) << 23);
 }
 
 template <int B>
@@ -331,12 +335,14 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 
   f32x4_t acc[MT][kTiles];
   float m[MT], l[MT], psum[MT];
-  ValueRange vr{1};
+  ProductUnit unit[MT];    // of acc and psum
+  constexpr int kRoom = 6;  // when it is set, the largest product so far becomes 2^8 to 2^9 of it: 2^6 and more below what fits
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    m[i] = kNegInf;
+    m[i] = kNoMax;
     l[i] = 0.f;
     psum[i] = 0.f;
+    unit[i].e = ProductUnit::kLeast + kRoom;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
@@ -411,30 +417,9 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
         for (int r = 0; r < 4; ++r) s[i][4 * b + r] = a[r] * (ks[b][r] * p.scale_log2e);
       }
     }
-    // value scales: those of hidden keys may be anything, and count as 0
-    float vn[8], vtop = 0.f;
+    float vtop = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      vn[j] = vs[j >> 2][j & 3];
-      if (masked && !(ok[j >> 2] && k0 + 16 * (j >> 2) + 4 * g + (j & 3) < vis)) vn[j] = 0.f;
-      vtop = fmaxf(vtop, vn[j]);
-    }
-    if (__any(ValueRange::of(vtop) > vr.e)) {
-      const int e = max(ValueRange::of(max_over_groups(vtop)), vr.e);
-      const float f = exp2_int(vr.e - e);
-      vr.e = e;
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        psum[i] *= f;
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][t][r] *= f;
-      }
-    }
-    const float down = vr.down();
-#pragma unroll
-    for (int j = 0; j < 8; ++j) vn[j] *= down;
+    for (int j = 0; j < 8; ++j) vtop = fmaxf(vtop, fabsf(vs[j >> 2][j & 3]));
     f16x8_t pop[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -451,26 +436,33 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       float mx = s[i][0];
 #pragma unroll
       for (int j = 1; j < 8; ++j) mx = fmaxf(mx, s[i][j]);
-      mx = max_over_groups(mx);
-      if (__any(mx > m[i])) {
-        const float mn = fmaxf(m[i], mx);
-        const float alpha = fast_exp2(m[i] - (mn == kNegInf ? 0.f : mn));
+      // m and the unit move when a weight is far above m, or its product with the largest scale would not fit
+      if (__any(mx - m[i] > 16.f || fast_exp2(mx - m[i]) * vtop * unit[i].down() > 32768.f)) {
+        const float mn = fmaxf(m[i], max_over_groups(mx));
+        const float alpha = fast_exp2(m[i] - mn);
+        float top = alpha * __uint_as_float(static_cast<uint32_t>(unit[i].e - kRoom) << 23);  // the largest product before
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (!masked || see[j]) top = fmaxf(top, fabsf(fast_exp2(s[i][j] - mn) * vs[j >> 2][j & 3]));
+        const int e = min(ProductUnit::of(max_over_groups(top)) + kRoom, ProductUnit::kMost);
+        const float f = alpha * exp2_int(unit[i].e - e);
         m[i] = mn;
+        unit[i].e = e;
         l[i] *= alpha;
-        psum[i] *= alpha;
+        psum[i] *= f;
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[i][t][r] *= alpha;
+          for (int r = 0; r < 4; ++r) acc[i][t][r] *= f;
       }
-      const float mm = m[i] == kNegInf ? 0.f : m[i];
+      const float down = unit[i].down();
       float pv[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float e = fast_exp2(s[i][j] - mm);
+        const float e = fast_exp2(s[i][j] - m[i]);
         l[i] += e;
-        pv[j] = e * vn[j];
-        if (masked && !see[j]) pv[j] = 0.f;  // a NaN scale reaches only the rows that see the key
+        pv[j] = e * vs[j >> 2][j & 3] * down;
+        if (masked && !see[j]) pv[j] = 0.f;  // the scale of a hidden key may be anything
       }
       const u32x4_t pk = {pack_f16(pv[0], pv[1]), pack_f16(pv[2], pv[3]), pack_f16(pv[4], pv[5]), pack_f16(pv[6], pv[7])};
       if (BITS == 4) {
@@ -523,10 +515,10 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
   float* part = p.partial + slot * (kM * (HDP + 2));
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    float top = kNegInf;
+    float top = kNoMax;
 #pragma unroll
     for (int v = 0; v < NW; ++v) top = fmaxf(top, wm[v][16 * i + c]);
-    const float f = fast_exp2(m[i] - (top == kNegInf ? 0.f : top)) * vr.up();
+    const float f = fast_exp2(m[i] - top), up = unit[i].up();
     // lane l: dims g HDP / 4 + r HDP / 16 + t
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -534,7 +526,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       for (int t = 0; t < kTiles; t += 4) {
         f32x4_t v;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = f * (acc[i][t + e][r] - (BITS == 4 ? 24.f * psum[i] : 0.f));
+        for (int e = 0; e < 4; ++e) v[e] = f * (acc[i][t + e][r] - (BITS == 4 ? 24.f * psum[i] : 0.f)) * up;
         *reinterpret_cast<f32x4_t*>(&wo[wave][c][g * (HDP / 4) + r * (HDP / 16) + t]) = v;
       }
     __syncthreads();
@@ -542,12 +534,12 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
       const int r = r0 + 16 * i + row;
       if (r >= rows || d >= p.hd) continue;  // nor does the join read the others
-      float t2 = kNegInf;
+      float t2 = kNoMax;
 #pragma unroll
       for (int v = 0; v < NW; ++v) t2 = fmaxf(t2, wm[v][16 * i + row]);
       float sum = 0.f;
 #pragma unroll
-      for (int v = 0; v < NW; ++v) sum += wl[v][16 * i + row] * fast_exp2(wm[v][16 * i + row] - (t2 == kNegInf ? 0.f : t2));
+      for (int v = 0; v < NW; ++v) sum += wl[v][16 * i + row] * fast_exp2(wm[v][16 * i + row] - t2);
       f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
@@ -558,7 +550,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       if (!whole) {
         *reinterpret_cast<f32x4_t*>(part + (16 * i + row) * HDP + d) = o;
         if (d == 0) {
-          part[kM * HDP + 16 * i + row] = t2;
+          part[kM * HDP + 16 * i + row] = t2;  // kNoMax: saw nothing
           part[kM * HDP + kM + 16 * i + row] = sum;
         }
       } else {
@@ -582,6 +574,13 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 //
 // Per tile the codes are turned into operands once, into LDS: the key codes
 // as bf16 integers, the values as fp16 code * (scale * 2^-range) (two roundings).
+// That holds while the scales of the keys so far lie within 2^8 of each other: then
+// values stay in fp16's normal range, and a weight is lost (below 2^-33 of the largest) only
+// where it and its value are that small against the row's largest.  From the first tile
+// that goes past it, values are bare codes (exact) and each weight carries its value's
+// scale, in units of the row's own largest product (scaled_tile): a slower path for
+// caches whose scales spread wider than those of activations do, or hold zeros (with
+// zeros among them the four prompts below take 7% longer, the chunks 35%).
 // 32x32x16 products: S^T = K Q^T leaves lane l (query row l % 32, half h = l / 32)
 // with keys 8 a + 4 h + b of a 32-key block; 16 of them in that order are the
 // P^T operand of O^T = V^T P^T, so V's operand holds keys 4 h + b and 8 + 4 h + b
@@ -591,9 +590,10 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 //
 // Two tiles of LDS: while one is multiplied, the next one's codes, loaded to
 // registers two tiles ahead, are converted into the other; one barrier a tile.
-// The row maximum is only moved when a lane's weights sum to more than 2^10 (fp16
-// holds 2^15; p keeps its relative precision): the usual tile then costs a multiply-add and
-// an exp2 per score, half a conversion and half a sum.
+// Weights are taken relative to 2^-8 of the largest, and the row maximum is only moved
+// when a lane's weights sum to more than 2^15, which fp16 holds; p keeps its relative
+// precision: the usual tile then costs a multiply-add and an exp2 per score, half a
+// conversion and half a sum.
 //
 // Bound: the products, the exponentials and the codes' conversion share the
 // waves' issue slots: a 64-key tile of 128 rows x 128 dims takes about 3740 cycles,
@@ -601,7 +601,9 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 // tokens, 32 heads of 128: 206 us (0.67 PFLOP/s of the causal half); long ones come
 // to 0.88 PFLOP/s.
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
-constexpr float kGrow = 1024.f;
+constexpr float kGrow = 32768.f;
+constexpr float kAbove = 8.f;    // log2 of the largest weight when the maximum moves
+constexpr int kSpread = 8;       // powers of two between the value scales that the plain path takes
 constexpr float kFar = 0x1p20f;  // maxima past this leave the plain tile: see careful_tile
 
 // what a thread holds of a tile on its way: its dims of one key or of one value
@@ -620,7 +622,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   constexpr int kSteps = HDP / 16, kDb = HDP / 32;
   constexpr int kKF = 2 * kSteps;  // key operands of a tile
   __shared__ __attribute__((aligned(16))) uint8_t lk[2][kKF * kFrag], lv[2][kKeys * HDP * 2];
-  __shared__ __attribute__((aligned(16))) float lks[2][kKeys];
+  __shared__ __attribute__((aligned(16))) float lks[2][kKeys], lvs[2][kKeys];
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int c = lane & 31, hf = lane >> 5;
@@ -669,7 +671,11 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[t][e] = 0.f;
   float m = kNoMax, l = 0.f;
-  ValueRange vr{1}, vr_next{1};
+  // largest and least exponents of the value scales so far, the next tile's among them, and whether they lie
+  // too far apart; range: the largest that acc is relative to
+  int range = ProductUnit::kLeast, top_next = ProductUnit::kLeast, low_next = ProductUnit::kMost;
+  float top_bound = 0.f, low_bound = __builtin_inff();  // scales in [low_bound, top_bound) change neither
+  bool spread = false;
 
   const int row_bytes = p.hd * BITS / 8;
   const int page_mask = (1 << p.page_shift) - 1;
@@ -743,29 +749,42 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   // codes in registers -> operands in LDS, in pieces: the range of the tile's
   // value scales, the key scales, 8 dims of the thread's key, 8 of its value
   auto convert_range = [&](float v) {
-    float top = fabsf(v) < __builtin_inff() ? v : 0.f;  // finite ones
-    if (__any(ValueRange::of(top) > vr_next.e)) {
+    if (__any(fabsf(v) >= top_bound || fabsf(v) < low_bound)) {
+      int top = v == v ? ProductUnit::of(fabsf(v)) : ProductUnit::kLeast;
+      int low = v == v ? top : ProductUnit::kMost;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-      vr_next.e = max(vr_next.e, uniform(ValueRange::of(top)));
+      for (int d = 1; d < 64; d <<= 1) {
+        top = max(top, __shfl_xor(top, d));
+        low = min(low, __shfl_xor(low, d));
+      }
+      top_next = max(top_next, uniform(top));
+      low_next = min(low_next, uniform(low));
+      top_bound = __uint_as_float(static_cast<uint32_t>(top_next + 1) << 23);
+      low_bound = low_next == ProductUnit::kLeast ? 0.f : __uint_as_float(static_cast<uint32_t>(low_next) << 23);
+      spread = top_next - low_next > kSpread;
     }
   };
   // A value whose scale is not finite makes the key's scores NaN (and its operand 0), so that it
   // reaches only the rows that see the key.  Every wave writes the same 64 scales.  Returns the value
-  // scale of key `lane` (0: no such key)
+  // scale of key `lane`, NaN if there is no such key or scale.
   auto key_scales = [&](int buf) {
-    const float v = vlive ? vall : 0.f;
-    lks[buf][lane] = fabsf(v) < __builtin_inff() ? ks * p.scale_log2e : __uint_as_float(0x7FC00000u);
-    return v;
+    const float nan = __uint_as_float(0x7FC00000u), v = fabsf(vall) < __builtin_inff() ? vall : nan;
+    lks[buf][lane] = vlive && v != v ? nan : ks * p.scale_log2e;
+    return vlive ? v : nan;
   };
   auto convert_key = [&](const R& t, int buf, int i) {
     const int d = kpart * R::kD + 8 * i;
     const bf16x8_t v = BITS == 8 ? row8(t.w[2 * i % R::kW], t.w[(2 * i + 1) % R::kW]) : row4(t.w[i % R::kW]);
     *reinterpret_cast<bf16x8_t*>(&lk[buf][((own >> 5) * kSteps + (d >> 4)) * kFrag + ((own & 31) + 4 * (d & 8)) * 16]) = v;
   };
-  // the factor of the thread's value, twice in fp16
-  auto value_factor = [&](float v) {
-    const float f = __shfl(fabsf(v) < __builtin_inff() ? v * vr_next.down() : 0.f, own);
+  // The factor of the thread's value, twice in fp16: under 2^7, so that values and weights of up to 2^8
+  // are in ProductUnit's unit together.  Or 1, and the scales go to LDS.
+  auto value_factor = [&](float v, int buf) {
+    if (spread) {
+      lvs[buf][lane] = v == v ? v : 0.f;
+      return f16x2_t{1, 1};
+    }
+    const float f = __shfl(v == v ? v * __uint_as_float(static_cast<uint32_t>(253 + 7 - top_next) << 23) : 0.f, own);
     return __builtin_bit_cast(f16x2_t, pack_f16(f, f));
   };
   auto convert_value = [&](const R& t, f16x2_t f, int buf, int i) {
@@ -816,18 +835,13 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   // m was: off by 2^-24 |m|.  Rows whose maximum lies past +-2^20 (or that have none)
   // stay here, where equal scores give equal weights at any magnitude.
   bool far = true;
-  auto careful_tile = [&](int base, int buf, uint64_t shown, int half, int range) {
+  // the scores of a tile's keys (from block `half`), -inf where hidden; returns their maximum
+  auto tile_scores = [&](int base, int buf, uint64_t shown, int half, f32x16_t (&s)[2]) {
     const int rel = lim - base - 4 * hf;
     auto seen = [&](int b, int e) {  // element e of block b: key 32 b + 8 (e / 4) + 4 hf + e % 4
       return 32 * b + 8 * (e >> 2) + (e & 3) <= rel && ((shown >> (32 * b + 16 * (e >> 3))) & 1u);  // 16 keys share a page
     };
-    float f = 1.f;
-    if (range > vr.e) {
-      f = exp2_int(vr.e - range);
-      vr.e = range;
-    }
-    f32x16_t s[2];
-    float mx = m;
+    float mx = kNoMax;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       if (b < half) continue;
@@ -851,16 +865,23 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
         }
       }
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
-    const float fm = fast_exp2(m - mx);
-    m = mx;
-    far = __any(fabsf(m) > kFar);
-    l *= fm;
-    f *= fm;
+    return fmaxf(mx, __shfl_xor(mx, 32));
+  };
+  auto rescale = [&](float f) {
 #pragma unroll
     for (int i = 0; i < kDb; ++i)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+  };
+  auto careful_tile = [&](int base, int buf, uint64_t shown, int half, int tile_range) {
+    f32x16_t s[2];
+    const float mx = fmaxf(m, tile_scores(base, buf, shown, half, s) - kAbove);
+    const float fm = fast_exp2(m - mx);
+    m = mx;
+    far = __any(fabsf(m) > kFar);
+    l *= fm;
+    rescale(fm * exp2_int(range - tile_range));
+    range = tile_range;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       if (b < half) continue;
@@ -870,6 +891,45 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
         pk[e >> 2][e & 3] = pack_f16(fast_exp2(s[b][2 * e] - m), fast_exp2(s[b][2 * e + 1] - m));
         l = add_f16(pk[e >> 2][e & 3], l);
       }
+#pragma unroll
+      for (int x = 0; x < kPv; ++x)
+        acc[x % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(value_operand(buf, b, x), __builtin_bit_cast(f16x8_t, pk[x / kDb]),
+                                                              acc[x % kDb], 0, 0, 0);
+    }
+  };
+  // A tile whose values are bare codes.  most: the row's largest product of weight and value scale, which
+  // gives acc's unit; m here is the maximum itself.
+  float most = 0.f;
+  auto scaled_tile = [&](int base, int buf, uint64_t shown) {
+    f32x16_t s[2];
+    const float mx = fmaxf(m, tile_scores(base, buf, shown, 0, s));
+    const float fm = fast_exp2(m - mx);
+    m = mx;
+    l *= fm;
+    float top = 0.f;
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const f32x4_t vs = *reinterpret_cast<const f32x4_t*>(&lvs[buf][32 * b + 8 * a + 4 * hf]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float p = fast_exp2(s[b][4 * a + e] - m);
+          l += p;
+          s[b][4 * a + e] = p * vs[e];
+          top = fmaxf(top, fabsf(s[b][4 * a + e]));
+        }
+      }
+    const int before = ProductUnit::of(most);
+    most = fmaxf(most * fm, fmaxf(top, __shfl_xor(top, 32)));
+    const ProductUnit unit{ProductUnit::of(most)};
+    rescale(fm * exp2_int(before - unit.e));
+    const float down = unit.down();
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      u32x4_t pk[2];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) pk[e >> 2][e & 3] = pack_f16(s[b][2 * e] * down, s[b][2 * e + 1] * down);
 #pragma unroll
       for (int x = 0; x < kPv; ++x)
         acc[x % kDb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(value_operand(buf, b, x), __builtin_bit_cast(f16x8_t, pk[x / kDb]),
@@ -891,25 +951,48 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
     load_keys(key0 + kKeys, tk);
     load_page(key0 + 2 * kKeys);
     convert_range(vs_next);
-    const f16x2_t f = value_factor(vs_next);
+    const f16x2_t f = value_factor(vs_next, 0);
 #pragma unroll
     for (int i = 0; i < R::kD / 8; ++i) convert_key(k0, 0, i);
 #pragma unroll
     for (int i = 0; i < R::kD / 8; ++i) convert_value(tv, f, 0, i);
   }
+  auto tile_barrier = [&] {  // a tile's operands are written, and the other buffer's have been read
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+  };
+  // the next tile's keys, and the loads behind them
+  auto next_keys = [&] {
+    shown_next = there;
+    load_values(tv);
+    vs_next = key_scales(buf ^ 1);
+#pragma unroll
+    for (int i = 0; i < R::kD / 8; ++i) convert_key(tk, buf ^ 1, i);
+    load_keys(base + 2 * kKeys, tk);
+    load_page(base + 3 * kKeys);
+  };
+  // its values; then it is the current tile
+  auto next_values = [&] {
+    convert_range(vs_next);
+    const f16x2_t f = value_factor(vs_next, buf ^ 1);
+#pragma unroll
+    for (int i = 0; i < R::kD / 8; ++i) convert_value(tv, f, buf ^ 1, i);
+    shown = shown_next;
+    base += kKeys;
+    buf ^= 1;
+  };
   // The next tile is converted past the last one too; nothing reads it then.
   while (base < key1) {
-    int half = 0, range = 0;
-    bool fits = true, keys_done = false;
+    int half = 0, tile_range = 0;
+    bool fits = true, keys_done = false, tile_spread = false;
     while (base < key1) {
-      // this tile's operands are written, and the other buffer's have been read
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+      tile_barrier();
       half = 0;
       keys_done = false;
-      range = vr_next.e;  // the one this tile's values were written in (the next tile's may be wider)
-      fits = base > key0 && base + kKeys - 1 <= wfirst && shown == ~uint64_t{0} && range == vr.e && !far;
+      tile_range = top_next;  // the one this tile's values were written in (the next tile's may be wider)
+      tile_spread = spread;
+      fits = base > key0 && base + kKeys - 1 <= wfirst && shown == ~uint64_t{0} && tile_range == range && !far && !tile_spread;
       if (!fits) break;
       // The plain tile: every key seen, the maximum and the range as they were.
       // Four groups of products, each with arithmetic between them that does not
@@ -989,7 +1072,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       if (!fits) break;
       l += l1;
       convert_range(vs_next);
-      const f16x2_t f = value_factor(vs_next);
+      const f16x2_t f = value_factor(vs_next, buf ^ 1);
 #pragma unroll
       for (int x = 0; x < kAhead; ++x) vo[x] = value_operand(buf, 1, x);
 #pragma unroll
@@ -1004,37 +1087,34 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       base += kKeys;
       buf ^= 1;
     }
-    if (fits) break;
-    if (!keys_done) {
-      shown_next = there;
-      load_values(tv);
-      vs_next = key_scales(buf ^ 1);
-#pragma unroll
-      for (int i = 0; i < R::kD / 8; ++i) convert_key(tk, buf ^ 1, i);
-      load_keys(base + 2 * kKeys, tk);
-      load_page(base + 3 * kKeys);
-    }
-    if (base <= wlast) careful_tile(base, buf, shown, half, range);  // else a causal tile past the wave's rows
-    convert_range(vs_next);
-    const f16x2_t f = value_factor(vs_next);
-#pragma unroll
-    for (int i = 0; i < R::kD / 8; ++i) convert_value(tv, f, buf ^ 1, i);
-    shown = shown_next;
-    base += kKeys;
-    buf ^= 1;
+    if (fits || tile_spread) break;
+    if (!keys_done) next_keys();
+    if (base <= wlast) careful_tile(base, buf, shown, half, tile_range);  // else a causal tile past the wave's rows
+    next_values();
+  }
+  // Scaled tiles, from one whose barrier is behind (all waves see the same scales, and come here at the same
+  // tile).  From here weights are relative to the largest itself.
+  m += kAbove;
+  l *= 0x1p-8f;
+  most = __uint_as_float(static_cast<uint32_t>(range) << 23);
+  while (base < key1) {
+    next_keys();
+    if (base <= wlast) scaled_tile(base, buf, shown);
+    next_values();
+    if (base < key1) tile_barrier();
   }
 
   // lane l: query row c, dims 32 i + 8 a + 4 hf + e
   l += __shfl_xor(l, 32);
   const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
-  const float up = vr.up();
+  const float up = ProductUnit{ProductUnit::of(most)}.up();
   if (!live) return;  // the join does not read such rows either
   if (w.n_split > 1) {
     if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(p.max_slots)) return;
     float* part = p.partial + slot * (kM * (HDP + 2));
     const int row = 32 * wave + c;
     if (hf == 0) {
-      part[kM * HDP + row] = m == kNoMax ? kNegInf : m;
+      part[kM * HDP + row] = m;
       part[kM * HDP + kM + row] = l;
     }
 #pragma unroll
@@ -1048,7 +1128,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       }
     return;
   }
-  const float inv = l == 0.f ? 0.f : up / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* dst = p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(h * p.group + qh) * p.hd;
 #pragma unroll
   for (int i = 0; i < kDb; ++i)
@@ -1056,8 +1136,8 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
     for (int a = 0; a < 4; ++a) {
       const int d = 32 * i + 8 * a + 4 * hf;
       if (d < p.hd)
-        *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_bf16(acc[i][4 * a] * inv, acc[i][4 * a + 1] * inv),
-                                                        pack_bf16(acc[i][4 * a + 2] * inv, acc[i][4 * a + 3] * inv));
+        *reinterpret_cast<uint2*>(dst + d) = make_uint2(pack_bf16(acc[i][4 * a] * inv * up, acc[i][4 * a + 1] * inv * up),
+                                                        pack_bf16(acc[i][4 * a + 2] * inv * up, acc[i][4 * a + 3] * inv * up));
     }
 }
 

@@ -87,3 +87,60 @@ def test_scores_far_below_zero(G, lens, heads, kv, hd, page, bits):
     c.q.fill_(2.0)
     c.q_host[:] = 2.0
     check(c, G.gptq_cache_attention(c.q, c.cache, *c.args), same_scores=True)
+
+
+def plant(c, key, score, ratio):
+    """Key `key` of every sequence scores `score` for every query, and its value scale is `ratio` times what it was."""
+    top = 127 if c.bits == 8 else 7
+    c.q[..., 0] = 8.0
+    c.q_host[..., 0] = 8.0
+    row = np.zeros(c.hd, np.int64)
+    row[0] = top if score > 0 else -top
+    for i, (_, length) in enumerate(c.lens):
+        page, at = c.table[i, key % length // c.page], key % length % c.page
+        c.codes[0][page, :, at] = S.pack_rows(row, c.bits)
+        c.scales[0][page, :, at] = abs(score) / (c.hd ** -0.5 * 8.0 * top)
+        c.scales[1][page, :, at] *= ratio
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", SHAPES)
+def test_large_values_of_little_weight(G, lens, heads, kv, hd, page, bits):
+    """One key of weight near e^-60 whose value scale is 2^r times the others': nothing of it shows up to r near 80."""
+    for r in (9, 13, 17, 20, 27, 45, 100):
+        for key in (0, 150, -1):
+            banner(f"attention: value scale 2^{r} at key {key}, {lens} {heads}/{kv}x{hd} int{bits}")
+            c = Case(G, lens, heads, kv, hd, page, bits, seed=22)
+            plant(c, key, -60.0, 2.0 ** r)
+            upload(G, c)
+            check(c, G.gptq_cache_attention(c.q, c.cache, *c.args))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", SHAPES)
+def test_small_values_of_all_weight(G, lens, heads, kv, hd, page, bits):
+    """One key that takes all the weight and has a small value, or none: the others' share shows."""
+    for ratio in (0.0, 2.0 ** -10, 2.0 ** -30, 2.0 ** -60):
+        for key in (0, 150):
+            banner(f"attention: value scale x {ratio} at key {key}, {lens} {heads}/{kv}x{hd} int{bits}")
+            c = Case(G, lens, heads, kv, hd, page, bits, seed=23)
+            plant(c, key, 40.0, ratio)
+            upload(G, c)
+            check(c, G.gptq_cache_attention(c.q, c.cache, *c.args))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+def test_values_of_every_size(G, bits):
+    """Value scales over forty powers of two, in falling and rising order and mixed; some of them zero."""
+    for lens, heads, kv, hd, page in SHAPES:
+        for how in ("fall", "rise", "mix"):
+            banner(f"attention: value scales that {how}, {lens} {heads}/{kv}x{hd} int{bits}")
+            c = Case(G, lens, heads, kv, hd, page, bits, seed=24)
+            r = np.random.default_rng(5)
+            length = lens[0][1]
+            power = {"fall": np.linspace(20, -20, length), "rise": np.linspace(-20, 20, length),
+                     "mix": r.uniform(-20, 20, length)}[how]
+            for j in range(length):
+                c.scales[1][c.table[0, j // page], :, j % page] *= 0.0 if j % 7 == 3 else np.float32(2.0 ** power[j])
+            upload(G, c)
+            check(c, G.gptq_cache_attention(c.q, c.cache, *c.args))
