@@ -205,6 +205,16 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+def _ws_bytes(ws: Optional[torch.Tensor]) -> int:
+    """The bytes of a workspace, of any dtype.  One whose elements do not lie one
+    behind the other (a strided or an expanded view) has no such size."""
+    if ws is None:
+        return 0
+    if not ws.is_contiguous():
+        raise ValueError("a workspace must be contiguous")
+    return ws.numel() * ws.element_size()
+
+
 # --------------------------------------------------------------------------
 # the four calls of the C ABI
 # --------------------------------------------------------------------------
@@ -229,7 +239,7 @@ def gptq_hessian_accumulate(S: torch.Tensor, X: torch.Tensor, ws: Optional[torch
     need = gptq_hessian_workspace_size(d, n, X.dtype)
     if ws is None:
         ws = _workspace(need, X.device)
-    _check(_lib().gptq_hessian_accumulate(_ptr(S), d, _ptr(X), code, n, X.stride(0), _ptr(ws), ws.numel(),
+    _check(_lib().gptq_hessian_accumulate(_ptr(S), d, _ptr(X), code, n, X.stride(0), _ptr(ws), _ws_bytes(ws),
                                           _stream(stream)), "gptq_hessian_accumulate")
     return S
 
@@ -252,7 +262,7 @@ def gptq_prepare_hinv(S: torch.Tensor, n_total: int, cfg: QuantizeConfig, U: Opt
     if ws is None:
         ws = _workspace(gptq_prepare_workspace_size(d), dev)
     _check(_lib().gptq_prepare_hinv(_ptr(S), d, int(n_total), ctypes.byref(cfg._c()), _ptr(U), _ptr(perm),
-                                    _ptr(info), _ptr(ws), ws.numel(), _stream(stream)), "gptq_prepare_hinv")
+                                    _ptr(info), _ptr(ws), _ws_bytes(ws), _stream(stream)), "gptq_prepare_hinv")
     if check:
         k = int(info.item())
         if k == -1:
@@ -291,7 +301,7 @@ def gptq_quantize_layer(W: torch.Tensor, U: torch.Tensor, perm: Optional[torch.T
     _check(_lib().gptq_quantize_layer(_ptr(W), _dtype_code(W), d_out, d_in, _ptr(U), _ptr(perm),
                                       ctypes.byref(cfg._c()), _ptr(o["codes"]), _ptr(o["scales"]),
                                       _ptr(o["zeros"]), _ptr(o["g_idx"]), _ptr(o.get("Q")),
-                                      _ptr(o.get("row_loss")), _ptr(ws), ws.numel(), _stream(stream)),
+                                      _ptr(o.get("row_loss")), _ptr(ws), _ws_bytes(ws), _stream(stream)),
            "gptq_quantize_layer")
     return o
 
@@ -331,7 +341,7 @@ def gptq_dequant_matmul(x: torch.Tensor, qweight: torch.Tensor, scales: torch.Te
         ws = _workspace(need, x.device) if need > 0 else None
     _check(_lib().gptq_dequant_matmul(_ptr(x), _dtype_code(x), m, d_in, _ptr(qweight.contiguous()),
                                       _ptr(scales.contiguous()), _ptr(zeros.contiguous()), _ptr(g_idx.contiguous()),
-                                      int(bits), d_out, n_groups, _ptr(y), _ptr(ws), 0 if ws is None else ws.numel(),
+                                      int(bits), d_out, n_groups, _ptr(y), _ptr(ws), _ws_bytes(ws),
                                       _stream(stream)),
            "gptq_dequant_matmul")
     return y
@@ -415,7 +425,7 @@ def gptq_dequant_matmul_ordered(x: torch.Tensor, qweight: torch.Tensor, scales: 
     _check(_lib().gptq_dequant_matmul_ordered(_ptr(x), _dtype_code(x), m, d_in, _ptr(qweight.contiguous()),
                                               _ptr(scales.contiguous()), _ptr(zeros.contiguous()),
                                               _ptr(g_idx.contiguous()), _ptr(order.contiguous()), int(bits), d_out,
-                                              n_groups, _ptr(y), _ptr(ws), ws.numel(), _stream(stream)),
+                                              n_groups, _ptr(y), _ptr(ws), _ws_bytes(ws), _stream(stream)),
            "gptq_dequant_matmul_ordered")
     return y
 
@@ -568,7 +578,7 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     _check(lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, _row_stride(x),
                                    w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), d_out, y.data_ptr(), yt, _ptr(ws),
-                                   0 if ws is None else ws.numel(), _raw_stream(dev)), what)
+                                   _ws_bytes(ws), _raw_stream(dev)), what)
     return y
 
 
@@ -729,5 +739,5 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
     _check(lib.gptq_cache_attention(cache._ref, q.data_ptr(), GPTQ_BF16, n, ldq, heads, page_table.data_ptr(), pages,
                                     q_starts.data_ptr(), kv_lens.data_ptr(), n_seq,
                                     hd ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(ws),
-                                    0 if ws is None else ws.numel(), _raw_stream(dev)), what)
+                                    _ws_bytes(ws), _raw_stream(dev)), what)
     return out

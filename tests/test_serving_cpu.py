@@ -189,3 +189,13 @@ def test_integer_workspace_follows_the_kernel(L):
     assert size(70, 2, 32768, 50) >= 2 * 70 * 50 * 4 and size(1030, 2, 8224, 1800) >= 2 * 1030 * 1800 * 4
     for m, d_in, d_out in ((1, 32, 1), (5, 4096, 64), (600, 4096, 512), (2048, 28672, 8192), (1 << 20, 32, 1)):
         assert size(m, 1, d_in, d_out) >= size(m, 2, d_in, d_out)
+
+
+def test_workspace_bytes(L):
+    """A given workspace counts in bytes whatever its dtype, and only if it is in one piece."""
+    assert L._ws_bytes(None) == 0 and L._ws_bytes(torch.empty(100, dtype=torch.uint8)) == 100
+    assert L._ws_bytes(torch.empty((5, 20), dtype=torch.float32)) == 400
+    for view in (torch.empty(1, dtype=torch.uint8).expand(4096), torch.empty(64, dtype=torch.uint8)[::2],
+                 torch.empty((8, 8)).t()):
+        with pytest.raises(ValueError, match="contiguous"):
+            L._ws_bytes(view)
