@@ -642,6 +642,13 @@ class QuantizedCache:
         return dev
 
 
+def _heads_together(t: torch.Tensor) -> bool:
+    """Of [tokens, heads, head_dim]: a token's heads lie one behind the other.  The
+    stride of a single head, and any of no tokens, says nothing."""
+    n, heads, hd = t.shape
+    return n == 0 or (t.stride(2) == 1 and (heads == 1 or t.stride(1) == hd))
+
+
 def _slots(what: str, slots: torch.Tensor) -> int:
     if slots.dim() != 1 or slots.dtype != torch.int64 or not slots.is_contiguous():
         raise ValueError(f"{what}: slots must be a contiguous int64 vector")
@@ -660,11 +667,11 @@ def gptq_cache_write(cache: QuantizedCache, k: torch.Tensor, v: torch.Tensor, sl
     n = _slots(what, slots)
     code = _type_code(what, k.dtype)
     heads, hd = cache.n_kv_heads, cache.head_dim
-    shape, sk, sv = (n, heads, hd), k.stride(), v.stride()
-    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or (n > 0 and (sk[1:] != (hd, 1) or sv[1:] != (hd, 1))):
+    shape = (n, heads, hd)
+    if k.shape != shape or v.shape != shape or k.dtype != v.dtype or not _heads_together(k) or not _heads_together(v):
         raise ValueError(f"{what}: k and v must be [n, {heads}, {hd}] of one dtype, heads contiguous")
     dev = cache._here(what, k, v, slots)
-    ldk, ldv = (sk[0], sv[0]) if n > 1 else (heads * hd, heads * hd)
+    ldk, ldv = (k.stride(0), v.stride(0)) if n > 1 else (heads * hd, heads * hd)
     _check(_lib().gptq_cache_write(cache._ref, k.data_ptr(), v.data_ptr(), code, n, ldk, ldv, slots.data_ptr(),
                                    _raw_stream(dev)), what)
 
@@ -714,7 +721,7 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
     n, heads = q.shape[0], q.shape[1]
     if heads < 1 or heads % cache.n_kv_heads != 0:
         raise ValueError(f"{what}: {heads} query heads do not divide over {cache.n_kv_heads} key heads")
-    if n > 0 and (q.stride(2) != 1 or q.stride(1) != hd):
+    if not _heads_together(q):
         raise ValueError(f"{what}: the heads of a token must be contiguous in q")
     if (page_table.dim() != 2 or page_table.dtype != torch.int32 or not page_table.is_contiguous()
             or kv_lens.dtype != torch.int32 or q_starts.dtype != torch.int32 or not kv_lens.is_contiguous()
@@ -725,8 +732,7 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
     width = heads * hd
     if out is None:
         out = q.new_empty((n, heads, hd))
-    elif (out.shape != q.shape or out.dtype != torch.bfloat16
-          or (n > 0 and (out.stride(2) != 1 or out.stride(1) != hd))):
+    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not _heads_together(out):
         raise ValueError(f"{what}: out must be bfloat16 like q, the heads of a token contiguous")
     dev = cache._here(what, q, page_table, q_starts, kv_lens, out, ws)
     n_seq, pages = page_table.shape

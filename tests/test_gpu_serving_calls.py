@@ -55,3 +55,25 @@ def test_workspaces(G):
         for view in views:
             with pytest.raises(ValueError, match="contiguous"):
                 call(view)
+
+
+def test_one_head_of_any_stride(G):
+    """k, v, q and out of one head as slices of wider rows, whose head stride is not head_dim."""
+    banner("cache and attention: one head, slices of wider rows")
+    c = Case(G, [(3, 40), (1, 70)], 1, 1, 64, 16, 8, seed=31)
+    wide = torch.randn(4, 1, 3 * 64, device=dev()).to(torch.bfloat16)
+    k, v = wide[..., 64:128], wide[..., 128:]
+    slots = torch.tensor([3, 17, 30, 5], device=dev())
+    caches = [G.QuantizedCache.empty(4, 16, 1, 64, 8, dev()) for _ in range(2)]
+    G.gptq_cache_write(caches[0], k, v, slots)
+    G.gptq_cache_write(caches[1], k.contiguous(), v.contiguous(), slots)
+    for a, b in zip((caches[0].k_codes, caches[0].v_codes, caches[0].k_scales, caches[0].v_scales),
+                    (caches[1].k_codes, caches[1].v_codes, caches[1].k_scales, caches[1].v_scales)):
+        assert torch.equal(a, b) and a.any()
+    wide[..., :64] = c.q
+    out = torch.zeros(4, 1, 128, dtype=torch.bfloat16, device=dev())
+    G.gptq_cache_attention(wide[..., :64], c.cache, *c.args, out=out[..., 64:])
+    assert torch.equal(out[..., 64:], G.gptq_cache_attention(c.q, c.cache, *c.args)) and not out[..., :64].any()
+    two = torch.randn(4, 2, 128, device=dev()).to(torch.bfloat16)[..., :64]     # of two heads it matters
+    with pytest.raises(ValueError, match="contiguous"):
+        G.gptq_cache_attention(two, c.cache, *c.args)
