@@ -400,7 +400,8 @@ typedef struct {
  *   slots    [n_tokens] int64; a slot outside [0, n_pages * page_size) is
  *            skipped (-1 marks padding).  Slots of one call have to differ: of
  *            tokens with the same slot, codes and scale may come from different ones
- * 0 <= n_tokens <= 2^30, n_tokens * n_kv_heads <= 2^33.
+ * 0 <= n_tokens <= 2^30, and n_tokens * n_kv_heads * P <= 2^37 - 2^13 with P =
+ * head_dim rounded up to a power of two (one launch; gptq_cache_read too).
  */
 gptq_status gptq_cache_write(const gptq_cache* cache, const void* k, const void* v, int32_t xt, int64_t n_tokens,
                              int64_t ldk, int64_t ldv, const int64_t* slots, void* stream);

@@ -60,6 +60,14 @@ bool cache_shape(const gptq_cache* c, gptq::CacheShape* out) {
   return true;
 }
 
+// A launch has fewer than 2^32 threads along x; the cache kernels give each row of
+// head_dim values, rounded up to a power of two P, P / 8 lanes for every four rows.
+bool cache_rows_ok(const gptq::CacheShape& c, int64_t n_tokens) {
+  int64_t p = 16;
+  while (p < c.hd) p *= 2;
+  return n_tokens * c.n_kv * p <= (int64_t{1} << 37) - (int64_t{1} << 13);  // n_tokens <= 2^30, n_kv <= 2^16: no overflow
+}
+
 }  // namespace
 
 extern "C" {
@@ -284,7 +292,7 @@ gptq_status gptq_cache_write(const gptq_cache* cache, const void* k, const void*
   gptq::CacheShape c;
   if (!cache_shape(cache, &c) || (xt != GPTQ_F32 && xt != GPTQ_BF16) || !rows_ok(n_tokens)) return GPTQ_ERR_INVALID_ARG;
   const int64_t vec = (xt == GPTQ_BF16) ? 8 : 4, width = int64_t{c.n_kv} * c.hd;
-  if (ldk < width || ldv < width || ldk % vec != 0 || ldv % vec != 0 || n_tokens * c.n_kv > (int64_t{1} << 33))
+  if (ldk < width || ldv < width || ldk % vec != 0 || ldv % vec != 0 || !cache_rows_ok(c, n_tokens))
     return GPTQ_ERR_INVALID_ARG;
   if (n_tokens == 0) return GPTQ_OK;
   if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return GPTQ_ERR_INVALID_ARG;
@@ -297,7 +305,7 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64
                             void* stream) {
   gptq::CacheShape c;
   if (!cache_shape(cache, &c) || (yt != GPTQ_F32 && yt != GPTQ_BF16) || !rows_ok(n_tokens)) return GPTQ_ERR_INVALID_ARG;
-  if (n_tokens * c.n_kv > (int64_t{1} << 33)) return GPTQ_ERR_INVALID_ARG;
+  if (!cache_rows_ok(c, n_tokens)) return GPTQ_ERR_INVALID_ARG;
   if (n_tokens == 0) return GPTQ_OK;
   if (!k || !v || !slots || !aligned16(k) || !aligned16(v)) return GPTQ_ERR_INVALID_ARG;
   return from_hip(gptq::cache_read_launch(c, cache->k_codes, cache->v_codes, cache->k_scales, cache->v_scales, slots,

@@ -199,3 +199,14 @@ def test_workspace_bytes(L):
                  torch.empty((8, 8)).t()):
         with pytest.raises(ValueError, match="contiguous"):
             L._ws_bytes(view)
+
+
+@pytest.mark.parametrize("head_dim", [16, 32, 48, 80, 128, 144, 256])
+def test_cache_calls_refuse_more_than_a_launch(L, head_dim):
+    """Sizes whose launch would have 2^32 threads are refused, not left to fail."""
+    lib, ref = L._lib(), ctypes.byref(_cache(L, n_kv_heads=4096, head_dim=head_dim))
+    p = max(16, 1 << (head_dim - 1).bit_length())
+    n = ((1 << 37) - (1 << 13)) // (4096 * p) + 1
+    width = 4096 * head_dim
+    assert lib.gptq_cache_write(ref, FAKE, FAKE, 1, n, width, width, FAKE, None) == 1
+    assert lib.gptq_cache_read(ref, FAKE, n, FAKE, FAKE, 1, None) == 1
