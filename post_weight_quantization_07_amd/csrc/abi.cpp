@@ -313,21 +313,29 @@ gptq_status gptq_cache_read(const gptq_cache* cache, const int64_t* slots, int64
 }
 
 namespace {
-// a launch has fewer than 2^32 threads: at most 2^23 tiles of 128 rows, or three
-// per (sequence, key head) of fewer rows, and a workgroup of 256 for each
-bool attention_sizes(const gptq::CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t pages_per_seq) {
-  return n_heads >= 1 && n_heads % c.n_kv == 0 && rows_ok(n_tokens) && n_tokens * n_heads < (int64_t{1} << 30) &&
-         n_seq >= 0 && n_seq <= (1 << 20) && int64_t{n_seq} * c.n_kv <= (int64_t{1} << 21) && pages_per_seq >= 1 &&
-         pages_per_seq * c.page <= (int64_t{1} << 30);
+// The plan of a call within the header's limits whose launch has fewer than 2^32
+// threads: of up to 64 rows a (sequence, key head) there are at most 64 / 16 + 1 tiles (heads
+// wider than 128; 64 / 32 + 1 otherwise), which 2^21 of those keep below it, and
+// of more rows tiles of 128, fewer than 2^23 + 2^21.
+bool attention_plan_of(const gptq::CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t pages_per_seq,
+                       gptq::AttnPlan* plan) {
+  if (n_heads < 1 || n_heads % c.n_kv != 0 || !rows_ok(n_tokens) || n_tokens * n_heads >= (int64_t{1} << 30) || n_seq < 0 ||
+      n_seq > (1 << 20) || int64_t{n_seq} * c.n_kv > (int64_t{1} << 21) || pages_per_seq < 1 ||
+      pages_per_seq * c.page > (int64_t{1} << 30))
+    return false;
+  *plan = gptq::AttnPlan{};
+  if (n_tokens == 0 || n_seq == 0) return true;
+  *plan = gptq::attention_plan(c, n_tokens, n_heads, n_seq, pages_per_seq, device_cus());
+  return plan->blocks * 256 < (int64_t{1} << 32);
 }
 }  // namespace
 
 size_t gptq_attention_workspace_size(const gptq_cache* cache, int64_t n_tokens, int32_t n_heads, int32_t n_seq,
                                      int64_t pages_per_seq) {
   gptq::CacheShape c;
-  if (!cache_shape(cache, &c) || !attention_sizes(c, n_tokens, n_heads, n_seq, pages_per_seq)) return 0;
-  if (n_tokens == 0 || n_seq == 0) return 0;
-  return gptq::attention_plan(c, n_tokens, n_heads, n_seq, pages_per_seq, device_cus()).ws_bytes;
+  gptq::AttnPlan plan;
+  if (!cache_shape(cache, &c) || !attention_plan_of(c, n_tokens, n_heads, n_seq, pages_per_seq, &plan)) return 0;
+  return plan.ws_bytes;
 }
 
 gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
@@ -337,12 +345,12 @@ gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t
   gptq::CacheShape c;
   if (!cache_shape(cache, &c) || qt != GPTQ_BF16 || !(scale > 0.0f && scale <= 3.402823466e38f))
     return GPTQ_ERR_INVALID_ARG;
-  if (!attention_sizes(c, n_tokens, n_heads, n_seq, pages_per_seq)) return GPTQ_ERR_INVALID_ARG;
+  gptq::AttnPlan plan;
+  if (!attention_plan_of(c, n_tokens, n_heads, n_seq, pages_per_seq, &plan)) return GPTQ_ERR_INVALID_ARG;
   const int64_t width = int64_t{n_heads} * c.hd;
   if (ldq < width || ldo < width || ldq % 8 != 0 || ldo % 8 != 0) return GPTQ_ERR_INVALID_ARG;
   if (n_tokens == 0 || n_seq == 0) return GPTQ_OK;
   if (!q || !out || !page_table || !q_starts || !kv_lens || !aligned16(q) || !aligned16(out)) return GPTQ_ERR_INVALID_ARG;
-  const gptq::AttnPlan plan = gptq::attention_plan(c, n_tokens, n_heads, n_seq, pages_per_seq, device_cus());
   if (plan.ws_bytes > 0 && (!ws || ws_bytes < plan.ws_bytes || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
   return from_hip(gptq::attention_launch(plan, c, q, ldq, n_tokens, n_heads, cache->k_codes, cache->v_codes,
                                          cache->k_scales, cache->v_scales, page_table, pages_per_seq, q_starts, kv_lens,

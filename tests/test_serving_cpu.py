@@ -210,3 +210,12 @@ def test_cache_calls_refuse_more_than_a_launch(L, head_dim):
     width = 4096 * head_dim
     assert lib.gptq_cache_write(ref, FAKE, FAKE, 1, n, width, width, FAKE, None) == 1
     assert lib.gptq_cache_read(ref, FAKE, n, FAKE, FAKE, 1, None) == 1
+
+
+@pytest.mark.parametrize("head_dim,rows", [(64, 16), (64, 64), (256, 64), (256, 65), (128, 500)])
+def test_attention_plans_the_largest_batches(L, head_dim, rows):
+    """2^21 (sequence, key head) pairs, the most that are allowed, fit one launch at any number of rows."""
+    lib, ref = L._lib(), ctypes.byref(_cache(L, n_kv_heads=2, head_dim=head_dim))
+    tokens = min(rows * (1 << 20), (1 << 29) - 1)                    # two heads, a row each a token
+    assert lib.gptq_attention_workspace_size(ref, tokens, 2, 1 << 20, 64) > 0
+    assert lib.gptq_attention_workspace_size(ref, tokens, 2, (1 << 20) + 1, 64) == 0
