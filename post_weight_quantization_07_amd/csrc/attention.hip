@@ -518,7 +518,11 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
     float top = kNoMax;
 #pragma unroll
     for (int v = 0; v < NW; ++v) top = fmaxf(top, wm[v][16 * i + c]);
-    const float f = fast_exp2(m[i] - top), up = unit[i].up();
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < NW; ++v) sum += wl[v][16 * i + c] * fast_exp2(wm[v][16 * i + c] - top);
+    // divided by the weights' sum before the unit comes off: a mean of values fits where their sum may not
+    const float f = fast_exp2(m[i] - top) * (sum == 0.f ? 0.f : 1.f / sum), up = unit[i].up();
     // lane l: dims g HDP / 4 + r HDP / 16 + t
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -534,12 +538,6 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       const int row = e / (HDP / 4), d = (e % (HDP / 4)) * 4;
       const int r = r0 + 16 * i + row;
       if (r >= rows || d >= p.hd) continue;  // nor does the join read the others
-      float t2 = kNoMax;
-#pragma unroll
-      for (int v = 0; v < NW; ++v) t2 = fmaxf(t2, wm[v][16 * i + row]);
-      float sum = 0.f;
-#pragma unroll
-      for (int v = 0; v < NW; ++v) sum += wl[v][16 * i + row] * fast_exp2(wm[v][16 * i + row] - t2);
       f32x4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int v = 0; v < NW; ++v) {
@@ -550,13 +548,17 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
       if (!whole) {
         *reinterpret_cast<f32x4_t*>(part + (16 * i + row) * HDP + d) = o;
         if (d == 0) {
-          part[kM * HDP + 16 * i + row] = t2;  // kNoMax: saw nothing
-          part[kM * HDP + kM + 16 * i + row] = sum;
+          float t2 = kNoMax, all = 0.f;  // kNoMax: saw nothing
+#pragma unroll
+          for (int v = 0; v < NW; ++v) t2 = fmaxf(t2, wm[v][16 * i + row]);
+#pragma unroll
+          for (int v = 0; v < NW; ++v) all += wl[v][16 * i + row] * fast_exp2(wm[v][16 * i + row] - t2);
+          part[kM * HDP + 16 * i + row] = t2;
+          part[kM * HDP + kM + 16 * i + row] = all;
         }
       } else {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int tok = div_by(r, p.group_mul, p.group_shift);
-        const uint2 b = make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        const uint2 b = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
         *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo +
                                   static_cast<int64_t>(h * p.group + r - tok * p.group) * p.hd + d) = b;
       }
@@ -1108,6 +1110,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   l += __shfl_xor(l, 32);
   const int64_t slot = static_cast<int64_t>(w.slot + w.split) * p.n_kv + h;
   const float up = ProductUnit{ProductUnit::of(most)}.up();
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   if (!live) return;  // the join does not read such rows either
   if (w.n_split > 1) {
     if (static_cast<uint64_t>(slot) >= static_cast<uint64_t>(p.max_slots)) return;
@@ -1123,12 +1126,11 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       for (int a = 0; a < 4; ++a) {
         f32x4_t o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = acc[i][4 * a + e] * up;
+        for (int e = 0; e < 4; ++e) o[e] = acc[i][4 * a + e] * inv * up;
         *reinterpret_cast<f32x4_t*>(part + row * HDP + 32 * i + 8 * a + 4 * hf) = o;
       }
     return;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t* dst = p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo + static_cast<int64_t>(h * p.group + qh) * p.hd;
 #pragma unroll
   for (int i = 0; i < kDb; ++i)
@@ -1141,8 +1143,9 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
     }
 }
 
-// Joins the splits of a tile, in their order.  One workgroup per (split tile, key
-// head) and 32 rows; the other tiles were written by the kernels above.
+// Joins the splits of a tile, in their order: means of values, by the sums of their
+// weights.  One workgroup per (split tile, key head) and 32 rows; the other tiles
+// were written by the kernels above.
 // Latency of the parts' loads bounds it: eight parts are in flight at a time
 // (32 tiles of 25 parts: 6.9 us; 16.4 us one at a time), and a tile of 128 rows
 // goes to four workgroups (11 sequences of 80 to 160 rows over 3600 to 18000 keys, 3
@@ -1184,26 +1187,31 @@ __global__ __launch_bounds__(512) void attn_join_kernel(AttnParams p) {
         if (s0 + j >= w.n_split) m[j] = kNegInf;
         mx = fmaxf(mx, m[j]);
       }
-      const float f0 = fast_exp2(top - mx);
+      sum *= fast_exp2(top - mx);
       top = mx;
-      sum *= f0;
+      float all = sum;
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        l[j] = s0 + j < w.n_split ? l[j] * fast_exp2(m[j] - top) : 0.f;  // 0 for a part that saw nothing
+        all += l[j];
+      }
+      const float inv = all == 0.f ? 0.f : 1.f / all, f0 = sum * inv;
+      sum = all;
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= f0;
 #pragma unroll
       for (int j = 0; j < kAt; ++j) {
-        const float f = fast_exp2(m[j] - top);  // 0 for a part that saw nothing
+        const float f = l[j] * inv;
         if (s0 + j < w.n_split) {
-          sum += f * l[j];
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] += f * v[j][i];
         }
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const int tok = div_by(r, p.group_mul, p.group_shift);
     *reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(w.s.q0 + tok) * p.ldo +
                               static_cast<int64_t>(h * p.group + r - tok * p.group) * p.hd + d) =
-        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+        make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
   }
 }
 

@@ -144,3 +144,18 @@ def test_values_of_every_size(G, bits):
                 c.scales[1][c.table[0, j // page], :, j % page] *= 0.0 if j % 7 == 3 else np.float32(2.0 ** power[j])
             upload(G, c)
             check(c, G.gptq_cache_attention(c.q, c.cache, *c.args))
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", SHAPES)
+def test_values_near_the_largest(G, lens, heads, kv, hd, page, bits):
+    """Values up to 1.5e38: their mean is finite, their sum is not."""
+    banner(f"attention: values near the largest, {lens} {heads}/{kv}x{hd} int{bits}")
+    c = Case(G, lens, heads, kv, hd, page, bits, seed=25)
+    top = 127 if bits == 8 else 7
+    c.codes[1] = S.pack_rows(np.full((*c.scales[1].shape, hd), top), bits)
+    c.scales[1] = np.where(np.isnan(c.scales[1]), np.nan, 2.0 ** (120 if bits == 8 else 124)).astype(np.float32)
+    upload(G, c)
+    out = G.gptq_cache_attention(c.q, c.cache, *c.args)
+    assert torch.isfinite(out).all()
+    check(c, out)
