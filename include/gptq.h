@@ -348,8 +348,9 @@ gptq_status gptq_integer_weight(const int32_t* qweight, const int32_t* zeros, in
  * y = x W^T in 8-bit integers, a scale per token and per output channel:
  *   y[t, n] = x_scale[t] w_scale[n] (sum_k cx[t, k] w[n, k] - offset[n] sum_k cx[t, k])
  * The sums are exact 32-bit integers; the result is rounded when the sum
- * becomes fp32, at each scale, and to y's type (relative 3 2^-24, and 2^-9 for
- * bf16).  Deterministic, and independent of how the work is split.
+ * becomes fp32, at each scale, and to y's type (relative 3 2^-24, and 2^-8 more
+ * for bf16, while the sum times x_scale stays in fp32's normal range).
+ * Deterministic, and independent of how the work is split.
  *   x        [m, ldx]: bf16 or fp32, quantized as by gptq_quantize_tokens in
  *            the workspace (x_scales and x_sums are not read); or GPTQ_I8 codes
  *            with x_scales [m] and, for layers with offsets, x_sums [m].

@@ -272,8 +272,8 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 // l % 16, dims g HDP / 4 ... in order.
 //
 // Bound: HBM, by the loads that fit in flight beside the operands' registers.
-// 64 ragged sequences (292 MB of 8-bit keys and values) 59 us, 4.9 TB/s; four of
-// 131000 keys at 4 bits (570 MB) 130 us, 4.4 TB/s; one of 1000 keys 6.5 us, four
+// 64 ragged sequences (292 MB of 8-bit keys and values) 56.5 us, 5.2 TB/s; four of
+// 131000 keys at 4 bits (570 MB) 118 us, 4.8 TB/s; one of 1000 keys 6.6 us, four
 // dependent trips to memory.  Four waves a workgroup and four workgroups a CU:
 // eight waves and two took 83 us for the ragged batch.
 constexpr int kSplitWaves = 4;
@@ -442,7 +442,7 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
         const float alpha = fast_exp2(m[i] - mn);
         float top = alpha * __uint_as_float(static_cast<uint32_t>(unit[i].e - kRoom) << 23);  // the largest product before
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)  // (a select here costs registers that 8-bit heads of 128 do not have: 69 -> 109 us)
           if (!masked || see[j]) top = fmaxf(top, fabsf(fast_exp2(s[i][j] - mn) * vs[j >> 2][j & 3]));
         const int e = min(ProductUnit::of(max_over_groups(top)) + kRoom, ProductUnit::kMost);
         const float f = alpha * exp2_int(unit[i].e - e);
@@ -598,10 +598,12 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 // conversion and half a sum.
 //
 // Bound: the products, the exponentials and the codes' conversion share the
-// waves' issue slots: a 64-key tile of 128 rows x 128 dims takes about 3740 cycles,
-// of which the products of a CU's two workgroups need 2048.  Four prompts of 2048
-// tokens, 32 heads of 128: 206 us (0.67 PFLOP/s of the causal half); long ones come
-// to 0.88 PFLOP/s.
+// waves' issue slots.  Four prompts of 2048 tokens, 32 heads of 128: 205 us (0.67
+// PFLOP/s of the causal half; the matrix cores are busy 28% of the cycles of a profiled run); one
+// of 16384 tokens 0.86 PFLOP/s.
+// A wave with rows past the sequence's last keeps to careful_tile: such rows have no
+// maximum (11 sequences of 80 to 160 tokens over 3600 to 18000 keys, 3 heads of 96:
+// 80 us; their bytes and products need 11).
 constexpr int kFrag = 1040;  // bytes of an operand in LDS
 constexpr float kGrow = 32768.f;
 constexpr float kAbove = 8.f;    // log2 of the largest weight when the maximum moves
@@ -1147,7 +1149,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
 // weights.  One workgroup per (split tile, key head) and 32 rows; the other tiles
 // were written by the kernels above.
 // Latency of the parts' loads bounds it: eight parts are in flight at a time
-// (32 tiles of 25 parts: 6.9 us; 16.4 us one at a time), and a tile of 128 rows
+// (32 tiles of 25 parts: 7.5 us; 16.4 us one at a time), and a tile of 128 rows
 // goes to four workgroups (11 sequences of 80 to 160 rows over 3600 to 18000 keys, 3
 // heads: 10.6 us, 32.9 in one; eight workgroups 7.7, but 2 us more where nothing is split).
 constexpr int kJoinRows = 32;
@@ -1242,14 +1244,14 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
   AttnPlan a{};
   const int64_t group = n_heads / c.n_kv;
   // Rows a sequence, on average: up to 16, one row block, for single tokens; up to
-  // 64, two row blocks that share the conversion of the keys (32 sequences of
-  // 4096 keys, 32 rows: 83 us in tiles of 16, 69 in tiles of 32; 48 rows over 2000
-  // keys: 13.4 us, 18.4 in tiles of 128; at 64 rows over 4096 keys 57.8 and 57.3).
+  // 64, two row blocks that share the conversion of the keys (in tiles of 16, 32 and
+  // 128, 8 key heads: 32 sequences of 32 rows over 4096 keys 90, 72 and 84 us, of 64
+  // rows 133, 103 and 101; but one sequence of 48 rows over 2000 keys 11.5, 15.6 and 19.9).
   // A batch that mixes the two goes by the average: 32 single tokens over 4096 keys
-  // with a prompt of 1024 take 147 us, 56 and 43 in two calls; launching both kernels
+  // with a prompt of 1024 take 135 us, 52 and 40 in two calls; launching both kernels
   // for every batch would cost short prompts two launches that find nothing.
-  // Heads wider than 128 have no registers for the second block (256 wide, over
-  // 4096 keys: 32 rows 148 us in tiles of 16, 278 in tiles of 128; 64 rows 109 and 168).
+  // Heads wider than 128 have no registers for the second block (256 wide, 16 sequences
+  // over 4096 keys: 32 rows 72 us in tiles of 16, 113 in tiles of 128; 64 rows 108 and 117).
   const int64_t per_seq = (n_tokens * group + n_seq - 1) / n_seq;
   a.tile_rows = per_seq > 64 ? 128 : per_seq > 16 && c.hd <= 128 ? 32 : 16;
   // split kernel: a little under the workgroups that fit (four a CU, two for wide

@@ -208,8 +208,8 @@ GPTQ_DEV void int_store(const IntParams& p, int64_t row, int64_t col, int acc, i
 // what the CUs load is x; R row blocks share each load of x where d_out gives
 // every CU a workgroup all the same (16 tokens through 28672 x 8192: 67 us with
 // R = 1, 63 with R = 4, 49 with x not read at all).
-// 16 tokens: 11008 x 4096 15.2 us (a kernel that only reads those 45 MB takes
-// 10 to 12), 8192 x 28672 57 us, 4.1 TB/s.  32 and 64 tokens of 11008 x 4096: 22 and 30 us.
+// 16 tokens: 11008 x 4096 15.1 us (a kernel that only reads those 45 MB takes
+// 12 to 15), 8192 x 28672 57 us, 4.1 TB/s.  32 and 64 tokens of 11008 x 4096: 22 and 30 us.
 // FUSED (one to four tokens): x is quantized here, by every workgroup for
 // itself and into LDS, while its first weights are on their way: one launch, and
 // reading the tokens again from L2 costs less than a second one (4096 x 4096: 7.2 us
@@ -435,7 +435,7 @@ void stream_go(const IntParams& p, int fused, hipStream_t st) {
 // LDS rows are 64 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 2) & 3), so
 // 16 lanes that read one chunk of 16 rows touch all 64 banks once.
 // Bound: the matrix cores, and the clock that they leave.  2048 x 28672 -> 8192 on
-// 256 x 256 tiles: 414 us, 2.32 POP/s.  Four waves of 128 x 128 read half the LDS
+// 256 x 256 tiles: 409 us, 2.35 POP/s, the matrix cores busy 62% of the cycles.  Four waves of 128 x 128 read half the LDS
 // bytes a product of 64 x 64; 128 x 128 tiles are for grids too small for the others
 // (509 x 11008 -> 4096: 36 us in four K slices, 1.28 POP/s; an eight-step ring, one
 // workgroup a CU, 38 us).
