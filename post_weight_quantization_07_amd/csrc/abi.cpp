@@ -321,7 +321,7 @@ bool attention_plan_of(const gptq::CacheShape& c, int64_t n_tokens, int32_t n_he
                        gptq::AttnPlan* plan) {
   if (n_heads < 1 || n_heads % c.n_kv != 0 || !rows_ok(n_tokens) || n_tokens * n_heads >= (int64_t{1} << 30) || n_seq < 0 ||
       n_seq > (1 << 20) || int64_t{n_seq} * c.n_kv > (int64_t{1} << 21) || pages_per_seq < 1 ||
-      pages_per_seq * c.page > (int64_t{1} << 30))
+      pages_per_seq > (int64_t{1} << 30) / c.page)
     return false;
   *plan = gptq::AttnPlan{};
   if (n_tokens == 0 || n_seq == 0) return true;

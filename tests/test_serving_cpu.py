@@ -219,3 +219,13 @@ def test_attention_plans_the_largest_batches(L, head_dim, rows):
     tokens = min(rows * (1 << 20), (1 << 29) - 1)                    # two heads, a row each a token
     assert lib.gptq_attention_workspace_size(ref, tokens, 2, 1 << 20, 64) > 0
     assert lib.gptq_attention_workspace_size(ref, tokens, 2, (1 << 20) + 1, 64) == 0
+
+
+@pytest.mark.parametrize("pages", [(1 << 26) + 1, 1 << 40, 1 << 59, 1 << 60, (1 << 63) - 1])
+def test_attention_refuses_longer_tables(L, pages):
+    """Tables past 2^30 keys of 16 a page, among them those whose key count passes 64 bits."""
+    lib, ref = L._lib(), ctypes.byref(_cache(L))
+    assert lib.gptq_attention_workspace_size(ref, 4, 8, 2, 1 << 26) > 0
+    assert lib.gptq_attention_workspace_size(ref, 4, 8, 2, pages) == 0
+    assert lib.gptq_cache_attention(ref, FAKE, 1, 4, 512, 8, FAKE, pages, FAKE, FAKE, 2, 0.125, FAKE, 512, FAKE, 1 << 40,
+                                    None) == 1
