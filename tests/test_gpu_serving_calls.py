@@ -77,3 +77,13 @@ def test_one_head_of_any_stride(G):
     two = torch.randn(4, 2, 128, device=dev()).to(torch.bfloat16)[..., :64]     # of two heads it matters
     with pytest.raises(ValueError, match="contiguous"):
         G.gptq_cache_attention(two, c.cache, *c.args)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("hd", [16, 48, 80, 112, 144, 176, 208, 240])
+def test_heads_of_an_odd_number_of_sixteens(G, hd, bits):
+    """Few and many rows over a cache without spare pages, whose last key ends the buffer."""
+    for lens, heads, kv in (([(1, 96)], 2, 2), ([(5, 64), (9, 32)], 4, 1), ([(90, 96)], 2, 1)):
+        banner(f"attention {lens} {heads}/{kv}x{hd} int{bits}, no spare pages")
+        c = Case(G, lens, heads, kv, hd, 32, bits, seed=41, extra=0)
+        c.check(G.gptq_cache_attention(c.q, c.cache, *c.args))
