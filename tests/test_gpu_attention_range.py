@@ -48,8 +48,9 @@ def upload(G, c):
     c.cache = G.QuantizedCache(*[d(x) for x in c.codes], *[d(x) for x in c.scales], c.bits)
 
 
-def check(c, out, same_scores=False):
-    """same_scores: the caller made all scores equal, so that q counts as zero."""
+def check(c, out, same_scores=False, last=0):
+    """same_scores: the caller made all scores equal, so that q counts as zero.  The `last` tokens of a sequence
+    are not looked at."""
     scale = c.hd ** -0.5
     got = out.double().cpu().numpy()
     for i, (n, length) in enumerate(c.lens):
@@ -59,6 +60,8 @@ def check(c, out, same_scores=False):
             if same_scores:
                 k = (k[0], np.ones_like(k[1]))
             for t in (np.arange(n) if n <= 24 else np.unique(np.r_[0:4, 30:34, n // 2:n // 2 + 3, n - 4:n])):
+                if t >= n - last:
+                    continue
                 seen = length - n + t + 1
                 q = c.q_host[a + t, h] * (0.0 if same_scores else 1.0)
                 k1, v1 = (k[0][:seen], k[1][:seen]), (v[0][:seen], v[1][:seen])
@@ -159,3 +162,31 @@ def test_values_near_the_largest(G, lens, heads, kv, hd, page, bits):
     out = G.gptq_cache_attention(c.q, c.cache, *c.args)
     assert torch.isfinite(out).all()
     check(c, out)
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("lens,heads,kv,hd,page", [x for x in SHAPES if x[0][0][0] > 2])
+def test_scales_that_are_not_finite(G, lens, heads, kv, hd, page, zeros, bits):
+    """A key or value scale of NaN makes the tokens that see it NaN, and no others; also among values some of which
+    are zero.  An infinite value scale holds infinities, and NaN for codes of 0, so what sees it is not finite; an
+    infinite key scale gives NaN or the value of a key with all the weight."""
+    n, length = lens[0]
+    for which in (0, 1):
+        for bad in (np.nan, np.inf):
+            banner(f"attention: {'kv'[which]} scale {bad}, zeros {zeros}, {lens} {heads}/{kv}x{hd} int{bits}")
+            c = Case(G, lens, heads, kv, hd, page, bits, seed=26)
+            if zeros:
+                for j in range(0, length, 5):
+                    c.scales[1][c.table[0, j // page], :, j % page] = 0.0
+            key = length - 2                              # the last two tokens see it
+            c.scales[which][c.table[0, key // page], :, key % page] = bad
+            upload(G, c)
+            out = G.gptq_cache_attention(c.q, c.cache, *c.args)
+            if np.isnan(bad):
+                assert torch.isnan(out[-2:]).all()
+            elif which == 1:
+                assert not torch.isfinite(out[-2:]).any()
+            assert torch.isfinite(out[:-2]).all()
+            c.scales[which][c.table[0, key // page], :, key % page] = 1.0      # hidden from the tokens that are checked
+            check(c, out, last=2)
