@@ -1057,7 +1057,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
         weights(s0, 0, 16 * x / kSteps, 16 * (x + 1) / kSteps, l0);
         __builtin_amdgcn_sched_barrier(0);
       }
-      // a lane's 16 weights sum to more than 2^10: one may be
+      // a lane's 16 weights sum to more than 2^15: one may be
       fits = !__any(l0 > kGrow);
       if (!fits) break;
       l += l0;
