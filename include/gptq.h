@@ -31,6 +31,13 @@
  *                             a paged key/value cache in 8- or 4-bit codes
  *   gptq_cache_attention      attention of new tokens over that cache
  *
+ * and what stands between those in a layer of a model:
+ *
+ *   gptq_norm_tokens          root-mean-square norm, with the residual's addition, into 8-bit codes
+ *   gptq_integer_linear       the integer product with bias, activation and residual
+ *   gptq_integer_gated        act(x G^T) * (x U^T): both products of a gated feed-forward layer at once
+ *   gptq_cache_attention_scores   attention with capped scores, a bias by distance, a prefix
+ *
  * Conventions shared by every call
  *   - All array pointers are DEVICE pointers on the current HIP device; the
  *     caller owns every buffer (inputs, outputs, workspaces).  The library
@@ -75,7 +82,7 @@ typedef enum {
 typedef enum {
   GPTQ_F32 = 0,
   GPTQ_BF16 = 1,
-  GPTQ_I8 = 2 /* codes of gptq_quantize_tokens; gptq_integer_matmul's x only */
+  GPTQ_I8 = 2 /* codes of gptq_quantize_tokens; x of the products in integers only */
 } gptq_dtype;
 
 /*
@@ -369,6 +376,81 @@ gptq_status gptq_integer_matmul(const void* x, int32_t xt, const float* x_scales
                                 const int32_t* w_offsets_or_null, int64_t d_out, void* y, int32_t yt, void* ws,
                                 size_t ws_bytes, void* stream);
 
+/* What a product's sums go through, passed as int32_t. */
+typedef enum {
+  GPTQ_ACT_NONE = 0,
+  GPTQ_ACT_RELU = 1,      /* max(z, 0) */
+  GPTQ_ACT_GELU = 2,      /* z Phi(z), Phi the normal distribution */
+  GPTQ_ACT_GELU_TANH = 3, /* z / (1 + e^(-2 u)), u = sqrt(2 / pi) (z + 0.044715 z^3) */
+  GPTQ_ACT_SILU = 4       /* z / (1 + e^-z) */
+} gptq_activation;
+
+/* A layer as gptq_integer_matmul reads it, and a bias. */
+typedef struct {
+  const int8_t* w;        /* [d_out, d_in], 16-byte aligned */
+  const float* scales;    /* [d_out] */
+  const int32_t* offsets; /* [d_out] in [-128, 128], or null */
+  const float* bias;      /* [d_out], or null */
+} gptq_integer_layer;
+
+/*
+ * gptq_integer_matmul with what follows it in a model, in the same kernel:
+ *   y[t, n] = act(z[t, n] + bias[n]) + residual[t, n],  z = gptq_integer_matmul's value
+ * z is taken in fp32 (relative 3 2^-24), as are the sums and the activation; y
+ * is rounded once to its type.
+ *   residual_or_null  [m, ldr] bf16 or fp32 (rt), d_out <= ldr <= 2^20.  y may be the residual
+ *            itself (same type, ldr = d_out or m = 1) and may not touch it otherwise
+ *   Others, workspace, limits and errors as for gptq_integer_matmul.  With
+ *   neither bias, activation nor residual it is that call.
+ */
+gptq_status gptq_integer_linear(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                                int64_t d_in, int64_t ldx, const gptq_integer_layer* layer, int64_t d_out,
+                                int32_t activation, const void* residual_or_null, int32_t rt, int64_t ldr, void* y,
+                                int32_t yt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The first half of a gated feed-forward layer in one kernel: x is read (and, if
+ * it is not codes, quantized) once for both products, and neither leaves the chip:
+ *   y[t, n] = act(zg[t, n] + bias_g[n]) (zu[t, n] + bias_u[n])
+ * zg, zu the values of gptq_integer_matmul for the two layers, in fp32; y is
+ * rounded once to its type.  The layers share d_in and d_out.
+ *   x_sums   for GPTQ_I8 x: needed if either layer has offsets
+ *   ws       device workspace of gptq_integer_gated_workspace_size(m, xt, d_in, d_out) bytes
+ * Requires d_out <= 2^19; others as for gptq_integer_matmul.
+ */
+size_t gptq_integer_gated_workspace_size(int64_t m, int32_t xt, int64_t d_in, int64_t d_out);
+gptq_status gptq_integer_gated(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                               int64_t d_in, int64_t ldx, const gptq_integer_layer* gate, const gptq_integer_layer* up,
+                               int64_t d_out, int32_t activation, void* y, int32_t yt, void* ws, size_t ws_bytes,
+                               void* stream);
+
+/*
+ * Root-mean-square norm of tokens, with the addition before it and the integer
+ * codes after it:
+ *   h = x + residual (x without one),  s = 1 / sqrt(mean h^2 + eps),  y = s h weight
+ * h and u = h weight are rounded to fp32, the squares are summed in fp64.
+ *   x        [n_tokens, ldx] bf16 or fp32, the first d entries of a row;
+ *            residual_or_null [n_tokens, ldr] likewise (rt)
+ *   weight_or_null  [d] bf16 or fp32 (wt); null: ones
+ *   eps      > 0 and finite
+ *   sum_or_null  [n_tokens, lds]: h, rounded to the residual's type.  It may be
+ *            the residual or, with x of that type, x (same address and row
+ *            stride); it needs a residual
+ *   y_or_null    [n_tokens, d] bf16 or fp32 (yt): y, rounded once
+ *   codes_or_null, scales, sums_or_null  y's rows as gptq_quantize_tokens holds
+ *            them (y itself, before any rounding to yt): the codes are those of u's row,
+ *            which has the same ones, the scale is s max|u| / 127.
+ * At least one of y and codes.  A row with a NaN or an infinity in u has scale
+ * NaN and codes 0.  Outputs may not touch the inputs or each other but for
+ * `sum` as said.  Any d up to 2^20 and any alignment (16-byte aligned rows and d % 8 == 0
+ * are read and written in whole vectors); row strides at most 2^31;
+ * 0 <= n_tokens <= 2^30.
+ */
+gptq_status gptq_norm_tokens(const void* x, int32_t xt, int64_t n_tokens, int64_t d, int64_t ldx, const void* residual_or_null,
+                             int32_t rt, int64_t ldr, const void* weight_or_null, int32_t wt, float eps, void* sum_or_null,
+                             int64_t lds, void* y_or_null, int32_t yt, int8_t* codes_or_null, float* scales,
+                             int32_t* sums_or_null, void* stream);
+
 /*
  * A paged key/value cache in integer codes.  A row (one head of one token's
  * key or value) is held as codes and one fp32 scale by the rule of
@@ -452,6 +534,29 @@ gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t
                                  int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
                                  const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale, void* out,
                                  int64_t ldo, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gptq_cache_attention for models that change the scores before the softmax or
+ * let every token see a prefix.  With a = kv_lens[i] - n + t the place of new
+ * token t and z_j = scale q . k_j:
+ *   s_j = cap tanh(z_j / cap) - slopes[head] |a - j|   (cap 0: z_j)
+ * and the token sees the keys j <= a and j < prefix_lens[i].
+ *   cap      0, or in [2^-20, 2^20]; a capped score is off by 2^-20 relative more
+ *   slopes   [n_heads] fp32, finite, or null; a bias that leaves fp32's range hides the key
+ *   prefix_lens  [n_seq] int32, clamped to [0, kv_lens[i]], or null
+ * A token that sees no key (kv_len < n, no prefix) gets zeros.  Everything else
+ * as for gptq_cache_attention, its workspace too; with nothing set it is that call.
+ */
+typedef struct {
+  float cap;
+  const float* slopes;
+  const int32_t* prefix_lens;
+} gptq_scores;
+gptq_status gptq_cache_attention_scores(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
+                                        int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
+                                        const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale,
+                                        const gptq_scores* scores, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                                        void* stream);
 
 /*
  * Per-phase launch timing, a measurement aid (not part of the solve; the pages

@@ -9,7 +9,9 @@ for one linear layer, and solve_layers_shared, which quantizes several layers
 that read the same input (q/k/v, gate/up) against one Hessian and one factor.
 For serving quantized layers: gptq_integer_matmul (8-bit integers, with
 gptq_quantize_tokens and gptq_integer_weight), QuantizedCache with
-gptq_cache_write / gptq_cache_read, and gptq_cache_attention over it.
+gptq_cache_write / gptq_cache_read, and gptq_cache_attention over it; between
+them gptq_norm_tokens (norm with the residual's addition, into 8-bit codes) and
+gptq_integer_gated (both products of a gated feed-forward layer).
 All arithmetic runs in libgptq.so's HIP kernels.
 """
 from __future__ import annotations
@@ -20,8 +22,8 @@ import torch
 
 from ._lib import (EXPORTS, GptqError, NonFiniteHessian, NotPositiveDefinite, QuantizeConfig,  # noqa: F401
                    QuantizedCache, gptq_attention_workspace_size, gptq_cache_attention, gptq_cache_read,
-                   gptq_cache_write, gptq_integer_matmul, gptq_integer_weight, gptq_integer_workspace_size,
-                   gptq_quantize_tokens, gptq_dequant_matmul, gptq_dequant_matmul_noalloc, gptq_dequant_matmul_ordered,
+                   gptq_cache_write, gptq_integer_gated, gptq_integer_gated_workspace_size, gptq_integer_matmul,
+                   gptq_integer_weight, gptq_integer_workspace_size, gptq_norm_tokens, gptq_quantize_tokens, gptq_dequant_matmul, gptq_dequant_matmul_noalloc, gptq_dequant_matmul_ordered,
                    gptq_dequant_noalloc_need, gptq_dequant_order, gptq_dequant_ordered_workspace_size,
                    gptq_dequant_scratch_bytes, gptq_dequant_workspace_size, gptq_hessian_accumulate,
                    gptq_hessian_workspace_size, gptq_pack, gptq_prepare_hinv, gptq_prepare_workspace_size,
@@ -32,7 +34,8 @@ __all__ = ["QuantizeConfig", "GptqError", "NotPositiveDefinite", "NonFiniteHessi
            "gptq_prepare_workspace_size", "gptq_workspace_size", "gptq_dequant_matmul", "gptq_dequant_workspace_size",
            "gptq_dequant_order", "gptq_dequant_matmul_ordered", "gptq_dequant_ordered_workspace_size",
            "gptq_dequant_matmul_noalloc", "gptq_dequant_noalloc_need", "gptq_dequant_scratch_bytes", "gptq_quantize_tokens",
-           "gptq_integer_weight", "gptq_integer_workspace_size", "gptq_integer_matmul", "QuantizedCache",
+           "gptq_integer_weight", "gptq_integer_workspace_size", "gptq_integer_matmul", "gptq_integer_gated",
+           "gptq_integer_gated_workspace_size", "gptq_norm_tokens", "QuantizedCache",
            "gptq_cache_write", "gptq_cache_read", "gptq_attention_workspace_size", "gptq_cache_attention", "solve_layer",
            "solve_layers_shared", "library_path"]
 

@@ -10,7 +10,7 @@ import ctypes
 import os
 from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 from dataclasses import dataclass
-from typing import Optional
+from typing import Mapping, Optional
 
 import torch
 
@@ -25,8 +25,10 @@ EXPORTS = ("gptq_config_validate", "gptq_status_string", "gptq_hessian_workspace
            "gptq_dequant_matmul", "gptq_dequant_order", "gptq_dequant_ordered_workspace_size",
            "gptq_dequant_matmul_ordered", "gptq_dequant_scratch_bytes", "gptq_dequant_noalloc_need",
            "gptq_dequant_matmul_noalloc", "gptq_quantize_tokens", "gptq_integer_weight",
-           "gptq_integer_workspace_size", "gptq_integer_matmul", "gptq_cache_write", "gptq_cache_read",
-           "gptq_attention_workspace_size", "gptq_cache_attention", "gptq_phase_timing", "gptq_phase_count", "gptq_phase_name",
+           "gptq_integer_workspace_size", "gptq_integer_matmul", "gptq_integer_linear",
+           "gptq_integer_gated_workspace_size", "gptq_integer_gated", "gptq_norm_tokens", "gptq_cache_write",
+           "gptq_cache_read", "gptq_attention_workspace_size", "gptq_cache_attention", "gptq_cache_attention_scores",
+           "gptq_phase_timing", "gptq_phase_count", "gptq_phase_name",
            "gptq_phase_read")
 
 
@@ -56,6 +58,14 @@ class _CCache(ctypes.Structure):
                 ("v_scales", c_void_p)]
 
 
+class _CLayer(ctypes.Structure):
+    _fields_ = [("w", c_void_p), ("scales", c_void_p), ("offsets", c_void_p), ("bias", c_void_p)]
+
+
+class _CScores(ctypes.Structure):
+    _fields_ = [("cap", c_float), ("slopes", c_void_p), ("prefix_lens", c_void_p)]
+
+
 _LIB = None
 
 
@@ -68,6 +78,7 @@ def _lib():
         lib = ctypes.CDLL(LIB_PATH)
         vp, i64, sz = c_void_p, c_int64, c_size_t
         cfgp, cachep = ctypes.POINTER(_CConfig), ctypes.POINTER(_CCache)
+        layerp, scoresp = ctypes.POINTER(_CLayer), ctypes.POINTER(_CScores)
         sig = {
             "gptq_config_validate": (c_int32, [cfgp]),
             "gptq_status_string": (ctypes.c_char_p, [c_int32]),
@@ -95,11 +106,20 @@ def _lib():
             "gptq_integer_workspace_size": (sz, [i64, c_int32, i64, i64]),
             "gptq_integer_matmul": (c_int32, [vp, c_int32, vp, vp, i64, i64, i64, vp, vp, vp, i64, vp, c_int32, vp, sz,
                                               vp]),
+            "gptq_integer_linear": (c_int32, [vp, c_int32, vp, vp, i64, i64, i64, layerp, i64, c_int32, vp, c_int32, i64, vp,
+                                              c_int32, vp, sz, vp]),
+            "gptq_integer_gated_workspace_size": (sz, [i64, c_int32, i64, i64]),
+            "gptq_integer_gated": (c_int32, [vp, c_int32, vp, vp, i64, i64, i64, layerp, layerp, i64, c_int32, vp, c_int32, vp,
+                                             sz, vp]),
+            "gptq_norm_tokens": (c_int32, [vp, c_int32, i64, i64, i64, vp, c_int32, i64, vp, c_int32, c_float, vp, i64, vp,
+                                           c_int32, vp, vp, vp, vp]),
             "gptq_cache_write": (c_int32, [cachep, vp, vp, c_int32, i64, i64, i64, vp, vp]),
             "gptq_cache_read": (c_int32, [cachep, vp, i64, vp, vp, c_int32, vp]),
             "gptq_attention_workspace_size": (sz, [cachep, i64, c_int32, c_int32, i64]),
             "gptq_cache_attention": (c_int32, [cachep, vp, c_int32, i64, i64, c_int32, vp, i64, vp, vp, c_int32, c_float,
                                                vp, i64, vp, sz, vp]),
+            "gptq_cache_attention_scores": (c_int32, [cachep, vp, c_int32, i64, i64, c_int32, vp, i64, vp, vp, c_int32, c_float,
+                                                      scoresp, vp, i64, vp, sz, vp]),
             "gptq_phase_timing": (c_int32, [c_int32]),
             "gptq_phase_count": (c_int32, []),
             "gptq_phase_name": (ctypes.c_char_p, [c_int32]),
@@ -530,17 +550,17 @@ def gptq_integer_workspace_size(m: int, dtype: torch.dtype, d_in: int, d_out: in
     return int(_lib().gptq_integer_workspace_size(m, code, d_in, d_out))
 
 
-def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Optional[torch.Tensor] = None,
-                        out_dtype: torch.dtype = torch.float32, y: Optional[torch.Tensor] = None,
-                        ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """y [m, d_out] = x W^T in 8-bit integers, W = w_scales (w - offsets) as laid
-    out by gptq_integer_weight (offsets None: all zero).  x is [m, d_in] bf16 or
-    fp32 (rows may be strided), quantized per token on the way, or what
-    gptq_quantize_tokens returned for it."""
-    if stream is not None:
-        with _on_stream(stream):
-            return gptq_integer_matmul(x, w, w_scales, offsets, out_dtype, y, ws)
-    what = "gptq_integer_matmul"
+ACTIVATIONS = {None: 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}  # gptq_activation
+
+
+def _activation(what: str, name: Optional[str]) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"{what}: unknown activation {name!r}: expected one of {[a for a in ACTIVATIONS if a]} or None")
+    return ACTIVATIONS[name]
+
+
+def _integer_x(what: str, x, offsets: bool):
+    """(x, its type code, scales, sums) of what a product in integers takes as x."""
     x_scales = x_sums = None
     if isinstance(x, tuple):
         x, x_scales, x_sums = x
@@ -550,36 +570,170 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
                 or not x_scales.is_contiguous() or (x_sums is not None and (x_sums.shape != (m,)
                                                     or x_sums.dtype != torch.int32 or not x_sums.is_contiguous()))):
             raise ValueError(f"{what}: expected the codes, scales and sums of gptq_quantize_tokens")
-        if offsets is not None and x_sums is None:
+        if offsets and x_sums is None:
             raise ValueError(f"{what}: a layer with offsets needs the sums of the codes")
     else:
         code = _type_code(what, x.dtype)
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError(f"{what}: x must be 2-D with unit column stride")
-    dev = _on_device(what, x, w, w_scales, offsets, x_scales, x_sums, y, ws)
-    m, d_in = x.shape
-    d_out = w.shape[0]
+    return x, code, x_scales, x_sums
+
+
+def _integer_layer_ok(what: str, d_in: int, d_out: int, w, w_scales, offsets, bias) -> None:
     if (w.shape != (d_out, d_in) or w.dtype != torch.int8 or not w.is_contiguous() or w_scales.numel() != d_out
             or w_scales.dtype != torch.float32 or not w_scales.is_contiguous()):
         raise ValueError(f"{what}: w and w_scales must be contiguous int8 [d_out, d_in] and float32 [d_out]")
     if offsets is not None and (offsets.shape != (d_out,) or offsets.dtype != torch.int32 or not offsets.is_contiguous()):
         raise ValueError(f"{what}: offsets must be contiguous int32 [d_out]")
+    if bias is not None and (bias.shape != (d_out,) or bias.dtype != torch.float32 or not bias.is_contiguous()):
+        raise ValueError(f"{what}: a bias must be contiguous float32 [d_out]")
+
+
+def _integer_y(what: str, x, m: int, d_out: int, out_dtype, y):
     if y is None:
         yt = _type_code(what, out_dtype)
-        y = x.new_empty((m, d_out), dtype=out_dtype)
-    else:
-        yt = _type_code(what, y.dtype)
-        if y.shape != (m, d_out) or not y.is_contiguous():
-            raise ValueError(f"{what}: y must be contiguous [m, d_out]")
+        return x.new_empty((m, d_out), dtype=out_dtype), yt
+    yt = _type_code(what, y.dtype)
+    if y.shape != (m, d_out) or not y.is_contiguous():
+        raise ValueError(f"{what}: y must be contiguous [m, d_out]")
+    return y, yt
+
+
+def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                        out_dtype: torch.dtype = torch.float32, y: Optional[torch.Tensor] = None,
+                        ws: Optional[torch.Tensor] = None, stream=None, bias: Optional[torch.Tensor] = None,
+                        activation: Optional[str] = None, residual: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [m, d_out] = act(x W^T + bias) + residual in 8-bit integers, W = w_scales
+    (w - offsets) as laid out by gptq_integer_weight (offsets None: all zero).  x
+    is [m, d_in] bf16 or fp32 (rows may be strided), quantized per token on the
+    way, or what gptq_quantize_tokens or gptq_norm_tokens returned for it.
+    bias: fp32 [d_out]; activation: "relu", "gelu", "gelu_tanh" or "silu"; residual:
+    [m, d_out] bf16 or fp32 (rows may be strided), which y may be itself.  They
+    are applied to the sums in fp32 (gptq_integer_linear of the C ABI)."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_integer_matmul(x, w, w_scales, offsets, out_dtype, y, ws, None, bias, activation, residual)
+    what = "gptq_integer_matmul"
+    x, code, x_scales, x_sums = _integer_x(what, x, offsets is not None)
+    act = _activation(what, activation)
+    dev = _on_device(what, x, w, w_scales, offsets, x_scales, x_sums, y, ws, bias, residual)
+    m, d_in = x.shape
+    d_out = w.shape[0]
+    _integer_layer_ok(what, d_in, d_out, w, w_scales, offsets, bias)
+    rt = ldr = 0
+    if residual is not None:
+        rt = _type_code(what, residual.dtype)
+        if residual.shape != (m, d_out) or (residual.stride(1) != 1 and d_out > 1):
+            raise ValueError(f"{what}: residual must be [m, d_out] with unit column stride")
+        ldr = _row_stride(residual)
+    y, yt = _integer_y(what, x, m, d_out, out_dtype, y)
     lib = _lib()
     if ws is None:
         need = lib.gptq_integer_workspace_size(m, code, d_in, d_out)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, _row_stride(x),
-                                   w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), d_out, y.data_ptr(), yt, _ptr(ws),
-                                   _ws_bytes(ws), _raw_stream(dev)), what)
+    if bias is None and act == 0 and residual is None:
+        st = lib.gptq_integer_matmul(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, _row_stride(x),
+                                     w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), d_out, y.data_ptr(), yt, _ptr(ws),
+                                     _ws_bytes(ws), _raw_stream(dev))
+    else:
+        layer = _CLayer(w.data_ptr(), w_scales.data_ptr(), _ptr(offsets), _ptr(bias))
+        st = lib.gptq_integer_linear(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, _row_stride(x), layer, d_out,
+                                     act, _ptr(residual), rt, ldr, y.data_ptr(), yt, _ptr(ws), _ws_bytes(ws),
+                                     _raw_stream(dev))
+    _check(st, what)
     return y
+
+
+def gptq_integer_gated_workspace_size(m: int, dtype: torch.dtype, d_in: int, d_out: int) -> int:
+    """dtype: of x (int8: codes)."""
+    code = GPTQ_I8 if dtype == torch.int8 else _type_code("gptq_integer_gated_workspace_size", dtype)
+    return int(_lib().gptq_integer_gated_workspace_size(m, code, d_in, d_out))
+
+
+def gptq_integer_gated(x, gate: Mapping[str, torch.Tensor], up: Mapping[str, torch.Tensor],
+                       activation: Optional[str] = "silu", out_dtype: torch.dtype = torch.float32,
+                       y: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [m, d_out] = act(x G^T + bias_g) * (x U^T + bias_u) in 8-bit integers, both
+    products in one kernel.  gate, up: layers as checkpoint.integer_layer gives
+    them ("w", "scales" and optionally "offsets"), and optionally a "bias" (fp32
+    [d_out]); x and activation as for gptq_integer_matmul."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_integer_gated(x, gate, up, activation, out_dtype, y, ws)
+    what = "gptq_integer_gated"
+    (gw, gs, go, gb), (uw, us, uo, ub) = ((t["w"], t["scales"], t.get("offsets"), t.get("bias")) for t in (gate, up))
+    x, code, x_scales, x_sums = _integer_x(what, x, go is not None or uo is not None)
+    act = _activation(what, activation)
+    dev = _on_device(what, x, gw, gs, go, gb, uw, us, uo, ub, x_scales, x_sums, y, ws)
+    m, d_in = x.shape
+    d_out = gw.shape[0]
+    _integer_layer_ok(what, d_in, d_out, gw, gs, go, gb)
+    _integer_layer_ok(what, d_in, d_out, uw, us, uo, ub)
+    y, yt = _integer_y(what, x, m, d_out, out_dtype, y)
+    lib = _lib()
+    if ws is None:
+        need = lib.gptq_integer_gated_workspace_size(m, code, d_in, d_out)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    g = _CLayer(gw.data_ptr(), gs.data_ptr(), _ptr(go), _ptr(gb))
+    u = _CLayer(uw.data_ptr(), us.data_ptr(), _ptr(uo), _ptr(ub))
+    _check(lib.gptq_integer_gated(x.data_ptr(), code, _ptr(x_scales), _ptr(x_sums), m, d_in, _row_stride(x), g, u, d_out, act,
+                                  y.data_ptr(), yt, _ptr(ws), _ws_bytes(ws), _raw_stream(dev)), what)
+    return y
+
+
+def gptq_norm_tokens(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, dtype: torch.dtype = torch.int8, total: Optional[torch.Tensor] = None,
+                     y: Optional[torch.Tensor] = None, stream=None):
+    """The root-mean-square norm of the rows of h = x + residual, times weight:
+    returns (rows, total).  x [m, d] and residual (None: h = x) are bf16 or fp32,
+    rows may be strided; weight [d] bf16 or fp32 (None: ones).
+    rows, for dtype int8: (codes, scales, sums) as gptq_quantize_tokens returns
+    them, which the products in integers take as x; for bfloat16 or float32: y
+    [m, d].  y given beside codes: it is written too.  total: h in the residual's type
+    (x itself without a residual), written to the given tensor, which may be the
+    residual or x, or to a new one."""
+    if stream is not None:
+        with _on_stream(stream):
+            return gptq_norm_tokens(x, weight, residual, eps, dtype, total, y)
+    what = "gptq_norm_tokens"
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError(f"{what}: x must be 2-D with unit column stride")
+    m, d = x.shape
+    xt = _type_code(what, x.dtype)
+    rt = wt = yt = ldr = lds = 0
+    dev = _on_device(what, x, weight, residual, total, y)
+    if weight is not None:
+        wt = _type_code(what, weight.dtype)
+        if weight.shape != (d,) or (weight.stride(0) != 1 and d > 1):
+            raise ValueError(f"{what}: weight must be [d], contiguous")
+    if residual is None:
+        if total is not None:
+            raise ValueError(f"{what}: without a residual there is no total to write")
+    else:
+        rt = _type_code(what, residual.dtype)
+        if residual.shape != (m, d) or (residual.stride(1) != 1 and d > 1):
+            raise ValueError(f"{what}: residual must be like x, with unit column stride")
+        if total is None:
+            total = torch.empty((m, d), dtype=residual.dtype, device=x.device)
+        elif total.shape != (m, d) or total.dtype != residual.dtype or (total.stride(1) != 1 and d > 1):
+            raise ValueError(f"{what}: total must be like the residual, with unit column stride")
+        ldr, lds = _row_stride(residual), _row_stride(total)
+    codes = scales = sums = None
+    if dtype == torch.int8:
+        codes = x.new_empty((m, d), dtype=torch.int8)
+        scales, sums = x.new_empty(m, dtype=torch.float32), x.new_empty(m, dtype=torch.int32)
+    elif y is None:
+        y = x.new_empty((m, d), dtype=dtype)
+    if y is not None:
+        yt = _type_code(what, y.dtype)
+        if y.shape != (m, d) or not y.is_contiguous() or (codes is None and y.dtype != dtype):
+            raise ValueError(f"{what}: y must be contiguous [m, d]" + ("" if codes is not None else f" {dtype}"))
+    _check(_lib().gptq_norm_tokens(x.data_ptr(), xt, m, d, _row_stride(x), _ptr(residual), rt, ldr, _ptr(weight), wt, eps,
+                                   _ptr(total), lds, _ptr(y), yt, _ptr(codes), _ptr(scales), _ptr(sums), _raw_stream(dev)),
+           what)
+    return (y if codes is None else (codes, scales, sums)), (x if residual is None else total)
 
 
 class QuantizedCache:
@@ -704,16 +858,21 @@ def gptq_attention_workspace_size(cache: QuantizedCache, n_tokens: int, n_heads:
 
 def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: torch.Tensor, q_starts: torch.Tensor,
                          kv_lens: torch.Tensor, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
-                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                         ws: Optional[torch.Tensor] = None, stream=None, cap: Optional[float] = None,
+                         slopes: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Causal attention of the new tokens q [n_tokens, n_heads, head_dim] bf16
     over the cache, which holds their keys and values already.  Sequence i owns
     the tokens q_starts[i] .. q_starts[i + 1] - 1 (int32 [n_seq + 1]), has
     kv_lens[i] keys (int32 [n_seq]) and its pages in page_table[i] (int32
     [n_seq, pages_per_seq]).  scale: 1 / sqrt(head_dim) unless given.  Rows of
-    out outside the sequences are left as they were."""
+    out outside the sequences are left as they were.
+    cap: scores s become cap tanh(s / cap), 2^-20 <= cap <= 2^20.  slopes: fp32
+    [n_heads]; slope |a - j| is then taken off the score of key j for the token
+    at place a.  prefix_lens: int32 [n_seq]; every token of a sequence sees that
+    many first keys (gptq_cache_attention_scores of the C ABI)."""
     if stream is not None:
         with _on_stream(stream):
-            return gptq_cache_attention(q, cache, page_table, q_starts, kv_lens, scale, out, ws)
+            return gptq_cache_attention(q, cache, page_table, q_starts, kv_lens, scale, out, ws, None, cap, slopes, prefix_lens)
     what = "gptq_cache_attention"
     hd = cache.head_dim
     if q.dim() != 3 or q.shape[2] != hd or q.dtype != torch.bfloat16:
@@ -734,7 +893,14 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
         out = q.new_empty((n, heads, hd))
     elif out.shape != q.shape or out.dtype != torch.bfloat16 or not _heads_together(out):
         raise ValueError(f"{what}: out must be bfloat16 like q, the heads of a token contiguous")
-    dev = cache._here(what, q, page_table, q_starts, kv_lens, out, ws)
+    if slopes is not None and (slopes.shape != (heads,) or slopes.dtype != torch.float32 or not slopes.is_contiguous()):
+        raise ValueError(f"{what}: slopes must be contiguous float32 [n_heads]")
+    if prefix_lens is not None and (prefix_lens.shape != kv_lens.shape or prefix_lens.dtype != torch.int32
+                                    or not prefix_lens.is_contiguous()):
+        raise ValueError(f"{what}: prefix_lens must be contiguous int32 [n_seq]")
+    if cap is not None and not 2.0 ** -20 <= cap <= 2.0 ** 20:
+        raise ValueError(f"{what}: cap must lie in [2^-20, 2^20], got {cap}")
+    dev = cache._here(what, q, page_table, q_starts, kv_lens, out, ws, slopes, prefix_lens)
     n_seq, pages = page_table.shape
     ldq, ldo = (q.stride(0), out.stride(0)) if n > 1 else (width, width)
     lib = _lib()
@@ -742,8 +908,15 @@ def gptq_cache_attention(q: torch.Tensor, cache: QuantizedCache, page_table: tor
         need = lib.gptq_attention_workspace_size(cache._ref, n, heads, n_seq, pages)
         if need:
             ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _check(lib.gptq_cache_attention(cache._ref, q.data_ptr(), GPTQ_BF16, n, ldq, heads, page_table.data_ptr(), pages,
-                                    q_starts.data_ptr(), kv_lens.data_ptr(), n_seq,
-                                    hd ** -0.5 if scale is None else scale, out.data_ptr(), ldo, _ptr(ws),
-                                    _ws_bytes(ws), _raw_stream(dev)), what)
+    scale = hd ** -0.5 if scale is None else scale
+    if cap is None and slopes is None and prefix_lens is None:
+        st = lib.gptq_cache_attention(cache._ref, q.data_ptr(), GPTQ_BF16, n, ldq, heads, page_table.data_ptr(), pages,
+                                      q_starts.data_ptr(), kv_lens.data_ptr(), n_seq, scale, out.data_ptr(), ldo, _ptr(ws),
+                                      _ws_bytes(ws), _raw_stream(dev))
+    else:
+        scores = _CScores(cap or 0.0, _ptr(slopes), _ptr(prefix_lens))
+        st = lib.gptq_cache_attention_scores(cache._ref, q.data_ptr(), GPTQ_BF16, n, ldq, heads, page_table.data_ptr(), pages,
+                                             q_starts.data_ptr(), kv_lens.data_ptr(), n_seq, scale, scores, out.data_ptr(),
+                                             ldo, _ptr(ws), _ws_bytes(ws), _raw_stream(dev))
+    _check(st, what)
     return out

@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgptq.so")
 SOURCES = ["hessian.hip", "gemm_f32.hip", "gemm_x3.hip", "prepare.hip", "sweep.hip", "pack.hip", "dequant.hip",
-           "integer.hip", "cache.hip", "attention.hip", "abi.cpp", "phase_timing.cpp"]
+           "integer.hip", "norm.hip", "cache.hip", "attention.hip", "abi.cpp", "phase_timing.cpp"]
 
 ARCH = os.environ.get("GPTQ_OFFLOAD_ARCH", "gfx950")
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -46,6 +46,7 @@ bool packable(int64_t d_in, int32_t bits) {
 // stays below 2^31
 constexpr int64_t kMaxRows = int64_t{1} << 30;
 constexpr int64_t kMaxIntDim = int64_t{1} << 16;  // 32-bit sums of int8 products stay exact
+constexpr int64_t kMaxLead = int64_t{1} << 31;   // distance of the rows of a norm: no byte count overflows
 bool rows_ok(int64_t n) { return n >= 0 && n <= kMaxRows; }
 
 bool cache_shape(const gptq_cache* c, gptq::CacheShape* out) {
@@ -266,25 +267,171 @@ size_t gptq_integer_workspace_size(int64_t m, int32_t xt, int64_t d_in, int64_t 
   return gptq::integer_matmul_workspace(m, d_in, d_out, xt == GPTQ_I8, device_cus());
 }
 
+namespace {
+// What every product in integers asks of x, its layer and its workspace; `rows`
+// are those of the weights that it reads.
+gptq_status integer_go(gptq::IntCall* c, int64_t rows, int32_t yt, void* ws, size_t ws_bytes, void* stream) {
+  if ((c->xt != GPTQ_F32 && c->xt != GPTQ_BF16 && c->xt != GPTQ_I8) || (yt != GPTQ_F32 && yt != GPTQ_BF16))
+    return GPTQ_ERR_INVALID_ARG;
+  if (!rows_ok(c->m) || !dim_ok(c->d_in) || !dim_ok(rows) || c->d_in % 32 != 0 || c->d_in > kMaxIntDim || c->ldx < c->d_in)
+    return GPTQ_ERR_INVALID_ARG;
+  if (c->m == 0) return GPTQ_OK;
+  const bool two = rows != c->d_out;
+  if (!c->x || !c->y || !c->layer.w || !c->layer.scales || !aligned16(c->layer.w)) return GPTQ_ERR_INVALID_ARG;
+  if (two && (!c->up.w || !c->up.scales || !aligned16(c->up.w))) return GPTQ_ERR_INVALID_ARG;
+  if (c->xt == GPTQ_I8) {
+    if (!c->x_scales || ((c->layer.offsets || c->up.offsets) && !c->x_sums) || c->ldx % 16 != 0 ||
+        c->ldx > (int64_t{1} << 22) || !aligned16(c->x))
+      return GPTQ_ERR_INVALID_ARG;
+  }
+  c->y_bf16 = yt == GPTQ_BF16;
+  const int cus = device_cus();
+  const size_t need = gptq::integer_matmul_workspace(c->m, c->d_in, rows, c->xt == GPTQ_I8, cus);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
+  return from_hip(gptq::integer_launch(*c, ws, cus, static_cast<hipStream_t>(stream)));
+}
+
+bool activation_ok(int32_t a) { return a >= GPTQ_ACT_NONE && a <= GPTQ_ACT_SILU; }
+int64_t size_of(int32_t t) { return t == GPTQ_F32 ? 4 : t == GPTQ_BF16 ? 2 : 1; }
+
+gptq::IntLayer layer_of(const gptq_integer_layer* l) {
+  return gptq::IntLayer{l->w, l->scales, l->offsets, l->bias};
+}
+
+// A matrix of m rows of `width` bytes, `lead` bytes apart.
+struct Rows {
+  const void* at;
+  int64_t lead, width;
+};
+// Whether two of them have a byte in common (with different distances of their rows:
+// whether their first and last bytes lie across each other).
+bool overlap(const Rows& a, const Rows& b, int64_t m) {
+  if (!a.at || !b.at || m == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
+  const uintptr_t lo = a0 < b0 ? a0 : b0, apart = a0 < b0 ? b0 - a0 : a0 - b0;
+  const Rows &first = lo == a0 ? a : b, &second = lo == a0 ? b : a;
+  const uintptr_t span = static_cast<uintptr_t>(m - 1) * static_cast<uintptr_t>(first.lead) + static_cast<uintptr_t>(first.width);
+  if (apart >= span) return false;
+  if (a.lead != b.lead || a.lead == 0) return true;
+  const int64_t off = static_cast<int64_t>(apart % static_cast<uintptr_t>(a.lead));  // inside a row of the first
+  return off < first.width || off + second.width > a.lead;
+}
+// Out may not touch in, unless it is in itself, element by element.
+bool clobbers(const Rows& out, const Rows& in, bool same_type, int64_t m) {
+  return overlap(out, in, m) && !(same_type && out.at == in.at && (out.lead == in.lead || m == 1));
+}
+}  // namespace
+
 gptq_status gptq_integer_matmul(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
                                 int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
                                 const int32_t* w_offsets_or_null, int64_t d_out, void* y, int32_t yt, void* ws,
                                 size_t ws_bytes, void* stream) {
-  if ((xt != GPTQ_F32 && xt != GPTQ_BF16 && xt != GPTQ_I8) || (yt != GPTQ_F32 && yt != GPTQ_BF16))
-    return GPTQ_ERR_INVALID_ARG;
-  if (!rows_ok(m) || !dim_ok(d_in) || !dim_ok(d_out) || d_in % 32 != 0 || d_in > kMaxIntDim || ldx < d_in)
-    return GPTQ_ERR_INVALID_ARG;
-  if (m == 0) return GPTQ_OK;
-  if (!x || !w || !w_scales || !y || !aligned16(w)) return GPTQ_ERR_INVALID_ARG;
-  if (xt == GPTQ_I8) {
-    if (!x_scales || (w_offsets_or_null && !x_sums) || ldx % 16 != 0 || ldx > (int64_t{1} << 22) || !aligned16(x))
-      return GPTQ_ERR_INVALID_ARG;
+  gptq::IntCall c{};
+  c.x = x;
+  c.xt = xt;
+  c.x_scales = x_scales;
+  c.x_sums = x_sums;
+  c.m = m;
+  c.d_in = d_in;
+  c.ldx = ldx;
+  c.layer = gptq::IntLayer{w, w_scales, w_offsets_or_null, nullptr};
+  c.d_out = d_out;
+  c.y = y;
+  return integer_go(&c, d_out, yt, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_integer_linear(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                                int64_t d_in, int64_t ldx, const gptq_integer_layer* layer, int64_t d_out,
+                                int32_t activation, const void* residual_or_null, int32_t rt, int64_t ldr, void* y,
+                                int32_t yt, void* ws, size_t ws_bytes, void* stream) {
+  if (!layer || !activation_ok(activation) || !rows_ok(m) || !dim_ok(d_out)) return GPTQ_ERR_INVALID_ARG;
+  if (residual_or_null) {
+    if ((rt != GPTQ_F32 && rt != GPTQ_BF16) || ldr < d_out || ldr > kMaxDim) return GPTQ_ERR_INVALID_ARG;
+    const Rows to{y, d_out * size_of(yt), d_out * size_of(yt)}, from{residual_or_null, ldr * size_of(rt), d_out * size_of(rt)};
+    if (y && (yt == GPTQ_F32 || yt == GPTQ_BF16) && clobbers(to, from, yt == rt, m)) return GPTQ_ERR_INVALID_ARG;
   }
-  const int cus = device_cus();
-  const size_t need = gptq::integer_matmul_workspace(m, d_in, d_out, xt == GPTQ_I8, cus);
-  if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
-  return from_hip(gptq::integer_matmul_launch(x, xt, x_scales, x_sums, m, d_in, ldx, w, w_scales, w_offsets_or_null,
-                                              d_out, y, yt == GPTQ_BF16, ws, cus, static_cast<hipStream_t>(stream)));
+  gptq::IntCall c{};
+  c.x = x;
+  c.xt = xt;
+  c.x_scales = x_scales;
+  c.x_sums = x_sums;
+  c.m = m;
+  c.d_in = d_in;
+  c.ldx = ldx;
+  c.layer = layer_of(layer);
+  c.d_out = d_out;
+  c.act = activation;
+  c.res = residual_or_null;
+  c.ldr = ldr;
+  c.res_bf16 = rt == GPTQ_BF16;
+  c.y = y;
+  return integer_go(&c, d_out, yt, ws, ws_bytes, stream);
+}
+
+size_t gptq_integer_gated_workspace_size(int64_t m, int32_t xt, int64_t d_in, int64_t d_out) {
+  return d_out <= 0 || d_out > kMaxDim / 2 ? 0 : gptq_integer_workspace_size(m, xt, d_in, 2 * d_out);
+}
+
+gptq_status gptq_integer_gated(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
+                               int64_t d_in, int64_t ldx, const gptq_integer_layer* gate, const gptq_integer_layer* up,
+                               int64_t d_out, int32_t activation, void* y, int32_t yt, void* ws, size_t ws_bytes,
+                               void* stream) {
+  if (!gate || !up || !activation_ok(activation) || d_out <= 0 || d_out > kMaxDim / 2) return GPTQ_ERR_INVALID_ARG;
+  gptq::IntCall c{};
+  c.x = x;
+  c.xt = xt;
+  c.x_scales = x_scales;
+  c.x_sums = x_sums;
+  c.m = m;
+  c.d_in = d_in;
+  c.ldx = ldx;
+  c.layer = layer_of(gate);
+  c.up = layer_of(up);
+  c.d_out = d_out;
+  c.act = activation;
+  c.y = y;
+  return integer_go(&c, 2 * d_out, yt, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_norm_tokens(const void* x, int32_t xt, int64_t n_tokens, int64_t d, int64_t ldx, const void* residual_or_null,
+                             int32_t rt, int64_t ldr, const void* weight_or_null, int32_t wt, float eps, void* sum_or_null,
+                             int64_t lds, void* y_or_null, int32_t yt, int8_t* codes_or_null, float* scales,
+                             int32_t* sums_or_null, void* stream) {
+  const auto real = [](int32_t t) { return t == GPTQ_F32 || t == GPTQ_BF16; };
+  if (!real(xt) || !rows_ok(n_tokens) || !dim_ok(d) || ldx < d || ldx > kMaxLead || !(eps > 0.0f && eps <= 3.402823466e38f))
+    return GPTQ_ERR_INVALID_ARG;
+  if (residual_or_null && (!real(rt) || ldr < d || ldr > kMaxLead)) return GPTQ_ERR_INVALID_ARG;
+  if (sum_or_null && (!residual_or_null || lds < d || lds > kMaxLead)) return GPTQ_ERR_INVALID_ARG;
+  if ((weight_or_null && !real(wt)) || (y_or_null && !real(yt)) || (codes_or_null && !scales)) return GPTQ_ERR_INVALID_ARG;
+  if (n_tokens == 0) return GPTQ_OK;
+  if (!x || (!y_or_null && !codes_or_null)) return GPTQ_ERR_INVALID_ARG;
+  const Rows in_x{x, ldx * size_of(xt), d * size_of(xt)}, in_r{residual_or_null, ldr * size_of(rt), d * size_of(rt)};
+  const Rows sum{sum_or_null, lds * size_of(rt), d * size_of(rt)}, y{y_or_null, d * size_of(yt), d * size_of(yt)};
+  const Rows codes{codes_or_null, d, d};
+  if (clobbers(sum, in_x, xt == rt, n_tokens) || clobbers(sum, in_r, true, n_tokens) || overlap(y, in_x, n_tokens) ||
+      overlap(y, in_r, n_tokens) || overlap(y, sum, n_tokens) || overlap(codes, in_x, n_tokens) ||
+      overlap(codes, in_r, n_tokens) || overlap(codes, sum, n_tokens) || overlap(codes, y, n_tokens))
+    return GPTQ_ERR_INVALID_ARG;
+  gptq::NormCall c{};
+  c.x = x;
+  c.res = residual_or_null;
+  c.weight = weight_or_null;
+  c.sum = sum_or_null;
+  c.y = y_or_null;
+  c.codes = codes_or_null;
+  c.scales = scales;
+  c.sums = sums_or_null;
+  c.m = n_tokens;
+  c.d = d;
+  c.ldx = ldx;
+  c.ldr = ldr;
+  c.lds = lds;
+  c.eps = eps;
+  c.x_bf16 = xt == GPTQ_BF16;
+  c.res_bf16 = rt == GPTQ_BF16;
+  c.w_bf16 = wt == GPTQ_BF16;
+  c.y_bf16 = yt == GPTQ_BF16;
+  return from_hip(gptq::norm_launch(c, static_cast<hipStream_t>(stream)));
 }
 
 gptq_status gptq_cache_write(const gptq_cache* cache, const void* k, const void* v, int32_t xt, int64_t n_tokens,
@@ -338,10 +485,11 @@ size_t gptq_attention_workspace_size(const gptq_cache* cache, int64_t n_tokens, 
   return plan.ws_bytes;
 }
 
-gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
-                                 int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
-                                 const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale, void* out,
-                                 int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+namespace {
+gptq_status attention_go(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq, int32_t n_heads,
+                         const int32_t* page_table, int64_t pages_per_seq, const int32_t* q_starts, const int32_t* kv_lens,
+                         int32_t n_seq, float scale, const gptq::AttnShape& shape, void* out, int64_t ldo, void* ws,
+                         size_t ws_bytes, void* stream) {
   gptq::CacheShape c;
   if (!cache_shape(cache, &c) || qt != GPTQ_BF16 || !(scale > 0.0f && scale <= 3.402823466e38f))
     return GPTQ_ERR_INVALID_ARG;
@@ -354,7 +502,28 @@ gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t
   if (plan.ws_bytes > 0 && (!ws || ws_bytes < plan.ws_bytes || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
   return from_hip(gptq::attention_launch(plan, c, q, ldq, n_tokens, n_heads, cache->k_codes, cache->v_codes,
                                          cache->k_scales, cache->v_scales, page_table, pages_per_seq, q_starts, kv_lens,
-                                         n_seq, scale, out, ldo, ws, static_cast<hipStream_t>(stream)));
+                                         n_seq, scale, shape, out, ldo, ws, static_cast<hipStream_t>(stream)));
+}
+}  // namespace
+
+gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
+                                 int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
+                                 const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale, void* out,
+                                 int64_t ldo, void* ws, size_t ws_bytes, void* stream) {
+  return attention_go(cache, q, qt, n_tokens, ldq, n_heads, page_table, pages_per_seq, q_starts, kv_lens, n_seq, scale,
+                      gptq::AttnShape{}, out, ldo, ws, ws_bytes, stream);
+}
+
+gptq_status gptq_cache_attention_scores(const gptq_cache* cache, const void* q, int32_t qt, int64_t n_tokens, int64_t ldq,
+                                        int32_t n_heads, const int32_t* page_table, int64_t pages_per_seq,
+                                        const int32_t* q_starts, const int32_t* kv_lens, int32_t n_seq, float scale,
+                                        const gptq_scores* scores, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  if (!scores) return GPTQ_ERR_INVALID_ARG;
+  const float cap = scores->cap;
+  if (!(cap == 0.0f || (cap >= 0x1p-20f && cap <= 0x1p20f))) return GPTQ_ERR_INVALID_ARG;
+  return attention_go(cache, q, qt, n_tokens, ldq, n_heads, page_table, pages_per_seq, q_starts, kv_lens, n_seq, scale,
+                      gptq::AttnShape{cap, scores->slopes, scores->prefix_lens}, out, ldo, ws, ws_bytes, stream);
 }
 
 gptq_status gptq_phase_timing(int32_t enable) { return from_hip(gptq::phase_timing_set(enable != 0)); }

@@ -63,6 +63,53 @@ struct AttnParams {
   float scale_log2e;
 };
 
+// What becomes of a score before the softmax (S: kAsIs, kBias, kCapped) and which
+// keys besides the causal ones a token sees.
+//   kBias    s' = s - slope_h |a - j|, keys j < prefix of the sequence are seen by every token
+//   kCapped  the same of cap tanh(s / cap)
+// Without slopes they are zeros, without prefixes nothing is added: two forms of
+// each kernel, for what costs time, and not eight.
+enum { kAsIs = 0, kBias = 1, kCapped = 2 };
+template <int S>
+struct Shape {
+  const float* slopes;      // [n_heads], or null
+  const int32_t* prefixes;  // [n_seq], or null
+  float cap;                // times log2(e), as scores t are here
+  float inv;                // 1 / that
+  float twice;              // 2^(twice t) = e^(2 t / cap in that unit)
+};
+template <>
+struct Shape<kAsIs> {};
+
+// keys of sequence i that all its tokens see
+template <int S>
+GPTQ_DEV int prefix_of(const Shape<S>& sh, int i, int len) {
+  if constexpr (S != kAsIs) {
+    if (sh.prefixes) return min(max(sh.prefixes[i], 0), len);
+  }
+  return 0;
+}
+template <int S>
+GPTQ_DEV float slope_of(const Shape<S>& sh, int head) {
+  if constexpr (S != kAsIs) {
+    if (sh.slopes) return sh.slopes[head] * 1.4426950408889634f;
+  }
+  return 0.f;
+}
+// cap tanh(t / cap): by 1 - 2 / (e^2x + 1), which is off by 2^-22 of 1, and where that
+// would be more than 2^-20 of tanh x (|x| < 0.3) by the series up to x^9, off by 2^-21.
+template <int S>
+GPTQ_DEV float shaped(const Shape<S>& sh, float t, float slope, float away) {
+  if constexpr (S == kAsIs) return t;
+  if constexpr (S == kCapped) {
+    const float x = t * sh.inv, x2 = x * x;
+    const float far = fmaf(-2.f * sh.cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t * sh.twice)), sh.cap);
+    const float near = fmaf(t * x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), t);
+    t = fabsf(x) < 0.3f ? near : far;
+  }
+  if constexpr (S != kAsIs) return fmaf(-slope, fabsf(away), t);
+}
+
 struct Seq {
   int q0, n, len, tiles, units;
 };
@@ -278,8 +325,8 @@ GPTQ_DEV void col4(const uint32_t (&w)[8], f16x8_t& lo, f16x8_t& hi) {
 // eight waves and two took 83 us for the ragged batch.
 constexpr int kSplitWaves = 4;
 
-template <int HDP, int BITS, int MT>
-__global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) void attn_split_kernel(AttnParams p) {
+template <int HDP, int BITS, int MT, int S>
+__global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) void attn_split_kernel(AttnParams p, Shape<S> sh) {
   using K = KeyLanes<HDP, BITS>;
   constexpr int kKW = K::kWords;               // words of K a lane holds per key: HDP / 4 dims
   constexpr int kVB = HDP * BITS / 128;        // bytes of V a lane holds per key: HDP / 16 dims
@@ -296,23 +343,26 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
   if (!find_work<true>(p, u, w)) return;
   const int rows = w.s.n * p.group;
   const int r0 = w.tile * kM;
+  const int prefix = uniform(prefix_of<S>(sh, w.seq, w.s.len));
   // last key of the tile's first row, and the keys any of its rows sees
-  const int first = w.s.len - w.s.n + uniform(div_by(r0, p.group_mul, p.group_shift));
-  const int vis = w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1;
+  const int first = max(w.s.len - w.s.n + uniform(div_by(r0, p.group_mul, p.group_shift)), prefix - 1);
+  const int vis = max(w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1, prefix);
   const int units = vis > 0 ? (vis - 1) / kUnit + 1 : 0;
   const int per = (units + w.n_split - 1) / w.n_split;
   const int key0 = w.split * per * kUnit, key1 = min(vis, (w.split + 1) * per * kUnit);
 
   // query operands, their sums (4 bits), and each row's last key
   bf16x8_t q[MT][kSteps];
-  float bias[MT];
-  int lim[MT];
+  float bias[MT], slope[MT];
+  int lim[MT], place[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int r = r0 + 16 * i + c;
     const bool live = r < rows;
     const int tok = live ? div_by(r, p.group_mul, p.group_shift) : 0;
-    lim[i] = live ? w.s.len - w.s.n + tok : -1;
+    place[i] = w.s.len - w.s.n + tok;
+    lim[i] = live ? max(place[i], prefix - 1) : -1;
+    slope[i] = live ? slope_of<S>(sh, h * p.group + r - tok * p.group) : 0.f;
     const uint16_t* src = p.q + static_cast<int64_t>(w.s.q0 + tok) * p.ldq +
                           static_cast<int64_t>(h * p.group + (live ? r - tok * p.group : 0)) * p.hd;
     float sum = 0.f;
@@ -414,7 +464,9 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 #pragma unroll
         for (int e = 0; e < kSteps; ++e) a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kop[e], q[i][e], a, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s[i][4 * b + r] = a[r] * (ks[b][r] * p.scale_log2e);
+        for (int r = 0; r < 4; ++r)
+          s[i][4 * b + r] = shaped<S>(sh, a[r] * (ks[b][r] * p.scale_log2e), slope[i],
+                                      static_cast<float>(place[i] - (k0 + 16 * b + 4 * g + r)));
       }
     }
     float vtop = 0.f;
@@ -619,8 +671,8 @@ struct TileShare {
   uint32_t w[kW];
 };
 
-template <int HDP, int BITS>
-__global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p) {
+template <int HDP, int BITS, int S>
+__global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_tile_kernel(AttnParams p, Shape<S> sh) {
   using R = TileShare<HDP, BITS>;
   constexpr int kKeys = 64, kM = 128;
   constexpr int kSteps = HDP / 16, kDb = HDP / 32;
@@ -636,7 +688,8 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   if (!find_work<true>(p, u, w)) return;
   const int rows = w.s.n * p.group;
   const int r0 = w.tile * kM;
-  const int vis = w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1;
+  const int prefix = uniform(prefix_of<S>(sh, w.seq, w.s.len));
+  const int vis = max(w.s.len - w.s.n + uniform(div_by(min(r0 + kM, rows) - 1, p.group_mul, p.group_shift)) + 1, prefix);
   const int units = vis > 0 ? (vis - 1) / kUnit + 1 : 0;
   const int per = (units + w.n_split - 1) / w.n_split;
   const int key0 = w.split * per * kUnit, key1 = min(vis, (w.split + 1) * per * kUnit);
@@ -645,9 +698,11 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   const int r = r0 + 32 * wave + c;
   const bool live = r < rows;
   const int tok = live ? div_by(r, p.group_mul, p.group_shift) : 0, qh = live ? r - tok * p.group : 0;
-  const int lim = live ? w.s.len - w.s.n + tok : -1;
-  const int wfirst = w.s.len - w.s.n + uniform(div_by(r0 + 32 * wave, p.group_mul, p.group_shift));  // last key of the wave's first row
-  const int wlast = r0 + 32 * wave < rows ? w.s.len - w.s.n + uniform(div_by(min(r0 + 32 * wave + 32, rows) - 1, p.group_mul, p.group_shift)) : -1;
+  const int place = w.s.len - w.s.n + tok;
+  const int lim = live ? max(place, prefix - 1) : -1;
+  const float slope = live ? slope_of<S>(sh, h * p.group + qh) : 0.f;
+  const int wfirst = max(w.s.len - w.s.n + uniform(div_by(r0 + 32 * wave, p.group_mul, p.group_shift)), prefix - 1);  // last key of the wave's first row
+  const int wlast = r0 + 32 * wave < rows ? max(w.s.len - w.s.n + uniform(div_by(min(r0 + 32 * wave + 32, rows) - 1, p.group_mul, p.group_shift)), prefix - 1) : -1;
   bf16x8_t q[kSteps];
   float bias = 0.f;
   {
@@ -842,6 +897,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   // the scores of a tile's keys (from block `half`), -inf where hidden; returns their maximum
   auto tile_scores = [&](int base, int buf, uint64_t shown, int half, f32x16_t (&s)[2]) {
     const int rel = lim - base - 4 * hf;
+    const float away = static_cast<float>(place - base - 4 * hf);
     auto seen = [&](int b, int e) {  // element e of block b: key 32 b + 8 (e / 4) + 4 hf + e % 4
       return 32 * b + 8 * (e >> 2) + (e & 3) <= rel && ((shown >> (32 * b + 16 * (e >> 3))) & 1u);  // 16 keys share a page
     };
@@ -863,7 +919,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
         const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[b][4 * a + e] *= ks[e];
+          s[b][4 * a + e] = shaped<S>(sh, s[b][4 * a + e] * ks[e], slope, away - static_cast<float>(32 * b + 8 * a + e));
           if (!seen(b, 4 * a + e)) s[b][4 * a + e] = kNegInf;
           mx = fmaxf(mx, s[b][4 * a + e]);
         }
@@ -1009,14 +1065,19 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       u32x4_t pk[4];
       f32x4_t ks[4];
       float l0 = 0.f, l1 = 0.f;
+      const float away = static_cast<float>(place - base - 4 * hf);
+      // log2 of the weight of element e of block b
+      auto power = [&](float score, int b, int e) {
+        if constexpr (S == kAsIs) return fmaf(score, ks[e >> 2][e & 3], -m);
+        return shaped<S>(sh, score * ks[e >> 2][e & 3], slope, away - static_cast<float>(32 * b + 8 * (e >> 2) + (e & 3))) - m;
+      };
       // n of the 16 weights 2^(s sk - m) of a block, rounded to fp16, and their sum
       auto weights = [&](const f32x16_t& s, int b, int from, int to, float& sum) {
         asm volatile("" : "+v"(m));  // not before this place between the products
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
           if (e >= from && e < to) {
-            const uint32_t two = pack_f16(fast_exp2(fmaf(s[e], ks[e >> 2][e & 3], -m)),
-                                          fast_exp2(fmaf(s[e + 1], ks[e >> 2][(e & 3) + 1], -m)));
+            const uint32_t two = pack_f16(fast_exp2(power(s[e], b, e)), fast_exp2(power(s[e + 1], b, e + 1)));
             pk[2 * b + (e >> 3)][(e >> 1) & 3] = two;
             sum = add_f16(two, sum);
           }
@@ -1229,13 +1290,27 @@ void exact_divisor(int32_t d, uint32_t* mul, uint32_t* shift) {
 
 int head_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 
-template <int HDP, int BITS>
-void attn_go(const AttnParams& p, unsigned blocks, unsigned joins, hipStream_t st) {
+template <int HDP, int BITS, int S>
+void attn_go(const AttnParams& p, const Shape<S>& sh, unsigned blocks, unsigned joins, hipStream_t st) {
   constexpr int t = 64 * kSplitWaves;
-  if (p.tile_rows == 128) attn_tile_kernel<HDP, BITS><<<blocks, 256, 0, st>>>(p);
-  else if (HDP <= 128 && p.tile_rows == 32) attn_split_kernel<HDP, BITS, HDP <= 128 ? 2 : 1><<<blocks, t, 0, st>>>(p);
-  else attn_split_kernel<HDP, BITS, 1><<<blocks, t, 0, st>>>(p);
+  if (p.tile_rows == 128) attn_tile_kernel<HDP, BITS, S><<<blocks, 256, 0, st>>>(p, sh);
+  else if (HDP <= 128 && p.tile_rows == 32) attn_split_kernel<HDP, BITS, HDP <= 128 ? 2 : 1, S><<<blocks, t, 0, st>>>(p, sh);
+  else attn_split_kernel<HDP, BITS, 1, S><<<blocks, t, 0, st>>>(p, sh);
   if (joins) attn_join_kernel<HDP><<<dim3(joins, (p.tile_rows + kJoinRows - 1) / kJoinRows), 512, 0, st>>>(p);
+}
+
+template <int S>
+void attn_head(const AttnParams& p, const Shape<S>& sh, int bits, unsigned b, unsigned j, hipStream_t st) {
+  const int hp = head_pad(p.hd);
+  if (bits == 8) {
+    if (hp == 64) attn_go<64, 8, S>(p, sh, b, j, st);
+    else if (hp == 128) attn_go<128, 8, S>(p, sh, b, j, st);
+    else attn_go<256, 8, S>(p, sh, b, j, st);
+  } else {
+    if (hp == 64) attn_go<64, 4, S>(p, sh, b, j, st);
+    else if (hp == 128) attn_go<128, 4, S>(p, sh, b, j, st);
+    else attn_go<256, 4, S>(p, sh, b, j, st);
+  }
 }
 
 }  // namespace
@@ -1282,7 +1357,7 @@ AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, 
 hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const void* q, int64_t ldq, int64_t n_tokens,
                             int32_t n_heads, const void* kc, const void* vc, const float* ks, const float* vs,
                             const int32_t* table, int64_t ld_table, const int32_t* starts, const int32_t* lens,
-                            int32_t n_seq, float scale, void* out, int64_t ldo, void* ws, hipStream_t st) {
+                            int32_t n_seq, float scale, const AttnShape& shape, void* out, int64_t ldo, void* ws, hipStream_t st) {
   AttnParams p{};
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
@@ -1315,15 +1390,14 @@ hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const voi
   exact_divisor(p.n_kv, &p.kv_mul, &p.kv_shift);
   p.scale_log2e = scale * 1.4426950408889634f;
   const unsigned b = static_cast<unsigned>(plan.blocks), j = static_cast<unsigned>(plan.joins);
-  const int hp = head_pad(c.hd);
-  if (c.bits == 8) {
-    if (hp == 64) attn_go<64, 8>(p, b, j, st);
-    else if (hp == 128) attn_go<128, 8>(p, b, j, st);
-    else attn_go<256, 8>(p, b, j, st);
+  if (shape.cap > 0.f) {
+    const double l2e = 1.4426950408889634, cap = shape.cap;
+    attn_head<kCapped>(p, {shape.slopes, shape.prefixes, static_cast<float>(cap * l2e), static_cast<float>(1.0 / (cap * l2e)),
+                           static_cast<float>(2.0 / cap)}, c.bits, b, j, st);
+  } else if (shape.slopes || shape.prefixes) {
+    attn_head<kBias>(p, {shape.slopes, shape.prefixes, 0.f, 0.f, 0.f}, c.bits, b, j, st);
   } else {
-    if (hp == 64) attn_go<64, 4>(p, b, j, st);
-    else if (hp == 128) attn_go<128, 4>(p, b, j, st);
-    else attn_go<256, 4>(p, b, j, st);
+    attn_head<kAsIs>(p, {}, c.bits, b, j, st);
   }
   return hipGetLastError();
 }

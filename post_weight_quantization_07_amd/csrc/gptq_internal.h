@@ -147,10 +147,45 @@ hipError_t token_codes_launch(const void* x, bool bf16, int64_t m, int64_t d, in
 hipError_t integer_weight_launch(const int32_t* qweight, const int32_t* zeros, int bits, int64_t d_in, int64_t d_out,
                                  int8_t* w, int32_t* offsets, hipStream_t stream);
 size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool codes_given, int n_cu);
-hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, const int32_t* x_sums, int64_t m,
-                                 int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
-                                 const int32_t* w_offsets, int64_t d_out, void* y, bool y_bf16, void* ws, int n_cu,
-                                 hipStream_t stream);
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };  // gptq_activation
+struct IntLayer {
+  const int8_t* w;  // [d_out, d_in]
+  const float* scales;
+  const int32_t* offsets;  // or null
+  const float* bias;       // or null
+};
+struct IntCall {
+  const void* x;
+  int xt;
+  const float* x_scales;
+  const int32_t* x_sums;
+  int64_t m, d_in, ldx;
+  IntLayer layer, up;  // up.w null: one layer
+  int64_t d_out;
+  int act;
+  const void* res;     // or null
+  int64_t ldr;
+  bool res_bf16, y_bf16;
+  void* y;
+};
+// workspace: integer_matmul_workspace of the rows of both layers
+hipError_t integer_launch(const IntCall& c, void* ws, int n_cu, hipStream_t stream);
+
+// ------------------------------------------------------------------- norm --
+struct NormCall {
+  const void* x;
+  const void* res;     // or null
+  const void* weight;  // or null
+  void* sum;           // or null; of res's type
+  void* y;             // or null
+  int8_t* codes;       // or null, scales and sums with it
+  float* scales;
+  int32_t* sums;       // or null
+  int64_t m, d, ldx, ldr, lds;
+  float eps;
+  bool x_bf16, res_bf16, w_bf16, y_bf16;
+};
+hipError_t norm_launch(const NormCall& c, hipStream_t stream);
 
 // ------------------------------------------------------------------ cache --
 struct CacheShape {
@@ -172,11 +207,17 @@ struct AttnPlan {
   int64_t slots;          // partial results
   size_t ws_bytes;
 };
+struct AttnShape {           // gptq_scores
+  float cap;               // 0: none
+  const float* slopes;     // or null
+  const int32_t* prefixes; // or null
+};
 AttnPlan attention_plan(const CacheShape& c, int64_t n_tokens, int32_t n_heads, int32_t n_seq, int64_t ld_table,
                         int n_cu);
 hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const void* q, int64_t ldq, int64_t n_tokens,
                             int32_t n_heads, const void* kc, const void* vc, const float* ks, const float* vs,
                             const int32_t* table, int64_t ld_table, const int32_t* starts, const int32_t* lens,
-                            int32_t n_seq, float scale, void* out, int64_t ldo, void* ws, hipStream_t stream);
+                            int32_t n_seq, float scale, const AttnShape& shape, void* out, int64_t ldo, void* ws,
+                            hipStream_t stream);
 
 }  // namespace gptq

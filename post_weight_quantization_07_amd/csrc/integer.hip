@@ -28,37 +28,6 @@ typedef __attribute__((address_space(3))) void lds_void_t;
 // 16-byte aligned and d a multiple of 8.  Bound: HBM (x read, codes written):
 // 2048 x 28672 bf16 in 42 us, 4.2 TB/s; 509 x 11008 fp32, all of it in flight at
 // once, 7.9 us; 16 x 4096 4.2 us, a launch and one trip to HBM.
-template <bool BF16, bool VEC>
-GPTQ_DEV void tok_load(const void* x, int64_t row0, int64_t e, int64_t d, float (&v)[8]) {
-  if (VEC) {
-    if (e < d) {
-      load8<BF16>(x, row0 + e, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (e + i < d) ? load1<BF16>(x, row0 + e + i) : 0.f;
-  }
-}
-
-template <bool VEC>
-GPTQ_DEV int tok_store(int8_t* codes, int64_t at, int64_t e, int64_t d, const float (&v)[8], const RowScale& rs) {
-  if (e >= d) return 0;
-  uint32_t w[2];
-  row_codes<127, 0>(v, rs, w);
-  const int sum = __builtin_amdgcn_sdot4(w[0], 0x01010101, __builtin_amdgcn_sdot4(w[1], 0x01010101, 0, false), false);
-  if (VEC) {
-    *reinterpret_cast<uint2*>(codes + at + e) = make_uint2(w[0], w[1]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (e + i < d) codes[at + e + i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
-  }
-  return sum;
-}
-
 template <int T, int CH, bool BF16, bool VEC>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void token_codes_kernel(const void* __restrict__ x, int64_t m, int64_t d,
                                                                         int64_t ldx, int8_t* __restrict__ codes,
@@ -187,15 +156,71 @@ struct IntParams {
   int32_t xvec;          // and whether its rows are 16-byte aligned
 };
 
+// What follows the scales (E: kPlain, kLinear, kGated).
+//   kLinear  y = act(z + bias) + residual
+//   kGated   y = act(z + bias) (z' + bias'), z' of a second layer over the same x
+enum { kPlain = 0, kLinear = 1, kGated = 2 };
+template <int E>
+struct Epilogue {};
+template <>
+struct Epilogue<kLinear> {
+  const float* bias;   // or null
+  const void* res;     // [m, ldr], or null
+  int64_t ldr;
+  int32_t act, res_bf16;
+};
+template <>
+struct Epilogue<kGated> {
+  const int8_t* w;     // the second layer: as in IntParams
+  const float* w_scales;
+  const int32_t* w_offsets;
+  const float* bias;   // of the first, or null
+  const float* bias2;  // of the second
+  int32_t act;
+};
+
+// Logistic forms go through 2^x and a reciprocal (an ulp each; the exponent's
+// rounding adds |z| 2^-24 where the result is next to 0); gelu takes erfc, whose
+// relative error holds where 1 + erf would cancel.  NaN passes through all of them.
+GPTQ_DEV float logistic(float z, float t) {  // z / (1 + e^-t)
+  return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * t));
+}
+GPTQ_DEV float activate(float z, int act) {
+  switch (act) {
+    case kActRelu: return z < 0.f ? 0.f : z;
+    case kActGelu: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case kActGeluTanh: return logistic(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
+    case kActSilu: return logistic(z, z);
+    default: return z;
+  }
+}
+
 GPTQ_DEV void int_put(const IntParams& p, int64_t row, int64_t col, float v) {
   if (p.y_bf16)
     static_cast<uint16_t*>(p.y)[row * p.d_out + col] = f32_to_bf16(v);
   else
     static_cast<float*>(p.y)[row * p.d_out + col] = v;
 }
-GPTQ_DEV void int_store(const IntParams& p, int64_t row, int64_t col, int acc, int off, float sw) {
-  if (p.w_offsets) acc -= off * p.x_sums[row];
-  int_put(p, row, col, (static_cast<float>(acc) * p.x_scales[row]) * sw);
+GPTQ_DEV float linear_out(const Epilogue<kLinear>& e, float z, float bias, float res) {
+  return activate(z + bias, e.act) + res;
+}
+// a value that has its scales, to y
+GPTQ_DEV void int_finish(const IntParams& p, const Epilogue<kPlain>&, int64_t row, int64_t col, float z) {
+  int_put(p, row, col, z);
+}
+GPTQ_DEV void int_finish(const IntParams& p, const Epilogue<kLinear>& e, int64_t row, int64_t col, float z) {
+  float r = 0.f;
+  if (e.res) r = e.res_bf16 ? load1<true>(e.res, row * e.ldr + col) : load1<false>(e.res, row * e.ldr + col);
+  int_put(p, row, col, linear_out(e, z, e.bias ? e.bias[col] : 0.f, r));
+}
+// the two sums of a gated product, to y
+GPTQ_DEV void gated_finish(const IntParams& p, const Epilogue<kGated>& e, int64_t row, int64_t col, int gate, int up,
+                           float sx, int xsum) {
+  if (p.w_offsets) gate -= p.w_offsets[col] * xsum;
+  if (e.w_offsets) up -= e.w_offsets[col] * xsum;
+  const float zg = (static_cast<float>(gate) * sx) * p.w_scales[col] + (e.bias ? e.bias[col] : 0.f);
+  const float zu = (static_cast<float>(up) * sx) * e.w_scales[col] + (e.bias2 ? e.bias2[col] : 0.f);
+  int_put(p, row, col, activate(zg, e.act) * zu);
 }
 
 // Few tokens: the weights are streamed once, bound by HBM.  A workgroup owns 16 R
@@ -217,17 +242,28 @@ GPTQ_DEV void int_store(const IntParams& p, int64_t row, int64_t col, int acc, i
 constexpr int kSW = 8;                // waves
 constexpr int kFusedElems = 16384;    // tokens * d_in at most
 
-template <int R, int MT, int FUSED>  // FUSED: 0 codes given, 1 bf16, 2 fp32
-__global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p) {
+// kGated: a block of 16 weight rows is eight channels of the gate and the same eight
+// of the second layer, so that both weights stream through one loop.
+template <int E>
+GPTQ_DEV const int8_t* block_row(const IntParams& p, const Epilogue<E>&, int64_t block, int c) {
+  return p.w + min(block * 16 + c, p.d_out - 1) * p.d_in;
+}
+template <>
+GPTQ_DEV const int8_t* block_row<kGated>(const IntParams& p, const Epilogue<kGated>& e, int64_t block, int c) {
+  return (c < 8 ? p.w : e.w) + min(block * 8 + (c & 7), p.d_out - 1) * p.d_in;
+}
+
+template <int R, int MT, int FUSED, int E>  // FUSED: 0 codes given, 1 bf16, 2 fp32
+__global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p, Epilogue<E> ep) {
   constexpr int kU = R == 1 && MT == 1 ? 8 : R == 4 || MT == 4 ? 2 : 4;
   constexpr int kTurn = kSW * 64 * kU;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16 * R;
+  const int64_t block0 = static_cast<int64_t>(blockIdx.x) * R;
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
   const int8_t* wrow[R];
 #pragma unroll
-  for (int j = 0; j < R; ++j) wrow[j] = p.w + min(n0 + 16 * j + c, p.d_out - 1) * p.d_in + 16 * g;
+  for (int j = 0; j < R; ++j) wrow[j] = block_row<E>(p, ep, block0 + j, c) + 16 * g;
   const int8_t* xrow[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) xrow[i] = p.x + min(t0 + 16 * i + c, p.m - 1) * p.ldx + 16 * g;
@@ -330,17 +366,24 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
 #pragma unroll
       for (int r = 0; r < 4; ++r) part[wave][j][i][4 * g + r][c] = acc[j][i][r];
   __syncthreads();
-  for (int e = threadIdx.x; e < R * MT * 256; e += 64 * kSW) {
-    const int tc = e & 15, j = (e >> 4) % R, tr = (e / (16 * R)) & 15, i = e / (256 * R);
-    const int64_t col = n0 + 16 * j + tc, row = t0 + 16 * i + tr;
+  constexpr int kC = E == kGated ? 8 : 16;  // channels of a block
+  for (int e = threadIdx.x; e < R * MT * 16 * kC; e += 64 * kSW) {
+    const int tc = e % kC, j = (e / kC) % R, tr = (e / (kC * R)) & 15, i = e / (16 * kC * R);
+    const int64_t col = (block0 + j) * kC + tc, row = t0 + 16 * i + tr;
     if (col >= p.d_out || row >= p.m) continue;
     int s = 0;
 #pragma unroll
     for (int w = 0; w < kSW; ++w) s += part[w][j][i][tr][tc];
-    const int off = p.w_offsets ? p.w_offsets[col] : 0;
-    const float sw = p.w_scales[col];
-    if (FUSED) int_put(p, row, col, (static_cast<float>(s - off * xsum[tr & 3]) * xs[tr & 3]) * sw);
-    else int_store(p, row, col, s, off, sw);
+    const float sx = FUSED ? xs[tr & 3] : p.x_scales[row];
+    if constexpr (E == kGated) {
+      int s2 = 0;
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) s2 += part[w][j][i][tr][tc + 8];
+      gated_finish(p, ep, row, col, s, s2, sx, FUSED ? xsum[tr & 3] : p.x_sums ? p.x_sums[row] : 0);
+    } else {
+      if (p.w_offsets) s -= p.w_offsets[col] * (FUSED ? xsum[tr & 3] : p.x_sums[row]);
+      int_finish(p, ep, row, col, (static_cast<float>(s) * sx) * p.w_scales[col]);
+    }
   }
 }
 
@@ -352,17 +395,19 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
 constexpr int kRW = 16, kRU = 4;
 constexpr int64_t kResidentBytes = 152 * 1024;  // codes, 16 bytes of padding a row (bank conflicts)
 
-__global__ __launch_bounds__(64 * kRW, 4) void integer_resident_kernel(IntParams p) {
+template <int E>
+__global__ __launch_bounds__(64 * kRW, 4) void integer_resident_kernel(IntParams p, Epilogue<E> ep) {
   constexpr int kTurn = kRW * 64 * kRU;
   extern __shared__ __attribute__((aligned(16))) int8_t xr[];  // [m][d_in + 16]
   __shared__ int sum[2][16][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int blocks = static_cast<int>((p.d_out + 15) / 16), m = static_cast<int>(p.m);
+  constexpr int kC = E == kGated ? 8 : 16;  // channels of a row block
+  const int blocks = static_cast<int>((p.d_out + kC - 1) / kC), m = static_cast<int>(p.m);
   const int k_first = wave * 64 * kRU + 16 * g;
   const i32x4_t zero = {0, 0, 0, 0};
   auto load_w = [&](int rb, int k0, i32x4_t (&b)[kRU]) {
-    const int8_t* w = p.w + min(static_cast<int64_t>(rb) * 16 + c, p.d_out - 1) * p.d_in;
+    const int8_t* w = block_row<E>(p, ep, rb, c);
 #pragma unroll
     for (int u = 0; u < kRU; ++u) {
       const int k = k0 + 64 * u;
@@ -401,10 +446,17 @@ __global__ __launch_bounds__(64 * kRW, 4) void integer_resident_kernel(IntParams
       __syncthreads();
       if (threadIdx.x < 256) {
         const int tr = threadIdx.x >> 4, tc = threadIdx.x & 15;
-        const int64_t col = static_cast<int64_t>(rb) * 16 + tc;
-        const int s = sum[buf][tr][tc];
+        const int64_t col = static_cast<int64_t>(rb) * kC + tc % kC;
+        int s = sum[buf][tr][tc];
         sum[buf][tr][tc] = 0;
-        if (col < p.d_out && tr < m) int_store(p, tr, col, s, p.w_offsets ? p.w_offsets[col] : 0, p.w_scales[col]);
+        if constexpr (E == kGated) {
+          const int s2 = __shfl_down(s, 8);  // all of a wave's lanes are here
+          if (tc < 8 && col < p.d_out && tr < m)
+            gated_finish(p, ep, tr, col, s, s2, p.x_scales[tr], p.x_sums ? p.x_sums[tr] : 0);
+        } else if (col < p.d_out && tr < m) {
+          if (p.w_offsets) s -= p.w_offsets[col] * p.x_sums[tr];
+          int_finish(p, ep, tr, col, (static_cast<float>(s) * p.x_scales[tr]) * p.w_scales[col]);
+        }
       }
       buf ^= 1;
     }
@@ -415,15 +467,16 @@ __global__ __launch_bounds__(64 * kRW, 4) void integer_resident_kernel(IntParams
   }
 }
 
-template <int R>
-void stream_go(const IntParams& p, int fused, hipStream_t st) {
-  const dim3 grid(static_cast<unsigned>((p.d_out + 16 * R - 1) / (16 * R)));
+template <int R, int E>
+void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t st) {
+  constexpr int kC = E == kGated ? 8 : 16;
+  const dim3 grid(static_cast<unsigned>((p.d_out + kC * R - 1) / (kC * R)));
   const int t = 64 * kSW;
-  if (fused == 1) integer_stream_kernel<R, 1, 1><<<grid, t, 0, st>>>(p);
-  else if (fused == 2) integer_stream_kernel<R, 1, 2><<<grid, t, 0, st>>>(p);
-  else if (p.m <= 16) integer_stream_kernel<R, 1, 0><<<grid, t, 0, st>>>(p);
-  else if (p.m <= 32) integer_stream_kernel<R, 2, 0><<<grid, t, 0, st>>>(p);
-  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0><<<dim3(grid.x, static_cast<unsigned>((p.m + 63) / 64)), t, 0, st>>>(p);
+  if (fused == 1) integer_stream_kernel<R, 1, 1, E><<<grid, t, 0, st>>>(p, ep);
+  else if (fused == 2) integer_stream_kernel<R, 1, 2, E><<<grid, t, 0, st>>>(p, ep);
+  else if (p.m <= 16) integer_stream_kernel<R, 1, 0, E><<<grid, t, 0, st>>>(p, ep);
+  else if (p.m <= 32) integer_stream_kernel<R, 2, 0, E><<<grid, t, 0, st>>>(p, ep);
+  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0, E><<<dim3(grid.x, static_cast<unsigned>((p.m + 63) / 64)), t, 0, st>>>(p, ep);
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
@@ -506,8 +559,13 @@ GPTQ_DEV void tile_of(const TileGrid& g, int b, int& tm, int& tn, int& slice) {
 
 enum { kOutF32 = 0, kOutBf16 = 1, kOutPart = 2 };
 
-template <int WM, int WN, int OUT>
-__global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid g) {
+// kGated: the 64 WN weight rows of a tile are 32 WN channels of both layers, in
+// blocks of 32 by turns: a wave's products 2 j and 2 j + 1 are the same channels of
+// the gate and of the second layer, in the same lanes.  A wave's loads, 16 WN of
+// the rows, never mix the layers inside a piece.
+template <int WM, int WN, int OUT, int E>
+__global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid g, Epilogue<E> ep) {
+  constexpr int kCols = E == kGated ? 32 * WN : 64 * WN;  // channels of a tile
   constexpr int kA = WM * 64 * kTStep, kB = WN * 64 * kTStep;
   // one array per slot: the compiler then sees that reads of one slot do not alias loads in flight into another
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA], sA3[kA];
@@ -517,11 +575,18 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const int64_t m0 = static_cast<int64_t>(tm) * (64 * WM), n0 = static_cast<int64_t>(tn) * (64 * WN);
+  const int64_t m0 = static_cast<int64_t>(tm) * (64 * WM), n0 = static_cast<int64_t>(tn) * kCols;
   const int mrows = static_cast<int>(min(p.m - m0, int64_t{64 * WM}));
-  const int nrows = static_cast<int>(min(p.d_out - n0, int64_t{64 * WN}));
+  const int nrows = static_cast<int>(min(p.d_out - n0, int64_t{kCols}));
   const __amdgpu_buffer_rsrc_t ra = rows_rsrc(p.x + m0 * p.ldx, (mrows - 1) * p.ldx + p.d_in);
-  const __amdgpu_buffer_rsrc_t rb = rows_rsrc(p.w + n0 * p.d_in, static_cast<int64_t>(nrows) * p.d_in);
+  // the layer of the wave's pieces: of all of them, or (kGated with four) of the first two and the last two
+  const int8_t *w_lo = p.w, *w_hi = p.w;
+  if constexpr (E == kGated) {
+    w_lo = WN == 2 && (wave & 1) ? ep.w : p.w;
+    w_hi = WN == 2 ? w_lo : ep.w;
+  }
+  const __amdgpu_buffer_rsrc_t rb = rows_rsrc(w_lo + n0 * p.d_in, static_cast<int64_t>(nrows) * p.d_in);
+  const __amdgpu_buffer_rsrc_t rb_hi = rows_rsrc(w_hi + n0 * p.d_in, static_cast<int64_t>(nrows) * p.d_in);
   const int kc = (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
   uint32_t va[WM], vb[WN];
 #pragma unroll
@@ -531,7 +596,8 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   }
 #pragma unroll
   for (int u = 0; u < WN; ++u) {
-    const int row = (wave * WN + u) * 16 + (lane >> 2);
+    const int piece = wave * WN + u;
+    const int row = (E == kGated ? 2 * (piece >> 2) + (piece & 1) : piece) * 16 + (lane >> 2);
     vb[u] = row < nrows ? static_cast<uint32_t>(row * p.d_in + kc) : 0x80000000u;
   }
   const int s0 = slice * g.per;
@@ -555,7 +621,7 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   auto issue_b = [&](int s, int slot) {
     const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in;
 #pragma unroll
-    for (int u = 0; u < WN; ++u) tile_dma(rb, slotB(slot) + (wave * WN + u) * 1024, vb[u], kc, k0, p.d_in);
+    for (int u = 0; u < WN; ++u) tile_dma(E == kGated && u >= 2 ? rb_hi : rb, slotB(slot) + (wave * WN + u) * 1024, vb[u], kc, k0, p.d_in);
   };
   // operand reads: row l % 32 of a 32-row tile, chunk 2 half + l / 32
   const int r = lane & 31, hi = lane >> 5;
@@ -601,20 +667,25 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   // columns past d_out (offset 2^31) are dropped in hardware.
   __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(0));  // the loads past the end still write LDS
   const int dout = static_cast<int>(p.d_out);
+  constexpr int kLayers = E == kGated ? 2 : 1;
+  auto col_of = [&](int j) {  // channel of the lane's products j
+    return static_cast<int>(n0) + (E == kGated ? (wn * WN + j) >> 1 : wn * WN + j) * 32 + r;
+  };
   const uint32_t row0 = static_cast<uint32_t>(wm * WM * 32 + 4 * hi);
   if (OUT == kOutPart) {
     const __amdgpu_buffer_rsrc_t rp =
-        rows_rsrc(reinterpret_cast<int8_t*>(g.partial + (static_cast<int64_t>(slice) * p.m + m0) * p.d_out),
-                  static_cast<int64_t>(mrows) * dout * 4);
+        rows_rsrc(reinterpret_cast<int8_t*>(g.partial + (static_cast<int64_t>(slice) * p.m + m0) * (p.d_out * kLayers)),
+                  static_cast<int64_t>(mrows) * dout * kLayers * 4);
 #pragma unroll
     for (int j = 0; j < WN; ++j) {
-      const int col = static_cast<int>(n0) + (wn * WN + j) * 32 + r;
+      const int col = col_of(j);
 #pragma unroll
       for (int i = 0; i < WM; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const uint32_t row = row0 + 32 * i + 8 * (e >> 2) + (e & 3);
-          __builtin_amdgcn_raw_buffer_store_b32(acc[i][j][e], rp, col < dout ? (row * dout + col) * 4 : 0x80000000u, 0, 0);
+          const uint32_t at = row * dout * kLayers + (E == kGated ? (j & 1) * dout : 0) + col;
+          __builtin_amdgcn_raw_buffer_store_b32(acc[i][j][e], rp, col < dout ? at * 4 : 0x80000000u, 0, 0);
         }
     }
     return;
@@ -624,20 +695,60 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   int* lsm = reinterpret_cast<int*>(sB0);
   for (int e = threadIdx.x; e < mrows; e += 256) {
     lsc[e] = p.x_scales[m0 + e];
-    lsm[e] = p.w_offsets ? p.x_sums[m0 + e] : 0;
+    lsm[e] = p.x_sums ? p.x_sums[m0 + e] : 0;
   }
   __syncthreads();
   constexpr int size = OUT == kOutBf16 ? 2 : 4;
   const __amdgpu_buffer_rsrc_t ry =
       rows_rsrc(static_cast<const int8_t*>(p.y) + m0 * p.d_out * size, static_cast<int64_t>(mrows) * dout * size);
+  // the tile's rows of the residual: past them, and past d_out, zeros are loaded
+  __amdgpu_buffer_rsrc_t rres = ry;
+  if constexpr (E == kLinear) {
+    const int rsize = ep.res_bf16 ? 2 : 4;
+    rres = rows_rsrc(static_cast<const int8_t*>(ep.res) + m0 * ep.ldr * rsize,
+                     ep.res ? ((mrows - 1) * ep.ldr + p.d_out) * rsize : 0);
+  }
+  auto put = [&](float v, uint32_t to) {
+    if (OUT == kOutBf16)
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(f32_to_bf16(v)), ry, to, 0, 0);
+    else
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), ry, to, 0, 0);
+  };
 #pragma unroll
-  for (int j = 0; j < WN; ++j) {
-    const int col = static_cast<int>(n0) + (wn * WN + j) * 32 + r;
-    const float sw = col < dout ? p.w_scales[col] : 0.f;
-    const int off = (col < dout && p.w_offsets) ? p.w_offsets[col] : 0;
-    const uint32_t at = col < dout ? static_cast<uint32_t>(col * size) : 0x80000000u;
+  for (int j = 0; j < WN; j += kLayers) {
+    const int col = col_of(j);
+    const bool in = col < dout;
+    const float sw = in ? p.w_scales[col] : 0.f;
+    const int off = (in && p.w_offsets) ? p.w_offsets[col] : 0;
+    const uint32_t at = in ? static_cast<uint32_t>(col * size) : 0x80000000u;
+    float bias = 0.f, bias2 = 0.f, sw2 = 0.f;
+    int off2 = 0;
+    if constexpr (E != kPlain) bias = (in && ep.bias) ? ep.bias[col] : 0.f;
+    if constexpr (E == kGated) {
+      sw2 = in ? ep.w_scales[col] : 0.f;
+      off2 = (in && ep.w_offsets) ? ep.w_offsets[col] : 0;
+      bias2 = (in && ep.bias2) ? ep.bias2[col] : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < WM; ++i) {
+      float res[16] = {};
+      if constexpr (E == kLinear) {
+        if (ep.res) {
+          const uint32_t lead = static_cast<uint32_t>(ep.ldr) << (ep.res_bf16 ? 1 : 2);
+          const uint32_t from = in ? static_cast<uint32_t>(col) << (ep.res_bf16 ? 1 : 2) : 0x80000000u;
+          if (ep.res_bf16) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              res[e] = bf16_to_f32(static_cast<uint16_t>(
+                  __builtin_amdgcn_raw_buffer_load_b16(rres, from + (row0 + 32 * i + 8 * (e >> 2) + (e & 3)) * lead, 0, 0)));
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              res[e] = __int_as_float(static_cast<int>(
+                  __builtin_amdgcn_raw_buffer_load_b32(rres, from + (row0 + 32 * i + 8 * (e >> 2) + (e & 3)) * lead, 0, 0)));
+          }
+        }
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t row = row0 + 32 * i + 8 * q;
@@ -645,12 +756,11 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
         const i32x4_t sm = *reinterpret_cast<const i32x4_t*>(lsm + row);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float v = (static_cast<float>(acc[i][j][4 * q + e] - off * sm[e]) * sc[e]) * sw;
-          const uint32_t to = at + (row + e) * static_cast<uint32_t>(dout * size);
-          if (OUT == kOutBf16)
-            __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(f32_to_bf16(v)), ry, to, 0, 0);
-          else
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), ry, to, 0, 0);
+          float v = (static_cast<float>(acc[i][j][4 * q + e] - off * sm[e]) * sc[e]) * sw;
+          if constexpr (E == kLinear) v = linear_out(ep, v, bias, res[4 * q + e]);
+          if constexpr (E == kGated)
+            v = activate(v + bias, ep.act) * ((static_cast<float>(acc[i][j + 1][4 * q + e] - off2 * sm[e]) * sc[e]) * sw2 + bias2);
+          put(v, at + (row + e) * static_cast<uint32_t>(dout * size));
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -661,8 +771,8 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
 // sums of the K slices (integers: any order gives the same), four columns a
 // thread where rows are whole vectors.  Bound: the caches and HBM (four slices
 // of 509 x 4096, 33 MB, in 10 us).
-template <int V>
-__global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid g) {
+template <int V, int E>
+__global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid g, Epilogue<E> ep) {
   typedef int ivec_t __attribute__((ext_vector_type(V)));
   const int64_t col = (blockIdx.x * 256ll + threadIdx.x) * V;
   if (col >= p.d_out) return;
@@ -673,13 +783,20 @@ __global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid
     sw[j] = p.w_scales[col + j];
     off[j] = p.w_offsets ? p.w_offsets[col + j] : 0;
   }
+  constexpr int kLayers = E == kGated ? 2 : 1;
   for (int64_t row = blockIdx.y; row < p.m; row += gridDim.y) {
-    ivec_t s = {};
-    for (int k = 0; k < g.slices; ++k) s += *reinterpret_cast<const ivec_t*>(g.partial + (k * p.m + row) * p.d_out + col);
-    const float sx = p.x_scales[row];
-    const int sum = p.w_offsets ? p.x_sums[row] : 0;
+    ivec_t s[kLayers] = {};
+    for (int k = 0; k < g.slices; ++k)
 #pragma unroll
-    for (int j = 0; j < V; ++j) int_put(p, row, col + j, (static_cast<float>(s[j] - off[j] * sum) * sx) * sw[j]);
+      for (int l = 0; l < kLayers; ++l)
+        s[l] += *reinterpret_cast<const ivec_t*>(g.partial + ((k * p.m + row) * kLayers + l) * p.d_out + col);
+    const float sx = p.x_scales[row];
+    const int sum = p.x_sums ? p.x_sums[row] : 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      if constexpr (E == kGated) gated_finish(p, ep, row, col + j, s[0][j], s[1][j], sx, sum);
+      else int_finish(p, ep, row, col + j, (static_cast<float>(s[0][j] - off[j] * sum) * sx) * sw[j]);
+    }
   }
 }
 
@@ -766,11 +883,17 @@ hipError_t integer_weight_launch(const int32_t* qweight, const int32_t* zeros, i
 }
 
 namespace {
-template <int WM, int WN>
-void tile_go(const IntParams& p, const TileGrid& g, unsigned blocks, hipStream_t st) {
-  if (g.slices > 1) integer_tile_kernel<WM, WN, kOutPart><<<blocks, 256, 0, st>>>(p, g);
-  else if (p.y_bf16) integer_tile_kernel<WM, WN, kOutBf16><<<blocks, 256, 0, st>>>(p, g);
-  else integer_tile_kernel<WM, WN, kOutF32><<<blocks, 256, 0, st>>>(p, g);
+// kLinear's slices are kPlain's: what follows the sums is the join's
+template <int WM, int WN, int E>
+void tile_go(const IntParams& p, const TileGrid& g, const Epilogue<E>& ep, unsigned blocks, hipStream_t st) {
+  if (g.slices > 1) {
+    if constexpr (E == kGated) integer_tile_kernel<WM, WN, kOutPart, E><<<blocks, 256, 0, st>>>(p, g, ep);
+    else integer_tile_kernel<WM, WN, kOutPart, kPlain><<<blocks, 256, 0, st>>>(p, g, {});
+  } else if (p.y_bf16) {
+    integer_tile_kernel<WM, WN, kOutBf16, E><<<blocks, 256, 0, st>>>(p, g, ep);
+  } else {
+    integer_tile_kernel<WM, WN, kOutF32, E><<<blocks, 256, 0, st>>>(p, g, ep);
+  }
 }
 size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
 }  // namespace
@@ -781,77 +904,96 @@ size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool cod
   return codes_given || fuses(m, d_in) ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
 }
 
-hipError_t integer_matmul_launch(const void* x, int xt, const float* x_scales, const int32_t* x_sums, int64_t m,
-                                 int64_t d_in, int64_t ldx, const int8_t* w, const float* w_scales,
-                                 const int32_t* w_offsets, int64_t d_out, void* y, bool y_bf16, void* ws, int n_cu,
-                                 hipStream_t st) {
-  const IntPlan plan = int_plan(m, d_in, d_out, n_cu);
-  IntParams p{};
-  p.x = static_cast<const int8_t*>(x);
-  p.ldx = ldx;
-  p.x_scales = x_scales;
-  p.x_sums = x_sums;
-  const int64_t vec = xt == kXBf16 ? 8 : 4;
-  const bool fused = xt != kXInt8 && fuses(m, d_in);
-  if (fused) {
-    p.xraw = x;
-    p.ldxraw = ldx;
-    p.xvec = ldx % vec == 0 && (reinterpret_cast<uintptr_t>(x) & 15u) == 0;
-  } else if (xt != kXInt8) {
-    uint8_t* b = static_cast<uint8_t*>(ws) + up256(plan.partial_bytes);
-    int8_t* codes = reinterpret_cast<int8_t*>(b);
-    float* sc = reinterpret_cast<float*>(b + up256(static_cast<size_t>(m) * d_in));
-    int32_t* sm = reinterpret_cast<int32_t*>(b + up256(static_cast<size_t>(m) * d_in) + up256(static_cast<size_t>(m) * 4));
-    const hipError_t e = token_codes_launch(x, xt == kXBf16, m, d_in, ldx, codes, sc, w_offsets ? sm : nullptr, st);
-    if (e != hipSuccess) return e;
-    p.x = codes;
-    p.ldx = d_in;
-    p.x_scales = sc;
-    p.x_sums = sm;
-  }
-  p.w = w;
-  p.w_scales = w_scales;
-  p.w_offsets = w_offsets;
-  p.y = y;
-  p.m = m;
-  p.d_out = d_out;
-  p.d_in = static_cast<int32_t>(d_in);
-  p.y_bf16 = y_bf16 ? 1 : 0;
+namespace {
+// The launches of a product whose x, layer and y stand in p (x in codes, or
+// FUSED: raw); rows: of all weights that it reads.
+template <int E>
+hipError_t product_go(const IntParams& p, const IntPlan& plan, const Epilogue<E>& ep, int f, int64_t rows, int32_t* partial,
+                      int n_cu, hipStream_t st) {
   if (plan.kind == 0) {
-    const int f = !fused ? 0 : xt == kXBf16 ? 1 : 2;
     // Sixteen tokens through 28672 x 8192: 53 us with the codes in LDS, 63 us with
     // four row blocks that share them.  With fewer row blocks than four a CU it
     // is no faster (11008 x 4096: 17.5 against 16.5 us): the codes are read once
     // a workgroup, and the CUs that have one row block more than the others end late.
-    if (f == 0 && m <= 16 && m * (d_in + 16) <= kResidentBytes && d_out >= 64ll * n_cu) {
-      integer_resident_kernel<<<static_cast<unsigned>(n_cu), 64 * kRW,
-                                static_cast<size_t>(m * (d_in + 16)), st>>>(p);
+    if (f == 0 && p.m <= 16 && p.m * (p.d_in + 16) <= kResidentBytes && rows >= 64ll * n_cu) {
+      integer_resident_kernel<E><<<static_cast<unsigned>(n_cu), 64 * kRW,
+                                   static_cast<size_t>(p.m * (p.d_in + 16)), st>>>(p, ep);
       return hipGetLastError();
     }
-    const int r = stream_rows(m, d_out, n_cu);
-    if (r == 4) stream_go<4>(p, f, st);
-    else if (r == 2) stream_go<2>(p, f, st);
-    else stream_go<1>(p, f, st);
+    const int r = stream_rows(p.m, rows, n_cu);
+    if (r == 4) stream_go<4, E>(p, ep, f, st);
+    else if (r == 2) stream_go<2, E>(p, ep, f, st);
+    else stream_go<1, E>(p, ep, f, st);
     return hipGetLastError();
   }
   const int64_t edge = plan.kind == 2 ? 256 : 128;
   TileGrid g{};
-  g.nm = static_cast<int32_t>((m + edge - 1) / edge);
-  g.nn = static_cast<int32_t>((d_out + edge - 1) / edge);
+  g.nm = static_cast<int32_t>((p.m + edge - 1) / edge);
+  g.nn = static_cast<int32_t>((rows + edge - 1) / edge);
   g.slices = plan.slices;
   g.per = plan.per;
-  g.partial = static_cast<int32_t*>(ws);
+  g.partial = partial;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(g.nm) * g.nn * g.slices);
-  if (plan.kind == 2) tile_go<4, 4>(p, g, blocks, st);
-  else tile_go<2, 2>(p, g, blocks, st);
+  if (plan.kind == 2) tile_go<4, 4, E>(p, g, ep, blocks, st);
+  else tile_go<2, 2, E>(p, g, ep, blocks, st);
   if (g.slices > 1) {
-    const unsigned rows = static_cast<unsigned>(std::min<int64_t>(m, 32768));
-    if (d_out % 4 == 0)
-      integer_join_kernel<4><<<dim3(static_cast<unsigned>((d_out / 4 + 255) / 256), rows), 256, 0, st>>>(p, g);
+    const unsigned along = static_cast<unsigned>(std::min<int64_t>(p.m, 32768));
+    if (p.d_out % 4 == 0)
+      integer_join_kernel<4, E><<<dim3(static_cast<unsigned>((p.d_out / 4 + 255) / 256), along), 256, 0, st>>>(p, g, ep);
     else
-      integer_join_kernel<1><<<dim3(static_cast<unsigned>((d_out + 255) / 256), rows), 256, 0, st>>>(p, g);
+      integer_join_kernel<1, E><<<dim3(static_cast<unsigned>((p.d_out + 255) / 256), along), 256, 0, st>>>(p, g, ep);
   }
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t integer_launch(const IntCall& c, void* ws, int n_cu, hipStream_t st) {
+  const bool gated = c.up.w != nullptr;
+  const int64_t rows = gated ? 2 * c.d_out : c.d_out;
+  const IntPlan plan = int_plan(c.m, c.d_in, rows, n_cu);
+  IntParams p{};
+  p.x = static_cast<const int8_t*>(c.x);
+  p.ldx = c.ldx;
+  const bool offsets = c.layer.offsets || c.up.offsets;
+  p.x_scales = c.x_scales;
+  p.x_sums = offsets ? c.x_sums : nullptr;
+  const int64_t vec = c.xt == kXBf16 ? 8 : 4;
+  const bool fused = c.xt != kXInt8 && fuses(c.m, c.d_in);
+  if (fused) {
+    p.xraw = c.x;
+    p.ldxraw = c.ldx;
+    p.xvec = c.ldx % vec == 0 && (reinterpret_cast<uintptr_t>(c.x) & 15u) == 0;
+  } else if (c.xt != kXInt8) {
+    uint8_t* b = static_cast<uint8_t*>(ws) + up256(plan.partial_bytes);
+    int8_t* codes = reinterpret_cast<int8_t*>(b);
+    float* sc = reinterpret_cast<float*>(b + up256(static_cast<size_t>(c.m) * c.d_in));
+    int32_t* sm = reinterpret_cast<int32_t*>(b + up256(static_cast<size_t>(c.m) * c.d_in) + up256(static_cast<size_t>(c.m) * 4));
+    const hipError_t e = token_codes_launch(c.x, c.xt == kXBf16, c.m, c.d_in, c.ldx, codes, sc, offsets ? sm : nullptr, st);
+    if (e != hipSuccess) return e;
+    p.x = codes;
+    p.ldx = c.d_in;
+    p.x_scales = sc;
+    p.x_sums = offsets ? sm : nullptr;
+  }
+  p.w = c.layer.w;
+  p.w_scales = c.layer.scales;
+  p.w_offsets = c.layer.offsets;
+  p.y = c.y;
+  p.m = c.m;
+  p.d_out = c.d_out;
+  p.d_in = static_cast<int32_t>(c.d_in);
+  p.y_bf16 = c.y_bf16 ? 1 : 0;
+  const int f = !fused ? 0 : c.xt == kXBf16 ? 1 : 2;
+  int32_t* partial = static_cast<int32_t*>(ws);
+  if (gated) {
+    const Epilogue<kGated> ep{c.up.w, c.up.scales, c.up.offsets, c.layer.bias, c.up.bias, c.act};
+    return product_go<kGated>(p, plan, ep, f, rows, partial, n_cu, st);
+  }
+  if (c.layer.bias || c.res || c.act != kActNone) {
+    const Epilogue<kLinear> ep{c.layer.bias, c.res, c.ldr, c.act, c.res_bf16 ? 1 : 0};
+    return product_go<kLinear>(p, plan, ep, f, rows, partial, n_cu, st);
+  }
+  return product_go<kPlain>(p, plan, {}, f, rows, partial, n_cu, st);
 }
 
 }  // namespace gptq

@@ -124,6 +124,39 @@ GPTQ_DEV float load1(const void* base, int64_t elem) {
   return BF16 ? bf16_to_f32(static_cast<const uint16_t*>(base)[elem]) : static_cast<const float*>(base)[elem];
 }
 
+// eight values of a row from element e on (zeros past its d; VEC: rows 16-byte
+// aligned, d a multiple of 8), and their codes; the store returns the codes' sum
+template <bool BF16, bool VEC>
+GPTQ_DEV void tok_load(const void* x, int64_t row0, int64_t e, int64_t d, float (&v)[8]) {
+  if (VEC) {
+    if (e < d) {
+      load8<BF16>(x, row0 + e, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = (e + i < d) ? load1<BF16>(x, row0 + e + i) : 0.f;
+  }
+}
+
+template <bool VEC>
+GPTQ_DEV int tok_store(int8_t* codes, int64_t at, int64_t e, int64_t d, const float (&v)[8], const RowScale& rs) {
+  if (e >= d) return 0;
+  uint32_t w[2];
+  row_codes<127, 0>(v, rs, w);
+  const int sum = __builtin_amdgcn_sdot4(w[0], 0x01010101, __builtin_amdgcn_sdot4(w[1], 0x01010101, 0, false), false);
+  if (VEC) {
+    *reinterpret_cast<uint2*>(codes + at + e) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (e + i < d) codes[at + e + i] = static_cast<int8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+  return sum;
+}
+
 // fp32 -> bf16, NaN kept (f32_to_bf16_rn is for finite values)
 GPTQ_DEV uint16_t f32_to_bf16(float x) {
   const uint16_t r = f32_to_bf16_rn(x);

@@ -1,0 +1,263 @@
+"""The integer product with bias, activation and residual, and the gated product,
+against their 64-bit forms.
+
+With u = 2^-24 and z the product's value, whose three roundings are (1 + u)^3 - 1
+relative (test_gpu_integer):
+  z + b    dz = ((1 + u)^3 - 1) |z| + u (|z| + |b|) (1 + 8 u)
+  act      its slope is at most 1.13 (gelu; silu 1.10, relu 1), so dz gives 1.13 dz;
+           its own evaluation, relative to the result:
+             silu       e^-z by 2^(-z log2 e): the exponent's constant and product 2^-24
+                        each, |z| 2^-23 in e^-z; 2^x, 1 + e, 1 / (1 + e) and the product at
+                        most 2^-23 each: (|z| + 4) 2^-23
+             gelu_tanh  the same of t = 2 c (z + 0.044715 z^3), whose terms have one
+                        sign: its own roundings 6 u |t|: (4 |t| + 4) 2^-23
+             gelu       erfc at an argument off by 2 u relative: z^2 2 u, and erfc's own
+                        error, at most 16 ulp: (z^2 + 18) 2^-23
+           and below 2^-100 what e^-z past fp32 leaves
+  + r      u |y|
+  store    2^-8 |y| for bf16
+Gated: y = a z', so |z'| da + |a| dz' + da dz' and one rounding."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import banner, dev, host, to_dev
+from oracle import layer_oracle as L
+from oracle import serving_oracle as S
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+ACTS = [None, "relu", "gelu", "gelu_tanh", "silu"]
+
+
+@pytest.fixture(scope="module")
+def G():
+    import post_weight_quantization_07_amd as G
+    assert torch.cuda.is_available()
+    return G
+
+
+def _d(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dev())
+
+
+def _x(m, d, dtype, seed):
+    r = np.random.default_rng(seed)
+    x = (r.standard_normal((m, d)) * np.exp(0.5 * r.standard_normal(d))).astype(np.float32)
+    if m > 2:
+        x[1] = 0.0                                        # a padded token
+    return to_dev(x, dtype)
+
+
+class Layer:
+    def __init__(self, d_out, d_in, seed, asym, bias):
+        r = np.random.default_rng(seed)
+        self.w = r.integers(-128 if asym else -127, 128, (d_out, d_in)).astype(np.int8)
+        # products of about 2, so that activations are met on both sides
+        self.s = (0.02 / np.sqrt(d_in) * np.exp(0.5 * r.standard_normal(d_out))).astype(np.float32)
+        self.off = r.integers(-20, 21, d_out).astype(np.int32) if asym else np.zeros(d_out, np.int32)
+        self.b = r.standard_normal(d_out).astype(np.float32) if bias else None
+        self.dict = {"w": _d(self.w), "scales": _d(self.s)}
+        if asym:
+            self.dict["offsets"] = _d(self.off)
+        if bias:
+            self.dict["bias"] = _d(self.b)
+
+    def product(self, codes, scales):
+        """z + b in fp64 and what the library's may be off by."""
+        z = S.integer_matmul(codes, scales, self.w, self.s, self.off)
+        err = ((1 + U) ** 3 - 1) * np.abs(z)
+        if self.b is not None:
+            b = self.b.astype(np.float64)
+            err = err + U * (np.abs(z) + np.abs(b)) * (1 + 8 * U)
+            z = z + b
+        return z, err
+
+
+def activated(z, dz, act):
+    a = L.activation(z, act)
+    if act is None or act == "relu":
+        return a, dz
+    t = z if act == "silu" else 2 * 0.7978845608 * (z + 0.044715 * z ** 3)
+    own = {"silu": np.abs(z) + 4, "gelu_tanh": 4 * np.abs(t) + 4, "gelu": z ** 2 + 18}[act] * 2.0 ** -23
+    return a, 1.13 * dz + own * np.abs(a) + 2.0 ** -100
+
+
+def near(y, ref, err):
+    store = (2.0 ** -8 if y.dtype == torch.bfloat16 else 0.0) * (np.abs(ref) + err) + 2.0 ** -126
+    off = np.abs(y.double().cpu().numpy() - ref)
+    assert (off <= err + U * np.abs(ref) + store).all(), float((off / (err + U * np.abs(ref) + store)).max())
+
+
+def linear_ref(x, layer, act, res):
+    codes, scales = S.row_codes(host(x), 127)
+    a, da = activated(*layer.product(codes, scales), act)
+    return (a, da) if res is None else (a + host(res).astype(np.float64), da + U * np.abs(a))
+
+
+def gated_ref(x, gate, up, act):
+    codes, scales = S.row_codes(host(x), 127)
+    a, da = activated(*gate.product(codes, scales), act)
+    z, dz = up.product(codes, scales)
+    return a * z, np.abs(z) * da + np.abs(a) * dz + da * dz
+
+
+SHAPES = [(1, 32, 1), (1, 96, 17), (1, 4096, 300), (2, 160, 33), (15, 4096, 64), (16, 224, 48), (17, 1024, 100), (31, 352, 257),
+          (33, 2048, 130), (64, 4096, 272), (65, 32, 500), (100, 4128, 260), (128, 768, 768), (129, 288, 511), (200, 11008, 70),
+          (257, 1056, 300), (300, 96, 1030), (513, 4096, 520), (4100, 96, 4200), (2049, 352, 8300), (16, 512, 16500),
+          (5, 8192, 9000), (16, 4096, 20000)]
+
+
+@pytest.mark.parametrize("m,d_in,d_out", SHAPES)
+@pytest.mark.parametrize("asym,xt,yt,rt,bias", [(False, "bf16", torch.bfloat16, "bf16", False),
+                                                (True, "f32", torch.float32, "f32", True),
+                                                (False, "bf16", torch.float32, None, True)])
+def test_linear(G, m, d_in, d_out, asym, xt, yt, rt, bias):
+    act = ACTS[(m + d_in + d_out) % 5]
+    banner(f"linear {m}x{d_in}->{d_out} asym={asym} x={xt} y={yt} act={act} residual={rt} bias={bias}")
+    x, layer = _x(m, d_in, xt, m + d_in), Layer(d_out, d_in, d_out + d_in, asym, bias)
+    res = None if rt is None else to_dev(np.random.default_rng(m).standard_normal((m, d_out)).astype(np.float32), rt)
+    t = layer.dict
+    args = (t["w"], t["scales"], t.get("offsets"))
+    kw = dict(out_dtype=yt, bias=t.get("bias"), activation=act, residual=res)
+    y = G.gptq_integer_matmul(x, *args, **kw)
+    assert y.dtype == yt
+    near(y, *linear_ref(x, layer, act, res))
+    assert torch.equal(y, G.gptq_integer_matmul(G.gptq_quantize_tokens(x), *args, **kw))
+    if res is not None and res.dtype == yt:                # over the residual
+        mine = res.clone()
+        kw["residual"] = mine
+        assert G.gptq_integer_matmul(x, *args, y=mine, **kw) is mine
+        assert torch.equal(mine, y)
+
+
+@pytest.mark.parametrize("m,d_in,d_out", SHAPES)
+@pytest.mark.parametrize("asym,xt,yt,bias", [((False, False), "bf16", torch.bfloat16, (False, False)),
+                                             ((True, True), "f32", torch.float32, (True, True)),
+                                             ((False, True), "bf16", torch.float32, (True, False))])
+def test_gated(G, m, d_in, d_out, asym, xt, yt, bias):
+    act = ACTS[(m + d_in + d_out) % 5]
+    banner(f"gated {m}x{d_in}->{d_out} asym={asym} x={xt} y={yt} act={act} bias={bias}")
+    x = _x(m, d_in, xt, m + d_in)
+    gate, up = (Layer(d_out, d_in, d_out + d_in + i, a, b) for i, (a, b) in enumerate(zip(asym, bias)))
+    kw = dict(activation=act, out_dtype=yt)
+    y = G.gptq_integer_gated(x, gate.dict, up.dict, **kw)
+    assert y.dtype == yt
+    near(y, *gated_ref(x, gate, up, act))
+    assert torch.equal(y, G.gptq_integer_gated(G.gptq_quantize_tokens(x), gate.dict, up.dict, **kw))
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_activations(G, act):
+    """Every activation from far below to far above 0, through both calls: the scale of a channel sets the size of its value."""
+    banner(f"activation {act}")
+    n = 4001
+    sizes = np.sort(np.concatenate([np.linspace(-12, 12, 2001), -np.logspace(-6, 4, 1000), np.logspace(-6, 4, 1000)]))
+    w = np.where(sizes < 0, -127, 127).astype(np.int8)[:, None] * np.ones((1, 32), np.int8)
+    layer = Layer(n, 32, 1, False, False)
+    layer.w, layer.s = w, (np.abs(sizes) / (127.0 * 32)).astype(np.float32)
+    layer.dict = {"w": _d(w), "scales": _d(layer.s)}
+    for m in (1, 40, 700):
+        x = torch.ones(m, 32, device=dev())
+        near(G.gptq_integer_matmul(x, layer.dict["w"], layer.dict["scales"], activation=act),
+             *linear_ref(x, layer, act, None)) if act else None
+        near(G.gptq_integer_gated(x, layer.dict, layer.dict, activation=act), *gated_ref(x, layer, layer, act))
+
+
+@pytest.mark.parametrize("m", [1, 20, 500])
+def test_not_finite_stays_in_its_row(G, m):
+    """A token with a NaN or an infinity, and a residual with one: NaN there, through relu too."""
+    banner(f"not finite, {m} tokens")
+    layer = Layer(90, 64, 3, True, True)
+    x, res = _x(m, 64, "f32", 1), torch.randn(m, 90, device=dev())
+    t = layer.dict
+    for act in ACTS:
+        kw = dict(bias=t["bias"], activation=act, residual=res)
+        want = G.gptq_integer_matmul(x, t["w"], t["scales"], t["offsets"], **kw)
+        want2 = G.gptq_integer_gated(x, t, t, activation=act)
+        for bad in (float("nan"), float("-inf")):
+            x2 = x.clone()
+            x2[m // 2, 9] = bad
+            y = G.gptq_integer_matmul(x2, t["w"], t["scales"], t["offsets"], **kw)
+            y2 = G.gptq_integer_gated(x2, t, t, activation=act)
+            assert torch.isnan(y[m // 2]).all() and torch.isnan(y2[m // 2]).all()
+            keep = torch.arange(m, device=dev()) != m // 2
+            assert torch.equal(y[keep], want[keep]) and torch.equal(y2[keep], want2[keep])
+        res2 = res.clone()
+        res2[0, 5] = float("inf")
+        y = G.gptq_integer_matmul(x, t["w"], t["scales"], t["offsets"], bias=t["bias"], activation=act, residual=res2)
+        assert y[0, 5] == float("inf")
+
+
+def test_strided_residual(G):
+    banner("linear: residual rows inside wider ones, and rows that overlap y refused")
+    for m, d_in, d_out in ((3, 64, 50), (40, 256, 130), (600, 512, 260)):
+        layer, x = Layer(d_out, d_in, 5, False, False), _x(m, d_in, "bf16", 6)
+        wide = torch.randn(m, 3 * d_out, device=dev())
+        res = wide[:, d_out:2 * d_out]
+        t = layer.dict
+        y = G.gptq_integer_matmul(x, t["w"], t["scales"], residual=res)
+        assert torch.equal(y, G.gptq_integer_matmul(x, t["w"], t["scales"], residual=res.contiguous()))
+        near(y, *linear_ref(x, layer, None, res))
+        flat = torch.randn((m + 1) * d_out, device=dev())
+        with pytest.raises(G.GptqError):
+            G.gptq_integer_matmul(x, t["w"], t["scales"], y=flat[:m * d_out].view(m, d_out),
+                                  residual=flat[d_out // 2:][:m * d_out].view(m, d_out))
+        with pytest.raises(G.GptqError):                   # another type at the same place
+            G.gptq_integer_matmul(x, t["w"], t["scales"], y=flat[:m * d_out].view(m, d_out),
+                                  residual=flat.view(torch.bfloat16)[:m * d_out].view(m, d_out))
+
+
+def test_refusals_and_empty(G):
+    banner("linear and gated: refusals, no tokens")
+    layer, other = Layer(40, 64, 1, True, True), Layer(41, 64, 2, True, True)
+    x, t = _x(5, 64, "bf16", 1), layer.dict
+    res = torch.randn(5, 40, device=dev())
+    mm = lambda **kw: G.gptq_integer_matmul(x, t["w"], t["scales"], t["offsets"], **kw)  # noqa: E731
+    for bad in (lambda: mm(activation="tanh"), lambda: mm(bias=t["bias"].double()), lambda: mm(bias=t["bias"][:39]),
+                lambda: mm(bias=t["bias"].cpu()), lambda: mm(residual=res[:4]), lambda: mm(residual=res.half()),
+                lambda: mm(residual=res.t().contiguous().t()), lambda: mm(residual=res.cpu()),
+                lambda: G.gptq_integer_gated(x, t, other.dict), lambda: G.gptq_integer_gated(x, t, t, activation="swish"),
+                lambda: G.gptq_integer_gated(x[:, :32], t, t), lambda: G.gptq_integer_gated(x, t, dict(t, bias=t["bias"][:3])),
+                lambda: G.gptq_integer_gated(x, t, t, y=torch.empty(5, 41, device=dev())),
+                lambda: G.gptq_integer_gated((*G.gptq_quantize_tokens(x)[:2], None), t, t)):
+        with pytest.raises(ValueError):
+            bad()
+    big = Layer(300, 4096, 3, False, False)
+    with pytest.raises(G.GptqError, match="workspace"):
+        G.gptq_integer_gated(_x(300, 4096, "bf16", 2), big.dict, big.dict, ws=torch.empty(256, dtype=torch.uint8, device=dev()))
+    assert G.gptq_integer_gated(x[:0], t, t).shape == (0, 40)
+    assert mm(residual=res).shape == (5, 40)
+    assert G.gptq_integer_matmul(x[:0], t["w"], t["scales"], t["offsets"], residual=res[:0]).shape == (0, 40)
+
+
+@pytest.mark.parametrize("m,d_in,d_out", [(1, 4096, 300), (20, 1024, 500), (300, 4096, 520)])
+def test_stream_and_graph(G, m, d_in, d_out):
+    """Captured once with given buffers, replayed on other tokens with eager work between."""
+    banner(f"linear and gated: another stream, a graph, {m}x{d_in}->{d_out}")
+    gate, up = Layer(d_out, d_in, 1, True, True), Layer(d_out, d_in, 2, False, False)
+    down = Layer(96, d_out - d_out % 32, 3, False, True)
+    x, res = _x(m, d_in, "bf16", 4), torch.randn(m, 96, device=dev())
+
+    def layer(x, res, y=None, **kw):
+        h = G.gptq_integer_gated(x, gate.dict, up.dict, out_dtype=torch.bfloat16, **kw)
+        t = down.dict
+        return G.gptq_integer_matmul(h[:, :d_out - d_out % 32], t["w"], t["scales"], bias=t["bias"], residual=res, y=y, **kw)
+    want = layer(x, res)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = layer(x, res, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    hold = torch.empty_like(want)
+    with torch.cuda.graph(graph):
+        layer(x, res, y=hold)
+    for i in range(4):
+        x.copy_(_x(m, d_in, "bf16", 10 + i))
+        res.normal_()
+        eager = layer(x, res)
+        hold.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(hold, eager)
