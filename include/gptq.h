@@ -541,7 +541,8 @@ gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t
  * token t and z_j = scale q . k_j:
  *   s_j = cap tanh(z_j / cap) - slopes[head] |a - j|   (cap 0: z_j)
  * and the token sees the keys j <= a and j < prefix_lens[i].
- *   cap      0, or in [2^-20, 2^20]; a capped score is off by 2^-20 relative more
+ *   cap      0, or in [2^-20, 2^20]; a capped score is off by 2^-20 of the cap more, past
+ *            caps of 2^8 by 2^-19 of itself
  *   slopes   [n_heads] fp32, finite, or null; a bias that leaves fp32's range hides the key
  *   prefix_lens  [n_seq] int32, clamped to [0, kv_lens[i]], or null
  * A token that sees no key (kv_len < n, no prefix) gets zeros.  Everything else

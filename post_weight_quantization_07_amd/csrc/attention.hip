@@ -63,25 +63,26 @@ struct AttnParams {
   float scale_log2e;
 };
 
-// What becomes of a score before the softmax (S: kAsIs, kBias, kCapped) and which
-// keys besides the causal ones a token sees.
-//   kBias    s' = s - slope_h |a - j|, keys j < prefix of the sequence are seen by every token
-//   kCapped  the same of cap tanh(s / cap)
-// Without slopes they are zeros, without prefixes nothing is added: two forms of
-// each kernel, for what costs time, and not eight.
-enum { kAsIs = 0, kBias = 1, kCapped = 2 };
+// What becomes of a score z (of scale q . k) before the softmax, in flags of a
+// kernel's S, since each costs instructions a score; any S but kAsIs takes a prefix.
+//   kCap     cap tanh(z / cap) = cap - 2 cap / (1 + e^(2 z / cap)), off by 2^-20 cap:
+//            1 + e, its reciprocal r and e are off by 2^-24, 2^-23 and 2^-23 relative, and r <= 1
+//   kWide    (with kCap) for caps past 2^8, where that would be half of what the weights'
+//            fp16 rounds: |z| < 0.3 cap by tanh's series up to x^9, all off by 2^-19 relative
+//   kBias    then less slope_h |a - j|
+enum { kAsIs = 0, kBias = 1, kCap = 2, kWide = 4, kPrefix = 8 };
+constexpr float kWideCap = 256.f;
+constexpr float kLog2e = 1.4426950408889634f;
 template <int S>
 struct Shape {
-  const float* slopes;      // [n_heads], or null
-  const int32_t* prefixes;  // [n_seq], or null
-  float cap;                // times log2(e), as scores t are here
-  float inv;                // 1 / that
-  float twice;              // 2^(twice t) = e^(2 t / cap in that unit)
+  const float* slopes;      // [n_heads], or null: zeros
+  const int32_t* prefixes;  // [n_seq], or null: keys of a sequence that all its tokens see
+  float cap;                // cap log2(e): scores are exponents of 2 here
+  float twice;              // 2 / cap: what turns z log2(e) into the exponent above
 };
 template <>
 struct Shape<kAsIs> {};
 
-// keys of sequence i that all its tokens see
 template <int S>
 GPTQ_DEV int prefix_of(const Shape<S>& sh, int i, int len) {
   if constexpr (S != kAsIs) {
@@ -91,23 +92,39 @@ GPTQ_DEV int prefix_of(const Shape<S>& sh, int i, int len) {
 }
 template <int S>
 GPTQ_DEV float slope_of(const Shape<S>& sh, int head) {
-  if constexpr (S != kAsIs) {
-    if (sh.slopes) return sh.slopes[head] * 1.4426950408889634f;
+  if constexpr ((S & kBias) != 0) {
+    if (sh.slopes) return sh.slopes[head] * kLog2e;
   }
   return 0.f;
 }
-// cap tanh(t / cap): by 1 - 2 / (e^2x + 1), which is off by 2^-22 of 1, and where that
-// would be more than 2^-20 of tanh x (|x| < 0.3) by the series up to x^9, off by 2^-21.
+// The factor of a key's products: its scale, the score's and, before a cap, twice.
+// Where a small cap takes a finite scale past fp32, the largest: tanh is 1 there.
 template <int S>
-GPTQ_DEV float shaped(const Shape<S>& sh, float t, float slope, float away) {
-  if constexpr (S == kAsIs) return t;
-  if constexpr (S == kCapped) {
-    const float x = t * sh.inv, x2 = x * x;
-    const float far = fmaf(-2.f * sh.cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(t * sh.twice)), sh.cap);
-    const float near = fmaf(t * x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), t);
-    t = fabsf(x) < 0.3f ? near : far;
+GPTQ_DEV float key_factor(const Shape<S>& sh, float ks, float scale_log2e) {
+  const float v = ks * scale_log2e;
+  if constexpr ((S & kCap) != 0) {
+    const float w = v * sh.twice;
+    return fabsf(w) == __builtin_inff() && fabsf(v) < __builtin_inff() ? copysignf(3.402823466e38f, w) : w;
   }
-  if constexpr (S != kAsIs) return fmaf(-slope, fabsf(away), t);
+  return v;
+}
+// rest + the capped score of a product that has its factor (kCap), or rest + itself; rest
+// has cap in it already unless kWide
+template <int S>
+GPTQ_DEV float capped(const Shape<S>& sh, float product, float factor, float rest) {
+  if constexpr ((S & kCap) == 0) return fmaf(product, factor, rest);
+  if constexpr ((S & kCap) != 0) {
+    const float y = product * factor, r = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y));
+    if constexpr ((S & kWide) == 0) return fmaf(-2.f * sh.cap, r, rest);
+    const float x = y * 0.34657359f, x2 = x * x;  // ln 2 / 2
+    const float near = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f), x);
+    return fmaf(sh.cap, fabsf(x) < 0.3f ? near : fmaf(-2.f, r, 1.f), rest);
+  }
+}
+template <int S>
+GPTQ_DEV float cap_rest(const Shape<S>& sh) {
+  if constexpr ((S & kCap) != 0 && (S & kWide) == 0) return sh.cap;
+  return 0.f;
 }
 
 struct Seq {
@@ -407,7 +424,11 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
   for (int e = 0; e < K::kLoads; ++e) koff[e] = static_cast<uint32_t>(c * row_bytes + K::begin(g, e, p.hd) * BITS / 8);
   // of V too a lane whose dims lie past head_dim reads the row's first ones: what it gives is not stored
   voff = static_cast<uint32_t>(4 * g * row_bytes + (c * (HDP / 16) < p.hd ? c * kVB : 0));
-  for (int k0 = key0 + 32 * wave; k0 < key1; k0 += 32 * NW) {
+  // With a bias the keys are taken from the last one: scores fall with the distance, so the maximum is met
+  // early, where the other order moves it at every turn.
+  constexpr bool kDown = (S & kBias) != 0;
+  for (int k0 = kDown ? key0 + ((key1 - 1 - key0) & ~31) - 32 * wave : key0 + 32 * wave; kDown ? k0 >= key0 : k0 < key1;
+       k0 += kDown ? -32 * NW : 32 * NW) {
     uint32_t kw[2][kKW], vw[kVW][8];
     f32x4_t ks[2], vs[2];
     bool ok[2];
@@ -464,9 +485,15 @@ __global__ __launch_bounds__(64 * kSplitWaves, HDP <= 128 && MT == 1 ? 4 : 2) vo
 #pragma unroll
         for (int e = 0; e < kSteps; ++e) a = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kop[e], q[i][e], a, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          s[i][4 * b + r] = shaped<S>(sh, a[r] * (ks[b][r] * p.scale_log2e), slope[i],
-                                      static_cast<float>(place[i] - (k0 + 16 * b + 4 * g + r)));
+        for (int r = 0; r < 4; ++r) {
+          if constexpr (S == kAsIs) {
+            s[i][4 * b + r] = a[r] * (ks[b][r] * p.scale_log2e);
+          } else {
+            const float away = static_cast<float>(place[i] - (k0 + 16 * b + 4 * g + r));
+            const float rest = (S & kBias) ? fmaf(-slope[i], fabsf(away), cap_rest<S>(sh)) : cap_rest<S>(sh);
+            s[i][4 * b + r] = capped<S>(sh, a[r], key_factor<S>(sh, ks[b][r], p.scale_log2e), rest);
+          }
+        }
       }
     }
     float vtop = 0.f;
@@ -701,8 +728,10 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   const int place = w.s.len - w.s.n + tok;
   const int lim = live ? max(place, prefix - 1) : -1;
   const float slope = live ? slope_of<S>(sh, h * p.group + qh) : 0.f;
-  const int wfirst = max(w.s.len - w.s.n + uniform(div_by(r0 + 32 * wave, p.group_mul, p.group_shift)), prefix - 1);  // last key of the wave's first row
-  const int wlast = r0 + 32 * wave < rows ? max(w.s.len - w.s.n + uniform(div_by(min(r0 + 32 * wave + 32, rows) - 1, p.group_mul, p.group_shift)), prefix - 1) : -1;
+  const int wplace = w.s.len - w.s.n + uniform(div_by(r0 + 32 * wave, p.group_mul, p.group_shift));  // the wave's first row's
+  const int wplast = w.s.len - w.s.n + uniform(div_by(min(r0 + 32 * wave + 32, rows) - 1, p.group_mul, p.group_shift));  // its last one's
+  const int wfirst = max(wplace, prefix - 1);  // last key of the first row
+  const int wlast = r0 + 32 * wave < rows ? max(wplast, prefix - 1) : -1;
   bf16x8_t q[kSteps];
   float bias = 0.f;
   {
@@ -773,7 +802,11 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   int page;              // its page entry, loaded a tile earlier
   uint64_t there;        // the keys of the tile whose page is there
   int64_t vrow = 0;      // the wave's 16 keys of that tile: their first row in the cache
-  auto load_page = [&](int base) { page = table[min(base + lane, key1 - 1) >> p.page_shift]; };
+  // Tiles are counted by `base` from key0 on; with a bias (scores fall with the distance) they are taken
+  // from the last one, so that the first ones have the maximum.  Past the end the first keys are loaded again.
+  const int turn = 2 * key0 + ((key1 - 1 - key0) & ~(kKeys - 1));
+  auto keys_of = [&](int base) { return (S & kBias) ? max(turn - base, key0) : base; };
+  auto load_page = [&](int base) { page = table[min(keys_of(base) + lane, key1 - 1) >> p.page_shift]; };
   auto load_codes = [&](const uint8_t* src, R& t) {
 #pragma unroll
     for (int i = 0; i < R::kD / R::kCD; ++i) {
@@ -791,8 +824,8 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       }
     }
   };
-  auto load_keys = [&](int base, R& t) {  // by `page`
-    const int key = base + lane;
+  auto load_keys = [&](int count, R& t) {  // by `page`
+    const int base = keys_of(count), key = base + lane;
     const bool ok = key < key1 && page >= 0 && page < p.n_pages;
     there = __ballot(ok);
     const int pg = ok ? page : 0;
@@ -828,7 +861,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   // scale of key `lane`, NaN if there is no such key or scale.
   auto key_scales = [&](int buf) {
     const float nan = __uint_as_float(0x7FC00000u), v = fabsf(vall) < __builtin_inff() ? vall : nan;
-    lks[buf][lane] = vlive && v != v ? nan : ks * p.scale_log2e;
+    lks[buf][lane] = vlive && v != v ? nan : key_factor<S>(sh, ks, p.scale_log2e);
     return vlive ? v : nan;
   };
   auto convert_key = [&](const R& t, int buf, int i) {
@@ -919,7 +952,13 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
         const f32x4_t ks = *reinterpret_cast<const f32x4_t*>(&lks[buf][32 * b + 8 * a + 4 * hf]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[b][4 * a + e] = shaped<S>(sh, s[b][4 * a + e] * ks[e], slope, away - static_cast<float>(32 * b + 8 * a + e));
+          if constexpr (S == kAsIs) {
+            s[b][4 * a + e] *= ks[e];
+          } else {
+            const float gap = fabsf(away - static_cast<float>(32 * b + 8 * a + e));
+            const float rest = (S & kBias) ? fmaf(-slope, gap, cap_rest<S>(sh)) : cap_rest<S>(sh);
+            s[b][4 * a + e] = capped<S>(sh, s[b][4 * a + e], ks[e], rest);
+          }
           if (!seen(b, 4 * a + e)) s[b][4 * a + e] = kNegInf;
           mx = fmaxf(mx, s[b][4 * a + e]);
         }
@@ -1052,7 +1091,9 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       keys_done = false;
       tile_range = top_next;  // the one this tile's values were written in (the next tile's may be wider)
       tile_spread = spread;
-      fits = base > key0 && base + kKeys - 1 <= wfirst && shown == ~uint64_t{0} && tile_range == range && !far && !tile_spread;
+      const int keys = keys_of(base);
+      const bool before = keys + kKeys - 1 <= wplace;
+      fits = base > key0 && keys + kKeys - 1 <= wfirst && (!(S & kBias) || before || keys >= wplast) && shown == ~uint64_t{0} && tile_range == range && !far && !tile_spread;
       if (!fits) break;
       // The plain tile: every key seen, the maximum and the range as they were.
       // Four groups of products, each with arithmetic between them that does not
@@ -1065,15 +1106,21 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
       u32x4_t pk[4];
       f32x4_t ks[4];
       float l0 = 0.f, l1 = 0.f;
-      const float away = static_cast<float>(place - base - 4 * hf);
+      // The bias of key keys + 4 hf + i for this row, away +- slope i: all keys of a plain tile lie before the
+      // places of the wave's rows, or all behind them (kBias).
+      const float toward = before ? slope : -slope;
+      const float away = toward * static_cast<float>(keys + 4 * hf - place);
+      float rest = 0.f;  // of a score, less the maximum
       // log2 of the weight of element e of block b
       auto power = [&](float score, int b, int e) {
-        if constexpr (S == kAsIs) return fmaf(score, ks[e >> 2][e & 3], -m);
-        return shaped<S>(sh, score * ks[e >> 2][e & 3], slope, away - static_cast<float>(32 * b + 8 * (e >> 2) + (e & 3))) - m;
+        const float f = ks[e >> 2][e & 3];
+        if constexpr (S == kAsIs) return fmaf(score, f, -m);
+        return capped<S>(sh, score, f, (S & kBias) ? fmaf(toward, static_cast<float>(32 * b + 8 * (e >> 2) + (e & 3)), rest) : rest);
       };
       // n of the 16 weights 2^(s sk - m) of a block, rounded to fp16, and their sum
       auto weights = [&](const f32x16_t& s, int b, int from, int to, float& sum) {
         asm volatile("" : "+v"(m));  // not before this place between the products
+        if constexpr (S != kAsIs) rest = cap_rest<S>(sh) + ((S & kBias) ? away : 0.f) - m;
 #pragma unroll
         for (int e = 0; e < 16; e += 2)
           if (e >= from && e < to) {
@@ -1154,7 +1201,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
     }
     if (fits || tile_spread) break;
     if (!keys_done) next_keys();
-    if (base <= wlast) careful_tile(base, buf, shown, half, tile_range);  // else a causal tile past the wave's rows
+    if (keys_of(base) <= wlast) careful_tile(keys_of(base), buf, shown, half, tile_range);  // else a causal tile past the wave's rows
     next_values();
   }
   // Scaled tiles, from one whose barrier is behind (all waves see the same scales, and come here at the same
@@ -1164,7 +1211,7 @@ __global__ __launch_bounds__(256, HDP <= 64 ? 3 : HDP <= 128 ? 2 : 1) void attn_
   most = __uint_as_float(static_cast<uint32_t>(range) << 23);
   while (base < key1) {
     next_keys();
-    if (base <= wlast) scaled_tile(base, buf, shown);
+    if (keys_of(base) <= wlast) scaled_tile(keys_of(base), buf, shown);
     next_values();
     if (base < key1) tile_barrier();
   }
@@ -1290,12 +1337,21 @@ void exact_divisor(int32_t d, uint32_t* mul, uint32_t* shift) {
 
 int head_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 
+template <int Q, int S>
+Shape<Q> split_shape(const Shape<S>& s) {
+  if constexpr (Q == kAsIs) return {};
+  else return {s.slopes, s.prefixes, s.cap, s.twice};
+}
+
 template <int HDP, int BITS, int S>
 void attn_go(const AttnParams& p, const Shape<S>& sh, unsigned blocks, unsigned joins, hipStream_t st) {
   constexpr int t = 64 * kSplitWaves;
+  // Slopes of zero cost the split kernel, which waits for memory, no time; the tile kernel has a form of its own without.
+  constexpr int Q = S == kAsIs ? kAsIs : (S & ~kPrefix) | kBias;
+  const Shape<Q> split = split_shape<Q>(sh);
   if (p.tile_rows == 128) attn_tile_kernel<HDP, BITS, S><<<blocks, 256, 0, st>>>(p, sh);
-  else if (HDP <= 128 && p.tile_rows == 32) attn_split_kernel<HDP, BITS, HDP <= 128 ? 2 : 1, S><<<blocks, t, 0, st>>>(p, sh);
-  else attn_split_kernel<HDP, BITS, 1, S><<<blocks, t, 0, st>>>(p, sh);
+  else if (HDP <= 128 && p.tile_rows == 32) attn_split_kernel<HDP, BITS, HDP <= 128 ? 2 : 1, Q><<<blocks, t, 0, st>>>(p, split);
+  else attn_split_kernel<HDP, BITS, 1, Q><<<blocks, t, 0, st>>>(p, split);
   if (joins) attn_join_kernel<HDP><<<dim3(joins, (p.tile_rows + kJoinRows - 1) / kJoinRows), 512, 0, st>>>(p);
 }
 
@@ -1390,15 +1446,18 @@ hipError_t attention_launch(const AttnPlan& plan, const CacheShape& c, const voi
   exact_divisor(p.n_kv, &p.kv_mul, &p.kv_shift);
   p.scale_log2e = scale * 1.4426950408889634f;
   const unsigned b = static_cast<unsigned>(plan.blocks), j = static_cast<unsigned>(plan.joins);
-  if (shape.cap > 0.f) {
-    const double l2e = 1.4426950408889634, cap = shape.cap;
-    attn_head<kCapped>(p, {shape.slopes, shape.prefixes, static_cast<float>(cap * l2e), static_cast<float>(1.0 / (cap * l2e)),
-                           static_cast<float>(2.0 / cap)}, c.bits, b, j, st);
-  } else if (shape.slopes || shape.prefixes) {
-    attn_head<kBias>(p, {shape.slopes, shape.prefixes, 0.f, 0.f, 0.f}, c.bits, b, j, st);
-  } else {
-    attn_head<kAsIs>(p, {}, c.bits, b, j, st);
-  }
+  const double cap = shape.cap;
+  auto go = [&](auto flags) {
+    constexpr int S = decltype(flags)::value;
+    attn_head<S>(p, Shape<S>{shape.slopes, shape.prefixes, static_cast<float>(cap * 1.4426950408889634),
+                             static_cast<float>(cap > 0 ? 2.0 / cap : 0.0)}, c.bits, b, j, st);
+  };
+  if (shape.cap > kWideCap) go(std::integral_constant<int, kCap | kWide | kBias>{});
+  else if (shape.cap > 0.f && shape.slopes) go(std::integral_constant<int, kCap | kBias>{});
+  else if (shape.cap > 0.f) go(std::integral_constant<int, kCap>{});
+  else if (shape.slopes) go(std::integral_constant<int, kBias>{});
+  else if (shape.prefixes) go(std::integral_constant<int, kPrefix>{});
+  else attn_head<kAsIs>(p, {}, c.bits, b, j, st);
   return hipGetLastError();
 }
 
