@@ -154,6 +154,7 @@ struct IntParams {
   const void* xraw;      // x not yet quantized (the fused stream kernel), its row stride,
   int64_t ldxraw;
   int32_t xvec;          // and whether its rows are 16-byte aligned
+  int32_t yvec;          // rows of y (and of a residual) take whole vectors of four
 };
 
 // What follows the scales (E: kPlain, kLinear, kGated).
@@ -180,18 +181,58 @@ struct Epilogue<kGated> {
 };
 
 // Logistic forms go through 2^x and a reciprocal (an ulp each; the exponent's
-// rounding adds |z| 2^-24 where the result is next to 0); gelu takes erfc, whose
-// relative error holds where 1 + erf would cancel.  NaN passes through all of them.
+// rounding adds |z| 2^-24 where the result is next to 0).  gelu takes z Phi(z) with
+// Phi(-a) = erfc(a / sqrt(2)) / 2 = t 2^(P(t) - a^2 log2(e) / 2), t = 1 / (1 + a / sqrt(8)),
+// P a polynomial of degree 9 fitted to the exponent, off by 2^-23 in all: the relative
+// error holds far below 0, where 1 + erf would cancel.  NaN passes through all of them.
 GPTQ_DEV float logistic(float z, float t) {  // z / (1 + e^-t)
   return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * t));
+}
+GPTQ_DEV float gelu(float z) {
+  const float a = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(0.35355339059327376f, a, 1.f));
+  float q = 0.24347086250782013f;
+  q = fmaf(q, t, -1.1733814477920532f);
+  q = fmaf(q, t, 2.1254589557647705f);
+  q = fmaf(q, t, -1.6174057722091675f);
+  q = fmaf(q, t, 0.3914777338504791f);
+  q = fmaf(q, t, -0.26540711522102356f);
+  q = fmaf(q, t, 0.1390586793422699f);
+  q = fmaf(q, t, 0.5397483110427856f);
+  q = fmaf(q, t, 1.4427276849746704f);
+  q = fmaf(q, t, -2.8257482051849365f);
+  const float below = a * (t * __builtin_amdgcn_exp2f(fmaf(-0.7213475204444817f * a, a, q)));  // a Phi(-a)
+  return z < 0.f ? -below : z - below;
 }
 GPTQ_DEV float activate(float z, int act) {
   switch (act) {
     case kActRelu: return z < 0.f ? 0.f : z;
-    case kActGelu: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case kActGelu: return gelu(z);
     case kActGeluTanh: return logistic(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
     case kActSilu: return logistic(z, z);
     default: return z;
+  }
+}
+// n values, the choice made once for all
+template <int N>
+GPTQ_DEV void activate(float (&z)[N], int act) {
+  switch (act) {
+    case kActRelu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = activate(z[i], kActRelu);
+      break;
+    case kActGelu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = activate(z[i], kActGelu);
+      break;
+    case kActGeluTanh:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = activate(z[i], kActGeluTanh);
+      break;
+    case kActSilu:
+#pragma unroll
+      for (int i = 0; i < N; ++i) z[i] = activate(z[i], kActSilu);
+      break;
+    default: break;
   }
 }
 
@@ -559,6 +600,193 @@ GPTQ_DEV void tile_of(const TileGrid& g, int b, int& tm, int& tn, int& slice) {
 
 enum { kOutF32 = 0, kOutBf16 = 1, kOutPart = 2 };
 
+struct TileRow {  // of x
+  float scale;
+  int sum;
+};
+
+// What follows the sums of a tile.  A wave's sums, two blocks of 32 rows at a time,
+// go through LDS that the operands have left (its own slots, so no barrier), and
+// come back as four channels of a row: whole vectors of y and of the residual,
+// which is loaded four rows ahead, and code for sixteen values instead of 256: with
+// the choice of an activation unrolled over all of them the code left the
+// instruction cache, 40 us of a call.  Rows lie bare in LDS, 32 WN words; row bit 2 flips word
+// bit 5, so that the two halves of a wave write to different banks.
+template <int WM, int WN, int OUT, int E>
+GPTQ_DEV void tile_out(const IntParams& p, const Epilogue<E>& ep, const i32x16_t (&acc)[WM][WN], uint8_t* r0, uint8_t* r1,
+                       const TileRow* rows, int64_t m0, int64_t n0, int wm, int wn, int mrows) {
+  constexpr int kLayers = E == kGated ? 2 : 1;
+  constexpr int kPitch = 32 * WN;               // words
+  constexpr int kWide = kPitch / kLayers;       // channels of the wave
+  constexpr int kAcross = kWide / 4;            // lanes of a row
+  constexpr int kRows = 64 / kAcross, kB = 4;   // rows at a time, and times in flight
+  const int lane = lane_id(), r = lane & 31, hi = lane >> 5;
+  const int ch = 4 * (lane % kAcross), sub = lane / kAcross;
+  const int at = E == kGated ? (ch >> 5) * 64 + (ch & 31) : ch;
+  const int64_t col = n0 + wn * kWide + ch;
+  const int live = static_cast<int>(max(min(p.d_out - col, int64_t{4}), int64_t{0}));
+  float sw[kLayers][4], bias[kLayers][4];
+  int off[kLayers][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t c = min(col + j, p.d_out - 1);
+    sw[0][j] = p.w_scales[c];
+    off[0][j] = p.w_offsets ? p.w_offsets[c] : 0;
+    bias[0][j] = 0.f;
+    if constexpr (E != kPlain) bias[0][j] = ep.bias ? ep.bias[c] : 0.f;
+    if constexpr (E == kGated) {
+      sw[1][j] = ep.w_scales[c];
+      off[1][j] = ep.w_offsets ? ep.w_offsets[c] : 0;
+      bias[1][j] = ep.bias2 ? ep.bias2[c] : 0.f;
+    }
+  }
+  // y and the residual through buffer resources over the tile's rows: what lies past m, or past
+  // d_out (offset 2^31), is dropped, or loaded as zeros
+  constexpr int kSize = OUT == kOutBf16 ? 2 : 4;
+  const int dout = static_cast<int>(p.d_out);
+  const __amdgpu_buffer_rsrc_t ry =
+      rows_rsrc(static_cast<const int8_t*>(p.y) + m0 * p.d_out * kSize, static_cast<int64_t>(mrows) * dout * kSize);
+  __amdgpu_buffer_rsrc_t rres = ry;
+  uint32_t lead = 0;
+  if constexpr (E == kLinear) {
+    const int size = ep.res_bf16 ? 2 : 4;
+    lead = static_cast<uint32_t>(ep.ldr) * size;
+    rres = rows_rsrc(static_cast<const int8_t*>(ep.res) + m0 * ep.ldr * size,
+                     ep.res ? ((mrows - 1) * ep.ldr + p.d_out) * size : 0);
+  }
+  const uint32_t outside = 0x80000000u;
+  // four values of the residual, as they lie there
+  auto load_res = [&](int row, u32x4_t& raw) {
+    raw = u32x4_t{0u, 0u, 0u, 0u};
+    if constexpr (E == kLinear) {
+      if (!ep.res) return;
+      const uint32_t at = static_cast<uint32_t>(row) * lead;
+      if (ep.res_bf16) {
+        const uint32_t c = static_cast<uint32_t>(col) * 2;
+        if (p.yvec) {
+          const auto two = __builtin_amdgcn_raw_buffer_load_b64(rres, live ? at + c : outside, 0, 0);
+          raw[0] = two[0];
+          raw[1] = two[1];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            raw[j >> 1] |= static_cast<uint32_t>(static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
+                               rres, j < live ? at + c + 2 * j : outside, 0, 0))) << (16 * (j & 1));
+        }
+      } else {
+        const uint32_t c = static_cast<uint32_t>(col) * 4;
+        if (p.yvec) {
+          raw = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rres, live ? at + c : outside, 0, 0));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) raw[j] = __builtin_amdgcn_raw_buffer_load_b32(rres, j < live ? at + c + 4 * j : outside, 0, 0);
+        }
+      }
+    }
+  };
+  auto res_of = [&](const u32x4_t& raw, int j) {
+    if constexpr (E == kLinear) {
+      if (ep.res_bf16) return __uint_as_float((j & 1) ? raw[j >> 1] & 0xFFFF0000u : raw[j >> 1] << 16);
+      return __uint_as_float(raw[j]);
+    }
+    return 0.f;
+  };
+  auto store = [&](int row, const float* v) {
+    const uint32_t to = static_cast<uint32_t>(row) * static_cast<uint32_t>(dout * kSize) + static_cast<uint32_t>(col) * kSize;
+    if (OUT == kOutBf16) {
+      typedef float f32x2v_t __attribute__((ext_vector_type(2)));
+      typedef __bf16 bf16x2v_t __attribute__((ext_vector_type(2)));
+      typedef __attribute__((__vector_size__(8))) uint32_t u32x2_t;
+      const u32x2_t two = {__builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2v_t{v[0], v[1]}), bf16x2v_t)),
+                           __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2v_t{v[2], v[3]}), bf16x2v_t))};
+      if (p.yvec) {
+        __builtin_amdgcn_raw_buffer_store_b64(two, ry, live ? to : outside, 0, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(two[j >> 1] >> (16 * (j & 1))), ry, j < live ? to + 2 * j : outside, 0, 0);
+      }
+    } else if (p.yvec) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, (f32x4_t{v[0], v[1], v[2], v[3]})), ry, live ? to : outside, 0, 0);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v[j]), ry, j < live ? to + 4 * j : outside, 0, 0);
+    }
+  };
+  // (row sums of codes and offsets fit 24 bits: 127 65536 < 2^23)
+  auto scaled = [&](int sum, int l, int j, int rowsum, float rowscale) {
+    return (static_cast<float>(sum - __mul24(off[l][j], rowsum)) * rowscale) * sw[l][j];
+  };
+#pragma unroll
+  for (int i = 0; i < WM; i += 2) {
+    const int row0 = (wm * WM + i) * 32 + sub;
+    u32x4_t ahead[kB];
+#pragma unroll
+    for (int b = 0; b < kB; ++b) load_res(row0 + b * kRows, ahead[b]);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int j = 0; j < WN; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          reinterpret_cast<int*>(half ? r1 : r0)[(8 * (e >> 2) + 4 * hi + (e & 3)) * kPitch + ((32 * j + r) ^ (32 * hi))] = acc[i + half][j][e];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
+    __builtin_amdgcn_wave_barrier();
+    struct Held {
+      i32x4_t sum[kLayers][kB];
+      float sc[kB];
+      int sm[kB];
+    } next;
+    auto read = [&](int q, Held& h) {
+      const uint8_t* from = q < 32 ? r0 : r1;
+#pragma unroll
+      for (int b = 0; b < kB; ++b) {
+        const int rr = (q & 31) + b * kRows + sub;
+        const int word = rr * kPitch + (at ^ (((rr >> 2) & 1) * 32));
+        h.sum[0][b] = reinterpret_cast<const i32x4_t*>(from)[word >> 2];
+        if constexpr (E == kGated) h.sum[1][b] = reinterpret_cast<const i32x4_t*>(from)[(word ^ 32) >> 2];
+        h.sc[b] = rows[row0 + q + b * kRows].scale;
+        h.sm[b] = rows[row0 + q + b * kRows].sum;
+      }
+    };
+    read(0, next);
+#pragma unroll 1
+    for (int q = 0; q < 64; q += kRows * kB) {
+      const Held now = next;
+      u32x4_t res[kB];
+#pragma unroll
+      for (int b = 0; b < kB; ++b) res[b] = ahead[b];
+      if (q + kRows * kB < 64) {
+        read(q + kRows * kB, next);
+#pragma unroll
+        for (int b = 0; b < kB; ++b) load_res(row0 + q + (kB + b) * kRows, ahead[b]);
+      }
+      float v[4 * kB];
+#pragma unroll
+      for (int b = 0; b < kB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * b + j] = scaled(now.sum[0][b][j], 0, j, now.sm[b], now.sc[b]);
+      if constexpr (E != kPlain) {
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[4 * b + j] += bias[0][j];
+        activate(v, ep.act);
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (E == kLinear) v[4 * b + j] += res_of(res[b], j);
+            if constexpr (E == kGated) v[4 * b + j] *= scaled(now.sum[1][b][j], 1, j, now.sm[b], now.sc[b]) + bias[1][j];
+          }
+      }
+#pragma unroll
+      for (int b = 0; b < kB; ++b) store(row0 + q + b * kRows, v + 4 * b);
+    }
+  }
+}
+
 // kGated: the 64 WN weight rows of a tile are 32 WN channels of both layers, in
 // blocks of 32 by turns: a wave's products 2 j and 2 j + 1 are the same channels of
 // the gate and of the second layer, in the same lanes.  A wave's loads, 16 WN of
@@ -570,6 +798,7 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   // one array per slot: the compiler then sees that reads of one slot do not alias loads in flight into another
   __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA], sA3[kA];
   __shared__ __attribute__((aligned(1024))) uint8_t sB0[kB], sB1[kB], sB2[kB], sB3[kB];
+  __shared__ TileRow rows[64 * WM];
   int tm, tn, slice;
   tile_of(g, static_cast<int>(blockIdx.x), tm, tn, slice);
   const int lane = threadIdx.x & 63;
@@ -662,9 +891,9 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
       tile_half<WM, WN>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
     }
   }
-  // Element e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.
-  // Stores go through buffer resources over the tile's rows: rows past m and
-  // columns past d_out (offset 2^31) are dropped in hardware.
+  // Element e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.  The K
+  // slices' stores go through buffer resources over the tile's rows: rows past m
+  // and columns past d_out (offset 2^31) are dropped in hardware.
   __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT(0));  // the loads past the end still write LDS
   const int dout = static_cast<int>(p.d_out);
   constexpr int kLayers = E == kGated ? 2 : 1;
@@ -690,82 +919,11 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
     }
     return;
   }
-  __syncthreads();  // the operands' LDS now holds the tile's row scales and code sums
-  float* lsc = reinterpret_cast<float*>(sA0);
-  int* lsm = reinterpret_cast<int*>(sB0);
-  for (int e = threadIdx.x; e < mrows; e += 256) {
-    lsc[e] = p.x_scales[m0 + e];
-    lsm[e] = p.x_sums ? p.x_sums[m0 + e] : 0;
-  }
-  __syncthreads();
-  constexpr int size = OUT == kOutBf16 ? 2 : 4;
-  const __amdgpu_buffer_rsrc_t ry =
-      rows_rsrc(static_cast<const int8_t*>(p.y) + m0 * p.d_out * size, static_cast<int64_t>(mrows) * dout * size);
-  // the tile's rows of the residual: past them, and past d_out, zeros are loaded
-  __amdgpu_buffer_rsrc_t rres = ry;
-  if constexpr (E == kLinear) {
-    const int rsize = ep.res_bf16 ? 2 : 4;
-    rres = rows_rsrc(static_cast<const int8_t*>(ep.res) + m0 * ep.ldr * rsize,
-                     ep.res ? ((mrows - 1) * ep.ldr + p.d_out) * rsize : 0);
-  }
-  auto put = [&](float v, uint32_t to) {
-    if (OUT == kOutBf16)
-      __builtin_amdgcn_raw_buffer_store_b16(static_cast<short>(f32_to_bf16(v)), ry, to, 0, 0);
-    else
-      __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), ry, to, 0, 0);
-  };
-#pragma unroll
-  for (int j = 0; j < WN; j += kLayers) {
-    const int col = col_of(j);
-    const bool in = col < dout;
-    const float sw = in ? p.w_scales[col] : 0.f;
-    const int off = (in && p.w_offsets) ? p.w_offsets[col] : 0;
-    const uint32_t at = in ? static_cast<uint32_t>(col * size) : 0x80000000u;
-    float bias = 0.f, bias2 = 0.f, sw2 = 0.f;
-    int off2 = 0;
-    if constexpr (E != kPlain) bias = (in && ep.bias) ? ep.bias[col] : 0.f;
-    if constexpr (E == kGated) {
-      sw2 = in ? ep.w_scales[col] : 0.f;
-      off2 = (in && ep.w_offsets) ? ep.w_offsets[col] : 0;
-      bias2 = (in && ep.bias2) ? ep.bias2[col] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < WM; ++i) {
-      float res[16] = {};
-      if constexpr (E == kLinear) {
-        if (ep.res) {
-          const uint32_t lead = static_cast<uint32_t>(ep.ldr) << (ep.res_bf16 ? 1 : 2);
-          const uint32_t from = in ? static_cast<uint32_t>(col) << (ep.res_bf16 ? 1 : 2) : 0x80000000u;
-          if (ep.res_bf16) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              res[e] = bf16_to_f32(static_cast<uint16_t>(
-                  __builtin_amdgcn_raw_buffer_load_b16(rres, from + (row0 + 32 * i + 8 * (e >> 2) + (e & 3)) * lead, 0, 0)));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              res[e] = __int_as_float(static_cast<int>(
-                  __builtin_amdgcn_raw_buffer_load_b32(rres, from + (row0 + 32 * i + 8 * (e >> 2) + (e & 3)) * lead, 0, 0)));
-          }
-        }
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t row = row0 + 32 * i + 8 * q;
-        const f32x4_t sc = *reinterpret_cast<const f32x4_t*>(lsc + row);
-        const i32x4_t sm = *reinterpret_cast<const i32x4_t*>(lsm + row);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = (static_cast<float>(acc[i][j][4 * q + e] - off * sm[e]) * sc[e]) * sw;
-          if constexpr (E == kLinear) v = linear_out(ep, v, bias, res[4 * q + e]);
-          if constexpr (E == kGated)
-            v = activate(v + bias, ep.act) * ((static_cast<float>(acc[i][j + 1][4 * q + e] - off2 * sm[e]) * sc[e]) * sw2 + bias2);
-          put(v, at + (row + e) * static_cast<uint32_t>(dout * size));
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
+  for (int e = threadIdx.x; e < mrows; e += 256) rows[e] = TileRow{p.x_scales[m0 + e], p.x_sums ? p.x_sums[m0 + e] : 0};
+  __syncthreads();  // and every wave is done with the operands' LDS
+  uint8_t* ra0 = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sA2 : sA3;
+  uint8_t* rb0 = wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sB2 : sB3;
+  tile_out<WM, WN, OUT, E>(p, ep, acc, ra0, rb0, rows, m0, n0, wm, wn, mrows);
 }
 
 // sums of the K slices (integers: any order gives the same), four columns a
@@ -983,6 +1141,8 @@ hipError_t integer_launch(const IntCall& c, void* ws, int n_cu, hipStream_t st) 
   p.d_out = c.d_out;
   p.d_in = static_cast<int32_t>(c.d_in);
   p.y_bf16 = c.y_bf16 ? 1 : 0;
+  const auto whole = [](const void* at, bool bf16) { return (reinterpret_cast<uintptr_t>(at) & (bf16 ? 7u : 15u)) == 0; };
+  p.yvec = c.d_out % 4 == 0 && whole(c.y, c.y_bf16) && (!c.res || (c.ldr % 4 == 0 && whole(c.res, c.res_bf16)));
   const int f = !fused ? 0 : c.xt == kXBf16 ? 1 : 2;
   int32_t* partial = static_cast<int32_t*>(ws);
   if (gated) {
