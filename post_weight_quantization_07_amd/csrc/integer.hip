@@ -324,48 +324,92 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
   __shared__ float xs[4];
   __shared__ int xsum[4];
   if (FUSED) {
+    // All tokens at once, eight values a thread and round: their maxima, then their code
+    // sums, meet in LDS, those of a single token one a wave, of several by atomics
+    // (integers: any order gives the same; four tokens of 4096 one behind the other 33 us
+    // a call, at once 30; but one token by atomics 26 instead of 25).
     constexpr bool kBf16 = FUSED == 1;
-    __shared__ uint32_t red[kSW];
-    __shared__ int redsum[kSW];
-    const int chunks = p.d_in / 8;
-    for (int t = 0; t < static_cast<int>(p.m); ++t) {
-      constexpr int kQ = kFusedElems / 8 / (64 * kSW);  // chunks a thread, at most
-      float v[kQ][8];
-      uint32_t am = 0u;
+    constexpr int kQ = kFusedElems / 8 / (64 * kSW);
+    __shared__ uint32_t most[4], wave_most[kSW];
+    __shared__ int wave_sum[kSW];
+    const bool one = p.m == 1;
+    if (!one && threadIdx.x < 4) {
+      most[threadIdx.x] = 0u;
+      xsum[threadIdx.x] = 0;
+    }
+    const int chunks = p.d_in / 8, all = static_cast<int>(p.m) * chunks;
+    float v[kQ][8];
+    int tok[kQ];
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) {
-        const int e = q * 64 * kSW + static_cast<int>(threadIdx.x);
-        if (e < chunks && p.xvec) {
-          load8<kBf16>(p.xraw, t * p.ldxraw + 8 * e, v[q]);
-        } else {
+    for (int q = 0; q < kQ; ++q) {
+      const int e = q * 64 * kSW + static_cast<int>(threadIdx.x);
+      tok[q] = e < all ? (e >= chunks) + (e >= 2 * chunks) + (e >= 3 * chunks) : 0;
+      const int64_t at = tok[q] * p.ldxraw + 8 * (e - tok[q] * chunks);
+      if (e < all && p.xvec) {
+        load8<kBf16>(p.xraw, at, v[q]);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[q][i] = e < chunks ? load1<kBf16>(p.xraw, t * p.ldxraw + 8 * e + i) : 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[q][i]));
+        for (int i = 0; i < 8; ++i) v[q][i] = e < all ? load1<kBf16>(p.xraw, at + i) : 0.f;
       }
-      am = group_max<64>(am);
-      if (lane == 0) red[wave] = am;
-      __syncthreads();
+    }
+    uint32_t am1 = 0u;
+    if (one) {
 #pragma unroll
-      for (int w = 0; w < kSW; ++w) am = max(am, red[w]);
-      const RowScale rs = row_scale(am, 127.f);
+      for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) am1 = max(am1, abs_bits(v[q][i]));
+      am1 = group_max<64>(am1);
+      if (lane == 0) wave_most[wave] = am1;
+    }
+    __syncthreads();
+    if (one) {
+#pragma unroll
+      for (int w = 0; w < kSW; ++w) am1 = max(am1, wave_most[w]);
+      const RowScale rs = row_scale(am1, 127.f);
       int sum = 0;
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) {
-        const int e = q * 64 * kSW + static_cast<int>(threadIdx.x);
-        if (e < chunks) sum += tok_store<true>(xl, static_cast<int64_t>(t) * p.d_in, 8 * e, p.d_in, v[q], rs);
-      }
+      for (int q = 0; q < kQ; ++q) sum += tok_store<true>(xl, 0, 8 * (q * 64 * kSW + static_cast<int>(threadIdx.x)), p.d_in, v[q], rs);
       sum = group_sum<64>(sum);
-      if (lane == 0) redsum[wave] = sum;
+      if (lane == 0) wave_sum[wave] = sum;
       __syncthreads();
       if (threadIdx.x == 0) {
-        int all = 0;
+        sum = 0;
 #pragma unroll
-        for (int w = 0; w < kSW; ++w) all += redsum[w];
-        xs[t] = rs.scale;
-        xsum[t] = all;
+        for (int w = 0; w < kSW; ++w) sum += wave_sum[w];
+        xs[0] = rs.scale;
+        xsum[0] = sum;
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        if (q * 64 * kSW >= all) break;
+        uint32_t am = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) am = max(am, abs_bits(v[q][i]));
+        am = group_max<4>(am);  // d_in % 32 == 0: four lanes have one token
+        if (__all(tok[q] == __builtin_amdgcn_readfirstlane(tok[q]))) {
+          am = group_max<64>(am);
+          if (lane == 0) atomicMax(&most[tok[q]], am);
+        } else if ((lane & 3) == 0) {
+          atomicMax(&most[tok[q]], am);
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        if (q * 64 * kSW >= all) break;
+        const int e = q * 64 * kSW + static_cast<int>(threadIdx.x);
+        const RowScale rs = row_scale(most[tok[q]], 127.f);
+        int sum = e < all ? tok_store<true>(xl, 0, 8 * e, 8 * all, v[q], rs) : 0;
+        sum = group_sum<4>(sum);
+        if (__all(tok[q] == __builtin_amdgcn_readfirstlane(tok[q]))) {
+          sum = group_sum<64>((lane & 3) == 0 ? sum : 0);
+          if (lane == 0) atomicAdd(&xsum[tok[q]], sum);
+        } else if ((lane & 3) == 0) {
+          atomicAdd(&xsum[tok[q]], sum);
+        }
+      }
+      if (threadIdx.x < 4) xs[threadIdx.x] = row_scale(most[threadIdx.x], 127.f).scale;
       __syncthreads();
     }
   }
@@ -533,7 +577,7 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
 // bytes a product of 64 x 64; 128 x 128 tiles are for grids too small for the others
 // (509 x 11008 -> 4096: 36 us in four K slices, 1.28 POP/s; an eight-step ring, one
 // workgroup a CU, 38 us).
-constexpr int kTStep = 64, kSlots = 4;
+constexpr int kTStep = 64;
 
 #define GPTQ_VMCNT(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0F70)
 
@@ -568,7 +612,7 @@ GPTQ_DEV void tile_half(const i32x4_t (&a)[WM], const i32x4_t (&b)[WN], const ui
 #pragma unroll
     for (int j = 0; j < WN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
   // the next half's reads and this half's loads spread over the products
-  constexpr int kProd = WM * WN / (WM + WN);
+  constexpr int kProd = WM == 1 ? 1 : WM * WN / (WM + WN);
 #pragma unroll
   for (int k = 0; k < WM + WN; ++k) {
     __builtin_amdgcn_sched_group_barrier(0x008, kProd, 0);                // products
@@ -717,15 +761,16 @@ GPTQ_DEV void tile_out(const IntParams& p, const Epilogue<E>& ep, const i32x16_t
   auto scaled = [&](int sum, int l, int j, int rowsum, float rowscale) {
     return (static_cast<float>(sum - __mul24(off[l][j], rowsum)) * rowscale) * sw[l][j];
   };
+  constexpr int kHalves = WM == 1 ? 1 : 2;
 #pragma unroll
-  for (int i = 0; i < WM; i += 2) {
+  for (int i = 0; i < WM; i += kHalves) {
     const int row0 = (wm * WM + i) * 32 + sub;
     u32x4_t ahead[kB];
 #pragma unroll
     for (int b = 0; b < kB; ++b) load_res(row0 + b * kRows, ahead[b]);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+    for (int half = 0; half < kHalves; ++half)
 #pragma unroll
       for (int j = 0; j < WN; ++j)
 #pragma unroll
@@ -752,12 +797,12 @@ GPTQ_DEV void tile_out(const IntParams& p, const Epilogue<E>& ep, const i32x16_t
     };
     read(0, next);
 #pragma unroll 1
-    for (int q = 0; q < 64; q += kRows * kB) {
+    for (int q = 0; q < 32 * kHalves; q += kRows * kB) {
       const Held now = next;
       u32x4_t res[kB];
 #pragma unroll
       for (int b = 0; b < kB; ++b) res[b] = ahead[b];
-      if (q + kRows * kB < 64) {
+      if (q + kRows * kB < 32 * kHalves) {
         read(q + kRows * kB, next);
 #pragma unroll
         for (int b = 0; b < kB; ++b) load_res(row0 + q + (kB + b) * kRows, ahead[b]);
@@ -795,9 +840,12 @@ template <int WM, int WN, int OUT, int E>
 __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid g, Epilogue<E> ep) {
   constexpr int kCols = E == kGated ? 32 * WN : 64 * WN;  // channels of a tile
   constexpr int kA = WM * 64 * kTStep, kB = WN * 64 * kTStep;
+  // tiles of 64 tokens wait for memory, with little to multiply: a ring of eight steps
+  constexpr int kSlots = WM == 1 ? 8 : 4;
+  constexpr int kA2 = kSlots == 8 ? kA : 16, kB2 = kSlots == 8 ? kB : 16;
   // one array per slot: the compiler then sees that reads of one slot do not alias loads in flight into another
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA], sA3[kA];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[kB], sB1[kB], sB2[kB], sB3[kB];
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA], sA3[kA], sA4[kA2], sA5[kA2], sA6[kA2], sA7[kA2];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[kB], sB1[kB], sB2[kB], sB3[kB], sB4[kB2], sB5[kB2], sB6[kB2], sB7[kB2];
   __shared__ TileRow rows[64 * WM];
   int tm, tn, slice;
   tile_of(g, static_cast<int>(blockIdx.x), tm, tn, slice);
@@ -833,12 +881,14 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   const int steps = min(g.per, (p.d_in + kTStep - 1) / kTStep - s0);
   auto slotA = [&](int u) -> uint8_t* {
     switch (u % kSlots) {
-      case 0: return sA0; case 1: return sA1; case 2: return sA2; default: return sA3;
+      case 0: return sA0; case 1: return sA1; case 2: return sA2; case 3: return sA3;
+      case 4: return sA4; case 5: return sA5; case 6: return sA6; default: return sA7;
     }
   };
   auto slotB = [&](int u) -> uint8_t* {
     switch (u % kSlots) {
-      case 0: return sB0; case 1: return sB1; case 2: return sB2; default: return sB3;
+      case 0: return sB0; case 1: return sB1; case 2: return sB2; case 3: return sB3;
+      case 4: return sB4; case 5: return sB5; case 6: return sB6; default: return sB7;
     }
   };
   // steps past the slice's end load nothing (every lane out of range: zeros)
@@ -921,9 +971,9 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   }
   for (int e = threadIdx.x; e < mrows; e += 256) rows[e] = TileRow{p.x_scales[m0 + e], p.x_sums ? p.x_sums[m0 + e] : 0};
   __syncthreads();  // and every wave is done with the operands' LDS
-  uint8_t* ra0 = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sA2 : sA3;
+  uint8_t* ra0 = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sA2 : sA3;  // (a single block of rows goes to the wider ones)
   uint8_t* rb0 = wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sB2 : sB3;
-  tile_out<WM, WN, OUT, E>(p, ep, acc, ra0, rb0, rows, m0, n0, wm, wn, mrows);
+  tile_out<WM, WN, OUT, E>(p, ep, acc, rb0, ra0, rows, m0, n0, wm, wn, mrows);
 }
 
 // sums of the K slices (integers: any order gives the same), four columns a
@@ -961,8 +1011,13 @@ __global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid
 // few tokens of few values: quantized by every workgroup of the stream kernel itself
 bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; }
 
-// row blocks a workgroup of the stream kernel takes: as many as leave every CU one
-int stream_rows(int64_t m, int64_t d_out, int n_cu) {
+// row blocks a workgroup of the stream kernel takes: as many as leave every CU one.
+// One token of few values is quantized by each workgroup, hardly more than its first weights take, and
+// workgroups of one block end more evenly (two layers of 11008 x 4096, gated: 21.6 us against
+// 25.0 with four blocks, of 28672 x 8192: 92 against 115); for two to four tokens that costs more than it gives
+// (four tokens, those layers: 36 and 30).
+int stream_rows(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
+  if (m == 1 && fuses(m, d_in) && d_out >= 64ll * n_cu) return 1;
   const int r = d_out >= 64ll * n_cu ? 4 : d_out >= 32ll * n_cu ? 2 : 1;
   return m > 32 ? std::min(r, 2) : r;
 }
@@ -977,7 +1032,7 @@ int stream_rows(int64_t m, int64_t d_out, int n_cu) {
 // 64 x 28672 -> 1024 71, 22; 256 x 2048 -> 2048 12.4, 13.5; 512 x 512 -> 512 4.4, 7.6.)
 bool streams(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   if (fuses(m, d_in)) return true;
-  const int64_t rows = 16 * stream_rows(m, d_out, n_cu), pad = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+  const int64_t rows = 16 * stream_rows(m, d_in, d_out, n_cu), pad = m <= 16 ? 16 : m <= 32 ? 32 : 64;
   const double blocks = static_cast<double>((d_out + rows - 1) / rows) * static_cast<double>((m + 63) / 64);
   const double extra = std::max(1.0, blocks / n_cu) * (1.0 + 31e-6 * static_cast<double>(pad * d_in));
   return extra <= 9.1 + 6.5e-8 * static_cast<double>(d_in) * static_cast<double>(d_out);
@@ -985,7 +1040,7 @@ bool streams(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
 
 // The launch of a product: kernel, tile and K slices.
 struct IntPlan {
-  int kind;  // 0: stream, 1: 128 x 128 tiles, 2: 256 x 256
+  int kind;  // 0: stream, 1: 128 x 128 tiles, 2: 256 x 256, 3: 64 x 128
   int slices, per;
   size_t partial_bytes;
 };
@@ -1078,21 +1133,22 @@ hipError_t product_go(const IntParams& p, const IntPlan& plan, const Epilogue<E>
                                    static_cast<size_t>(p.m * (p.d_in + 16)), st>>>(p, ep);
       return hipGetLastError();
     }
-    const int r = stream_rows(p.m, rows, n_cu);
+    const int r = stream_rows(p.m, p.d_in, rows, n_cu);
     if (r == 4) stream_go<4, E>(p, ep, f, st);
     else if (r == 2) stream_go<2, E>(p, ep, f, st);
     else stream_go<1, E>(p, ep, f, st);
     return hipGetLastError();
   }
-  const int64_t edge = plan.kind == 2 ? 256 : 128;
+  const int64_t edge = plan.kind == 2 ? 256 : 128, high = plan.kind == 3 ? 64 : edge;
   TileGrid g{};
-  g.nm = static_cast<int32_t>((p.m + edge - 1) / edge);
+  g.nm = static_cast<int32_t>((p.m + high - 1) / high);
   g.nn = static_cast<int32_t>((rows + edge - 1) / edge);
   g.slices = plan.slices;
   g.per = plan.per;
   g.partial = partial;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(g.nm) * g.nn * g.slices);
   if (plan.kind == 2) tile_go<4, 4, E>(p, g, ep, blocks, st);
+  else if (plan.kind == 3) tile_go<1, 2, E>(p, g, ep, blocks, st);
   else tile_go<2, 2, E>(p, g, ep, blocks, st);
   if (g.slices > 1) {
     const unsigned along = static_cast<unsigned>(std::min<int64_t>(p.m, 32768));
