@@ -565,21 +565,20 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
-// of 32 WM x 32 WN each.  Rows of both operands are k-contiguous, so a 64-byte
-// step of a tile goes to LDS by buffer_load ... lds as it lies in memory, through
-// a ring of four steps, and the MFMA operands are 16-byte LDS reads.  Each half
-// step's operands are read while the previous half's products run; one barrier
-// a step publishes the next step's data and frees the slot read two halves ago.
-// LDS rows are 64 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 2) & 3), so
+// of 32 WM x 32 WN each.  Rows of both operands are k-contiguous, so a step of 128
+// bytes of a tile's rows goes to LDS by buffer_load ... lds as it lies in memory,
+// through a ring of steps, and the MFMA operands are 16-byte LDS reads.  Each
+// quarter step's operands are read while the previous quarter's products run; one barrier
+// a step publishes the next step's data and frees the slot that has just been read.
+// LDS rows are 128 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7), so
 // 16 lanes that read one chunk of 16 rows touch all 64 banks once.
-// Bound: the matrix cores, and the clock that they leave.  2048 x 28672 -> 8192 on
-// 256 x 256 tiles: 409 us, 2.35 POP/s, the matrix cores busy 62% of the cycles.  Four waves of 128 x 128 read half the LDS
-// bytes a product of 64 x 64; 128 x 128 tiles are for grids too small for the others
-// (509 x 11008 -> 4096: 36 us in four K slices, 1.28 POP/s; an eight-step ring, one
-// workgroup a CU, 38 us).
-constexpr int kTStep = 64;
+// The way into LDS is what the tiles wait for: a KB of it takes a CU some 66 cycles in
+// pieces of 64 bytes and 45 in whole lines of 128 (2048 x 28672 -> 8192: 405 us
+// and 356; wider pieces of a row are no faster), whatever the depth of the ring.
+constexpr int kTStep = 128;
 
 #define GPTQ_VMCNT(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0F70)
+#define GPTQ_VMCNT_LDS(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0070)  // and no LDS read on its way
 
 GPTQ_DEV __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* base, int64_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -590,35 +589,40 @@ GPTQ_DEV __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* base, int64_t bytes) {
                                            static_cast<short>(0), n, 0x00020000);
 }
 
-// one piece (16 rows x 64 bytes) of a step to LDS
-GPTQ_DEV void tile_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* piece, uint32_t voff, int kc, int k0, int d_in) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)piece, 16, (k0 + kc < d_in) ? voff + k0 : 0x80000000u, 0, 0,
-                                           0);
+// one piece (8 rows x 128 bytes) of a step to LDS, k0 bytes into the rows
+GPTQ_DEV void tile_dma(__amdgpu_buffer_rsrc_t rs, uint8_t* piece, uint32_t voff, uint32_t k0) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void_t*)piece, 16, voff, k0, 0, 0);
 }
 
 template <int W>
 GPTQ_DEV void tile_read(const uint8_t* op, uint32_t off, i32x4_t (&f)[W]) {
 #pragma unroll
-  for (int i = 0; i < W; ++i) f[i] = *reinterpret_cast<const i32x4_t*>(op + off + i * 2048);
+  for (int i = 0; i < W; ++i) f[i] = *reinterpret_cast<const i32x4_t*>(op + off + i * 4096);
 }
 
-template <int WM, int WN>
-GPTQ_DEV void tile_half(const i32x4_t (&a)[WM], const i32x4_t (&b)[WN], const uint8_t* nA, const uint8_t* nB,
-                        uint32_t offA, uint32_t offB, i32x4_t (&na)[WM], i32x4_t (&nb)[WN], i32x16_t (&acc)[WM][WN]) {
+// after product K of N: its share of the LDS reads and of the loads to LDS
+template <int K, int N, int READS, int LOADS>
+GPTQ_DEV void tile_spread() {
+  if constexpr (K < N) {
+    constexpr int reads = (K + 1) * READS / N - K * READS / N, loads = (K + 1) * LOADS / N - K * LOADS / N;
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+    if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+    tile_spread<K + 1, N, READS, LOADS>();
+  }
+}
+
+// The products of a quarter step, with the next one's reads, and LOADS loads to LDS issued before, spread over them.
+template <int WM, int WN, int LOADS>
+GPTQ_DEV void tile_quarter(const i32x4_t (&a)[WM], const i32x4_t (&b)[WN], const uint8_t* nA, const uint8_t* nB,
+                           uint32_t offA, uint32_t offB, i32x4_t (&na)[WM], i32x4_t (&nb)[WN], i32x16_t (&acc)[WM][WN]) {
   tile_read<WM>(nA, offA, na);
   tile_read<WN>(nB, offB, nb);
 #pragma unroll
   for (int i = 0; i < WM; ++i)
 #pragma unroll
     for (int j = 0; j < WN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[i], b[j], acc[i][j], 0, 0, 0);
-  // the next half's reads and this half's loads spread over the products
-  constexpr int kProd = WM == 1 ? 1 : WM * WN / (WM + WN);
-#pragma unroll
-  for (int k = 0; k < WM + WN; ++k) {
-    __builtin_amdgcn_sched_group_barrier(0x008, kProd, 0);                // products
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                    // one LDS read
-    if ((k & 1) == 0) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // one load to LDS
-  }
+  tile_spread<0, WM * WN, WM + WN, LOADS>();
 }
 
 struct TileGrid {
@@ -840,12 +844,12 @@ template <int WM, int WN, int OUT, int E>
 __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid g, Epilogue<E> ep) {
   constexpr int kCols = E == kGated ? 32 * WN : 64 * WN;  // channels of a tile
   constexpr int kA = WM * 64 * kTStep, kB = WN * 64 * kTStep;
-  // tiles of 64 tokens wait for memory, with little to multiply: a ring of eight steps
-  constexpr int kSlots = WM == 1 ? 8 : 4;
-  constexpr int kA2 = kSlots == 8 ? kA : 16, kB2 = kSlots == 8 ? kB : 16;
+  // Tiles of 64 tokens have little to multiply: a deeper ring.
+  constexpr int kSlots = WM == 1 ? 4 : 2;
+  constexpr int kA2 = kSlots == 4 ? kA : 16, kB2 = kSlots == 4 ? kB : 16;
   // one array per slot: the compiler then sees that reads of one slot do not alias loads in flight into another
-  __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA], sA3[kA], sA4[kA2], sA5[kA2], sA6[kA2], sA7[kA2];
-  __shared__ __attribute__((aligned(1024))) uint8_t sB0[kB], sB1[kB], sB2[kB], sB3[kB], sB4[kB2], sB5[kB2], sB6[kB2], sB7[kB2];
+  __shared__ __attribute__((aligned(1024))) uint8_t sA0[kA], sA1[kA], sA2[kA2], sA3[kA2];
+  __shared__ __attribute__((aligned(1024))) uint8_t sB0[kB], sB1[kB], sB2[kB2], sB3[kB2];
   __shared__ TileRow rows[64 * WM];
   int tm, tn, slice;
   tile_of(g, static_cast<int>(blockIdx.x), tm, tn, slice);
@@ -856,7 +860,7 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   const int mrows = static_cast<int>(min(p.m - m0, int64_t{64 * WM}));
   const int nrows = static_cast<int>(min(p.d_out - n0, int64_t{kCols}));
   const __amdgpu_buffer_rsrc_t ra = rows_rsrc(p.x + m0 * p.ldx, (mrows - 1) * p.ldx + p.d_in);
-  // the layer of the wave's pieces: of all of them, or (kGated with four) of the first two and the last two
+  // the layer of the wave's pieces: of all of them, or (kGated in wide tiles) of the first four and the last four
   const int8_t *w_lo = p.w, *w_hi = p.w;
   if constexpr (E == kGated) {
     w_lo = WN == 2 && (wave & 1) ? ep.w : p.w;
@@ -864,52 +868,56 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   }
   const __amdgpu_buffer_rsrc_t rb = rows_rsrc(w_lo + n0 * p.d_in, static_cast<int64_t>(nrows) * p.d_in);
   const __amdgpu_buffer_rsrc_t rb_hi = rows_rsrc(w_hi + n0 * p.d_in, static_cast<int64_t>(nrows) * p.d_in);
-  const int kc = (((lane & 3) ^ ((lane >> 4) & 3)) * 16);
-  uint32_t va[WM], vb[WN];
+  // A piece is 8 rows; lane l has row l / 8 of it and writes position l % 8 of that row.
+  constexpr int kPA = 2 * WM, kPB = 2 * WN;  // pieces of a step, per wave
+  const int prow = lane >> 3;
+  uint32_t va[kPA], vb[kPB];
+  const int kc = ((lane & 7) ^ ((prow >> 1) & 3)) * 16;  // pieces of even number; the others' rows are four pairs on
 #pragma unroll
-  for (int u = 0; u < WM; ++u) {
-    const int row = (wave * WM + u) * 16 + (lane >> 2);
-    va[u] = row < mrows ? static_cast<uint32_t>(row * static_cast<int>(p.ldx) + kc) : 0x80000000u;
+  for (int u = 0; u < kPA; ++u) {
+    const int row = (wave * kPA + u) * 8 + prow;
+    va[u] = row < mrows ? static_cast<uint32_t>(row * static_cast<int>(p.ldx) + (kc ^ ((u & 1) * 64))) : 0x80000000u;
   }
 #pragma unroll
-  for (int u = 0; u < WN; ++u) {
-    const int piece = wave * WN + u;
-    const int row = (E == kGated ? 2 * (piece >> 2) + (piece & 1) : piece) * 16 + (lane >> 2);
-    vb[u] = row < nrows ? static_cast<uint32_t>(row * p.d_in + kc) : 0x80000000u;
+  for (int u = 0; u < kPB; ++u) {
+    const int piece = wave * kPB + u;  // kGated: 4 pieces of the one layer, 4 of the other
+    const int row = (E == kGated ? 4 * (piece >> 3) + (piece & 3) : piece) * 8 + prow;
+    vb[u] = row < nrows ? static_cast<uint32_t>(row * p.d_in + (kc ^ ((u & 1) * 64))) : 0x80000000u;
   }
   const int s0 = slice * g.per;
   const int steps = min(g.per, (p.d_in + kTStep - 1) / kTStep - s0);
   auto slotA = [&](int u) -> uint8_t* {
     switch (u % kSlots) {
-      case 0: return sA0; case 1: return sA1; case 2: return sA2; case 3: return sA3;
-      case 4: return sA4; case 5: return sA5; case 6: return sA6; default: return sA7;
+      case 0: return sA0; case 1: return sA1; case 2: return sA2; default: return sA3;
     }
   };
   auto slotB = [&](int u) -> uint8_t* {
     switch (u % kSlots) {
-      case 0: return sB0; case 1: return sB1; case 2: return sB2; case 3: return sB3;
-      case 4: return sB4; case 5: return sB5; case 6: return sB6; default: return sB7;
+      case 0: return sB0; case 1: return sB1; case 2: return sB2; default: return sB3;
     }
   };
-  // steps past the slice's end load nothing (every lane out of range: zeros)
-  auto issue_a = [&](int s, int slot) {
-    const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in;
+  // What lies past the row's end is loaded as zeros, and steps past the slice's end as nothing but them
+  // (offset 2^31: out of range).
+  auto issue = [&](int s, int slot) {
+    const int k0 = (s0 + s) * kTStep, left = p.d_in - k0;
+    const uint32_t from = s < steps ? static_cast<uint32_t>(k0) : 0x80000000u;
+    const bool even = kc < left, odd = (kc ^ 64) < left;
 #pragma unroll
-    for (int u = 0; u < WM; ++u) tile_dma(ra, slotA(slot) + (wave * WM + u) * 1024, va[u], kc, k0, p.d_in);
-  };
-  auto issue_b = [&](int s, int slot) {
-    const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in;
+    for (int u = 0; u < kPA; ++u)
+      tile_dma(ra, slotA(slot) + (wave * kPA + u) * 1024, ((u & 1) ? odd : even) ? va[u] : 0x80000000u, from);
 #pragma unroll
-    for (int u = 0; u < WN; ++u) tile_dma(E == kGated && u >= 2 ? rb_hi : rb, slotB(slot) + (wave * WN + u) * 1024, vb[u], kc, k0, p.d_in);
+    for (int u = 0; u < kPB; ++u)
+      tile_dma(E == kGated && u >= 4 ? rb_hi : rb, slotB(slot) + (wave * kPB + u) * 1024,
+               ((u & 1) ? odd : even) ? vb[u] : 0x80000000u, from);
   };
-  // operand reads: row l % 32 of a 32-row tile, chunk 2 half + l / 32
+  // operand reads: row l % 32 of a 32-row tile, chunk 2 quarter + l / 32
   const int r = lane & 31, hi = lane >> 5;
-  uint32_t oa[2], ob[2];
+  uint32_t oa[4], ob[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t o = static_cast<uint32_t>(r * 64 + (((2 * h + hi) ^ ((r >> 2) & 3)) * 16));
-    oa[h] = o + wm * WM * 2048;
-    ob[h] = o + wn * WN * 2048;
+  for (int h = 0; h < 4; ++h) {
+    const uint32_t o = static_cast<uint32_t>(r * 128 + (((2 * h + hi) ^ ((r >> 1) & 7)) * 16));
+    oa[h] = o + wm * WM * 4096;
+    ob[h] = o + wn * WN * 4096;
   }
   i32x16_t acc[WM][WN];
 #pragma unroll
@@ -919,26 +927,29 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
   i32x4_t a0[WM], b0[WN], a1[WM], b1[WN];
-  constexpr int kL = WM + WN;  // loads of one step, per wave
+  constexpr int kL = kPA + kPB;  // loads of one step, per wave
 #pragma unroll
-  for (int u = 0; u < kSlots - 1; ++u) {
-    issue_a(u, u);
-    issue_b(u, u);
-  }
-  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 2) * kL));
+  for (int u = 0; u < kSlots; ++u) issue(u, u);
+  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 1) * kL));
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
   tile_read<WM>(sA0, oa[0], a0);
   tile_read<WN>(sB0, ob[0], b0);
   // steps in blocks of a ring's length; the ones past the end multiply zeros
   for (int s = 0; s < steps; s += kSlots) {
 #pragma unroll
     for (int u = 0; u < kSlots; ++u) {
-      __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 3) * kL));
+      tile_quarter<WM, WN, 0>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
+      tile_quarter<WM, WN, 0>(a1, b1, slotA(u), slotB(u), oa[2], ob[2], a0, b0, acc);
+      tile_quarter<WM, WN, 0>(a0, b0, slotA(u), slotB(u), oa[3], ob[3], a1, b1, acc);
+      // the last quarter's operands are in registers, in every wave past the barrier, and the next step's data in LDS
+      __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT_LDS((kSlots - 2) * kL));
+      asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
-      issue_a(s + u + kSlots - 1, u + kSlots - 1);
-      tile_half<WM, WN>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
-      issue_b(s + u + kSlots - 1, u + kSlots - 1);
-      tile_half<WM, WN>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
+      asm volatile("" ::: "memory");
+      issue(s + u + kSlots, u);
+      tile_quarter<WM, WN, kL>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
     }
   }
   // Element e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.  The K
@@ -971,9 +982,8 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   }
   for (int e = threadIdx.x; e < mrows; e += 256) rows[e] = TileRow{p.x_scales[m0 + e], p.x_sums ? p.x_sums[m0 + e] : 0};
   __syncthreads();  // and every wave is done with the operands' LDS
-  uint8_t* ra0 = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sA2 : sA3;  // (a single block of rows goes to the wider ones)
-  uint8_t* rb0 = wave == 0 ? sB0 : wave == 1 ? sB1 : wave == 2 ? sB2 : sB3;
-  tile_out<WM, WN, OUT, E>(p, ep, acc, rb0, ra0, rows, m0, n0, wm, wn, mrows);
+  uint8_t* own = wave == 0 ? sA0 : wave == 1 ? sA1 : wave == 2 ? sB0 : sB1;
+  tile_out<WM, WN, OUT, E>(p, ep, acc, own, own + 4096 * WN, rows, m0, n0, wm, wn, mrows);
 }
 
 // sums of the K slices (integers: any order gives the same), four columns a
@@ -1058,7 +1068,7 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   const int steps = static_cast<int>((d_in + kTStep - 1) / kTStep);
   const int64_t room = a.kind == 2 ? n_cu : 2 * n_cu;
   int64_t sl = std::max<int64_t>(1, room / tiles);
-  sl = std::min<int64_t>(sl, std::max(1, steps / 16));
+  sl = std::min<int64_t>(sl, std::max(1, steps / 8));
   a.per = static_cast<int>((steps + sl - 1) / sl);
   a.slices = (steps + a.per - 1) / a.per;
   if (a.slices > 1) a.partial_bytes = static_cast<size_t>(a.slices) * m * d_out * 4;
