@@ -13,6 +13,7 @@
 #include "quant_row.h"
 
 #include <algorithm>
+#include <cmath>
 
 namespace gptq {
 namespace {
@@ -301,13 +302,12 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int64_t block0 = static_cast<int64_t>(blockIdx.x) * R;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
   const int8_t* wrow[R];
 #pragma unroll
   for (int j = 0; j < R; ++j) wrow[j] = block_row<E>(p, ep, block0 + j, c) + 16 * g;
   const int8_t* xrow[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) xrow[i] = p.x + min(t0 + 16 * i + c, p.m - 1) * p.ldx + 16 * g;
+  for (int i = 0; i < MT; ++i) xrow[i] = p.x + min(static_cast<int64_t>(16 * i + c), p.m - 1) * p.ldx + 16 * g;
   const i32x4_t zero = {0, 0, 0, 0};
   auto load_w = [&](int k0, i32x4_t (&b)[kU][R]) {
 #pragma unroll
@@ -454,7 +454,7 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
   constexpr int kC = E == kGated ? 8 : 16;  // channels of a block
   for (int e = threadIdx.x; e < R * MT * 16 * kC; e += 64 * kSW) {
     const int tc = e % kC, j = (e / kC) % R, tr = (e / (kC * R)) & 15, i = e / (16 * kC * R);
-    const int64_t col = (block0 + j) * kC + tc, row = t0 + 16 * i + tr;
+    const int64_t col = (block0 + j) * kC + tc, row = 16 * i + tr;
     if (col >= p.d_out || row >= p.m) continue;
     int s = 0;
 #pragma unroll
@@ -561,7 +561,7 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
   else if (fused == 2) integer_stream_kernel<R, 1, 2, E><<<grid, t, 0, st>>>(p, ep);
   else if (p.m <= 16) integer_stream_kernel<R, 1, 0, E><<<grid, t, 0, st>>>(p, ep);
   else if (p.m <= 32) integer_stream_kernel<R, 2, 0, E><<<grid, t, 0, st>>>(p, ep);
-  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0, E><<<dim3(grid.x, static_cast<unsigned>((p.m + 63) / 64)), t, 0, st>>>(p, ep);
+  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0, E><<<grid, t, 0, st>>>(p, ep);
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
@@ -898,17 +898,20 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   };
   // What lies past the row's end is loaded as zeros, and steps past the slice's end as nothing but them
   // (offset 2^31: out of range).
-  auto issue = [&](int s, int slot) {
+  auto issue_x = [&](int s, int slot) {
     const int k0 = (s0 + s) * kTStep, left = p.d_in - k0;
     const uint32_t from = s < steps ? static_cast<uint32_t>(k0) : 0x80000000u;
-    const bool even = kc < left, odd = (kc ^ 64) < left;
 #pragma unroll
     for (int u = 0; u < kPA; ++u)
-      tile_dma(ra, slotA(slot) + (wave * kPA + u) * 1024, ((u & 1) ? odd : even) ? va[u] : 0x80000000u, from);
+      tile_dma(ra, slotA(slot) + (wave * kPA + u) * 1024, (kc ^ ((u & 1) * 64)) < left ? va[u] : 0x80000000u, from);
+  };
+  auto issue_w = [&](int s, int slot) {
+    const int k0 = (s0 + s) * kTStep, left = p.d_in - k0;
+    const uint32_t from = s < steps ? static_cast<uint32_t>(k0) : 0x80000000u;
 #pragma unroll
     for (int u = 0; u < kPB; ++u)
       tile_dma(E == kGated && u >= 4 ? rb_hi : rb, slotB(slot) + (wave * kPB + u) * 1024,
-               ((u & 1) ? odd : even) ? vb[u] : 0x80000000u, from);
+               (kc ^ ((u & 1) * 64)) < left ? vb[u] : 0x80000000u, from);
   };
   // operand reads: row l % 32 of a 32-row tile, chunk 2 quarter + l / 32
   const int r = lane & 31, hi = lane >> 5;
@@ -929,8 +932,11 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   i32x4_t a0[WM], b0[WN], a1[WM], b1[WN];
   constexpr int kL = kPA + kPB;  // loads of one step, per wave
 #pragma unroll
-  for (int u = 0; u < kSlots; ++u) issue(u, u);
-  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 1) * kL));
+  for (int u = 0; u < kSlots; ++u) {
+    issue_w(u, u);
+    if (u < kSlots - 1) issue_x(u, u);
+  }
+  __builtin_amdgcn_s_waitcnt(GPTQ_VMCNT((kSlots - 1) * kL - kPA));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -940,7 +946,10 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
   for (int s = 0; s < steps; s += kSlots) {
 #pragma unroll
     for (int u = 0; u < kSlots; ++u) {
-      tile_quarter<WM, WN, 0>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
+      // half of a step's loads in each of two quarters: all in one keep the wave waiting at the address unit,
+      // later ones arrive late (2048 x 28672 -> 8192 419 us with all in the first, 422 in three, 410 so)
+      issue_x(s + u + kSlots - 1, u + kSlots - 1);
+      tile_quarter<WM, WN, kPA>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
       tile_quarter<WM, WN, 0>(a1, b1, slotA(u), slotB(u), oa[2], ob[2], a0, b0, acc);
       tile_quarter<WM, WN, 0>(a0, b0, slotA(u), slotB(u), oa[3], ob[3], a1, b1, acc);
       // the last quarter's operands are in registers, in every wave past the barrier, and the next step's data in LDS
@@ -948,8 +957,8 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      issue(s + u + kSlots, u);
-      tile_quarter<WM, WN, kL>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
+      issue_w(s + u + kSlots, u);
+      tile_quarter<WM, WN, kPB>(a1, b1, slotA(u + 1), slotB(u + 1), oa[0], ob[0], a0, b0, acc);
     }
   }
   // Element e of lane l: row 8 (e / 4) + 4 (l / 32) + e % 4, column l % 32.  The K
@@ -1032,22 +1041,6 @@ int stream_rows(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   return m > 32 ? std::min(r, 2) : r;
 }
 
-// The stream kernel reads the weights with less ado than the tiles do, but a
-// workgroup's turns also load its tokens' codes.  What that costs, fitted to
-// both kernels' times over 2 to 512 tokens and weights of 512 x 512 to
-// 28672 x 8192: 1 us and 31 ps a token (of its padded block) and k, for each
-// round of workgroups; against it the tiles' prologue, slices and join, 9.1 us and
-// 65 ns per MB of weights.  (us, stream and tiles: 64 x 4096 -> 4096 14.0, 14.8;
-// 100 of them 20.6, 15.8; 64 x 11008 -> 4096 30.7, 25.2; 24 of them 17.4, 22.9;
-// 64 x 28672 -> 1024 71, 22; 256 x 2048 -> 2048 12.4, 13.5; 512 x 512 -> 512 4.4, 7.6.)
-bool streams(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
-  if (fuses(m, d_in)) return true;
-  const int64_t rows = 16 * stream_rows(m, d_in, d_out, n_cu), pad = m <= 16 ? 16 : m <= 32 ? 32 : 64;
-  const double blocks = static_cast<double>((d_out + rows - 1) / rows) * static_cast<double>((m + 63) / 64);
-  const double extra = std::max(1.0, blocks / n_cu) * (1.0 + 31e-6 * static_cast<double>(pad * d_in));
-  return extra <= 9.1 + 6.5e-8 * static_cast<double>(d_in) * static_cast<double>(d_out);
-}
-
 // The launch of a product: kernel, tile and K slices.
 struct IntPlan {
   int kind;  // 0: stream, 1: 128 x 128 tiles, 2: 256 x 256, 3: 64 x 128
@@ -1055,23 +1048,58 @@ struct IntPlan {
   size_t partial_bytes;
 };
 
+// Of the stream kernel (up to 64 tokens) and the tiles, in 1 to 16 slices of K, the
+// one that should take least, by what each costs (us), fitted to the times of all of
+// them over 5 to 2048 tokens and twelve shapes of weights, 1024 x 1024 to 28672 x 8192:
+//   stream  a launch, the weights at 6.9 TB/s (some come from the caches), and past 16
+//           tokens 1 us and 31 ps a token (of its padded block) and k for every round of
+//           workgroups, which load their tokens' codes beside the weights; up to 16
+//           tokens the round's K alone
+//   tiles   a launch, then the longer of a round's steps and of the bytes at 6.6 TB/s;
+//           K slices cost a second launch and their sums' way to memory and back
+// The choice is 2% slower than the best of them in the mean.  (us, stream and 64-row,
+// 128-row, 256-row tiles in their best slices: 17 x 4096 -> 4096 10.2, 14.2, 14.4, 22;
+// 64 x 4096 -> 11008 28.8, 16.5, 20.4, -; 64 x 28672 -> 8192 94, 48, 51, -;
+// 512 x 4096 -> 4096 -, 17.4, 25.9, 29.8; 2048 x 4096 -> 1024 -, 13.5, 23.5, 28;
+// 2048 x 4096 -> 4096 -, 63, 39.9, 53;
+// 1024 x 8192 -> 8192 -, 115, 77, 81; 2048 x 8192 -> 8192 -, 222, 143, 114.)
 IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   IntPlan a{0, 1, 0, 0};
-  if (streams(m, d_in, d_out, n_cu)) return a;
-  // 256 x 256 tiles where they give more than half the CUs one, or where K is
-  // long enough for slices of 2048 that do (1024 x 11008 -> 4096 in four slices: 70 us, 88
-  // in 128 x 128 tiles; 2048 x 28672 -> 1024 in eight: 82 and 105; but 1024 x 1024 -> 4096: 23
-  // and 11; 509 x 11008 -> 4096 with its codes and join, in eight slices of 1376: 53.2 and 52.0)
-  const int64_t t256 = ((m + 255) / 256) * ((d_out + 255) / 256), t128 = ((m + 127) / 128) * ((d_out + 127) / 128);
-  a.kind = t256 > n_cu / 2 || (d_in >= 8192 && m > 128 && t256 * 8 >= n_cu && t256 * d_in >= 2048ll * n_cu) ? 2 : 1;
-  const int64_t tiles = a.kind == 2 ? t256 : t128;
-  const int steps = static_cast<int>((d_in + kTStep - 1) / kTStep);
-  const int64_t room = a.kind == 2 ? n_cu : 2 * n_cu;
-  int64_t sl = std::max<int64_t>(1, room / tiles);
-  sl = std::min<int64_t>(sl, std::max(1, steps / 8));
-  a.per = static_cast<int>((steps + sl - 1) / sl);
-  a.slices = (steps + a.per - 1) / a.per;
-  if (a.slices > 1) a.partial_bytes = static_cast<size_t>(a.slices) * m * d_out * 4;
+  if (fuses(m, d_in)) return a;
+  const double k = static_cast<double>(d_in), n = static_cast<double>(d_out), rows = static_cast<double>(m);
+  double least = 1e300;
+  if (m <= 64) {
+    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, n_cu))), rounds = std::max(1.0, blocks / n_cu);
+    if (m <= 16) least = 5.0 + std::max(k * n / 6.9e6, 0.83e-3 * k * rounds);
+    else least = 1.0 + 1.04 * (k * n / 5e6 + rounds * (1.0 + 31e-6 * (m <= 32 ? 32 : 64) * k));
+  }
+  const int64_t steps = (d_in + kTStep - 1) / kTStep;
+  struct Tile {
+    int kind, high, wide;
+    double step, full;  // us a step: of a round with one workgroup a CU, with two
+  };
+  constexpr Tile tiles[3] = {{3, 64, 128, 0.44, 0.44}, {1, 128, 128, 0.84, 1.05}, {2, 256, 256, 1.34, 1.34}};
+  for (const Tile& t : tiles) {
+    // Many tokens of long rows leave the L2s between their strips of 64 (2048 x 11008 -> 2048: 77 us, 62 in slices
+    // of 256-row tiles; 1500 x 8224 -> 1800: 67 and 50, though 1030 of them 39 and 42).
+    if (t.kind == 3 && m > 1024 && d_in > 8192) continue;
+    const int64_t count = ((m + t.high - 1) / t.high) * ((d_out + t.wide - 1) / t.wide);
+    for (int64_t sl = 1; sl <= 16 && (sl == 1 || steps / sl >= 4); sl *= 2) {
+      const int64_t per = (steps + sl - 1) / sl, slices = (steps + per - 1) / per;
+      const int64_t room = t.kind == 1 ? 2 * n_cu : n_cu, whole = count * slices / room, rest = count * slices % room;
+      const double last = rest == 0 ? 0.0 : rest <= n_cu ? t.step : t.full;
+      const double work = static_cast<double>(per) * (static_cast<double>(whole) * t.full + last);
+      double cost = 4.9 + std::max(work, k * (n + rows) / 6.6e6);
+      if (slices > 1) cost += 5.0 + 8.0 * static_cast<double>(slices) * rows * n / 4.3e6;
+      if (cost < least) {
+        least = cost;
+        a.kind = t.kind;
+        a.slices = static_cast<int>(slices);
+        a.per = static_cast<int>(per);
+      }
+    }
+  }
+  a.partial_bytes = a.slices > 1 ? static_cast<size_t>(a.slices) * m * d_out * 4 : 0;
   return a;
 }
 
