@@ -431,7 +431,7 @@ gptq_status gptq_norm_tokens(const void* x, int32_t xt, int64_t n_tokens, int64_
   c.res_bf16 = rt == GPTQ_BF16;
   c.w_bf16 = wt == GPTQ_BF16;
   c.y_bf16 = yt == GPTQ_BF16;
-  return from_hip(gptq::norm_launch(c, static_cast<hipStream_t>(stream)));
+  return from_hip(gptq::norm_launch(c, device_cus(), static_cast<hipStream_t>(stream)));
 }
 
 gptq_status gptq_cache_write(const gptq_cache* cache, const void* k, const void* v, int32_t xt, int64_t n_tokens,

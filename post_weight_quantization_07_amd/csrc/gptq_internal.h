@@ -185,7 +185,7 @@ struct NormCall {
   float eps;
   bool x_bf16, res_bf16, w_bf16, y_bf16;
 };
-hipError_t norm_launch(const NormCall& c, hipStream_t stream);
+hipError_t norm_launch(const NormCall& c, int n_cu, hipStream_t stream);
 
 // ------------------------------------------------------------------ cache --
 struct CacheShape {
