@@ -20,17 +20,22 @@ plumbing and runs in torch (fp32); the layer solves run in libgptq.so.  For a
 model that will be served with a quantized key/value cache, cache_bits runs
 the attention over such a cache, so that o_proj and the layers after it are
 calibrated on the outputs they will see.
+
+serve_block is the block as it is served once quantized: its layers in 8-bit
+integers (checkpoint.integer_layer), its keys and values in a QuantizedCache,
+and everything between them in libgptq.so's kernels.
 """
 from __future__ import annotations
 
 from dataclasses import dataclass, field
-from typing import Dict, List, Optional
+from typing import Dict, List, Mapping, Optional
 
 import torch
 import torch.nn.functional as F
 
 from . import solve_layers_shared
-from ._lib import QuantizeConfig, QuantizedCache, gptq_cache_attention, gptq_cache_write
+from ._lib import (QuantizeConfig, QuantizedCache, gptq_cache_attention, gptq_cache_write, gptq_integer_gated,
+                   gptq_integer_matmul, gptq_norm_tokens)
 
 QUANT_ORDER: List[List[str]] = [["k_proj", "v_proj", "q_proj"], ["o_proj"], ["up_proj", "gate_proj"],
                                 ["down_proj"]]
@@ -157,3 +162,36 @@ def quantize_block(block: Block, x0: torch.Tensor, n_seq: int, seq_len: int, cfg
         tags = sorted({t.rsplit(" ", 1)[0] for t in ev})
         res.ms = {t: ev[t + " start"].elapsed_time(ev[t + " end"]) for t in tags}
     return res
+
+
+def serve_block(layers: Mapping[str, Mapping[str, torch.Tensor]], x: torch.Tensor, cache: QuantizedCache,
+                slots: torch.Tensor, page_table: torch.Tensor, q_starts: torch.Tensor, kv_lens: torch.Tensor,
+                n_heads: int, norms: Optional[Mapping[str, torch.Tensor]] = None, eps: float = 1e-6, activation: str = "silu",
+                cap: Optional[float] = None, slopes: Optional[torch.Tensor] = None,
+                prefix_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The block's output for the hidden states x [n_tokens, d_model] (bf16 or
+    fp32) of new tokens, prompts and single tokens alike, in x's dtype.
+
+    layers: the seven layers of QUANT_ORDER as checkpoint.integer_layer gives
+    them, each optionally with a "bias" (fp32 [d_out]).  norms: the weights of
+    the norms before the attention ("input") and after it ("post_attention"),
+    ones where absent.  The new tokens' keys and values are written to `slots`
+    of the cache; page_table, q_starts, kv_lens, cap, slopes and prefix_lens as
+    for gptq_cache_attention, activation as for gptq_integer_gated.  Between
+    the layers values are bf16 or 8-bit codes; sums, norms and softmax are fp32."""
+    n = x.shape[0]
+    hd = cache.head_dim
+    norms = norms or {}
+
+    def apply(inp, name, dtype=torch.bfloat16, residual=None):
+        t = layers[name]
+        return gptq_integer_matmul(inp, t["w"], t["scales"], t.get("offsets"), out_dtype=dtype, bias=t.get("bias"),
+                                   residual=residual)
+    rows, _ = gptq_norm_tokens(x, norms.get("input"), eps=eps)
+    q, k, v = (apply(rows, name) for name in ("q_proj", "k_proj", "v_proj"))
+    gptq_cache_write(cache, k.view(n, cache.n_kv_heads, hd), v.view(n, cache.n_kv_heads, hd), slots)
+    att = gptq_cache_attention(q.view(n, n_heads, hd), cache, page_table, q_starts, kv_lens, cap=cap, slopes=slopes,
+                               prefix_lens=prefix_lens)
+    rows, h = gptq_norm_tokens(apply(att.view(n, n_heads * hd), "o_proj"), norms.get("post_attention"), residual=x, eps=eps)
+    m = gptq_integer_gated(rows, layers["gate_proj"], layers["up_proj"], activation, out_dtype=torch.bfloat16)
+    return apply(m, "down_proj", x.dtype, residual=h)
