@@ -456,18 +456,19 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
     const int tc = e % kC, j = (e / kC) % R, tr = (e / (kC * R)) & 15, i = e / (16 * kC * R);
     const int64_t col = (block0 + j) * kC + tc, row = 16 * i + tr;
     if (col >= p.d_out || row >= p.m) continue;
+    const int off = p.w_offsets ? p.w_offsets[col] : 0;
+    const float sx = FUSED ? xs[tr & 3] : p.x_scales[row], sw = p.w_scales[col];
     int s = 0;
 #pragma unroll
     for (int w = 0; w < kSW; ++w) s += part[w][j][i][tr][tc];
-    const float sx = FUSED ? xs[tr & 3] : p.x_scales[row];
     if constexpr (E == kGated) {
       int s2 = 0;
 #pragma unroll
       for (int w = 0; w < kSW; ++w) s2 += part[w][j][i][tr][tc + 8];
       gated_finish(p, ep, row, col, s, s2, sx, FUSED ? xsum[tr & 3] : p.x_sums ? p.x_sums[row] : 0);
     } else {
-      if (p.w_offsets) s -= p.w_offsets[col] * (FUSED ? xsum[tr & 3] : p.x_sums[row]);
-      int_finish(p, ep, row, col, (static_cast<float>(s) * sx) * p.w_scales[col]);
+      if (p.w_offsets) s -= off * (FUSED ? xsum[tr & 3] : p.x_sums[row]);
+      int_finish(p, ep, row, col, (static_cast<float>(s) * sx) * sw);
     }
   }
 }
@@ -539,8 +540,10 @@ __global__ __launch_bounds__(64 * kRW, 4) void integer_resident_kernel(IntParams
           if (tc < 8 && col < p.d_out && tr < m)
             gated_finish(p, ep, tr, col, s, s2, p.x_scales[tr], p.x_sums ? p.x_sums[tr] : 0);
         } else if (col < p.d_out && tr < m) {
-          if (p.w_offsets) s -= p.w_offsets[col] * p.x_sums[tr];
-          int_finish(p, ep, tr, col, (static_cast<float>(s) * p.x_scales[tr]) * p.w_scales[col]);
+          const int off = p.w_offsets ? p.w_offsets[col] : 0;
+          const float sx = p.x_scales[tr], sw = p.w_scales[col];
+          if (p.w_offsets) s -= off * p.x_sums[tr];
+          int_finish(p, ep, tr, col, (static_cast<float>(s) * sx) * sw);
         }
       }
       buf ^= 1;
