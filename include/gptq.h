@@ -399,7 +399,7 @@ typedef struct {
  * z is taken in fp32 (relative 3 2^-24), as are the sums and the activation; y
  * is rounded once to its type.
  *   residual_or_null  [m, ldr] bf16 or fp32 (rt), d_out <= ldr <= 2^20.  y may be the residual
- *            itself (same type, ldr = d_out or m = 1) and may not touch it otherwise
+ *            itself (same type, ldr = d_out or m = 1) and may not touch it otherwise, nor x
  *   Others, workspace, limits and errors as for gptq_integer_matmul.  With
  *   neither bias, activation nor residual it is that call.
  */
@@ -413,7 +413,7 @@ gptq_status gptq_integer_linear(const void* x, int32_t xt, const float* x_scales
  * it is not codes, quantized) once for both products, and neither leaves the chip:
  *   y[t, n] = act(zg[t, n] + bias_g[n]) (zu[t, n] + bias_u[n])
  * zg, zu the values of gptq_integer_matmul for the two layers, in fp32; y is
- * rounded once to its type.  The layers share d_in and d_out.
+ * rounded once to its type, and may not touch x.  The layers share d_in and d_out.
  *   x_sums   for GPTQ_I8 x: needed if either layer has offsets
  *   ws       device workspace of gptq_integer_gated_workspace_size(m, xt, d_in, d_out) bytes
  * Requires d_out <= 2^19; others as for gptq_integer_matmul.
@@ -428,7 +428,8 @@ gptq_status gptq_integer_gated(const void* x, int32_t xt, const float* x_scales,
  * Root-mean-square norm of tokens, with the addition before it and the integer
  * codes after it:
  *   h = x + residual (x without one),  s = 1 / sqrt(mean h^2 + eps),  y = s h weight
- * h and u = h weight are rounded to fp32, the squares are summed in fp64.
+ * h and u = h weight are rounded to fp32 (and have to stay in its range), the
+ * squares are summed in fp64.
  *   x        [n_tokens, ldx] bf16 or fp32, the first d entries of a row;
  *            residual_or_null [n_tokens, ldr] likewise (rt)
  *   weight_or_null  [d] bf16 or fp32 (wt); null: ones
@@ -543,7 +544,8 @@ gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t
  * and the token sees the keys j <= a and j < prefix_lens[i].
  *   cap      0, or in [2^-20, 2^20]; a capped score is off by 2^-20 of the cap more, past
  *            caps of 2^8 by 2^-19 of itself
- *   slopes   [n_heads] fp32, finite, or null; a bias that leaves fp32's range hides the key
+ *   slopes   [n_heads] fp32 or null; slopes[head] |a - j| has to stay in fp32's range
+ *            (distances past 2^24 are rounded to it)
  *   prefix_lens  [n_seq] int32, clamped to [0, kv_lens[i]], or null
  * A token that sees no key (kv_len < n, no prefix) gets zeros.  Everything else
  * as for gptq_cache_attention, its workspace too; with nothing set it is that call.

@@ -316,6 +316,11 @@ bool overlap(const Rows& a, const Rows& b, int64_t m) {
   const int64_t off = static_cast<int64_t>(apart % static_cast<uintptr_t>(a.lead));  // inside a row of the first
   return off < first.width || off + second.width > a.lead;
 }
+// Whether y [m, d_out] touches x (every workgroup of a product reads all of its tokens; sizes of a valid call only).
+bool touches_x(const void* y, int32_t yt, int64_t d_out, const void* x, int32_t xt, int64_t ldx, int64_t d_in, int64_t m) {
+  if (d_in < 1 || d_in > ldx || ldx > kMaxLead) return false;
+  return overlap(Rows{y, d_out * size_of(yt), d_out * size_of(yt)}, Rows{x, ldx * size_of(xt), d_in * size_of(xt)}, m);
+}
 // Out may not touch in, unless it is in itself, element by element.
 bool clobbers(const Rows& out, const Rows& in, bool same_type, int64_t m) {
   return overlap(out, in, m) && !(same_type && out.at == in.at && (out.lead == in.lead || m == 1));
@@ -345,6 +350,7 @@ gptq_status gptq_integer_linear(const void* x, int32_t xt, const float* x_scales
                                 int32_t activation, const void* residual_or_null, int32_t rt, int64_t ldr, void* y,
                                 int32_t yt, void* ws, size_t ws_bytes, void* stream) {
   if (!layer || !activation_ok(activation) || !rows_ok(m) || !dim_ok(d_out)) return GPTQ_ERR_INVALID_ARG;
+  if (touches_x(y, yt, d_out, x, xt, ldx, d_in, m)) return GPTQ_ERR_INVALID_ARG;
   if (residual_or_null) {
     if ((rt != GPTQ_F32 && rt != GPTQ_BF16) || ldr < d_out || ldr > kMaxDim) return GPTQ_ERR_INVALID_ARG;
     const Rows to{y, d_out * size_of(yt), d_out * size_of(yt)}, from{residual_or_null, ldr * size_of(rt), d_out * size_of(rt)};
@@ -376,7 +382,9 @@ gptq_status gptq_integer_gated(const void* x, int32_t xt, const float* x_scales,
                                int64_t d_in, int64_t ldx, const gptq_integer_layer* gate, const gptq_integer_layer* up,
                                int64_t d_out, int32_t activation, void* y, int32_t yt, void* ws, size_t ws_bytes,
                                void* stream) {
-  if (!gate || !up || !activation_ok(activation) || d_out <= 0 || d_out > kMaxDim / 2) return GPTQ_ERR_INVALID_ARG;
+  if (!gate || !up || !activation_ok(activation) || !rows_ok(m) || d_out <= 0 || d_out > kMaxDim / 2)
+    return GPTQ_ERR_INVALID_ARG;
+  if (touches_x(y, yt, d_out, x, xt, ldx, d_in, m)) return GPTQ_ERR_INVALID_ARG;
   gptq::IntCall c{};
   c.x = x;
   c.xt = xt;

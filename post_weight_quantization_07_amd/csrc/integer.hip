@@ -900,21 +900,19 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
     }
   };
   // What lies past the row's end is loaded as zeros, and steps past the slice's end as nothing but them
-  // (offset 2^31: out of range).
+  // (the lane's offset 2^31: out of range; k0, the scalar one, never passes the rows' bytes).
   auto issue_x = [&](int s, int slot) {
-    const int k0 = (s0 + s) * kTStep, left = p.d_in - k0;
-    const uint32_t from = s < steps ? static_cast<uint32_t>(k0) : 0x80000000u;
+    const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in, left = p.d_in - k0;
 #pragma unroll
     for (int u = 0; u < kPA; ++u)
-      tile_dma(ra, slotA(slot) + (wave * kPA + u) * 1024, (kc ^ ((u & 1) * 64)) < left ? va[u] : 0x80000000u, from);
+      tile_dma(ra, slotA(slot) + (wave * kPA + u) * 1024, (kc ^ ((u & 1) * 64)) < left ? va[u] : 0x80000000u, k0);
   };
   auto issue_w = [&](int s, int slot) {
-    const int k0 = (s0 + s) * kTStep, left = p.d_in - k0;
-    const uint32_t from = s < steps ? static_cast<uint32_t>(k0) : 0x80000000u;
+    const int k0 = s < steps ? (s0 + s) * kTStep : p.d_in, left = p.d_in - k0;
 #pragma unroll
     for (int u = 0; u < kPB; ++u)
       tile_dma(E == kGated && u >= 4 ? rb_hi : rb, slotB(slot) + (wave * kPB + u) * 1024,
-               (kc ^ ((u & 1) * 64)) < left ? vb[u] : 0x80000000u, from);
+               (kc ^ ((u & 1) * 64)) < left ? vb[u] : 0x80000000u, k0);
   };
   // operand reads: row l % 32 of a 32-row tile, chunk 2 quarter + l / 32
   const int r = lane & 31, hi = lane >> 5;

@@ -261,3 +261,65 @@ def test_stream_and_graph(G, m, d_in, d_out):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(hold, eager)
+
+
+def _product64(layer, codes, scales):
+    """Layer.product with the integer sums taken on the GPU in 64 bits (exact below 2^53)."""
+    c = torch.from_numpy(codes).to(dev()).double()
+    w = layer.dict["w"]
+    z = np.empty((c.shape[0], w.shape[0]))
+    for a in range(0, w.shape[0], 4096):
+        wd = w[a:a + 4096].double() - torch.from_numpy(layer.off[a:a + 4096]).to(dev()).double()[:, None]
+        z[:, a:a + 4096] = torch.mm(c, wd.t().contiguous()).cpu().numpy()
+    z *= scales.astype(np.float64)[:, None] * layer.s.astype(np.float64)
+    err = ((1 + U) ** 3 - 1) * np.abs(z)
+    if layer.b is not None:
+        b = layer.b.astype(np.float64)
+        err = err + U * (np.abs(z) + np.abs(b)) * (1 + 8 * U)
+        z = z + b
+    return z, err
+
+
+# one or more for each launch that the rule on sizes chooses: stream kernel with one to four row blocks and
+# token blocks, x quantized on the way for one to four tokens, codes resident, the three tiles whole and in K slices
+LAUNCHES = [(1, 32, 8200), (1, 96, 16500), (2, 32, 16500), (3, 4096, 40), (4, 96, 70), (4, 4096, 18), (3, 160, 8200), (5, 32, 8200),
+            (17, 32, 8200), (17, 96, 16500), (33, 32, 8300), (65, 32, 17000), (400, 32, 17000), (65, 2048, 100), (70, 32768, 50),
+            (600, 224, 8200), (1100, 8192, 130), (1100, 8224, 66), (4100, 8192, 130), (1000, 8192, 2100), (300, 4128, 4100),
+            (16, 9728, 16400)]
+
+
+@pytest.mark.parametrize("m,d_in,rows", LAUNCHES)
+@pytest.mark.parametrize("gated", [False, True])
+def test_every_launch(G, m, d_in, rows, gated):
+    act = ACTS[1 + (m + d_in + rows) % 4]
+    d_out = rows // 2 if gated else rows
+    banner(f"every launch: {m}x{d_in}->{d_out} gated={gated} act={act}")
+    wide = _x(m, d_in + 8, "bf16", m + d_in)
+    first, second = Layer(d_out, d_in, 1, True, True), Layer(d_out, d_in, 2, False, False) if gated else None
+    res = None if gated else torch.randn(m, d_out, device=dev()).to(torch.bfloat16)
+    for x in (wide[:, :d_in].contiguous(), wide[:, 3:3 + d_in]):            # whole vectors, and rows of any alignment
+        codes, scales = S.row_codes(host(x.contiguous()), 127)
+        a, da = activated(*_product64(first, codes, scales), act)
+        t = first.dict
+        if gated:
+            z, dz = _product64(second, codes, scales)
+            ref, err = a * z, np.abs(z) * da + np.abs(a) * dz + da * dz
+            call = lambda inp, dtype: G.gptq_integer_gated(inp, first.dict, second.dict, act, out_dtype=dtype)  # noqa: E731
+        else:
+            ref, err = a + host(res).astype(np.float64), da + U * np.abs(a)
+            call = lambda inp, dtype: G.gptq_integer_matmul(inp, t["w"], t["scales"], t["offsets"], out_dtype=dtype,  # noqa: E731
+                                                            bias=t["bias"], activation=act, residual=res)
+        y = call(x, torch.float32)
+        near(y, ref, err)
+        assert torch.equal(y, call(G.gptq_quantize_tokens(x), torch.float32))
+        near(call(x, torch.bfloat16), ref, err)
+
+
+@pytest.mark.parametrize("m,d_in,rows", LAUNCHES)
+def test_every_plain_launch(G, m, d_in, rows):
+    """The product alone: the same sums, by the same launches."""
+    banner(f"every plain launch: {m}x{d_in}->{rows}")
+    x, layer = _x(m, d_in, "f32", m + rows), Layer(rows, d_in, 3, True, False)
+    codes, scales = S.row_codes(host(x), 127)
+    t = layer.dict
+    near(G.gptq_integer_matmul(x, t["w"], t["scales"], t["offsets"]), *_product64(layer, codes, scales))

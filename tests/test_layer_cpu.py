@@ -111,7 +111,8 @@ def test_linear_and_gated_refuse(L):
         return lib.gptq_integer_gated(x, t, xs, sums, m, d, ld, g, u, o, act, y, yt, ws, nb, None)
     both = (dict(x=None), dict(t=3), dict(m=-1), dict(m=(1 << 30) + 1), dict(d=48), dict(d=1 << 17, ld=1 << 17), dict(ld=32),
             dict(o=0), dict(o=-4), dict(y=None), dict(yt=2), dict(t=2), dict(t=2, xs=at(11), x=at(1, 8)),
-            dict(t=2, xs=at(11), ld=72), dict(act=-1), dict(act=5))
+            dict(t=2, xs=at(11), ld=72), dict(act=-1), dict(act=5),
+            dict(y=at(1)), dict(y=at(1, 64 * 2 * 4 - 4)), dict(t=0, y=at(1, 64 * 4 * 3)))             # y over x
     for kw in both:
         assert linear(**kw) == 1 and gated(**kw) == 1, kw
     off = layer(offsets=at(12))
