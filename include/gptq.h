@@ -544,7 +544,7 @@ gptq_status gptq_cache_attention(const gptq_cache* cache, const void* q, int32_t
  * and the token sees the keys j <= a and j < prefix_lens[i].
  *   cap      0, or in [2^-20, 2^20]; a capped score is off by 2^-20 of the cap more, past
  *            caps of 2^8 by 2^-19 of itself
- *   slopes   [n_heads] fp32 or null; slopes[head] |a - j| has to stay in fp32's range
+ *   slopes   [n_heads] fp32 or null; |slopes[head] (a - j)| has to stay below 2^126
  *            (distances past 2^24 are rounded to it)
  *   prefix_lens  [n_seq] int32, clamped to [0, kv_lens[i]], or null
  * A token that sees no key (kv_len < n, no prefix) gets zeros.  Everything else

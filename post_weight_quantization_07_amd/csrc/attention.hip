@@ -70,6 +70,8 @@ struct AttnParams {
 //   kWide    (with kCap) for caps past 2^8, where that would be half of what the weights'
 //            fp16 rounds: |z| < 0.3 cap by tanh's series up to x^9, all off by 2^-19 relative
 //   kBias    then less slope_h |a - j|
+// Two prompts of 2048 tokens, 32/16 heads of 128, 8 bits: as they are 115 us, with slopes 113 (154 with the
+// keys taken from the first one), capped 136; 48 ragged sequences of single tokens 57, with slopes 59.
 enum { kAsIs = 0, kBias = 1, kCap = 2, kWide = 4, kPrefix = 8 };
 constexpr float kWideCap = 256.f;
 constexpr float kLog2e = 1.4426950408889634f;

@@ -276,7 +276,8 @@ GPTQ_DEV void gated_finish(const IntParams& p, const Epilogue<kGated>& e, int64_
 // every CU a workgroup all the same (16 tokens through 28672 x 8192: 67 us with
 // R = 1, 63 with R = 4, 49 with x not read at all).
 // 16 tokens: 11008 x 4096 15.1 us (a kernel that only reads those 45 MB takes
-// 12 to 15), 8192 x 28672 57 us, 4.1 TB/s.  32 and 64 tokens of 11008 x 4096: 22 and 30 us.
+// 12 to 15), 8192 x 28672 57 us, 4.1 TB/s; one token through both layers of a gated 11008 x 4096
+// 22.6 us with its activation, 4.0 TB/s.
 // FUSED (one to four tokens): x is quantized here, by every workgroup for
 // itself and into LDS, while its first weights are on their way: one launch, and
 // reading the tokens again from L2 costs less than a second one (4096 x 4096: 7.2 us
@@ -575,9 +576,12 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
 // a step publishes the next step's data and frees the slot that has just been read.
 // LDS rows are 128 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7), so
 // 16 lanes that read one chunk of 16 rows touch all 64 banks once.
-// The way into LDS is what the tiles wait for: a KB of it takes a CU some 66 cycles in
-// pieces of 64 bytes and 45 in whole lines of 128 (2048 x 28672 -> 8192: 405 us
-// and 356; wider pieces of a row are no faster), whatever the depth of the ring.
+// The way into LDS is what the tiles wait for beside the products: a KB of it takes a CU
+// some 66 cycles in pieces of 64 bytes and 45 in whole lines of 128 (2048 x 28672 ->
+// 8192: 405 us and 356; wider pieces of a row are no faster), whatever the depth of
+// the ring; with nothing else to do 33, through registers too.  2048 x 28672 -> 8192 with a residual
+// 370 us, 2.6 POP/s, the gated 2048 x 8192 -> 2 x 28672 770 us, 2.5 POP/s (an 8192-cubed library
+// product 2.07), matrix cores busy two thirds of the cycles; 509 x 11008 -> 4096 36 us.
 constexpr int kTStep = 128;
 
 #define GPTQ_VMCNT(n) (((n) & 15) | (((n) >> 4) << 14) | 0x0F70)

