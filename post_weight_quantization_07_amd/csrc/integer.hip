@@ -202,7 +202,7 @@ GPTQ_DEV float gelu(float z) {
   q = fmaf(q, t, 1.4427276849746704f);
   q = fmaf(q, t, -2.8257482051849365f);
   const float below = a * (t * __builtin_amdgcn_exp2f(fmaf(-0.7213475204444817f * a, a, q)));  // a Phi(-a)
-  return z < 0.f ? -below : z - below;
+  return z < 0.f ? -below : z - fminf(below, 1.f);  // (it is less than 0.18; at infinity inf 0, and infinity is kept)
 }
 GPTQ_DEV float activate(float z, int act) {
   switch (act) {

@@ -165,6 +165,26 @@ def test_activations(G, act):
 
 
 @pytest.mark.parametrize("m", [1, 20, 500])
+def test_infinite_values(G, m):
+    """A channel whose value passes fp32, or whose bias is infinite: infinity through every activation, and relu's 0 below."""
+    banner(f"infinite values, {m} tokens")
+    layer = Layer(90, 64, 3, False, True)
+    t = dict(layer.dict)
+    t["bias"] = layer.dict["bias"].clone()
+    t["bias"][7], t["bias"][8] = float("inf"), float("-inf")
+    x = _x(m, 64, "f32", 1)
+    for act in ACTS:
+        y = G.gptq_integer_matmul(x, t["w"], t["scales"], bias=t["bias"], activation=act)
+        assert (y[:, 7] == float("inf")).all()
+        if act is None:
+            assert (y[:, 8] == float("-inf")).all()
+        if act == "relu":
+            assert (y[:, 8] == 0).all()
+        keep = torch.tensor([i not in (7, 8) for i in range(90)], device=dev())
+        assert torch.equal(y[:, keep], G.gptq_integer_matmul(x, t["w"], t["scales"], bias=layer.dict["bias"], activation=act)[:, keep])
+
+
+@pytest.mark.parametrize("m", [1, 20, 500])
 def test_not_finite_stays_in_its_row(G, m):
     """A token with a NaN or an infinity, and a residual with one: NaN there, through relu too."""
     banner(f"not finite, {m} tokens")
