@@ -276,14 +276,19 @@ GPTQ_DEV void gated_finish(const IntParams& p, const Epilogue<kGated>& e, int64_
 // every CU a workgroup all the same (16 tokens through 28672 x 8192: 67 us with
 // R = 1, 63 with R = 4, 49 with x not read at all).
 // 16 tokens: 11008 x 4096 15.1 us (a kernel that only reads those 45 MB takes
-// 12 to 15), 8192 x 28672 57 us, 4.1 TB/s; one token through both layers of a gated 11008 x 4096
-// 22.6 us with its activation, 4.0 TB/s.
+// 12 to 15), 8192 x 28672 57 us, 4.1 TB/s.
 // FUSED (one to four tokens): x is quantized here, by every workgroup for
 // itself and into LDS, while its first weights are on their way: one launch, and
-// reading the tokens again from L2 costs less than a second one (4096 x 4096: 7.2 us
-// against 6.5 + 4.2).
+// reading the tokens again from L2 costs less than a second one.  bf16 tokens are loaded
+// before those weights, since loads come back in their order (11008 -> 4096, one token:
+// 15.9 us against 17.3; two layers 8192 -> 28672, gated: 88 against 95; fp32 ones, twice
+// the registers, 5% slower so).
+// ONCE (FUSED, up to kOnceElems values): one turn has all of K, so no next weights are held, and
+// three workgroups run on a CU instead of two (one token in a replayed graph, 4096 -> 4096 6.3 us, 7.1
+// without; -> 11008 12.3 and 15.8, through two such layers, gated, 19.3 and 25.5).
 constexpr int kSW = 8;                // waves
 constexpr int kFusedElems = 16384;    // tokens * d_in at most
+constexpr int kOnceElems = 4096;      // tokens * d_in of ONCE at most, a turn of R = 1
 
 // kGated: a block of 16 weight rows is eight channels of the gate and the same eight
 // of the second layer, so that both weights stream through one loop.
@@ -296,10 +301,12 @@ GPTQ_DEV const int8_t* block_row<kGated>(const IntParams& p, const Epilogue<kGat
   return (c < 8 ? p.w : e.w) + min(block * 8 + (c & 7), p.d_out - 1) * p.d_in;
 }
 
-template <int R, int MT, int FUSED, int E>  // FUSED: 0 codes given, 1 bf16, 2 fp32
-__global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p, Epilogue<E> ep) {
+template <int R, int MT, int FUSED, bool ONCE, int E>  // FUSED: 0 codes given, 1 bf16, 2 fp32
+__global__ __launch_bounds__(64 * kSW, ONCE ? 6 : 2) void integer_stream_kernel(IntParams p, Epilogue<E> ep) {
   constexpr int kU = R == 1 && MT == 1 ? 8 : R == 4 || MT == 4 ? 2 : 4;
   constexpr int kTurn = kSW * 64 * kU;
+  static_assert(!ONCE || kTurn >= kOnceElems, "one turn has all of K");
+  constexpr int kElems = ONCE ? kOnceElems : kFusedElems;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int64_t block0 = static_cast<int64_t>(blockIdx.x) * R;
@@ -319,9 +326,9 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
     }
   };
   i32x4_t b[kU][R];
-  load_w(wave * 64 * kU, b);
+  if (FUSED != 1) load_w(wave * 64 * kU, b);
 
-  __shared__ __attribute__((aligned(16))) int8_t xl[FUSED ? kFusedElems : 16];
+  __shared__ __attribute__((aligned(16))) int8_t xl[FUSED ? kElems : 16];
   __shared__ float xs[4];
   __shared__ int xsum[4];
   if (FUSED) {
@@ -330,7 +337,7 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
     // (integers: any order gives the same; four tokens of 4096 one behind the other 33 us
     // a call, at once 30; but one token by atomics 26 instead of 25).
     constexpr bool kBf16 = FUSED == 1;
-    constexpr int kQ = kFusedElems / 8 / (64 * kSW);
+    constexpr int kQ = kElems / 8 / (64 * kSW);
     __shared__ uint32_t most[4], wave_most[kSW];
     __shared__ int wave_sum[kSW];
     const bool one = p.m == 1;
@@ -352,6 +359,10 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[q][i] = e < all ? load1<kBf16>(p.xraw, at + i) : 0.f;
       }
+    }
+    if (kBf16) {
+      load_w(wave * 64 * kU, b);
+      asm volatile("" ::: "memory");  // (not before x's loads, which come back in their order)
     }
     uint32_t am1 = 0u;
     if (one) {
@@ -432,13 +443,14 @@ __global__ __launch_bounds__(64 * kSW, 2) void integer_stream_kernel(IntParams p
         else a[u][i] = in ? *reinterpret_cast<const i32x4_t*>(xrow[i] + k) : zero;
       }
     }
-    load_w(k0 + kTurn, next);
+    if (!ONCE) load_w(k0 + kTurn, next);
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
       for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u][i], b[u][j], acc[j][i], 0, 0, 0);
+    if (ONCE) break;
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -561,11 +573,18 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
   constexpr int kC = E == kGated ? 8 : 16;
   const dim3 grid(static_cast<unsigned>((p.d_out + kC * R - 1) / (kC * R)));
   const int t = 64 * kSW;
-  if (fused == 1) integer_stream_kernel<R, 1, 1, E><<<grid, t, 0, st>>>(p, ep);
-  else if (fused == 2) integer_stream_kernel<R, 1, 2, E><<<grid, t, 0, st>>>(p, ep);
-  else if (p.m <= 16) integer_stream_kernel<R, 1, 0, E><<<grid, t, 0, st>>>(p, ep);
-  else if (p.m <= 32) integer_stream_kernel<R, 2, 0, E><<<grid, t, 0, st>>>(p, ep);
-  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0, E><<<grid, t, 0, st>>>(p, ep);
+  if constexpr (R == 1) {
+    if (fused && p.m * p.d_in <= kOnceElems) {
+      if (fused == 1) integer_stream_kernel<1, 1, 1, true, E><<<grid, t, 0, st>>>(p, ep);
+      else integer_stream_kernel<1, 1, 2, true, E><<<grid, t, 0, st>>>(p, ep);
+      return;
+    }
+  }
+  if (fused == 1) integer_stream_kernel<R, 1, 1, false, E><<<grid, t, 0, st>>>(p, ep);
+  else if (fused == 2) integer_stream_kernel<R, 1, 2, false, E><<<grid, t, 0, st>>>(p, ep);
+  else if (p.m <= 16) integer_stream_kernel<R, 1, 0, false, E><<<grid, t, 0, st>>>(p, ep);
+  else if (p.m <= 32) integer_stream_kernel<R, 2, 0, false, E><<<grid, t, 0, st>>>(p, ep);
+  else if constexpr (R <= 2) integer_stream_kernel<R, 4, 0, false, E><<<grid, t, 0, st>>>(p, ep);
 }
 
 // Many tokens: 64 WM x 64 WN output tiles on v_mfma_i32_32x32x32_i8, four waves
@@ -1039,9 +1058,11 @@ bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; 
 // One token of few values is quantized by each workgroup, hardly more than its first weights take, and
 // workgroups of one block end more evenly (two layers of 11008 x 4096, gated: 21.6 us against
 // 25.0 with four blocks, of 28672 x 8192: 92 against 115); for two to four tokens that costs more than it gives
-// (four tokens, those layers: 36 and 30).
+// (four tokens, those layers: 36 and 30), unless they are a turn and the blocks few (two tokens of 2048 -> 11008:
+// 7.8 and 10.0 us, -> 32000: 17.7 and 17.6; two of 1024 through two layers of 32000: 28 and 22).
 int stream_rows(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
-  if (m == 1 && fuses(m, d_in) && d_out >= 64ll * n_cu) return 1;
+  if (m == 1 && fuses(m, d_in) && (d_in <= kOnceElems || d_out >= 64ll * n_cu)) return 1;
+  if (m <= 4 && m * d_in <= kOnceElems && d_out < 96ll * n_cu) return 1;
   const int r = d_out >= 64ll * n_cu ? 4 : d_out >= 32ll * n_cu ? 2 : 1;
   return m > 32 ? std::min(r, 2) : r;
 }

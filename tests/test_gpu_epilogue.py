@@ -343,3 +343,20 @@ def test_every_plain_launch(G, m, d_in, rows):
     codes, scales = S.row_codes(host(x), 127)
     t = layer.dict
     near(G.gptq_integer_matmul(x, t["w"], t["scales"], t["offsets"]), *_product64(layer, codes, scales))
+
+
+@pytest.mark.parametrize("m,d_in,d_out", [(1, 4096, 33000), (4, 1024, 700), (3, 1344, 17), (2, 2048, 13000), (2, 2048, 26000),
+                                          (1, 4128, 17), (4, 4096, 90), (3, 4128, 24600)])
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+def test_few_values(G, m, d_in, d_out, xt):
+    """Tokens quantized by the product's workgroups, whole in one turn or not, rows aligned and not."""
+    banner(f"few values {m}x{d_in}->{d_out} x={xt}")
+    gate, up = Layer(d_out, d_in, 1, True, True), Layer(d_out, d_in, 2, False, False)
+    t = gate.dict
+    wide = torch.zeros(m, d_in + 5, dtype=torch.bfloat16 if xt == "bf16" else torch.float32, device=dev())
+    wide[:, 3:3 + d_in] = _x(m, d_in, xt, 7)
+    for x in (wide[:, 3:3 + d_in].contiguous(), wide[:, 3:3 + d_in]):
+        rows = x.contiguous()
+        near(G.gptq_integer_matmul(x, t["w"], t["scales"], t["offsets"], bias=t["bias"], activation="silu"),
+             *linear_ref(rows, gate, "silu", None))
+        near(G.gptq_integer_gated(x, gate.dict, up.dict), *gated_ref(rows, gate, up, "silu"))
