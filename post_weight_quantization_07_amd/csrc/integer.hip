@@ -1082,7 +1082,7 @@ struct IntPlan {
 // one that should take least, by what each costs (us), fitted to the times of all of
 // them over 5 to 2048 tokens and twelve shapes of weights, 1024 x 1024 to 28672 x 8192:
 //   stream  a launch, the weights at 6.9 TB/s (some come from the caches), and past 16
-//           tokens 1 us and 31 ps a token (of its padded block) and k for every round of
+//           tokens 1 us and 31 ps a token (of its padded block) and k for every begun round of
 //           workgroups, which load their tokens' codes beside the weights; up to 16
 //           tokens the round's K alone
 //   tiles   a launch, then the longer of a round's steps and of the bytes at 6.6 TB/s;
@@ -1101,7 +1101,7 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   if (m <= 64) {
     const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, n_cu))), rounds = std::max(1.0, blocks / n_cu);
     if (m <= 16) least = 5.0 + std::max(k * n / 6.9e6, 0.83e-3 * k * rounds);
-    else least = 1.0 + 1.04 * (k * n / 5e6 + rounds * (1.0 + 31e-6 * (m <= 32 ? 32 : 64) * k));
+    else least = 1.0 + 1.04 * (k * n / 5e6 + std::ceil(rounds) * (1.0 + 31e-6 * (m <= 32 ? 32 : 64) * k));
   }
   const int64_t steps = (d_in + kTStep - 1) / kTStep;
   struct Tile {
