@@ -364,7 +364,9 @@ gptq_status gptq_integer_weight(const int32_t* qweight, const int32_t* zeros, in
  *            GPTQ_I8: 16-byte aligned, ldx % 16 == 0, ldx <= 2^22
  *   w        [d_out, d_in] int8, 16-byte aligned; w_scales [d_out] fp32;
  *            w_offsets_or_null [d_out] int32 in [-128, 128]
- *   y        [m, d_out] fp32 or bf16 (yt)
+ *   y        [m, d_out] fp32 or bf16 (yt).  It may not touch x where the product reads x itself
+ *            (codes, or up to 4 tokens of up to 16384 values in all); other tokens are
+ *            read before y is written
  *   ws       device workspace of gptq_integer_workspace_size(m, xt, d_in, d_out)
  *            bytes, 256-byte aligned; may be null when that size is 0
  * Requires d_in % 32 == 0, d_in <= 2^16 (so the sums cannot overflow) and
@@ -401,7 +403,7 @@ typedef struct {
  *   residual_or_null  [m, ldr] bf16 or fp32 (rt), d_out <= ldr <= 2^20.  y may be the residual
  *            itself (same type, ldr = d_out or m = 1) and may not touch it otherwise, nor x
  *   Others, workspace, limits and errors as for gptq_integer_matmul.  With
- *   neither bias, activation nor residual it is that call.
+ *   neither bias, activation nor residual y is what that call gives.
  */
 gptq_status gptq_integer_linear(const void* x, int32_t xt, const float* x_scales, const int32_t* x_sums, int64_t m,
                                 int64_t d_in, int64_t ldx, const gptq_integer_layer* layer, int64_t d_out,

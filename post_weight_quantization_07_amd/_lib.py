@@ -606,7 +606,8 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
     """y [m, d_out] = act(x W^T + bias) + residual in 8-bit integers, W = w_scales
     (w - offsets) as laid out by gptq_integer_weight (offsets None: all zero).  x
     is [m, d_in] bf16 or fp32 (rows may be strided), quantized per token on the
-    way, or what gptq_quantize_tokens or gptq_norm_tokens returned for it.
+    way, or what gptq_quantize_tokens or gptq_norm_tokens returned for it; y may not
+    lie over codes or over up to four tokens.
     bias: fp32 [d_out]; activation: "relu", "gelu", "gelu_tanh" or "silu"; residual:
     [m, d_out] bf16 or fp32 (rows may be strided), which y may be itself.  They
     are applied to the sums in fp32 (gptq_integer_linear of the C ABI)."""

@@ -303,23 +303,38 @@ struct Rows {
   const void* at;
   int64_t lead, width;
 };
-// Whether two of them have a byte in common (with different distances of their rows:
+typedef unsigned __int128 wide_t;  // of addresses: no sum of them wraps
+// Whether one of a's rows has a byte in [lo, hi).
+bool meets(const Rows& a, int64_t m, wide_t lo, wide_t hi) {
+  const wide_t a0 = reinterpret_cast<uintptr_t>(a.at), lead = static_cast<wide_t>(a.lead), width = static_cast<wide_t>(a.width);
+  const wide_t row = lo < a0 + width ? 0 : (lo - a0 - width) / lead + 1;  // the first that ends behind lo
+  return row < static_cast<wide_t>(m) && a0 + row * lead < hi;
+}
+// Whether two of them have a byte in common (of two with gaps between their rows and different distances of them:
 // whether their first and last bytes lie across each other).
 bool overlap(const Rows& a, const Rows& b, int64_t m) {
   if (!a.at || !b.at || m == 0) return false;
+  const auto end = [&](const Rows& r) {
+    return static_cast<wide_t>(reinterpret_cast<uintptr_t>(r.at)) + static_cast<wide_t>(m - 1) * static_cast<wide_t>(r.lead) +
+           static_cast<wide_t>(r.width);
+  };
+  const auto whole = [&](const Rows& r) { return m == 1 || r.lead == r.width; };
+  if (whole(a)) return meets(b, m, reinterpret_cast<uintptr_t>(a.at), end(a));
+  if (whole(b)) return meets(a, m, reinterpret_cast<uintptr_t>(b.at), end(b));
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
-  const uintptr_t lo = a0 < b0 ? a0 : b0, apart = a0 < b0 ? b0 - a0 : a0 - b0;
-  const Rows &first = lo == a0 ? a : b, &second = lo == a0 ? b : a;
-  const uintptr_t span = static_cast<uintptr_t>(m - 1) * static_cast<uintptr_t>(first.lead) + static_cast<uintptr_t>(first.width);
-  if (apart >= span) return false;
-  if (a.lead != b.lead || a.lead == 0) return true;
+  const Rows &first = a0 < b0 ? a : b, &second = a0 < b0 ? b : a;
+  const uintptr_t apart = a0 < b0 ? b0 - a0 : a0 - b0;
+  if (wide_t{reinterpret_cast<uintptr_t>(second.at)} >= end(first)) return false;
+  if (a.lead != b.lead) return true;
   const int64_t off = static_cast<int64_t>(apart % static_cast<uintptr_t>(a.lead));  // inside a row of the first
   return off < first.width || off + second.width > a.lead;
 }
-// Whether y [m, d_out] touches x (every workgroup of a product reads all of its tokens; sizes of a valid call only).
+// Whether y [m, d_out] touches x (sizes of a valid call only; no memory holds rows further apart).
 bool touches_x(const void* y, int32_t yt, int64_t d_out, const void* x, int32_t xt, int64_t ldx, int64_t d_in, int64_t m) {
-  if (d_in < 1 || d_in > ldx || ldx > kMaxLead) return false;
-  return overlap(Rows{y, d_out * size_of(yt), d_out * size_of(yt)}, Rows{x, ldx * size_of(xt), d_in * size_of(xt)}, m);
+  if (d_in < 1 || d_in > ldx || d_out < 1) return false;
+  const int64_t lead = m > 1 ? ldx : d_in;
+  if (lead > int64_t{1} << 40) return false;
+  return overlap(Rows{y, d_out * size_of(yt), d_out * size_of(yt)}, Rows{x, lead * size_of(xt), d_in * size_of(xt)}, m);
 }
 // Out may not touch in, unless it is in itself, element by element.
 bool clobbers(const Rows& out, const Rows& in, bool same_type, int64_t m) {
@@ -342,6 +357,9 @@ gptq_status gptq_integer_matmul(const void* x, int32_t xt, const float* x_scales
   c.layer = gptq::IntLayer{w, w_scales, w_offsets_or_null, nullptr};
   c.d_out = d_out;
   c.y = y;
+  // where every workgroup reads the tokens themselves, one's y would be another's x
+  if (rows_ok(m) && dim_ok(d_out) && gptq::integer_reads_x(m, d_in, xt == GPTQ_I8) && touches_x(y, yt, d_out, x, xt, ldx, d_in, m))
+    return GPTQ_ERR_INVALID_ARG;
   return integer_go(&c, d_out, yt, ws, ws_bytes, stream);
 }
 

@@ -168,6 +168,8 @@ struct IntCall {
   bool res_bf16, y_bf16;
   void* y;
 };
+// whether the product's own kernel reads x (not only the codes' kernel before it)
+bool integer_reads_x(int64_t m, int64_t d_in, bool codes_given);
 // workspace: integer_matmul_workspace of the rows of both layers
 hipError_t integer_launch(const IntCall& c, void* ws, int n_cu, hipStream_t stream);
 

@@ -1185,6 +1185,8 @@ size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool cod
   return codes_given || fuses(m, d_in) ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
 }
 
+bool integer_reads_x(int64_t m, int64_t d_in, bool codes_given) { return codes_given || fuses(m, d_in); }
+
 namespace {
 // The launches of a product whose x, layer and y stand in p (x in codes, or
 // FUSED: raw); rows: of all weights that it reads.
