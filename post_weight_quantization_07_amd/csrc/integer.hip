@@ -310,9 +310,10 @@ __global__ __launch_bounds__(64 * kSW, ONCE ? 6 : 2) void integer_stream_kernel(
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
   const int64_t block0 = static_cast<int64_t>(blockIdx.x) * R;
-  // 0; but taken from the grid it has the compiler wait for the first weights before it asks for the others,
-  // which then arrive earlier (16 tokens' codes through 11008 x 4096 16.3 us against 17.1, 8192 x 28672 51.2
-  // against 52.4; where one round of loads is all, 4096 x 4096, 0.2 us later).
+  // Block of tokens (64 of them where there are more).  Taken from the grid for fewer too: the compiler then waits
+  // for the first weights before it asks for the others, which arrive earlier so (16 tokens' codes through
+  // 11008 x 4096 16.3 us against 17.1, 8192 x 28672 51.2 against 52.4; where one round of loads is all, 4096 x
+  // 4096, 0.2 us later).
   const int64_t t0 = static_cast<int64_t>(blockIdx.y) * 16 * MT;
   const int8_t* wrow[R];
 #pragma unroll
@@ -471,7 +472,7 @@ __global__ __launch_bounds__(64 * kSW, ONCE ? 6 : 2) void integer_stream_kernel(
   constexpr int kC = E == kGated ? 8 : 16;  // channels of a block
   for (int e = threadIdx.x; e < R * MT * 16 * kC; e += 64 * kSW) {
     const int tc = e % kC, j = (e / kC) % R, tr = (e / (kC * R)) & 15, i = e / (16 * kC * R);
-    const int64_t col = (block0 + j) * kC + tc, row = 16 * i + tr;
+    const int64_t col = (block0 + j) * kC + tc, row = t0 + 16 * i + tr;
     if (col >= p.d_out || row >= p.m) continue;
     const int off = p.w_offsets ? p.w_offsets[col] : 0;
     const float sx = FUSED ? xs[tr & 3] : p.x_scales[row], sw = p.w_scales[col];
@@ -575,7 +576,7 @@ __global__ __launch_bounds__(64 * kRW, 4) void integer_resident_kernel(IntParams
 template <int R, int E>
 void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t st) {
   constexpr int kC = E == kGated ? 8 : 16;
-  const dim3 grid(static_cast<unsigned>((p.d_out + kC * R - 1) / (kC * R)));
+  const dim3 grid(static_cast<unsigned>((p.d_out + kC * R - 1) / (kC * R)), static_cast<unsigned>((p.m + 63) / 64));
   const int t = 64 * kSW;
   if constexpr (R == 1) {
     if (fused && p.m * p.d_in <= kOnceElems) {
@@ -1078,7 +1079,8 @@ struct IntPlan {
   size_t partial_bytes;
 };
 
-// Of the stream kernel (up to 64 tokens) and the tiles, in 1 to 16 slices of K, the
+// Of the stream kernel (up to 1024 tokens, in blocks of 64: 128 x 1024 -> 1024 5.4 us, 6.7 in tiles; 256 x 768
+// -> 768 4.9 and 6.8) and the tiles, in 1 to 16 slices of K, the
 // one that should take least, by what each costs (us), fitted to the times of all of
 // them over 5 to 2048 tokens and twelve shapes of weights, 1024 x 1024 to 28672 x 8192:
 //   stream  a launch, the weights at 6.9 TB/s (some come from the caches), and past 16
@@ -1098,8 +1100,9 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   if (fuses(m, d_in)) return a;
   const double k = static_cast<double>(d_in), n = static_cast<double>(d_out), rows = static_cast<double>(m);
   double least = 1e300;
-  if (m <= 64) {
-    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, n_cu))), rounds = std::max(1.0, blocks / n_cu);
+  if (m <= 1024) {
+    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, n_cu))) * static_cast<double>((m + 63) / 64);
+    const double rounds = std::max(1.0, blocks / n_cu);
     if (m <= 16) least = 5.0 + std::max(k * n / 6.9e6, 0.83e-3 * k * rounds);
     else least = 1.0 + 1.04 * (k * n / 5e6 + std::ceil(rounds) * (1.0 + 31e-6 * (m <= 32 ? 32 : 64) * k));
   }
