@@ -1059,16 +1059,33 @@ __global__ __launch_bounds__(256) void integer_join_kernel(IntParams p, TileGrid
 // few tokens of few values: quantized by every workgroup of the stream kernel itself
 bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; }
 
-// row blocks a workgroup of the stream kernel takes: as many as leave every CU one.
-// One token of few values is quantized by each workgroup, hardly more than its first weights take, and
-// workgroups of one block end more evenly (two layers of 11008 x 4096, gated: 21.6 us against
-// 25.0 with four blocks, of 28672 x 8192: 92 against 115); for two to four tokens that costs more than it gives
-// (four tokens, those layers: 36 and 30), unless they are a turn and the blocks few (two tokens of 2048 -> 11008:
-// 7.8 and 10.0 us, -> 32000: 17.7 and 17.6; two of 1024 through two layers of 32000: 28 and 22).
-int stream_rows(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
-  if (m == 1 && fuses(m, d_in) && (d_in <= kOnceElems || d_out >= 64ll * n_cu)) return 1;
-  if (m <= 4 && m * d_in <= kOnceElems && d_out < 96ll * n_cu) return 1;
-  const int r = d_out >= 64ll * n_cu ? 4 : d_out >= 32ll * n_cu ? 2 : 1;
+// Row blocks a workgroup of the stream kernel takes: as many as leave every CU one, where the tokens are
+// given in codes (us of one token's codes with 1, 2 and 4: 1024 -> 11008 5.9, 5.2, 5.3; 2048 -> 32000 19.3, 17.2,
+// 17.7; but up to four tokens 4096 -> 11008 13.5, 14.7, 16.1, 5120 -> 13824 19.3, 19.8, 20.9).
+// Tokens quantized by each workgroup for itself (fused) are read and rounded once a block more in blocks of one,
+// hardly longer than its first weights take, and those end more evenly.
+//   one token  a round of the workgroups of ONCE, three a CU, has 48 blocks of rows a CU: up to there one block
+//              (2048 -> 11008 8.1, 10.3, 10.5; 256 -> 8192 5.1, 5.7, 5.6).  Past it short rows are mostly their
+//              quantization (512 -> 32000 11.0, 10.4, 7.1; 1024 -> 16384 8.6, 7.4, 7.8), longer ones as
+//              long as two rounds do (1536 -> 24576 12.9, 12.7, 13.6; -> 64000 27.8, 26.1, 24.1), from 2560
+//              values on one block again (3200 -> 24576 18.5, 22, 22.2; 14336 -> 20480 56, 63, 81), but for rows
+//              past 4096 values that are not many (6144 -> 13824 23, 22, 24).  Gated, whose blocks end with two
+//              products for one, from 2048 (2048 -> 2 x 16000 17.7, 19.0, 19.4; 1024 -> 2 x 16000 14.7, 13.8, 12.3)
+//   two to four  that costs more than it gives (four tokens of 4096 -> 2 x 11008 36 and 30 with one and
+//              four), unless they are a turn and the blocks few (two of 2048 -> 11008 7.8 and 10.0;
+//              -> 32000 17.7 and 17.6; two of 512 -> 16384 7.7 and 6.2)
+int stream_rows(int64_t m, int64_t d_in, int64_t d_out, bool fused, bool gated, int n_cu) {
+  const int64_t a_cu = d_out / n_cu;  // rows of a CU
+  const int r = a_cu >= 64 ? 4 : a_cu >= 32 ? 2 : 1;
+  if (fused && m == 1) {
+    if (d_out <= 48ll * n_cu) return 1;
+    if (d_in <= (gated ? 512 : 1024) || (d_in < (gated ? 2048 : 2560) && d_out > 96ll * n_cu)) return 4;
+    if (d_in <= kOnceElems || a_cu >= 64) return 1;
+  } else if (fused) {
+    if (m * d_in <= kOnceElems && d_out < (m * d_in <= 1024 ? 48ll : 96ll) * n_cu) return 1;
+  } else if (m <= 4 && d_in >= 4096 && d_in < 8192 && a_cu < 64) {
+    return 1;
+  }
   return m > 32 ? std::min(r, 2) : r;
 }
 
@@ -1101,7 +1118,7 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   const double k = static_cast<double>(d_in), n = static_cast<double>(d_out), rows = static_cast<double>(m);
   double least = 1e300;
   if (m <= 1024) {
-    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, n_cu))) * static_cast<double>((m + 63) / 64);
+    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, false, false, n_cu))) * static_cast<double>((m + 63) / 64);
     const double rounds = std::max(1.0, blocks / n_cu);
     if (m <= 16) least = 5.0 + std::max(k * n / 6.9e6, 0.83e-3 * k * rounds);
     else least = 1.0 + 1.04 * (k * n / 5e6 + std::ceil(rounds) * (1.0 + 31e-6 * (m <= 32 ? 32 : 64) * k));
@@ -1206,7 +1223,7 @@ hipError_t product_go(const IntParams& p, const IntPlan& plan, const Epilogue<E>
                                    static_cast<size_t>(p.m * (p.d_in + 16)), st>>>(p, ep);
       return hipGetLastError();
     }
-    const int r = stream_rows(p.m, p.d_in, rows, n_cu);
+    const int r = stream_rows(p.m, p.d_in, rows, f != 0, E == kGated, n_cu);
     if (r == 4) stream_go<4, E>(p, ep, f, st);
     else if (r == 2) stream_go<2, E>(p, ep, f, st);
     else stream_go<1, E>(p, ep, f, st);
