@@ -301,7 +301,7 @@ GPTQ_DEV const int8_t* block_row<kGated>(const IntParams& p, const Epilogue<kGat
   return (c < 8 ? p.w : e.w) + min(block * 8 + (c & 7), p.d_out - 1) * p.d_in;
 }
 
-template <int R, int MT, int FUSED, bool ONCE, int E>  // FUSED: 0 codes given, 1 bf16, 2 fp32
+template <int R, int MT, int FUSED, bool ONCE, int E>  // FUSED: 0 codes given, 1 bf16, 2 fp32, 3 bf16 after the weights
 __global__ __launch_bounds__(64 * kSW, ONCE ? 6 : 2) void integer_stream_kernel(IntParams p, Epilogue<E> ep) {
   constexpr int kU = R == 1 && MT == 1 ? 8 : R == 4 || MT == 4 ? 2 : 4;
   constexpr int kTurn = kSW * 64 * kU;
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(64 * kSW, ONCE ? 6 : 2) void integer_stream_kernel(
     // sums, meet in LDS, those of a single token one a wave, of several by atomics
     // (integers: any order gives the same; four tokens of 4096 one behind the other 33 us
     // a call, at once 30; but one token by atomics 26 instead of 25).
-    constexpr bool kBf16 = FUSED == 1;
+    constexpr bool kBf16 = FUSED != 2;
     constexpr int kQ = kElems / 8 / (64 * kSW);
     __shared__ uint32_t most[4], wave_most[kSW];
     __shared__ int wave_sum[kSW];
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(64 * kSW, ONCE ? 6 : 2) void integer_stream_kernel(
         for (int i = 0; i < 8; ++i) v[q][i] = e < all ? load1<kBf16>(p.xraw, at + i) : 0.f;
       }
     }
-    if (kBf16) {
+    if (FUSED == 1) {
       load_w(wave * 64 * kU, b);
       asm volatile("" ::: "memory");  // (not before x's loads, which come back in their order)
     }
@@ -582,6 +582,14 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
     if (fused && p.m * p.d_in <= kOnceElems) {
       if (fused == 1) integer_stream_kernel<1, 1, 1, true, E><<<grid, t, 0, st>>>(p, ep);
       else integer_stream_kernel<1, 1, 2, true, E><<<grid, t, 0, st>>>(p, ep);
+      return;
+    }
+  }
+  if constexpr (R == 2) {
+    // One token's blocks of two, past ONCE: the weights first (5120 -> 13824 19.2 us, 20.2 with the token first, 4128
+    // -> 13824 16.8 and 19.1; but 8192 -> 13824 28.7 and 28.5, 14336 -> 13824 44.1 and 42.0, two tokens of 5120 21.0 and 20.0).
+    if (fused == 1 && p.m == 1 && p.d_in < 8192) {
+      integer_stream_kernel<2, 1, 3, false, E><<<grid, t, 0, st>>>(p, ep);
       return;
     }
   }
@@ -1061,7 +1069,8 @@ bool fuses(int64_t m, int64_t d_in) { return m <= 4 && m * d_in <= kFusedElems; 
 
 // Row blocks a workgroup of the stream kernel takes: as many as leave every CU one, where the tokens are
 // given in codes (us of one token's codes with 1, 2 and 4: 1024 -> 11008 5.9, 5.2, 5.3; 2048 -> 32000 19.3, 17.2,
-// 17.7; but up to four tokens 4096 -> 11008 13.5, 14.7, 16.1, 5120 -> 13824 19.3, 19.8, 20.9).
+// 17.7; but up to four tokens 4096 -> 11008 13.5, 14.7, 16.1, 5120 -> 13824 19.3, 19.8, 20.9; 7168 -> 14336 23.2,
+// 22.1).
 // Tokens quantized by each workgroup for itself (fused) are read and rounded once a block more in blocks of one,
 // hardly longer than its first weights take, and those end more evenly.
 //   one token  a round of the workgroups of ONCE, three a CU, has 48 blocks of rows a CU: up to there one block
@@ -1083,7 +1092,7 @@ int stream_rows(int64_t m, int64_t d_in, int64_t d_out, bool fused, bool gated, 
     if (d_in <= kOnceElems || a_cu >= 64) return 1;
   } else if (fused) {
     if (m * d_in <= kOnceElems && d_out < (m * d_in <= 1024 ? 48ll : 96ll) * n_cu) return 1;
-  } else if (m <= 4 && d_in >= 4096 && d_in < 8192 && a_cu < 64) {
+  } else if (m <= 4 && d_in >= 4096 && d_in < 6144 && a_cu < 64) {
     return 1;
   }
   return m > 32 ? std::min(r, 2) : r;

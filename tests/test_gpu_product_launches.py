@@ -65,7 +65,8 @@ def test_blocks_of_tokens(G, m, d_in, rows, gated):
 
 # row blocks of one, two and four for few tokens, quantized on the way and given in codes, on both sides of each limit
 FEW = [(1, 256, 12288), (1, 256, 12300), (1, 1024, 16390), (1, 1056, 24576), (1, 1056, 24600), (1, 2560, 24600), (1, 4128, 12300),
-       (1, 4128, 16400), (1, 4096, 8200), (2, 512, 12400), (2, 544, 12400), (2, 544, 24600), (4, 4096, 8200), (3, 4128, 16400)]
+       (1, 4128, 16400), (1, 4096, 8200), (2, 512, 12400), (2, 544, 12400), (2, 544, 24600), (4, 4096, 8200), (3, 4128, 16400),
+       (1, 8192, 12300), (3, 4128, 8200)]
 
 
 @pytest.mark.parametrize("m,d_in,rows", FEW)
