@@ -1105,32 +1105,33 @@ struct IntPlan {
   size_t partial_bytes;
 };
 
-// Of the stream kernel (up to 1024 tokens, in blocks of 64: 128 x 1024 -> 1024 5.4 us, 6.7 in tiles; 256 x 768
-// -> 768 4.9 and 6.8) and the tiles, in 1 to 16 slices of K, the
-// one that should take least, by what each costs (us), fitted to the times of all of
-// them over 5 to 2048 tokens and twelve shapes of weights, 1024 x 1024 to 28672 x 8192:
-//   stream  a launch, the weights at 6.9 TB/s (some come from the caches), and past 16
-//           tokens 1 us and 31 ps a token (of its padded block) and k for every begun round of
-//           workgroups, which load their tokens' codes beside the weights; up to 16
-//           tokens the round's K alone
-//   tiles   a launch, then the longer of a round's steps and of the bytes at 6.6 TB/s;
-//           K slices cost a second launch and their sums' way to memory and back
-// The choice is 2% slower than the best of them in the mean.  (us, stream and 64-row,
-// 128-row, 256-row tiles in their best slices: 17 x 4096 -> 4096 10.2, 14.2, 14.4, 22;
-// 64 x 4096 -> 11008 28.8, 16.5, 20.4, -; 64 x 28672 -> 8192 94, 48, 51, -;
-// 512 x 4096 -> 4096 -, 17.4, 25.9, 29.8; 2048 x 4096 -> 1024 -, 13.5, 23.5, 28;
-// 2048 x 4096 -> 4096 -, 63, 39.9, 53;
+// Of the stream kernel (up to 1024 tokens) and the tiles, in 1 to 16 slices of K, the one that should take
+// least, by what each costs (us), fitted to the times of all of them over 5 to 4096 tokens and twenty shapes of
+// weights, 256 x 4096 to 28672 x 8192, codes given, in replayed graphs.  For k values a token, n rows of weights:
+//   stream, up to 16 tokens   kStreamLaunch and the longer of the weights at 6.9 TB/s (some come from the caches)
+//           and of the rounds' K
+//   stream, more tokens       kBlockLaunch, the weights at 3.8 TB/s and for every begun round of workgroups
+//           kBlockRound and 38 ps a token (up to 64) and k: a workgroup loads its tokens' codes beside the weights
+//   tiles   kTileLaunch, then the longer of the rounds' steps and of the bytes at 6.6 TB/s; K slices cost a
+//           second launch and their sums' way to memory and back
+// The choice is 1.5% slower than the best of them in the mean.  (us, stream and 64-row, 128-row, 256-row tiles in
+// their best slices: 17 x 4096 -> 4096 8.3, 10.9, 13.6, -; 64 x 4096 -> 11008 28.9, 17.3, 19.7, -;
+// 64 x 28672 -> 8192 93, 48, 55, -; 128 x 1024 -> 1024 5.4, 6.6, 8.4, -; 512 x 4096 -> 4096 -, 17.4, 25.9, 29.8;
+// 2048 x 4096 -> 1024 -, 13.5, 23.5, 28; 2048 x 4096 -> 4096 -, 63, 39.9, 53;
 // 1024 x 8192 -> 8192 -, 115, 77, 81; 2048 x 8192 -> 8192 -, 222, 143, 114.)
+constexpr double kStreamLaunch = 5.0, kStreamRate = 6.9e6, kStreamTurn = 0.7e-3;   // us, bytes a us, us a k
+constexpr double kBlockLaunch = 1.0, kBlockRate = 3.8e6, kBlockRound = 1.4, kBlockToken = 38e-6;
+constexpr double kTileLaunch = 4.5, kTileRate = 6.6e6, kJoinLaunch = 5.0, kJoinRate = 4.3e6;
 IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   IntPlan a{0, 1, 0, 0};
   if (fuses(m, d_in)) return a;
   const double k = static_cast<double>(d_in), n = static_cast<double>(d_out), rows = static_cast<double>(m);
   double least = 1e300;
   if (m <= 1024) {
-    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, false, false, n_cu))) * static_cast<double>((m + 63) / 64);
+    const double blocks = std::ceil(n / (16.0 * stream_rows(m, d_in, d_out, false, false, n_cu))) * std::ceil(rows / 64.0);
     const double rounds = std::max(1.0, blocks / n_cu);
-    if (m <= 16) least = 5.0 + std::max(k * n / 6.9e6, 0.83e-3 * k * rounds);
-    else least = 1.0 + 1.04 * (k * n / 5e6 + std::ceil(rounds) * (1.0 + 31e-6 * (m <= 32 ? 32 : 64) * k));
+    if (m <= 16) least = kStreamLaunch + std::max(k * n / kStreamRate, kStreamTurn * k * rounds);
+    else least = kBlockLaunch + k * n / kBlockRate + std::ceil(rounds) * (kBlockRound + kBlockToken * std::min(rows, 64.0) * k);
   }
   const int64_t steps = (d_in + kTStep - 1) / kTStep;
   struct Tile {
@@ -1140,7 +1141,7 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
   constexpr Tile tiles[3] = {{3, 64, 128, 0.44, 0.44}, {1, 128, 128, 0.84, 1.05}, {2, 256, 256, 1.34, 1.34}};
   for (const Tile& t : tiles) {
     // Many tokens of long rows leave the L2s between their strips of 64 (2048 x 11008 -> 2048: 77 us, 62 in slices
-    // of 256-row tiles; 1500 x 8224 -> 1800: 67 and 50, though 1030 of them 39 and 42).
+    // of 256-row tiles; 1500 x 8224 -> 1800: 67 and 50, though 1030 of them 39 and 42): outside the fitted terms.
     if (t.kind == 3 && m > 1024 && d_in > 8192) continue;
     const int64_t count = ((m + t.high - 1) / t.high) * ((d_out + t.wide - 1) / t.wide);
     for (int64_t sl = 1; sl <= 16 && (sl == 1 || steps / sl >= 4); sl *= 2) {
@@ -1148,8 +1149,8 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
       const int64_t room = t.kind == 1 ? 2 * n_cu : n_cu, whole = count * slices / room, rest = count * slices % room;
       const double last = rest == 0 ? 0.0 : rest <= n_cu ? t.step : t.full;
       const double work = static_cast<double>(per) * (static_cast<double>(whole) * t.full + last);
-      double cost = 4.9 + std::max(work, k * (n + rows) / 6.6e6);
-      if (slices > 1) cost += 5.0 + 8.0 * static_cast<double>(slices) * rows * n / 4.3e6;
+      double cost = kTileLaunch + std::max(work, k * (n + rows) / kTileRate);
+      if (slices > 1) cost += kJoinLaunch + 8.0 * static_cast<double>(slices) * rows * n / kJoinRate;
       if (cost < least) {
         least = cost;
         a.kind = t.kind;

@@ -73,3 +73,13 @@ FEW = [(1, 256, 12288), (1, 256, 12300), (1, 1024, 16390), (1, 1056, 24576), (1,
 @pytest.mark.parametrize("gated", [False, True])
 def test_row_blocks(G, m, d_in, rows, gated):
     check(G, m, d_in, rows, gated)
+
+
+# sizes whose kernel the estimate chooses by few per cent: streamed, in tiles, in K slices of them
+CLOSE = [(8, 11008, 2048), (17, 4096, 6150), (33, 4096, 4100), (40, 4096, 4096), (100, 4128, 1030), (300, 1024, 4100), (17, 10016, 4100)]
+
+
+@pytest.mark.parametrize("m,d_in,rows", CLOSE)
+@pytest.mark.parametrize("gated", [False, True])
+def test_close_choices(G, m, d_in, rows, gated):
+    check(G, m, d_in, rows, gated, "gelu_tanh")
