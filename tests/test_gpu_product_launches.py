@@ -83,3 +83,17 @@ CLOSE = [(8, 11008, 2048), (17, 4096, 6150), (33, 4096, 4100), (40, 4096, 4096),
 @pytest.mark.parametrize("gated", [False, True])
 def test_close_choices(G, m, d_in, rows, gated):
     check(G, m, d_in, rows, gated, "gelu_tanh")
+
+
+# Tiles without K slices whose ring of LDS slots turns several times: 128 x 128 (two slots) in 4 to 17 steps, 256 x 256 (two) in 6
+# to 16, 64 x 128 (four) in 9 to 17, whole numbers of turns and broken ones, with edges inside a tile
+PASSES = [(1100, 1024, 4100), (777, 1056, 8200), (1100, 512, 2200), (700, 2080, 4170),
+          (2100, 768, 4200), (2050, 1056, 8200), (4100, 2048, 2100),
+          (600, 1568, 2070), (300, 2080, 2100), (100, 1056, 8200)]
+
+
+@pytest.mark.parametrize("m,d_in,rows", PASSES)
+@pytest.mark.parametrize("gated", [False, True])
+def test_passes(G, m, d_in, rows, gated):
+    assert G.gptq_integer_workspace_size(m, torch.int8, d_in, rows) == 0   # codes given: room for K slices only
+    check(G, m, d_in, rows, gated, ("relu", "gelu", "gelu_tanh", "silu")[(m + rows) % 4])
