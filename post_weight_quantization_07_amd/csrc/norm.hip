@@ -132,6 +132,28 @@ GPTQ_DEV double wave_sum(double v) {
   return v;
 }
 
+// A row's factor s = 1 / sqrt(mean h^2 + eps), in two: below fp32's normal range (rows past 2^126) it would keep
+// fewer bits, so that it is held times 2^64 there, and what it multiplies times 2^-64 first (exact, or of a product
+// that vanishes).
+struct RowFactor {
+  float s, first;
+};
+GPTQ_DEV RowFactor row_factor(double mean_and_eps) {
+  const double s = rsqrt(mean_and_eps);
+  const bool small = s < 0x1p-126;
+  return {static_cast<float>(small ? s * 0x1p64 : s), small ? 0x1p-64f : 1.0f};
+}
+GPTQ_DEV float row_times(const RowFactor& f, float u) { return u * f.first * f.s; }
+// eight of them, the first factor only where it is one
+GPTQ_DEV void row_times(const RowFactor& f, float (&u)[8]) {
+  if (f.first != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] *= f.first;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] *= f.s;
+}
+
 // T threads per row (T = 64: four rows a workgroup), up to 8 CH T values of it in
 // registers between the sum and the store.  A workgroup walks over rows: the weight
 // is loaded once, and with AHEAD the next row's loads go out before this row's
@@ -205,9 +227,9 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormParams p) {
         p.sums[before] = all;
       }
     }
-    const float rstd = static_cast<float>(rsqrt(fma(ss, p.inv_d, p.eps)));
+    const RowFactor factor = row_factor(fma(ss, p.inv_d, p.eps));
     RowScale rs = row_scale(am, 127.f);
-    if (am < 0x7F800000u) rs.scale = __fdiv_rn(__uint_as_float(am) * rstd, 127.f);
+    if (am < 0x7F800000u) rs.scale = __fdiv_rn(row_times(factor, __uint_as_float(am)), 127.f);
     int sum = 0;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -218,8 +240,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void norm_kernel(NormParams p) {
       if (RES && p.sum) row_store<TAIL>(RES == 1, static_cast<char*>(p.sum) + (row * p.lds + e) * kR, left, h[c]);
       if (p.codes) sum += code_store<TAIL>(p.codes + row * p.d + e, left, u, rs);
       if (p.y) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] *= rstd;
+        row_times(factor, u);
         row_store<TAIL>(p.y_bf16 != 0, static_cast<char*>(p.y) + (row * p.d + e) * (p.y_bf16 ? 2 : 4), left, u);
       }
     }
@@ -288,9 +309,9 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(NormParams p) {
     ss += red[v];
     am = max(am, redmax[v]);
   }
-  const float rstd = static_cast<float>(rsqrt(fma(ss, p.inv_d, p.eps)));
+  const RowFactor factor = row_factor(fma(ss, p.inv_d, p.eps));
   RowScale rs = row_scale(am, 127.f);
-  if (am < 0x7F800000u) rs.scale = __fdiv_rn(__uint_as_float(am) * rstd, 127.f);
+  if (am < 0x7F800000u) rs.scale = __fdiv_rn(row_times(factor, __uint_as_float(am)), 127.f);
   int sum = 0;
   for (int64_t e = static_cast<int64_t>(threadIdx.x) * 8; e < p.d; e += kLongT * 8) {
     load(e, h, w);
@@ -299,8 +320,7 @@ __global__ __launch_bounds__(kLongT) void norm_long_kernel(NormParams p) {
     for (int i = 0; i < 8; ++i) h[i] *= w[i];
     if (p.codes) sum += code_store<TAIL>(p.codes + row * p.d + e, p.d - e, h, rs);
     if (p.y) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[i] *= rstd;
+      row_times(factor, h);
       row_store<TAIL>(p.y_bf16 != 0, static_cast<char*>(p.y) + (row * p.d + e) * (p.y_bf16 ? 2 : 4), p.d - e, h);
     }
   }
