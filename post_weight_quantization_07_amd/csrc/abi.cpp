@@ -329,6 +329,12 @@ bool overlap(const Rows& a, const Rows& b, int64_t m) {
   const int64_t off = static_cast<int64_t>(apart % static_cast<uintptr_t>(a.lead));  // inside a row of the first
   return off < first.width || off + second.width > a.lead;
 }
+// Whether one of a's rows touches a single row.
+bool on_row(const Rows& a, const Rows& row, int64_t m) {
+  if (!a.at || !row.at || m == 0) return false;
+  const wide_t at = reinterpret_cast<uintptr_t>(row.at);
+  return meets(a, m, at, at + static_cast<wide_t>(row.width));
+}
 // Whether y [m, d_out] touches x (sizes of a valid call only; no memory holds rows further apart).
 bool touches_x(const void* y, int32_t yt, int64_t d_out, const void* x, int32_t xt, int64_t ldx, int64_t d_in, int64_t m) {
   if (d_in < 1 || d_in > ldx || d_out < 1) return false;
@@ -434,9 +440,17 @@ gptq_status gptq_norm_tokens(const void* x, int32_t xt, int64_t n_tokens, int64_
   const Rows in_x{x, ldx * size_of(xt), d * size_of(xt)}, in_r{residual_or_null, ldr * size_of(rt), d * size_of(rt)};
   const Rows sum{sum_or_null, lds * size_of(rt), d * size_of(rt)}, y{y_or_null, d * size_of(yt), d * size_of(yt)};
   const Rows codes{codes_or_null, d, d};
+  const Rows weight{weight_or_null, d * size_of(wt), d * size_of(wt)};  // one row
+  const Rows sc{codes_or_null ? scales : nullptr, 4, 4}, sm{codes_or_null ? sums_or_null : nullptr, 4, 4};
   if (clobbers(sum, in_x, xt == rt, n_tokens) || clobbers(sum, in_r, true, n_tokens) || overlap(y, in_x, n_tokens) ||
       overlap(y, in_r, n_tokens) || overlap(y, sum, n_tokens) || overlap(codes, in_x, n_tokens) ||
       overlap(codes, in_r, n_tokens) || overlap(codes, sum, n_tokens) || overlap(codes, y, n_tokens))
+    return GPTQ_ERR_INVALID_ARG;
+  for (const Rows& small : {sc, sm})
+    if (overlap(small, in_x, n_tokens) || overlap(small, in_r, n_tokens) || overlap(small, sum, n_tokens) ||
+        overlap(small, y, n_tokens) || overlap(small, codes, n_tokens) || on_row(small, weight, n_tokens))
+      return GPTQ_ERR_INVALID_ARG;
+  if (overlap(sc, sm, n_tokens) || on_row(sum, weight, n_tokens) || on_row(y, weight, n_tokens) || on_row(codes, weight, n_tokens))
     return GPTQ_ERR_INVALID_ARG;
   gptq::NormCall c{};
   c.x = x;

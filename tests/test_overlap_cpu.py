@@ -54,3 +54,28 @@ def test_products_beside_rows_with_gaps(L):
         assert linear(at(2, off), r=at(2), ldr=1024) == st, off
     # over the residual itself
     assert linear(at(2), r=at(2)) == 4
+
+
+def test_norm_over_what_it_reads_or_writes(L):
+    """Every pair of what the norm reads and writes but the total over x or the residual."""
+    lib = L._lib()
+    base = dict(x=at(1), r=at(2), w=at(3), s=at(4), y=at(5), c=at(6), sc=at(7), sm=at(8))
+
+    def call(n=4, d=64, ld=64, lds=64, **kw):
+        a = dict(base, **kw)
+        return lib.gptq_norm_tokens(a["x"], 1, n, d, ld, a["r"], 1, ld, a["w"], 0, 1e-6, a["s"], lds, a["y"], 1, a["c"], a["sc"],
+                                    a["sm"], None)
+    place = dict(x=1, r=2, w=3, s=4, y=5, c=6, sc=7, sm=8)
+    size = dict(x=512, r=512, w=256, s=512, y=512, c=256, sc=16, sm=16)
+    for out in ("s", "y", "c", "sc", "sm"):
+        for other in place:
+            if other == out:
+                continue
+            for off in (0, size[other] - 2, 2 - size[out]):              # its first bytes, its last ones, from before it
+                if off == 0 and out == "s" and other in ("x", "r") or off == 0 and out in ("x", "r") and other == "s":
+                    continue                                              # the total in place
+                assert call(**{out: at(place[other], off)}) == 1, (out, other, off)
+    # in the middle of rows far apart
+    assert call(ld=4096, s=None, w=at(1, 3 * 8192 + 60), y=at(1, 3 * 8192 + 60)) == 1
+    assert call(ld=4096, lds=4096, s=at(3, -4096 * 2 * 2)) == 1          # the third row of the total on the weight
+    assert call(n=0) == 0
