@@ -14,6 +14,7 @@ layer `name`:
   name.scales   float16 [n_groups, d_out]          (the solve's fp32 scales, rounded)
   name.zeros    float16 [n_groups, d_out]          integer zero points (exact in float16)
   name.g_idx    int32   [d_in]                     original column -> group
+  name.bias     float   [d_out]                    only for layers that have one, as given
 and quantize_config.json with BaseQuantizeConfig's fields plus
 model_name_or_path and model_file_base_name.
 """
@@ -21,13 +22,20 @@ from __future__ import annotations
 
 import json
 import os
-from typing import Dict, Mapping, Tuple
+from typing import Dict, Mapping, Optional, Tuple
 
 import torch
 
 from ._lib import QuantizeConfig
 
 CONFIG_NAME = "quantize_config.json"
+
+
+def _bias(what: str, r: Mapping[str, torch.Tensor], d_out: int) -> Optional[torch.Tensor]:
+    bias = r.get("bias")
+    if bias is not None and (bias.shape != (d_out,) or not bias.is_floating_point()):
+        raise ValueError(f"{what}: a bias must be floating point [d_out], {d_out} entries")
+    return bias
 
 
 def model_file_base_name(bits: int, group_size: int) -> str:
@@ -37,8 +45,8 @@ def model_file_base_name(bits: int, group_size: int) -> str:
 def save_quantized(out_dir: str, layers: Mapping[str, Mapping[str, torch.Tensor]], cfg: QuantizeConfig,
                    model_name_or_path: str = "", true_sequential: bool = True) -> str:
     """Write the layers' qweight / scales / zeros / g_idx (as returned by
-    solve_layer or solve_layers_shared) and quantize_config.json into out_dir;
-    returns the weight file's path."""
+    solve_layer or solve_layers_shared), a layer's "bias" where it has one, and
+    quantize_config.json into out_dir; returns the weight file's path."""
     from safetensors.torch import save_file
     os.makedirs(out_dir, exist_ok=True)
     tensors: Dict[str, torch.Tensor] = {}
@@ -54,6 +62,9 @@ def save_quantized(out_dir: str, layers: Mapping[str, Mapping[str, torch.Tensor]
         tensors[f"{name}.scales"] = scales.detach().to(torch.float16).contiguous().cpu()
         tensors[f"{name}.zeros"] = zeros.detach().to(torch.float16).contiguous().cpu()
         tensors[f"{name}.g_idx"] = g_idx.detach().contiguous().cpu()
+        bias = _bias(f"save_quantized: {name}", r, qweight.shape[1])
+        if bias is not None:
+            tensors[f"{name}.bias"] = bias.detach().contiguous().cpu()
     base = model_file_base_name(cfg.bits, cfg.group_size)
     path = os.path.join(out_dir, base + ".safetensors")
     save_file(tensors, path, metadata={"format": "pt"})
@@ -68,7 +79,7 @@ def save_quantized(out_dir: str, layers: Mapping[str, Mapping[str, torch.Tensor]
 
 def load_quantized(in_dir: str, device="cpu") -> Tuple[QuantizeConfig, Dict[str, Dict[str, torch.Tensor]]]:
     """Read quantize_config.json, then the weight file it names; returns the
-    config and, per layer, qweight, scales, zeros (float16 as stored) and g_idx."""
+    config and, per layer, qweight, scales, zeros (float16 as stored), g_idx and a bias where the file has one."""
     from safetensors.torch import load_file
     with open(os.path.join(in_dir, CONFIG_NAME)) as f:
         conf = json.load(f)
@@ -92,7 +103,8 @@ def dequant_layer(r: Mapping[str, torch.Tensor], bits: int, device="cuda:0") -> 
     int32 qweight, zeros and g_idx, fp32 scales (the stored float16 values).
     When some 32-channel chunk spans several groups (act-order with dynamic
     groups) the layer is put in group order once by gptq_dequant_order, which
-    replaces qweight and g_idx and adds `order`; apply it with dequant_apply."""
+    replaces qweight and g_idx and adds `order`; apply it with dequant_apply.
+    A layer's bias is no part of this product: it is added to what that gives."""
     from ._lib import gptq_dequant_order
     g_host = r["g_idx"].detach().to("cpu", torch.int32)
     out = {"qweight": r["qweight"].to(device, torch.int32).contiguous(),
@@ -120,8 +132,8 @@ def dequant_apply(x: torch.Tensor, layer: Mapping[str, torch.Tensor], bits: int,
 def integer_layer(r: Mapping[str, torch.Tensor], bits: int, device="cuda:0") -> Dict[str, torch.Tensor]:
     """A loaded layer with one group per output channel (group_size -1) in the
     form the integer product reads, on `device`: int8 w [d_out, d_in], fp32
-    scales [d_out] (the stored float16 values) and, unless they are all zero,
-    int32 offsets [d_out].  It takes d_in * d_out bytes; the packed layer is
+    scales [d_out] (the stored float16 values), unless they are all zero int32
+    offsets [d_out], and the layer's bias, where it has one, in fp32.  It takes d_in * d_out bytes; the packed layer is
     not needed any more.  Apply it with integer_apply."""
     from ._lib import gptq_integer_weight
     if r["scales"].shape[0] != 1 or r["zeros"].shape[0] != 1:
@@ -137,12 +149,17 @@ def integer_layer(r: Mapping[str, torch.Tensor], bits: int, device="cuda:0") -> 
         raise ValueError(f"integer_layer: zero points outside the codes of {bits} bits")
     if most > 0:
         out["offsets"] = offsets
+    bias = _bias("integer_layer", r, out["scales"].numel())
+    if bias is not None:
+        out["bias"] = bias.to(dev, torch.float32).contiguous()
     return out
 
 
 def integer_apply(x, layer: Mapping[str, torch.Tensor], **kw) -> torch.Tensor:
-    """y = x W^T in 8-bit integers for a layer prepared by integer_layer; x as
-    gptq_integer_matmul takes it.  Layers that read the same x share its codes:
-    pass them what gptq_quantize_tokens returned for it."""
+    """y = x W^T + bias in 8-bit integers for a layer prepared by integer_layer
+    (without a "bias": x W^T); x, activation and residual as gptq_integer_matmul
+    takes them.  Layers that read the same x share its codes: pass them what
+    gptq_quantize_tokens returned for it."""
     from ._lib import gptq_integer_matmul
+    kw.setdefault("bias", layer.get("bias"))
     return gptq_integer_matmul(x, layer["w"], layer["scales"], layer.get("offsets"), **kw)
