@@ -559,24 +559,17 @@ def _activation(what: str, name: Optional[str]) -> int:
     return ACTIVATIONS[name]
 
 
-def _integer_x(what: str, x, offsets: bool):
-    """(x, its type code, scales, sums) of what a product in integers takes as x."""
-    x_scales = x_sums = None
-    if isinstance(x, tuple):
-        x, x_scales, x_sums = x
-        code = GPTQ_I8
-        m = x.shape[0]
-        if (x.dtype != torch.int8 or x_scales.shape != (m,) or x_scales.dtype != torch.float32
-                or not x_scales.is_contiguous() or (x_sums is not None and (x_sums.shape != (m,)
-                                                    or x_sums.dtype != torch.int32 or not x_sums.is_contiguous()))):
-            raise ValueError(f"{what}: expected the codes, scales and sums of gptq_quantize_tokens")
-        if offsets and x_sums is None:
-            raise ValueError(f"{what}: a layer with offsets needs the sums of the codes")
-    else:
-        code = _type_code(what, x.dtype)
-    if x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError(f"{what}: x must be 2-D with unit column stride")
-    return x, code, x_scales, x_sums
+def _integer_codes(what: str, x, offsets: bool):
+    """Codes, scales and sums that a product in integers takes as x."""
+    x, x_scales, x_sums = x
+    m = x.shape[0]
+    if (x.dtype != torch.int8 or x_scales.shape != (m,) or x_scales.dtype != torch.float32
+            or not x_scales.is_contiguous() or (x_sums is not None and (x_sums.shape != (m,)
+                                                or x_sums.dtype != torch.int32 or not x_sums.is_contiguous()))):
+        raise ValueError(f"{what}: expected the codes, scales and sums of gptq_quantize_tokens")
+    if offsets and x_sums is None:
+        raise ValueError(f"{what}: a layer with offsets needs the sums of the codes")
+    return x, x_scales, x_sums
 
 
 def _integer_layer_ok(what: str, d_in: int, d_out: int, w, w_scales, offsets, bias) -> None:
@@ -589,14 +582,11 @@ def _integer_layer_ok(what: str, d_in: int, d_out: int, w, w_scales, offsets, bi
         raise ValueError(f"{what}: a bias must be contiguous float32 [d_out]")
 
 
-def _integer_y(what: str, x, m: int, d_out: int, out_dtype, y):
-    if y is None:
-        yt = _type_code(what, out_dtype)
-        return x.new_empty((m, d_out), dtype=out_dtype), yt
-    yt = _type_code(what, y.dtype)
+def _integer_y(what: str, m: int, d_out: int, y: torch.Tensor) -> int:
+    """The type code of a y that the caller gives."""
     if y.shape != (m, d_out) or not y.is_contiguous():
         raise ValueError(f"{what}: y must be contiguous [m, d_out]")
-    return y, yt
+    return _type_code(what, y.dtype)
 
 
 def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Optional[torch.Tensor] = None,
@@ -615,8 +605,15 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
         with _on_stream(stream):
             return gptq_integer_matmul(x, w, w_scales, offsets, out_dtype, y, ws, None, bias, activation, residual)
     what = "gptq_integer_matmul"
-    x, code, x_scales, x_sums = _integer_x(what, x, offsets is not None)
-    act = _activation(what, activation)
+    x_scales = x_sums = None
+    if isinstance(x, tuple):
+        x, x_scales, x_sums = _integer_codes(what, x, offsets is not None)
+        code = GPTQ_I8
+    else:
+        code = _type_code(what, x.dtype)
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError(f"{what}: x must be 2-D with unit column stride")
+    act = 0 if activation is None else _activation(what, activation)
     dev = _on_device(what, x, w, w_scales, offsets, x_scales, x_sums, y, ws, bias, residual)
     m, d_in = x.shape
     d_out = w.shape[0]
@@ -627,7 +624,11 @@ def gptq_integer_matmul(x, w: torch.Tensor, w_scales: torch.Tensor, offsets: Opt
         if residual.shape != (m, d_out) or (residual.stride(1) != 1 and d_out > 1):
             raise ValueError(f"{what}: residual must be [m, d_out] with unit column stride")
         ldr = _row_stride(residual)
-    y, yt = _integer_y(what, x, m, d_out, out_dtype, y)
+    if y is None:
+        yt = _type_code(what, out_dtype)
+        y = x.new_empty((m, d_out), dtype=out_dtype)
+    else:
+        yt = _integer_y(what, m, d_out, y)
     lib = _lib()
     if ws is None:
         need = lib.gptq_integer_workspace_size(m, code, d_in, d_out)
@@ -664,14 +665,25 @@ def gptq_integer_gated(x, gate: Mapping[str, torch.Tensor], up: Mapping[str, tor
             return gptq_integer_gated(x, gate, up, activation, out_dtype, y, ws)
     what = "gptq_integer_gated"
     (gw, gs, go, gb), (uw, us, uo, ub) = ((t["w"], t["scales"], t.get("offsets"), t.get("bias")) for t in (gate, up))
-    x, code, x_scales, x_sums = _integer_x(what, x, go is not None or uo is not None)
+    x_scales = x_sums = None
+    if isinstance(x, tuple):
+        x, x_scales, x_sums = _integer_codes(what, x, go is not None or uo is not None)
+        code = GPTQ_I8
+    else:
+        code = _type_code(what, x.dtype)
+    if x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError(f"{what}: x must be 2-D with unit column stride")
     act = _activation(what, activation)
     dev = _on_device(what, x, gw, gs, go, gb, uw, us, uo, ub, x_scales, x_sums, y, ws)
     m, d_in = x.shape
     d_out = gw.shape[0]
     _integer_layer_ok(what, d_in, d_out, gw, gs, go, gb)
     _integer_layer_ok(what, d_in, d_out, uw, us, uo, ub)
-    y, yt = _integer_y(what, x, m, d_out, out_dtype, y)
+    if y is None:
+        yt = _type_code(what, out_dtype)
+        y = x.new_empty((m, d_out), dtype=out_dtype)
+    else:
+        yt = _integer_y(what, m, d_out, y)
     lib = _lib()
     if ws is None:
         need = lib.gptq_integer_gated_workspace_size(m, code, d_in, d_out)

@@ -285,10 +285,9 @@ gptq_status integer_go(gptq::IntCall* c, int64_t rows, int32_t yt, void* ws, siz
       return GPTQ_ERR_INVALID_ARG;
   }
   c->y_bf16 = yt == GPTQ_BF16;
-  const int cus = device_cus();
-  const size_t need = gptq::integer_matmul_workspace(c->m, c->d_in, rows, c->xt == GPTQ_I8, cus);
-  if (need > 0 && (!ws || ws_bytes < need || !aligned256(ws))) return GPTQ_ERR_WORKSPACE;
-  return from_hip(gptq::integer_launch(*c, ws, cus, static_cast<hipStream_t>(stream)));
+  bool fits = false;
+  const hipError_t e = gptq::integer_launch(*c, ws, ws_bytes, device_cus(), static_cast<hipStream_t>(stream), &fits);
+  return fits ? from_hip(e) : GPTQ_ERR_WORKSPACE;
 }
 
 bool activation_ok(int32_t a) { return a >= GPTQ_ACT_NONE && a <= GPTQ_ACT_SILU; }
@@ -318,13 +317,13 @@ bool overlap(const Rows& a, const Rows& b, int64_t m) {
     return static_cast<wide_t>(reinterpret_cast<uintptr_t>(r.at)) + static_cast<wide_t>(m - 1) * static_cast<wide_t>(r.lead) +
            static_cast<wide_t>(r.width);
   };
+  if (wide_t{reinterpret_cast<uintptr_t>(a.at)} >= end(b) || wide_t{reinterpret_cast<uintptr_t>(b.at)} >= end(a)) return false;
   const auto whole = [&](const Rows& r) { return m == 1 || r.lead == r.width; };
   if (whole(a)) return meets(b, m, reinterpret_cast<uintptr_t>(a.at), end(a));
   if (whole(b)) return meets(a, m, reinterpret_cast<uintptr_t>(b.at), end(b));
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
   const Rows &first = a0 < b0 ? a : b, &second = a0 < b0 ? b : a;
   const uintptr_t apart = a0 < b0 ? b0 - a0 : a0 - b0;
-  if (wide_t{reinterpret_cast<uintptr_t>(second.at)} >= end(first)) return false;
   if (a.lead != b.lead) return true;
   const int64_t off = static_cast<int64_t>(apart % static_cast<uintptr_t>(a.lead));  // inside a row of the first
   return off < first.width || off + second.width > a.lead;

@@ -170,8 +170,9 @@ struct IntCall {
 };
 // whether the product's own kernel reads x (not only the codes' kernel before it)
 bool integer_reads_x(int64_t m, int64_t d_in, bool codes_given);
-// workspace: integer_matmul_workspace of the rows of both layers
-hipError_t integer_launch(const IntCall& c, void* ws, int n_cu, hipStream_t stream);
+// workspace: integer_matmul_workspace of the rows of both layers; where it does not fit (missing, too small or misaligned)
+// nothing is launched
+hipError_t integer_launch(const IntCall& c, void* ws, size_t ws_bytes, int n_cu, hipStream_t stream, bool* fits);
 
 // ------------------------------------------------------------------- norm --
 struct NormCall {

@@ -1134,6 +1134,7 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
     else least = kBlockLaunch + k * n / kBlockRate + std::ceil(rounds) * (kBlockRound + kBlockToken * std::min(rows, 64.0) * k);
   }
   const int64_t steps = (d_in + kTStep - 1) / kTStep;
+  const double sums = 8.0 * rows * n / kJoinRate;  // of a slice, there and back
   struct Tile {
     int kind, high, wide;
     double step, full;  // us a step: of a round with one workgroup a CU, with two
@@ -1143,14 +1144,14 @@ IntPlan int_plan(int64_t m, int64_t d_in, int64_t d_out, int n_cu) {
     // Many tokens of long rows leave the L2s between their strips of 64 (2048 x 11008 -> 2048: 77 us, 62 in slices
     // of 256-row tiles; 1500 x 8224 -> 1800: 67 and 50, though 1030 of them 39 and 42): outside the fitted terms.
     if (t.kind == 3 && m > 1024 && d_in > 8192) continue;
-    const int64_t count = ((m + t.high - 1) / t.high) * ((d_out + t.wide - 1) / t.wide);
-    for (int64_t sl = 1; sl <= 16 && (sl == 1 || steps / sl >= 4); sl *= 2) {
-      const int64_t per = (steps + sl - 1) / sl, slices = (steps + per - 1) / per;
-      const int64_t room = t.kind == 1 ? 2 * n_cu : n_cu, whole = count * slices / room, rest = count * slices % room;
-      const double last = rest == 0 ? 0.0 : rest <= n_cu ? t.step : t.full;
-      const double work = static_cast<double>(per) * (static_cast<double>(whole) * t.full + last);
-      double cost = kTileLaunch + std::max(work, k * (n + rows) / kTileRate);
-      if (slices > 1) cost += kJoinLaunch + 8.0 * static_cast<double>(slices) * rows * n / kJoinRate;
+    const double count = static_cast<double>(((m + t.high - 1) / t.high) * ((d_out + t.wide - 1) / t.wide));
+    const double room = t.kind == 1 ? 2.0 * n_cu : n_cu, bytes = k * (n + rows) / kTileRate;
+    for (int sl = 0; sl <= 4 && (sl == 0 || steps >> sl >= 4); ++sl) {  // 2^sl slices
+      const int64_t per = (steps + (int64_t{1} << sl) - 1) >> sl, slices = (steps + per - 1) / per;
+      const double parts = count * static_cast<double>(slices), whole = std::floor(parts / room), rest = parts - whole * room;
+      const double last = rest <= 0.0 ? 0.0 : rest <= n_cu ? t.step : t.full;
+      double cost = kTileLaunch + std::max(static_cast<double>(per) * (whole * t.full + last), bytes);
+      if (slices > 1) cost += kJoinLaunch + static_cast<double>(slices) * sums;
       if (cost < least) {
         least = cost;
         a.kind = t.kind;
@@ -1209,10 +1210,16 @@ void tile_go(const IntParams& p, const TileGrid& g, const Epilogue<E>& ep, unsig
 size_t up256(size_t v) { return (v + 255) & ~size_t{255}; }
 }  // namespace
 
+namespace {
+size_t plan_workspace(const IntPlan& plan, int64_t m, int64_t d_in, bool codes_given) {
+  const size_t part = up256(plan.partial_bytes);
+  return codes_given || fuses(m, d_in) ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
+}
+}  // namespace
+
 // workspace: the K slices' sums, then (x not given as codes) codes, scales and sums
 size_t integer_matmul_workspace(int64_t m, int64_t d_in, int64_t d_out, bool codes_given, int n_cu) {
-  const size_t part = up256(int_plan(m, d_in, d_out, n_cu).partial_bytes);
-  return codes_given || fuses(m, d_in) ? part : part + up256(static_cast<size_t>(m) * d_in) + 2 * up256(static_cast<size_t>(m) * 4);
+  return plan_workspace(int_plan(m, d_in, d_out, n_cu), m, d_in, codes_given);
 }
 
 bool integer_reads_x(int64_t m, int64_t d_in, bool codes_given) { return codes_given || fuses(m, d_in); }
@@ -1261,10 +1268,13 @@ hipError_t product_go(const IntParams& p, const IntPlan& plan, const Epilogue<E>
 }
 }  // namespace
 
-hipError_t integer_launch(const IntCall& c, void* ws, int n_cu, hipStream_t st) {
+hipError_t integer_launch(const IntCall& c, void* ws, size_t ws_bytes, int n_cu, hipStream_t st, bool* fits) {
   const bool gated = c.up.w != nullptr;
   const int64_t rows = gated ? 2 * c.d_out : c.d_out;
   const IntPlan plan = int_plan(c.m, c.d_in, rows, n_cu);
+  const size_t need = plan_workspace(plan, c.m, c.d_in, c.xt == kXInt8);
+  *fits = need == 0 || (ws && ws_bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
+  if (!*fits) return hipSuccess;
   IntParams p{};
   p.x = static_cast<const int8_t*>(c.x);
   p.ldx = c.ldx;
