@@ -100,7 +100,7 @@ GPTQ_DEV float slope_of(const Shape<S>& sh, int head) {
   return 0.f;
 }
 // The factor of a key's products: its scale, the score's and, before a cap, twice.
-// Where a small cap takes a finite scale past fp32, the largest: tanh is 1 there.
+// Where a small cap takes a finite scale past fp32, the largest: tanh is 1 there, for products from 2^-122 on.
 template <int S>
 GPTQ_DEV float key_factor(const Shape<S>& sh, float ks, float scale_log2e) {
   const float v = ks * scale_log2e;

@@ -182,10 +182,12 @@ struct Epilogue<kGated> {
 };
 
 // Logistic forms go through 2^x and a reciprocal (an ulp each; the exponent's
-// rounding adds |z| 2^-24 where the result is next to 0).  gelu takes z Phi(z) with
-// Phi(-a) = erfc(a / sqrt(2)) / 2 = t 2^(P(t) - a^2 log2(e) / 2), t = 1 / (1 + a / sqrt(8)),
-// P a polynomial of degree 9 fitted to the exponent, off by 2^-23 in all: the relative
-// error holds far below 0, where 1 + erf would cancel.  NaN passes through all of them.
+// rounding adds |z| 2^-24 where the result is next to 0).  gelu takes z Phi(z), Phi(-a) = erfc(a / sqrt(2)) / 2, with erfc in
+// the form t exp(P(t) - x^2), t = 1 / (1 + x / 2), of Press, Teukolsky, Vetterling and Flannery (Numerical Recipes,
+// the chapter on special functions): here t 2^(P(t) - a^2 log2(e) / 2), t = 1 / (1 + a / sqrt(8)), P of degree 9 fitted anew to
+// the exponent.  The fit is off by 2^-22 relative at any a, so that the result holds far below 0, where 1 + erf would
+// cancel; the exponent is rounded in fp32 at its own size, which adds about a^2 2^-24: 2^-20 in all at
+// a = 4, 2^-17 at 12, always under (a^2 + 18) 2^-23.  NaN passes through all of them.
 GPTQ_DEV float logistic(float z, float t) {  // z / (1 + e^-t)
   return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * t));
 }
@@ -609,9 +611,9 @@ void stream_go(const IntParams& p, const Epilogue<E>& ep, int fused, hipStream_t
 // LDS rows are 128 bytes; 16-byte chunk c of row r sits at c ^ ((r >> 1) & 7), so
 // 16 lanes that read one chunk of 16 rows touch all 64 banks once.
 // The way into LDS is what the tiles wait for beside the products: a KB of it takes a CU
-// some 66 cycles in pieces of 64 bytes and 45 in whole lines of 128 (2048 x 28672 ->
-// 8192: 405 us and 356; wider pieces of a row are no faster), whatever the depth of
-// the ring; with nothing else to do 33, through registers too.  2048 x 28672 -> 8192 with a residual
+// some 66 cycles in pieces of 64 bytes and 45 in whole lines of 128 (the kernel of 2048 x 28672 ->
+// 8192 alone, without a residual: 405 us and 356; wider pieces of a row are no faster), whatever the depth of
+// the ring; with nothing else to do 33, through registers too.  That kernel with a residual
 // 370 us, 2.6 POP/s, the gated 2048 x 8192 -> 2 x 28672 770 us, 2.5 POP/s (an 8192-cubed library
 // product 2.07), matrix cores busy two thirds of the cycles; 509 x 11008 -> 4096 36 us.
 constexpr int kTStep = 128;
@@ -984,7 +986,8 @@ __global__ __launch_bounds__(256) void integer_tile_kernel(IntParams p, TileGrid
 #pragma unroll
     for (int u = 0; u < kSlots; ++u) {
       // half of a step's loads in each of two quarters: all in one keep the wave waiting at the address unit,
-      // later ones arrive late (2048 x 28672 -> 8192 419 us with all in the first, 422 in three, 410 so)
+      // later ones arrive late (a call of 2048 x 28672 -> 8192 with a residual, codes' launch included, 419 us with all in
+      // the first, 422 in three, 410 so)
       issue_x(s + u + kSlots - 1, u + kSlots - 1);
       tile_quarter<WM, WN, kPA>(a0, b0, slotA(u), slotB(u), oa[1], ob[1], a1, b1, acc);
       tile_quarter<WM, WN, 0>(a1, b1, slotA(u), slotB(u), oa[2], ob[2], a0, b0, acc);
